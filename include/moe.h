@@ -416,6 +416,129 @@ int moe_router_backward(const moe_config_t* cfg, const moe_routes_t* routes, con
                         const float* dprob, void* dx, float* dw_router, float* dbias,
                         void* workspace, size_t ws_bytes, cudaStream_t stream);
 
+/* ---- Shared expert ----------------------------------------------------------
+ * A gated feed-forward block that every token passes, next to the routed
+ * experts (an extension beyond the pages, which describe the routed experts
+ * only): no routing, no capacity, any number of tokens.
+ *   g = x W_gate, u = x W_up, h = act(g) u, y = h W_down (+ add)
+ * Products are summed in fp32; h is rounded to bf16 once, y once after `add`.
+ *
+ * Training keeps the pre-activations [g | u] in 8 bits (an activation
+ * checkpoint) instead of in bf16: MX blocks of 32 consecutive values, one E4M3
+ * code a value and one E8M0 byte a block, value = decode(code) * 2^(byte-127),
+ * quantised from the fp32 sums as moe_quantize_mx_fp8 does (power-of-two scale
+ * floor(log2(max|v|)) - 8, nearest even, saturating at +-448). A block that
+ * holds an infinity or a NaN gets the byte 255, which reads as NaN. The
+ * backward takes act, its derivative and h from the kept values. */
+
+/* Shape of the block.
+ *  n_tokens   N  0 or more (0: outputs of no rows; gradients of weights are zero)
+ *  hidden     H  multiple of 8
+ *  inter      I  multiple of 32
+ *  activation MOE_ACT_SWIGLU or MOE_ACT_GEGLU
+ *  grad_f32   0: dw13, dw2 are bf16; 1: they are f32
+ * N, H and 2*I at most 2^24, N*H and N*2I may pass 2^31. */
+typedef struct moe_shared_config {
+  int32_t n_tokens;
+  int32_t hidden;
+  int32_t inter;
+  int32_t activation;
+  int32_t grad_f32;
+} moe_shared_config_t;
+
+/* Forward. All matrices row-major, contiguous, 16-byte aligned.
+ *  x   [N,H] bf16
+ *  w13 [2I,H] bf16: rows [0,I) are W_gate^T, rows [I,2I) W_up^T (as one expert
+ *      of moe_pack_w13)
+ *  w2  [H,I] bf16: row j is W_down[:,j] (as one expert of moe_pack_w2)
+ *  add [N,H] bf16 added to the result (for example the routed experts' y), or
+ *      NULL; may be y itself
+ *  h   [N,I] bf16 scratch, receives act(g) u
+ *  y   [N,H] bf16 output */
+int moe_shared_forward(const moe_shared_config_t* cfg, const void* x, const void* w13,
+                       const void* w2, const void* add, void* h, void* y, cudaStream_t stream);
+
+/* moe_shared_forward that also writes the checkpoint.
+ *  ck    [N,2I] u8 E4M3 codes of g (columns [0,I)) and u (columns [I,2I))
+ *  ck_sf [N,2I/32] u8 E8M0 bytes */
+int moe_shared_forward_train(const moe_shared_config_t* cfg, const void* x, const void* w13,
+                             const void* w2, const void* add, void* h, void* y, void* ck,
+                             void* ck_sf, cudaStream_t stream);
+
+/* Bytes of scratch moe_shared_backward needs: [dg | du] and h in bf16. */
+int64_t moe_shared_backward_workspace_bytes(const moe_shared_config_t* cfg);
+
+/* Backward from the checkpoint: with g, u its values and a = act(g) u,
+ *   da = dy W_down^T, dg = da u act'(g), du = da act(g)
+ *   dx = dg W_gate^T + du W_up^T (+ dx_add), dw13 = [dg du]^T x, dw2 = dy^T a
+ *  dy     [N,H] bf16
+ *  dx_add [N,H] bf16 added to dx (for example the routed experts' dX), or NULL;
+ *         may be dx itself
+ *  dx     [N,H] bf16 output
+ *  dw13   [2I,H], dw2 [H,I] outputs, bf16 or f32 (cfg->grad_f32), overwritten
+ *  workspace/ws_bytes  moe_shared_backward_workspace_bytes, 16-byte aligned
+ * fp32 sums; dg, du and a are rounded to bf16 as operands of the products.
+ * Deterministic. */
+int moe_shared_backward(const moe_shared_config_t* cfg, const void* x, const void* w13,
+                        const void* w2, const void* ck, const void* ck_sf, const void* dy,
+                        const void* dx_add, void* dx, void* dw13, void* dw2, void* workspace,
+                        size_t ws_bytes, cudaStream_t stream);
+
+/* ---- 4-bit weights for a few tokens ------------------------------------------
+ * Products for the decode steps of serving, where the time is that of reading
+ * the weights (an extension beyond the pages). A 4-bit matrix [R, C]: byte j of
+ * row r holds columns 2j (low half) and 2j+1 (high half) as value + 8, value in
+ * -8..7, and scale[r, c/group] (bf16) multiplies `group` consecutive columns:
+ *   w[r,c] = scale[r, c/group] * (code - 8)
+ * group is 32, 64 or 128 and divides C. */
+
+/* Codes and scales of a bf16 matrix of finite values: scale = bf16(max|w| / 7)
+ * of the group (1 where that is 0), code = w / scale rounded to nearest even,
+ * within -8..7, plus 8.
+ *  m [rows, cols] bf16; q [rows, cols/2] u8; scale [rows, cols/group] bf16 */
+int moe_w4_quantize(const void* m, int64_t rows, int cols, int group, void* q, void* scale,
+                    cudaStream_t stream);
+
+/* y[t,:] = w x[t,:] for n tokens: x [n, cols] bf16, q/scale [rows, cols], y
+ * [n, rows] bf16; fp32 sums, rounded once. n 0..1024. x and q 16-byte aligned. */
+int moe_w4_matvec(const void* x, const void* q, const void* scale, int n, int rows, int cols,
+                  int group, void* y, cudaStream_t stream);
+
+/* Shape of a decode batch through 4-bit experts.
+ *  n_tokens N, hidden H, n_experts E (1..256), top_k K (1..16), inter I;
+ *  group divides H and I; N*K at most 1024. */
+typedef struct moe_w4_config {
+  int32_t n_tokens;
+  int32_t hidden;
+  int32_t n_experts;
+  int32_t top_k;
+  int32_t inter;
+  int32_t group;
+  int32_t activation;
+} moe_w4_config_t;
+
+/* Bytes of scratch moe_w4_ffn_forward needs (h of every route). */
+int64_t moe_w4_workspace_bytes(const moe_w4_config_t* cfg);
+
+/* The experts of a decode batch, from the router's choice to the layer's output:
+ *   y[t] = add[t] + sum_k topk_p[t,k] W2[e] (act(W13g[e] x_t) * (W13u[e] x_t)),
+ *   e = topk_ids[t,k]
+ *  topk_ids  [N,K] i32, topk_p [N,K] f32: as in moe_routes (moe_route_align); a
+ *            route whose id is outside 0..E-1 (-1: no route) contributes nothing,
+ *            whatever its probability holds
+ *  x         [N,H] bf16
+ *  w13q      [E,2I,H/2] u8, w13_scale [E,2I,H/group] bf16 (packed w13 rows)
+ *  w2q       [E,H,I/2] u8, w2_scale [E,H,I/group] bf16 (packed w2 rows)
+ *  add       [N,H] bf16, or NULL; may be y itself
+ *  y         [N,H] bf16 output (add, or 0, for a token without routes)
+ *  workspace/ws_bytes  moe_w4_workspace_bytes, 16-byte aligned
+ * fp32 sums; the activations are rounded to bf16 between the two products.
+ * Deterministic: routes are summed in a fixed order. */
+int moe_w4_ffn_forward(const moe_w4_config_t* cfg, const int32_t* topk_ids, const float* topk_p,
+                       const void* x, const void* w13q, const void* w13_scale, const void* w2q,
+                       const void* w2_scale, const void* add, void* y, void* workspace,
+                       size_t ws_bytes, cudaStream_t stream);
+
 /* Where moe_route_align leaves the router logits l [N,E] f32 (before the
  * softmax, bias included) inside its workspace; NULL for an invalid config or
  * workspace. Host-side pointer arithmetic only. */

@@ -31,6 +31,11 @@ __all__ = [
     "ffn_forward_train", "backward_workspace_bytes", "alloc_backward_workspace", "ffn_backward",
     "router_backward_workspace_bytes", "alloc_router_backward_workspace", "router_backward",
     "Ladder", "ladder_pick",
+    "SharedConfig", "alloc_shared_buffers", "alloc_shared_checkpoint",
+    "shared_backward_workspace_bytes", "alloc_shared_backward_workspace", "shared_forward",
+    "shared_forward_train", "shared_backward",
+    "W4Config", "W4Weights", "w4_quantize", "w4_workspace_bytes", "alloc_w4_workspace",
+    "w4_matvec", "w4_ffn_forward",
 ]
 
 _PKG = os.path.dirname(os.path.abspath(__file__))
@@ -72,6 +77,27 @@ class Config(ctypes.Structure):
                          renorm, len(lad), ladder_den,
                          ctypes.cast(self._ladder, ctypes.POINTER(ctypes.c_int32)), activation,
                          int(bool(prob_in_act)), None)
+
+
+class SharedConfig(ctypes.Structure):
+    """Mirror of moe_shared_config_t: the shared expert's shape. grad_f32: weight
+    gradients in f32 instead of bf16."""
+    _fields_ = [(n, ctypes.c_int32) for n in ("n_tokens", "hidden", "inter", "activation",
+                                              "grad_f32")]
+
+    def __init__(self, n_tokens, hidden, inter, activation=ACT_SWIGLU, grad_f32=0):
+        super().__init__(n_tokens, hidden, inter, activation, int(bool(grad_f32)))
+
+
+class W4Config(ctypes.Structure):
+    """Mirror of moe_w4_config_t: a decode batch through experts with 4-bit
+    weights, one bf16 scale per `group` (32, 64 or 128) columns."""
+    _fields_ = [(n, ctypes.c_int32) for n in ("n_tokens", "hidden", "n_experts", "top_k", "inter",
+                                              "group", "activation")]
+
+    def __init__(self, n_tokens, hidden, n_experts, top_k, inter, group=128,
+                 activation=ACT_SWIGLU):
+        super().__init__(n_tokens, hidden, n_experts, top_k, inter, group, activation)
 
 
 class _RoutesC(ctypes.Structure):
@@ -137,6 +163,20 @@ def lib():
         L.moe_ladder_forward.argtypes = [P, ctypes.c_int32, P, ctypes.POINTER(ctypes.c_int)]
         L.moe_ladder_destroy.argtypes = [P]
         for name in ("moe_ladder_create", "moe_ladder_forward", "moe_ladder_destroy"):
+            getattr(L, name).restype = I32
+        SP, WP = ctypes.POINTER(SharedConfig), ctypes.POINTER(W4Config)
+        L.moe_shared_backward_workspace_bytes.argtypes = [SP]
+        L.moe_w4_workspace_bytes.argtypes = [WP]
+        L.moe_shared_forward.argtypes = [SP] + [P] * 7
+        L.moe_shared_forward_train.argtypes = [SP] + [P] * 9
+        L.moe_shared_backward.argtypes = [SP] + [P] * 11 + [SZ, P]
+        L.moe_w4_quantize.argtypes = [P, I64, I32, I32, P, P, P]
+        L.moe_w4_matvec.argtypes = [P, P, P, I32, I32, I32, I32, P, P]
+        L.moe_w4_ffn_forward.argtypes = [WP] + [P] * 10 + [SZ, P]
+        for name in ("moe_shared_backward_workspace_bytes", "moe_w4_workspace_bytes"):
+            getattr(L, name).restype = I64
+        for name in ("moe_shared_forward", "moe_shared_forward_train", "moe_shared_backward",
+                     "moe_w4_quantize", "moe_w4_matvec", "moe_w4_ffn_forward"):
             getattr(L, name).restype = I32
         L.moe_pack_w13.argtypes = [CP, P, P, P, P]
         L.moe_pack_w2.argtypes = [CP, P, P, P]
@@ -469,6 +509,180 @@ def forward(cfg: Config, x, w_router, bias, w13, w2, routes: Routes, workspace, 
     route_align(cfg, x, w_router, bias, routes, workspace, stream)
     ffn_forward(cfg, routes, x, w13, w2, h, o, stream)
     combine(cfg, routes, o, y, stream)
+
+
+# ------------------------------------------------------------------ shared expert
+def _need(fn: str, dtype, **named) -> None:
+    """Refuses a tensor of another shape or type, one in host memory, or one
+    whose rows do not lie one after another (the library is given addresses
+    only). Each keyword is (tensor, shape)."""
+    for name, (t, shape) in named.items():
+        if t.dtype != dtype or t.shape != shape or not t.is_contiguous() or not t.is_cuda:
+            raise ValueError("%s: %s must be a contiguous %s CUDA tensor of shape %s, got %s %s on %s%s" % (
+                fn, name, str(dtype).replace("torch.", ""), tuple(shape),
+                str(t.dtype).replace("torch.", ""), tuple(t.shape), t.device,
+                "" if t.is_contiguous() else ", not contiguous"))
+
+
+def alloc_shared_buffers(cfg: SharedConfig, device):
+    """h [N,I] and y [N,H] bf16 for shared_forward."""
+    import torch
+    bf = dict(dtype=torch.bfloat16, device=device)
+    return (torch.empty((cfg.n_tokens, cfg.inter), **bf),
+            torch.empty((cfg.n_tokens, cfg.hidden), **bf))
+
+
+def alloc_shared_checkpoint(cfg: SharedConfig, device):
+    """ck [N,2I] and ck_sf [N,2I/32] u8: the 8-bit pre-activations of one step."""
+    import torch
+    u8 = dict(dtype=torch.uint8, device=device)
+    return (torch.empty((cfg.n_tokens, 2 * cfg.inter), **u8),
+            torch.empty((cfg.n_tokens, cfg.inter // 16), **u8))
+
+
+def shared_backward_workspace_bytes(cfg: SharedConfig) -> int:
+    return _q("moe_shared_backward_workspace_bytes", cfg)
+
+
+def alloc_shared_backward_workspace(cfg: SharedConfig, device):
+    import torch
+    return torch.empty(max(shared_backward_workspace_bytes(cfg), 256), dtype=torch.uint8,
+                       device=device)
+
+
+def _shared_operands(fn, cfg, x, w13, w2, add, add_name):
+    import torch
+    N, H, I = cfg.n_tokens, cfg.hidden, cfg.inter
+    _need(fn, torch.bfloat16, x=(x, (N, H)), w13=(w13, (2 * I, H)), w2=(w2, (H, I)))
+    if add is not None:
+        _need(fn, torch.bfloat16, **{add_name: (add, (N, H))})
+
+
+def shared_forward(cfg: SharedConfig, x, w13, w2, h, y, add=None, stream=None) -> None:
+    """y = (act(x W_gate) * (x W_up)) W_down (+ add): w13 [2I,H] and w2 [H,I] bf16
+    (one expert of pack_w13 / pack_w2), h [N,I] scratch; add may be y."""
+    import torch
+    _shared_operands("shared_forward", cfg, x, w13, w2, add, "add")
+    _need("shared_forward", torch.bfloat16, h=(h, (cfg.n_tokens, cfg.inter)),
+          y=(y, (cfg.n_tokens, cfg.hidden)))
+    _check("moe_shared_forward",
+           lib().moe_shared_forward(ctypes.byref(cfg), _ptr(x), _ptr(w13), _ptr(w2), _ptr(add),
+                                    _ptr(h), _ptr(y), _stream(stream)))
+
+
+def shared_forward_train(cfg: SharedConfig, x, w13, w2, h, y, ck, ck_sf, add=None,
+                         stream=None) -> None:
+    """shared_forward that also keeps the pre-activations [g | u] in 8 bits
+    (alloc_shared_checkpoint) for shared_backward."""
+    import torch
+    _shared_operands("shared_forward_train", cfg, x, w13, w2, add, "add")
+    N, H, I = cfg.n_tokens, cfg.hidden, cfg.inter
+    _need("shared_forward_train", torch.bfloat16, h=(h, (N, I)), y=(y, (N, H)))
+    _need("shared_forward_train", torch.uint8, ck=(ck, (N, 2 * I)), ck_sf=(ck_sf, (N, I // 16)))
+    _check("moe_shared_forward_train",
+           lib().moe_shared_forward_train(ctypes.byref(cfg), _ptr(x), _ptr(w13), _ptr(w2),
+                                          _ptr(add), _ptr(h), _ptr(y), _ptr(ck), _ptr(ck_sf),
+                                          _stream(stream)))
+
+
+def shared_backward(cfg: SharedConfig, x, w13, w2, ck, ck_sf, dy, dx, dw13, dw2, workspace,
+                    dx_add=None, stream=None) -> None:
+    """Gradients from the 8-bit checkpoint: dx [N,H] bf16 (+ dx_add, which may be
+    dx), dw13 [2I,H] and dw2 [H,I] (bf16, or f32 with cfg.grad_f32; overwritten)."""
+    import torch
+    _shared_operands("shared_backward", cfg, x, w13, w2, dx_add, "dx_add")
+    N, H, I = cfg.n_tokens, cfg.hidden, cfg.inter
+    _need("shared_backward", torch.bfloat16, dy=(dy, (N, H)), dx=(dx, (N, H)))
+    _need("shared_backward", torch.uint8, ck=(ck, (N, 2 * I)), ck_sf=(ck_sf, (N, I // 16)))
+    _need("shared_backward", torch.float32 if cfg.grad_f32 else torch.bfloat16,
+          dw13=(dw13, (2 * I, H)), dw2=(dw2, (H, I)))
+    _check("moe_shared_backward",
+           lib().moe_shared_backward(ctypes.byref(cfg), _ptr(x), _ptr(w13), _ptr(w2), _ptr(ck),
+                                     _ptr(ck_sf), _ptr(dy), _ptr(dx_add), _ptr(dx), _ptr(dw13),
+                                     _ptr(dw2), _ptr(workspace),
+                                     workspace.numel() * workspace.element_size(),
+                                     _stream(stream)))
+
+
+# ------------------------------------------------------------------ 4-bit weights
+def w4_quantize(m, group: int, q, scale, stream=None) -> None:
+    """4-bit codes q [rows, cols/2] u8 and bf16 scales [rows, cols/group] of a
+    bf16 matrix m [rows, cols]."""
+    import torch
+    rows, cols = m.shape
+    _need("w4_quantize", torch.bfloat16, m=(m, (rows, cols)), scale=(scale, (rows, cols // group)))
+    _need("w4_quantize", torch.uint8, q=(q, (rows, cols // 2)))
+    _check("moe_w4_quantize", lib().moe_w4_quantize(_ptr(m), int(rows), int(cols), int(group),
+                                                    _ptr(q), _ptr(scale), _stream(stream)))
+
+
+class W4Weights:
+    """Packed expert weights w13 [E,2I,H] and w2 [E,H,I] in 4 bits, quantised once."""
+
+    def __init__(self, w13, w2, group: int = 128, stream=None):
+        import torch
+        E, I2, H = w13.shape
+        I = w2.shape[2]
+        dev = w13.device
+        self.group = group
+        self.w13q = torch.empty((E, I2, H // 2), dtype=torch.uint8, device=dev)
+        self.w13_scale = torch.empty((E, I2, H // group), dtype=torch.bfloat16, device=dev)
+        self.w2q = torch.empty((E, H, I // 2), dtype=torch.uint8, device=dev)
+        self.w2_scale = torch.empty((E, H, I // group), dtype=torch.bfloat16, device=dev)
+        w4_quantize(w13.view(E * I2, H), group, self.w13q.view(E * I2, H // 2),
+                    self.w13_scale.view(E * I2, H // group), stream)
+        w4_quantize(w2.view(E * H, I), group, self.w2q.view(E * H, I // 2),
+                    self.w2_scale.view(E * H, I // group), stream)
+
+
+def w4_workspace_bytes(cfg: W4Config) -> int:
+    return _q("moe_w4_workspace_bytes", cfg)
+
+
+def alloc_w4_workspace(cfg: W4Config, device):
+    import torch
+    return torch.empty(max(w4_workspace_bytes(cfg), 256), dtype=torch.uint8, device=device)
+
+
+def w4_matvec(x, q, scale, y, stream=None) -> None:
+    """y [n, rows] = x [n, cols] . w^T for a 4-bit matrix: q [rows, cols/2] u8,
+    scale [rows, cols/group] bf16."""
+    import torch
+    n, cols = x.shape
+    rows, groups = scale.shape
+    group = cols // groups if groups else 0
+    _need("w4_matvec", torch.bfloat16, x=(x, (n, cols)), scale=(scale, (rows, groups)),
+          y=(y, (n, rows)))
+    _need("w4_matvec", torch.uint8, q=(q, (rows, cols // 2)))
+    if group * groups != cols:
+        raise ValueError("w4_matvec: %d scales a row do not divide %d columns" % (groups, cols))
+    _check("moe_w4_matvec", lib().moe_w4_matvec(_ptr(x), _ptr(q), _ptr(scale), n, rows, cols, group,
+                                                _ptr(y), _stream(stream)))
+
+
+def w4_ffn_forward(cfg: W4Config, topk_ids, topk_p, x, w13q, w13_scale, w2q, w2_scale, y,
+                   workspace, add=None, stream=None) -> None:
+    """The chosen experts of a decode batch: y[t] = add[t] + sum_k p[t,k] FFN_e(x_t),
+    e = topk_ids[t,k] (routes.topk_ids and routes.topk_p of route_align); an id of
+    -1 is no route."""
+    import torch
+    N, H, E, K, I, g = cfg.n_tokens, cfg.hidden, cfg.n_experts, cfg.top_k, cfg.inter, cfg.group
+    fn = "w4_ffn_forward"
+    if g <= 0:
+        raise MoEError("moe_w4_ffn_forward", MOE_ERR_INVALID_ARG)
+    _need(fn, torch.int32, topk_ids=(topk_ids, (N, K)))
+    _need(fn, torch.float32, topk_p=(topk_p, (N, K)))
+    _need(fn, torch.uint8, w13q=(w13q, (E, 2 * I, H // 2)), w2q=(w2q, (E, H, I // 2)))
+    _need(fn, torch.bfloat16, x=(x, (N, H)), y=(y, (N, H)),
+          w13_scale=(w13_scale, (E, 2 * I, H // g)), w2_scale=(w2_scale, (E, H, I // g)))
+    if add is not None:
+        _need(fn, torch.bfloat16, add=(add, (N, H)))
+    _check("moe_w4_ffn_forward",
+           lib().moe_w4_ffn_forward(ctypes.byref(cfg), _ptr(topk_ids), _ptr(topk_p), _ptr(x),
+                                    _ptr(w13q), _ptr(w13_scale), _ptr(w2q), _ptr(w2_scale),
+                                    _ptr(add), _ptr(y), _ptr(workspace),
+                                    workspace.numel() * workspace.element_size(),
+                                    _stream(stream)))
 
 
 def launch_count() -> int:

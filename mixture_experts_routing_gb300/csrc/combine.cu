@@ -7,6 +7,7 @@
 // row; 16-byte vector loads and stores; fp32 accumulation in k order.
 #include <cuda_fp8.h>
 
+#include "act.cuh"
 #include "moe_internal.h"
 #include "ptx.cuh"
 
@@ -281,21 +282,6 @@ __global__ void __launch_bounds__(kQuantWarps * 32) quantize_rows_fp8_reg_kernel
 // 4b..4b+3 hold block b's 32 values (one 16-byte group each) and combine their
 // maxima with two shuffles.
 constexpr int kMxWarps = 8;
-
-// 2^-s for s in [-127, 127], from its bits (2^-127 is the subnormal 0x00400000).
-__device__ __forceinline__ float pow2_neg(int s) {
-  const int e = 127 - s;
-  return e > 0 ? __int_as_float(e << 23) : __int_as_float(0x00400000);
-}
-
-// floor(log2(a)) - 8 clamped to [-127, 127] for a finite a >= 0; -127 for a = 0.
-__device__ __forceinline__ int mx_block_exponent(float a) {
-  const uint32_t b = __float_as_uint(a);
-  if (b == 0u) return -127;
-  const int ef = (int)(b >> 23);
-  const int fl = ef > 0 ? ef - 127 : (31 - __clz((int)(b & 0x7FFFFFu))) - 149;
-  return min(127, max(-127, fl - 8));
-}
 
 // atoms: scale bytes in the layout the GEMM's tensor-core copies read (rows and
 // columns multiples of 128): for a row tile rt = r/128 and a k tile kt = b/4,

@@ -41,6 +41,7 @@
 #include <cudaTypedefs.h>
 #include <cuda_bf16.h>
 
+#include "act.cuh"
 #include "moe_internal.h"
 #include "ptx.cuh"
 #include "tmap.h"
@@ -222,31 +223,6 @@ __device__ __forceinline__ void store_rows16_of(uint32_t stg_u, int lane, F valu
 __device__ __forceinline__ void store_rows16(uint32_t stg_u, int lane, const float (&v)[16],
                                              uint16_t* dst, int ld) {
   store_rows16_of(stg_u, lane, [&](int j) { return v[j]; }, dst, ld);
-}
-
-// Gated activation act(gate) of the FFN and its derivative ("Permute-Free
-// Grouped GEMM for MoE (bf16, gfx950)", section 3 act(gate)*up; section 8:
-// silu and gelu): 0 = silu(v) = v sigma(v); 1 = gelu(v) = v Phi(v) (the erf
-// form); act_grad: sigma(v)(1 + v(1 - sigma(v))), Phi(v) + v phi(v).
-template <int act>
-__device__ __forceinline__ float act_fwd(float v) {
-  if (act == 1) return 0.5f * v * (1.0f + erff(v * 0.70710678118654752f));
-  return __fdividef(v, 1.0f + __expf(-v));
-}
-
-// The factor both share: act(v) = v c(v) with c = sigma (silu) or Phi (gelu),
-// and act'(v) from c: c (1 + v (1 - c)) for silu, c + v phi(v) for gelu. The
-// backward evaluates c once per element and derives both from it.
-template <int act>
-__device__ __forceinline__ float act_core(float v) {
-  if (act == 1) return 0.5f * (1.0f + erff(v * 0.70710678118654752f));
-  return __fdividef(1.0f, 1.0f + __expf(-v));
-}
-
-template <int act>
-__device__ __forceinline__ float act_grad_core(float v, float c) {
-  if (act == 1) return c + v * (__expf(-0.5f * v * v) * 0.39894228040143268f);
-  return c * (1.0f + v * (1.0f - c));
 }
 
 // p' of slot c0 + lane of the tile for lanes 0..15 (0 past the kept rows).

@@ -7,6 +7,7 @@
 
 #include "../../include/moe.h"
 #include "moe_internal.h"
+#include "shared_internal.h"
 
 namespace {
 
@@ -668,6 +669,205 @@ int moe_router_backward(const moe_config_t* cfg, const moe_routes_t* routes, con
   a.dbias = dbias;
   a.dx = static_cast<uint16_t*>(dx);
   return finish(moe::launch_router_backward(a, stream));
+}
+
+// ---------------------------------------------------------------- shared expert
+static int check_shared(const moe_shared_config_t* c) {
+  if (!c || c->n_tokens < 0 || c->hidden <= 0 || c->inter <= 0 ||
+      (c->activation != MOE_ACT_SWIGLU && c->activation != MOE_ACT_GEGLU) ||
+      (c->grad_f32 != 0 && c->grad_f32 != 1))
+    return MOE_ERR_INVALID_ARG;
+  if (c->hidden % 8 != 0 || c->inter % 32 != 0 || c->n_tokens > (1 << 24) ||
+      c->hidden > (1 << 24) || c->inter > (1 << 23))
+    return MOE_ERR_UNSUPPORTED_SHAPE;
+  return MOE_OK;
+}
+
+struct SharedBwdLayout {
+  size_t dpre, h, total;
+};
+
+static SharedBwdLayout shared_bwd_layout(const moe_shared_config_t* c) {
+  SharedBwdLayout L{};
+  const int64_t N = c->n_tokens, I = c->inter;
+  L.h = L.dpre + (size_t)roundup(N * 2 * I * 2, 256);
+  L.total = L.h + (size_t)roundup(N * I * 2, 256);
+  return L;
+}
+
+static int shared_forward(const moe_shared_config_t* cfg, const void* x, const void* w13,
+                          const void* w2, const void* add, void* h, void* y, void* ck, void* ck_sf,
+                          cudaStream_t stream) {
+  if (cfg->n_tokens == 0) return MOE_OK;
+  if (!x || !w13 || !w2 || !h || !y || !aligned16(x) || !aligned16(w13) || !aligned16(w2) ||
+      !aligned16(add) || !aligned16(h) || !aligned16(y))
+    return MOE_ERR_INVALID_ARG;
+  moe::SharedArgs a{};
+  a.err = error_word_ptr();
+  if (!a.err) return MOE_ERR_CUDA;
+  a.N = cfg->n_tokens;
+  a.H = cfg->hidden;
+  a.I = cfg->inter;
+  a.activation = cfg->activation;
+  a.x = static_cast<const uint16_t*>(x);
+  a.w13 = static_cast<const uint16_t*>(w13);
+  a.w2 = static_cast<const uint16_t*>(w2);
+  a.add = static_cast<const uint16_t*>(add);
+  a.h = static_cast<uint16_t*>(h);
+  a.y = static_cast<uint16_t*>(y);
+  a.ck = static_cast<uint8_t*>(ck);
+  a.ck_sf = static_cast<uint8_t*>(ck_sf);
+  return finish(moe::launch_shared_forward(a, stream));
+}
+
+int moe_shared_forward(const moe_shared_config_t* cfg, const void* x, const void* w13,
+                       const void* w2, const void* add, void* h, void* y, cudaStream_t stream) {
+  const int rc = check_shared(cfg);
+  if (rc != MOE_OK) return rc;
+  return shared_forward(cfg, x, w13, w2, add, h, y, nullptr, nullptr, stream);
+}
+
+int moe_shared_forward_train(const moe_shared_config_t* cfg, const void* x, const void* w13,
+                             const void* w2, const void* add, void* h, void* y, void* ck,
+                             void* ck_sf, cudaStream_t stream) {
+  const int rc = check_shared(cfg);
+  if (rc != MOE_OK) return rc;
+  if (cfg->n_tokens > 0 && (!ck || !ck_sf || !aligned16(ck) || !aligned16(ck_sf)))
+    return MOE_ERR_INVALID_ARG;
+  return shared_forward(cfg, x, w13, w2, add, h, y, ck, ck_sf, stream);
+}
+
+int64_t moe_shared_backward_workspace_bytes(const moe_shared_config_t* cfg) {
+  const int rc = check_shared(cfg);
+  return rc != MOE_OK ? rc : (int64_t)shared_bwd_layout(cfg).total;
+}
+
+int moe_shared_backward(const moe_shared_config_t* cfg, const void* x, const void* w13,
+                        const void* w2, const void* ck, const void* ck_sf, const void* dy,
+                        const void* dx_add, void* dx, void* dw13, void* dw2, void* workspace,
+                        size_t ws_bytes, cudaStream_t stream) {
+  const int rc = check_shared(cfg);
+  if (rc != MOE_OK) return rc;
+  if (!dw13 || !dw2 || !aligned16(dw13) || !aligned16(dw2)) return MOE_ERR_INVALID_ARG;
+  const size_t w = (size_t)cfg->hidden * cfg->inter * (cfg->grad_f32 ? 4 : 2);
+  if (cfg->n_tokens == 0) {  // no token: zero gradients
+    if (cudaMemsetAsync(dw13, 0, 2 * w, stream) != cudaSuccess ||
+        cudaMemsetAsync(dw2, 0, w, stream) != cudaSuccess)
+      return finish(-1);
+    return MOE_OK;
+  }
+  const SharedBwdLayout L = shared_bwd_layout(cfg);
+  if (!workspace || ws_bytes < L.total || !aligned16(workspace)) return MOE_ERR_WORKSPACE;
+  if (!x || !w13 || !w2 || !ck || !ck_sf || !dy || !dx || !aligned16(x) || !aligned16(w13) ||
+      !aligned16(w2) || !aligned16(ck) || !aligned16(ck_sf) || !aligned16(dy) ||
+      !aligned16(dx_add) || !aligned16(dx))
+    return MOE_ERR_INVALID_ARG;
+  uint8_t* ws = static_cast<uint8_t*>(workspace);
+  moe::SharedArgs a{};
+  a.err = error_word_ptr();
+  if (!a.err) return MOE_ERR_CUDA;
+  a.N = cfg->n_tokens;
+  a.H = cfg->hidden;
+  a.I = cfg->inter;
+  a.activation = cfg->activation;
+  a.grad_f32 = cfg->grad_f32;
+  a.x = static_cast<const uint16_t*>(x);
+  a.w13 = static_cast<const uint16_t*>(w13);
+  a.w2 = static_cast<const uint16_t*>(w2);
+  a.add = static_cast<const uint16_t*>(dx_add);
+  a.ck = static_cast<uint8_t*>(const_cast<void*>(ck));
+  a.ck_sf = static_cast<uint8_t*>(const_cast<void*>(ck_sf));
+  a.dy = static_cast<const uint16_t*>(dy);
+  a.dx = static_cast<uint16_t*>(dx);
+  a.dw13 = dw13;
+  a.dw2 = dw2;
+  a.dpre = reinterpret_cast<uint16_t*>(ws + L.dpre);
+  a.h = reinterpret_cast<uint16_t*>(ws + L.h);
+  return finish(moe::launch_shared_backward(a, stream));
+}
+
+// ---------------------------------------------------------------- 4-bit weights
+static bool w4_group_ok(int group) { return group == 32 || group == 64 || group == 128; }
+
+static constexpr int kW4MaxRoutes = 1024;
+
+int moe_w4_quantize(const void* m, int64_t rows, int cols, int group, void* q, void* scale,
+                    cudaStream_t stream) {
+  if (rows < 0 || cols <= 0 || !w4_group_ok(group) || cols % group != 0 ||
+      rows > ((int64_t)1 << 40) / cols)
+    return MOE_ERR_INVALID_ARG;
+  if (rows == 0) return MOE_OK;
+  if (!m || !q || !scale || !aligned16(m) || !aligned16(q) || !aligned16(scale))
+    return MOE_ERR_INVALID_ARG;
+  return finish(moe::launch_w4_quantize(static_cast<const uint16_t*>(m), rows, cols, group,
+                                        static_cast<uint8_t*>(q), static_cast<uint16_t*>(scale),
+                                        stream));
+}
+
+int moe_w4_matvec(const void* x, const void* q, const void* scale, int n, int rows, int cols,
+                  int group, void* y, cudaStream_t stream) {
+  if (n < 0 || rows <= 0 || cols <= 0 || !w4_group_ok(group) || cols % group != 0)
+    return MOE_ERR_INVALID_ARG;
+  if (n > kW4MaxRoutes || rows > (1 << 24) || cols > (1 << 24)) return MOE_ERR_UNSUPPORTED_SHAPE;
+  if (n == 0) return MOE_OK;
+  if (!x || !q || !scale || !y || !aligned16(x) || !aligned16(q) || !aligned16(scale) ||
+      !aligned16(y))
+    return MOE_ERR_INVALID_ARG;
+  return finish(moe::launch_w4_matvec(static_cast<const uint16_t*>(x),
+                                      static_cast<const uint8_t*>(q),
+                                      static_cast<const uint16_t*>(scale), n, rows, cols, group,
+                                      static_cast<uint16_t*>(y), stream));
+}
+
+static int check_w4(const moe_w4_config_t* c) {
+  if (!c || c->n_tokens < 0 || c->hidden <= 0 || c->n_experts <= 0 || c->top_k <= 0 ||
+      c->inter <= 0 || !w4_group_ok(c->group) ||
+      (c->activation != MOE_ACT_SWIGLU && c->activation != MOE_ACT_GEGLU))
+    return MOE_ERR_INVALID_ARG;
+  if (c->n_experts > moe::kMaxExperts || c->top_k > moe::kMaxTopK || c->hidden % c->group != 0 ||
+      c->inter % c->group != 0 || c->hidden > (1 << 24) || c->inter > (1 << 23) ||
+      (int64_t)c->n_tokens * c->top_k > kW4MaxRoutes)
+    return MOE_ERR_UNSUPPORTED_SHAPE;
+  return MOE_OK;
+}
+
+int64_t moe_w4_workspace_bytes(const moe_w4_config_t* cfg) {
+  const int rc = check_w4(cfg);
+  return rc != MOE_OK ? rc : roundup((int64_t)cfg->n_tokens * cfg->top_k * cfg->inter * 2, 256);
+}
+
+int moe_w4_ffn_forward(const moe_w4_config_t* cfg, const int32_t* topk_ids, const float* topk_p,
+                       const void* x, const void* w13q, const void* w13_scale, const void* w2q,
+                       const void* w2_scale, const void* add, void* y, void* workspace,
+                       size_t ws_bytes, cudaStream_t stream) {
+  const int rc = check_w4(cfg);
+  if (rc != MOE_OK) return rc;
+  if (cfg->n_tokens == 0) return MOE_OK;
+  if (!workspace || (int64_t)ws_bytes < moe_w4_workspace_bytes(cfg) || !aligned16(workspace))
+    return MOE_ERR_WORKSPACE;
+  if (!topk_ids || !topk_p || !x || !w13q || !w13_scale || !w2q || !w2_scale || !y ||
+      !aligned16(x) || !aligned16(w13q) || !aligned16(w13_scale) || !aligned16(w2q) ||
+      !aligned16(w2_scale) || !aligned16(add) || !aligned16(y))
+    return MOE_ERR_INVALID_ARG;
+  moe::W4Args a{};
+  a.N = cfg->n_tokens;
+  a.H = cfg->hidden;
+  a.E = cfg->n_experts;
+  a.K = cfg->top_k;
+  a.I = cfg->inter;
+  a.group = cfg->group;
+  a.activation = cfg->activation;
+  a.topk_ids = topk_ids;
+  a.topk_p = topk_p;
+  a.x = static_cast<const uint16_t*>(x);
+  a.w13 = static_cast<const uint8_t*>(w13q);
+  a.w13_scale = static_cast<const uint16_t*>(w13_scale);
+  a.w2 = static_cast<const uint8_t*>(w2q);
+  a.w2_scale = static_cast<const uint16_t*>(w2_scale);
+  a.add = static_cast<const uint16_t*>(add);
+  a.h = static_cast<uint16_t*>(workspace);
+  a.y = static_cast<uint16_t*>(y);
+  return finish(moe::launch_w4_ffn(a, stream));
 }
 
 const char* moe_status_string(int status) {
