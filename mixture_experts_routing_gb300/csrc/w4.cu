@@ -96,19 +96,21 @@ struct Block {
   uint4 w[MT][2];
   uint16_t s[MT][2][kBlock / GROUP];
 
-  // q[m][i], sc[m][i]: this lane's rows; cols columns
-  __device__ __forceinline__ void load(const uint8_t* const (&q)[MT][2],
-                                       const uint16_t* const (&sc)[MT][2], int kb, int t,
-                                       int cols) {
+  // q, sc: this lane's row g of the first tile; row g + 8 is `eight` rows on (8,
+  // unless the matrix ends before it), the next tile `tile` rows
+  __device__ __forceinline__ void load(const uint8_t* q, const uint16_t* sc, int eight, int tile,
+                                       int kb, int t, int cols) {
 #pragma unroll
     for (int m = 0; m < MT; ++m)
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
-        w[m][i] = load_codes<GROUP>(q[m][i], kb, t, cols);
+        const size_t rows = (size_t)(m * tile + i * eight);
+        w[m][i] = load_codes<GROUP>(q + rows * (cols / 2), kb, t, cols);
 #pragma unroll
         for (int j = 0; j < kBlock / GROUP; ++j)
           s[m][i][j] = (kb * kBlock + j * GROUP < cols)
-                           ? __ldg(sc[m][i] + kb * (kBlock / GROUP) + j) : (uint16_t)0;
+                           ? __ldg(sc + rows * (cols / GROUP) + kb * (kBlock / GROUP) + j)
+                           : (uint16_t)0;
       }
   }
 
@@ -178,24 +180,24 @@ struct Block {
 };
 
 // Every kWarps-th block of a row tile from this warp's own on, kAhead loads ahead.
-template <int MT, int NT, int GROUP, int kAhead>
-__device__ __forceinline__ void stream_rows(const uint8_t* const (&q)[MT][2],
-                                            const uint16_t* const (&sc)[MT][2],
+template <int NT, int GROUP, int kAhead>
+__device__ __forceinline__ void stream_rows(const uint8_t* q, const uint16_t* sc, int eight,
                                             const uint16_t* const (&x)[NT], uint32_t live, int warp,
-                                            int t, int cols, float (&acc)[MT][NT][4]) {
+                                            int t, int cols, float (&acc)[1][NT][4]) {
   const int blocks = (cols + kBlock - 1) / kBlock;
   const float none[NT][2] = {};
-  Block<MT, GROUP> ring[kAhead];
+  Block<1, GROUP> ring[kAhead];
 #pragma unroll
   for (int d = 0; d < kAhead; ++d)
-    if (warp + d * kWarps < blocks) ring[d].load(q, sc, warp + d * kWarps, t, cols);
+    if (warp + d * kWarps < blocks) ring[d].load(q, sc, eight, 0, warp + d * kWarps, t, cols);
   for (int kb = warp; kb < blocks; kb += kAhead * kWarps) {
 #pragma unroll
     for (int d = 0; d < kAhead; ++d) {
       const int at = kb + d * kWarps;
       if (at < blocks) {
         ring[d].template multiply<NT, false>(x, live, at, t, cols, none, acc);
-        if (at + kAhead * kWarps < blocks) ring[d].load(q, sc, at + kAhead * kWarps, t, cols);
+        if (at + kAhead * kWarps < blocks)
+          ring[d].load(q, sc, eight, 0, at + kAhead * kWarps, t, cols);
       }
     }
   }
@@ -220,19 +222,12 @@ template <int NT, int GROUP>
 __global__ void __launch_bounds__(kThreads) w4_matvec_kernel(const uint16_t* x, const uint8_t* q,
                                                              const uint16_t* scale, int N, int rows,
                                                              int cols, uint16_t* y) {
-  __shared__ float part[kWarps * 16 * 8 * NT];
+  __shared__ __align__(16) float part[kWarps * 16 * 8 * NT];
   griddep_wait();
   griddep_launch_dependents();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
   const int r0 = blockIdx.x * 16, t0 = blockIdx.y * 8 * NT;
-  const uint8_t* qr[1][2];
-  const uint16_t* sr[1][2];
-#pragma unroll
-  for (int i = 0; i < 2; ++i) {  // a row past the last one reads the last one
-    const size_t r = (size_t)min(r0 + g + 8 * i, rows - 1);
-    qr[0][i] = q + r * (cols / 2);
-    sr[0][i] = scale + r * (cols / GROUP);
-  }
+  const int row = min(r0 + g, rows - 1);  // a row past the last one reads the last one
   const uint16_t* xt[NT];
   uint32_t live = 0;
 #pragma unroll
@@ -242,7 +237,8 @@ __global__ void __launch_bounds__(kThreads) w4_matvec_kernel(const uint16_t* x, 
     live |= (t0 + 8 * n < N) ? 1u << n : 0u;
   }
   float acc[1][NT][4] = {};
-  stream_rows<1, NT, GROUP, NT == 1 ? 4 : 2>(qr, sr, xt, live, warp, t, cols, acc);
+  stream_rows<NT, GROUP, NT == 1 ? 4 : 2>(q + (size_t)row * (cols / 2), scale + (size_t)row * (cols / GROUP),
+                                          min(8, rows - 1 - row), xt, live, warp, t, cols, acc);
   leave_parts<1, NT>(part, warp, g, t, acc);
   __syncthreads();
   for (int i = threadIdx.x; i < 16 * 8 * NT; i += kThreads) {
@@ -255,85 +251,203 @@ __global__ void __launch_bounds__(kThreads) w4_matvec_kernel(const uint16_t* x, 
   }
 }
 
-// First product: block (16 features, route r). The first route of an expert does
-// the work of all its routes, in passes of 8 NT; the others leave.
+// Routes grouped by expert, in shared memory, by the whole block: pieces of at
+// most `most` routes of one expert, experts ascending, routes in their order.
+struct Groups {
+  int16_t order[kMaxRoutes];                          // routes, sorted by expert
+  int16_t expert[kMaxExperts + kMaxRoutes / 8];       // of each piece
+  int16_t first[kMaxExperts + kMaxRoutes / 8];        // its first place in `order`
+  int16_t count[kMaxExperts + kMaxRoutes / 8];
+  int16_t rank[kMaxRoutes];                           // of a route among its expert's
+  int16_t routes[kMaxExperts];                        // of each expert
+  int scan[2][kWarps];
+  int pieces;
+};
+
+__device__ __forceinline__ void group_routes(Groups& G, const int32_t* ids, int R, int E,
+                                             int most) {
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  static_assert(kThreads == kMaxExperts, "one thread per expert");
+  G.routes[threadIdx.x] = 0;
+  __syncthreads();
+  if (warp == 0) {  // 32 routes at a time, in order: each gets its rank within its expert
+    for (int i0 = 0; i0 < R; i0 += 32) {
+      const int i = i0 + lane;
+      const int id = i < R ? ids[i] : -1;
+      const int e = id >= 0 && id < E ? id : -1;
+      const uint32_t same = __match_any_sync(0xFFFFFFFFu, e);
+      const int before = __popc(same & ((1u << lane) - 1u));
+      const int base = e >= 0 ? G.routes[e] : 0;
+      __syncwarp();
+      if (e >= 0 && before == 0) G.routes[e] = (int16_t)(base + __popc(same));
+      if (i < R) G.rank[i] = (int16_t)(base + before);
+      __syncwarp();
+    }
+  }
+  __syncthreads();
+  // exclusive sums over the experts of their routes and of their pieces
+  const int n = G.routes[threadIdx.x], np = (n + most - 1) / most;
+  int sn = n, sp = np;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int vn = __shfl_up_sync(0xFFFFFFFFu, sn, o), vp = __shfl_up_sync(0xFFFFFFFFu, sp, o);
+    if (lane >= o) {
+      sn += vn;
+      sp += vp;
+    }
+  }
+  if (lane == 31) {
+    G.scan[0][warp] = sn;
+    G.scan[1][warp] = sp;
+  }
+  __syncthreads();
+  int on = sn - n, op = sp - np;
+  for (int w = 0; w < warp; ++w) {
+    on += G.scan[0][w];
+    op += G.scan[1][w];
+  }
+  G.routes[threadIdx.x] = (int16_t)on;  // now: where the expert's routes begin
+  for (int j = 0; j < np; ++j) {
+    G.expert[op + j] = (int16_t)threadIdx.x;
+    G.first[op + j] = (int16_t)(on + j * most);
+    G.count[op + j] = (int16_t)min(most, n - j * most);
+  }
+  if (threadIdx.x == kThreads - 1) G.pieces = op + np;
+  __syncthreads();
+  for (int i = threadIdx.x; i < R; i += kThreads) {
+    const int e = ids[i];
+    if (e >= 0 && e < E) G.order[G.routes[e] + G.rank[i]] = (int16_t)i;
+  }
+  __syncthreads();
+}
+
+// First product. A unit is 16 features (their gate and up rows) of one expert's
+// piece of at most 8 NT routes; a team of S warps, which split the columns,
+// takes every teams-th unit, its loads running on from unit to unit. Teams of
+// a block take neighbouring features of the same expert.
 template <int NT, int GROUP>
-__global__ void __launch_bounds__(kThreads) w4_fc1_kernel(const W4Args a) {
-  __shared__ float part[kWarps * 2 * 16 * 8 * NT];
-  __shared__ int16_t routes[kMaxRoutes];
-  __shared__ int count;
+__global__ void __launch_bounds__(kThreads, 2) w4_fc1_kernel(const W4Args a, const int S) {
+  constexpr int kAhead = 2, kPart = 2 * 16 * 8 * NT;
+  __shared__ Groups G;
+  __shared__ __align__(16) float part[kWarps * kPart];
   griddep_wait();
   griddep_launch_dependents();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
-  const int r = blockIdx.y, R = a.N * a.K;
-  const int e = a.topk_ids[r];
-  if (e < 0 || e >= a.E) return;
-  if (warp == 0) {
-    int n = 0;
-    for (int i0 = 0; i0 < R; i0 += 32) {
-      const int i = i0 + lane;
-      const bool same = i < R && a.topk_ids[i] == e;
-      const uint32_t b = __ballot_sync(0xFFFFFFFFu, same);
-      if (same) routes[n + __popc(b & ((1u << lane) - 1u))] = (int16_t)i;
-      n += __popc(b);
+  group_routes(G, a.topk_ids, a.N * a.K, a.E, 8 * NT);
+  const int team = (blockIdx.x * kWarps + warp) / S, teams = gridDim.x * kWarps / S;
+  const int member = warp % S, i_tiles = a.I / 16, units = G.pieces * i_tiles;
+  const int blocks = (a.H + kBlock - 1) / kBlock;
+
+  Block<2, GROUP> ring[kAhead];
+  int unit_l = team, kb_l = member;  // what is loaded next
+  const uint8_t* q_l = nullptr;
+  const uint16_t* s_l = nullptr;
+  int have_l = -1;
+  auto load_next = [&](Block<2, GROUP>& b) {
+    while (kb_l >= blocks && unit_l < units) {
+      kb_l = member;
+      unit_l += teams;
     }
-    if (lane == 0) count = n;
-  }
-  __syncthreads();
-  if (routes[0] != r) return;
-  const int n_routes = count, i0 = blockIdx.x * 16;
-  const uint8_t* qr[2][2];
-  const uint16_t* sr[2][2];
-#pragma unroll
-  for (int m = 0; m < 2; ++m)
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      const size_t row = (size_t)e * 2 * a.I + (size_t)m * a.I + i0 + g + 8 * i;
-      qr[m][i] = a.w13 + row * (a.H / 2);
-      sr[m][i] = a.w13_scale + row * (a.H / GROUP);
+    if (unit_l >= units) return;
+    if (unit_l != have_l) {
+      have_l = unit_l;
+      const int piece = unit_l / i_tiles, i0 = (unit_l - piece * i_tiles) * 16;
+      const size_t row = (size_t)G.expert[piece] * 2 * a.I + i0 + g;
+      q_l = a.w13 + row * (a.H / 2);
+      s_l = a.w13_scale + row * (a.H / GROUP);
     }
-  for (int c0 = 0; c0 < n_routes; c0 += 8 * NT) {
-    const uint16_t* xt[NT];
-    uint32_t live = 0;
+    b.load(q_l, s_l, 8, a.I, kb_l, t, a.H);
+    kb_l += S;
+  };
 #pragma unroll
-    for (int n = 0; n < NT; ++n) {
-      const int at = c0 + 8 * n + g;
-      xt[n] = at < n_routes ? a.x + (size_t)(routes[at] / a.K) * a.H : nullptr;
-      live |= (c0 + 8 * n < n_routes) ? 1u << n : 0u;
+  for (int d = 0; d < kAhead; ++d) load_next(ring[d]);
+
+  const float none[NT][2] = {};
+  float acc[2][NT][4] = {};
+  const uint16_t* xt[NT];
+  uint32_t live = 0;
+  int unit = team, kb = member;
+  auto begin = [&]() {  // the tokens of the unit's piece
+    const int piece = unit / i_tiles, first = G.first[piece], n = G.count[piece];
+    live = 0;
+#pragma unroll
+    for (int j = 0; j < NT; ++j) {
+      const int at = 8 * j + g;
+      xt[j] = at < n ? a.x + (size_t)(G.order[first + at] / a.K) * a.H : nullptr;
+      live |= 8 * j < n ? 1u << j : 0u;
     }
-    float acc[2][NT][4] = {};
-    stream_rows<2, NT, GROUP, 2>(qr, sr, xt, live, warp, t, a.H, acc);
-    leave_parts<2, NT>(part, warp, g, t, acc);
-    __syncthreads();
-    for (int i = threadIdx.x; i < 16 * 8 * NT; i += kThreads) {
-      const int at = c0 + (i >> 4);
-      if (at >= n_routes) continue;
-      float gv = 0.0f, uv = 0.0f;
 #pragma unroll
-      for (int w = 0; w < kWarps; ++w) {
-        gv += part[((w * 2) * 16 + (i & 15)) * 8 * NT + (i >> 4)];
-        uv += part[((w * 2 + 1) * 16 + (i & 15)) * 8 * NT + (i >> 4)];
+    for (int m = 0; m < 2; ++m)
+#pragma unroll
+      for (int j = 0; j < NT; ++j)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) acc[m][j][i] = 0.0f;
+  };
+  auto end = [&]() {  // h of the unit
+    const int piece = unit / i_tiles, i0 = (unit - piece * i_tiles) * 16;
+    const int first = G.first[piece], n = G.count[piece];
+    if (S > 1) {
+      float* mine = part + warp * kPart;
+      leave_parts<2, NT>(mine, 0, g, t, acc);
+      asm volatile("bar.sync %0, %1;" ::"r"(1 + warp / S), "r"(32 * S) : "memory");
+      const float* all = part + (warp - member) * kPart;
+      for (int i = member * 32 + lane; i < 16 * 8 * NT; i += 32 * S) {
+        if ((i >> 4) >= n) break;
+        float gv = 0.0f, uv = 0.0f;
+        for (int w = 0; w < S; ++w) {
+          gv += all[w * kPart + (i & 15) * 8 * NT + (i >> 4)];
+          uv += all[w * kPart + (16 + (i & 15)) * 8 * NT + (i >> 4)];
+        }
+        const float h = (a.activation ? act_fwd<1>(gv) : act_fwd<0>(gv)) * uv;
+        a.h[(size_t)G.order[first + (i >> 4)] * a.I + i0 + (i & 15)] =
+            __bfloat16_as_ushort(__float2bfloat16_rn(h));
       }
-      const float h = (a.activation ? act_fwd<1>(gv) : act_fwd<0>(gv)) * uv;
-      a.h[(size_t)routes[at] * a.I + i0 + (i & 15)] = __bfloat16_as_ushort(__float2bfloat16_rn(h));
+      asm volatile("bar.sync %0, %1;" ::"r"(1 + warp / S), "r"(32 * S) : "memory");
+    } else {
+#pragma unroll
+      for (int j = 0; j < NT; ++j)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int at = 8 * j + 2 * t + (i & 1);
+          if (at >= n) continue;
+          const float gv = acc[0][j][i];
+          const float h = (a.activation ? act_fwd<1>(gv) : act_fwd<0>(gv)) * acc[1][j][i];
+          a.h[(size_t)G.order[first + at] * a.I + i0 + g + 8 * (i >> 1)] =
+              __bfloat16_as_ushort(__float2bfloat16_rn(h));
+        }
     }
-    __syncthreads();
+  };
+  if (unit < units) begin();
+  while (unit < units) {
+#pragma unroll
+    for (int d = 0; d < kAhead; ++d) {
+      while (kb >= blocks && unit < units) {
+        end();
+        kb = member;
+        unit += teams;
+        if (unit < units) begin();
+      }
+      if (unit >= units) break;
+      ring[d].template multiply<NT, false>(xt, live, kb, t, a.H, none, acc);
+      load_next(ring[d]);
+      kb += S;
+    }
   }
 }
 
 // Second product and the sum over a token's routes: block (16 output columns,
 // 8 NT tokens) goes through the experts that its tokens chose, in ascending
-// order, the (expert, block of columns) pairs dealt out to the warps; a column
-// of the products is a token, weighted by its probability for the expert.
-// Dynamic shared memory: prob [items][8 NT] f32, slot [items][8 NT] i8; at the
-// end the warps' sums.
-template <int NT, int GROUP>
-__global__ void __launch_bounds__(kThreads) w4_fc2_kernel(const W4Args a) {
+// order; a team of S warps, which split the columns, takes every teams-th
+// expert. A column of the products is a token, weighted by its probability for
+// the expert. Dynamic shared memory: prob [items][8 NT] f32, slot [items][8 NT]
+// i8; at the end the warps' sums.
+template <int NT, int GROUP, int W>
+__global__ void __launch_bounds__(W * 32, W == 16 ? 1 : 2) w4_fc2_kernel(const W4Args a, const int S) {
   constexpr int kTok = 8 * NT;
-  extern __shared__ float prob[];
+  extern __shared__ __align__(16) float prob[];
   float* part = prob;
   __shared__ int16_t item_of[kMaxExperts], expert_of[kMaxExperts];
-  __shared__ int warp_items[kWarps];
+  __shared__ int warp_items[kMaxExperts / 32];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
   const int r0 = blockIdx.x * 16, t0 = blockIdx.y * kTok;
   const int tokens = min(kTok, a.N - t0), R = tokens * a.K;
@@ -341,31 +455,32 @@ __global__ void __launch_bounds__(kThreads) w4_fc2_kernel(const W4Args a) {
   const float* ps = a.topk_p + (size_t)t0 * a.K;
   // The first product's kernel let this one start after every earlier kernel had
   // finished, and writes neither the routes nor the weights: only h has to wait.
-  for (int e = threadIdx.x; e < kMaxExperts; e += kThreads) item_of[e] = -1;
+  static_assert(W * 32 >= kMaxExperts, "a thread for each expert");
+  const int e_mine = threadIdx.x;
+  if (e_mine < kMaxExperts) item_of[e_mine] = -1;
   __syncthreads();
-  for (int i = threadIdx.x; i < R; i += kThreads) {
+  for (int i = threadIdx.x; i < R; i += W * 32) {
     const int e = __ldcg(ids + i);
     if (e >= 0 && e < a.E) item_of[e] = 0;
   }
   __syncthreads();
-  static_assert(kThreads == kMaxExperts, "one thread per expert");
-  const bool used = item_of[threadIdx.x] == 0;
+  const bool used = e_mine < kMaxExperts && item_of[e_mine] == 0;
   const uint32_t ballot = __ballot_sync(0xFFFFFFFFu, used);
-  if (lane == 0) warp_items[warp] = __popc(ballot);
+  if (lane == 0 && e_mine < kMaxExperts) warp_items[warp] = __popc(ballot);
   __syncthreads();
   int before = 0, items = 0;
 #pragma unroll
-  for (int w = 0; w < kWarps; ++w) {
+  for (int w = 0; w < kMaxExperts / 32; ++w) {
     before += w < warp ? warp_items[w] : 0;
     items += warp_items[w];
   }
   if (used) {
     const int at = before + __popc(ballot & ((1u << lane) - 1u));
-    item_of[threadIdx.x] = (int16_t)at;
-    expert_of[at] = (int16_t)threadIdx.x;
+    item_of[e_mine] = (int16_t)at;
+    expert_of[at] = (int16_t)e_mine;
   }
   int8_t* slot = reinterpret_cast<int8_t*>(prob + items * kTok);
-  for (int i = threadIdx.x; i < items * kTok; i += kThreads) {
+  for (int i = threadIdx.x; i < items * kTok; i += W * 32) {
     prob[i] = 0.0f;
     slot[i] = -1;
   }
@@ -382,27 +497,27 @@ __global__ void __launch_bounds__(kThreads) w4_fc2_kernel(const W4Args a) {
   }
   __syncthreads();
 
-  const int blocks = (a.I + kBlock - 1) / kBlock;
-  constexpr int kAhead = NT == 1 ? 4 : 2;
+  constexpr int kAhead = NT == 4 ? 2 : 4;
+  const int teams = W / S;
+  const int blocks = (a.I + kBlock - 1) / kBlock, member = warp % S;
   Block<1, GROUP> ring[kAhead];
-  int item_l = 0, kb_l = warp;  // what is loaded next
+  int item_l = warp / S, kb_l = member, have_l = -1;  // what is loaded next
+  const uint8_t* q_l = nullptr;
+  const uint16_t* s_l = nullptr;
   auto load_next = [&](Block<1, GROUP>& b) {
-    while (kb_l >= blocks) {
-      kb_l -= blocks;
-      ++item_l;
+    while (kb_l >= blocks && item_l < items) {
+      kb_l = member;
+      item_l += teams;
     }
-    if (item_l < items) {
-      const uint8_t* q[1][2];
-      const uint16_t* sc[1][2];
-#pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        const size_t row = (size_t)expert_of[item_l] * a.H + r0 + g + 8 * i;
-        q[0][i] = a.w2 + row * (a.I / 2);
-        sc[0][i] = a.w2_scale + row * (a.I / GROUP);
-      }
-      b.load(q, sc, kb_l, t, a.I);
+    if (item_l >= items) return;
+    if (item_l != have_l) {
+      have_l = item_l;
+      const size_t row = (size_t)expert_of[item_l] * a.H + r0 + g;
+      q_l = a.w2 + row * (a.I / 2);
+      s_l = a.w2_scale + row * (a.I / GROUP);
     }
-    kb_l += kWarps;
+    b.load(q_l, s_l, 8, 0, kb_l, t, a.I);
+    kb_l += S;
   };
 #pragma unroll
   for (int d = 0; d < kAhead; ++d) load_next(ring[d]);
@@ -413,19 +528,15 @@ __global__ void __launch_bounds__(kThreads) w4_fc2_kernel(const W4Args a) {
   const uint16_t* ht[NT];
   float p[NT][2];
   uint32_t live = 0;
-  int item = 0, kb = warp, have = -1;
-  bool more = true;
-  while (more) {
+  int item = warp / S, kb = member, have = -1;
+  while (item < items) {
 #pragma unroll
     for (int d = 0; d < kAhead; ++d) {
-      while (kb >= blocks) {
-        kb -= blocks;
-        ++item;
+      while (kb >= blocks && item < items) {
+        kb = member;
+        item += teams;
       }
-      if (item >= items) {
-        more = false;
-        break;
-      }
+      if (item >= items) break;
       if (item != have) {
         have = item;
         live = 0;
@@ -440,19 +551,19 @@ __global__ void __launch_bounds__(kThreads) w4_fc2_kernel(const W4Args a) {
       }
       ring[d].template multiply<NT, true>(ht, live, kb, t, a.I, p, acc);
       load_next(ring[d]);
-      kb += kWarps;
+      kb += S;
     }
   }
   __syncthreads();  // every warp is done with prob and slot
   leave_parts<1, NT>(part, warp, g, t, acc);
   __syncthreads();
-  for (int i = threadIdx.x; i < 16 * kTok; i += kThreads) {
+  for (int i = threadIdx.x; i < 16 * kTok; i += W * 32) {
     const int tok = t0 + (i >> 4), c = r0 + (i & 15);
     if (tok >= a.N) continue;
     const size_t at = (size_t)tok * a.H + c;
     float v = a.add ? bf(a.add[at]) : 0.0f;
 #pragma unroll
-    for (int w = 0; w < kWarps; ++w) v += part[(w * 16 + (i & 15)) * kTok + (i >> 4)];
+    for (int w = 0; w < W; ++w) v += part[(w * 16 + (i & 15)) * kTok + (i >> 4)];
     a.y[at] = __bfloat16_as_ushort(__float2bfloat16_rn(v));
   }
 }
@@ -505,25 +616,48 @@ cudaError_t matvec(const uint16_t* x, const uint8_t* q, const uint16_t* scale, i
   return launch_pdl(k, grid, dim3(kThreads), 0, s, x, q, scale, N, rows, cols, y);
 }
 
-template <int NT>
+template <int NT, int GROUP>
 cudaError_t fc1(const W4Args& a, cudaStream_t s) {
-  const dim3 grid(a.I / 16, a.N * a.K);
-  auto* k = a.group == 128 ? w4_fc1_kernel<NT, 128>
-                           : a.group == 64 ? w4_fc1_kernel<NT, 64> : w4_fc1_kernel<NT, 32>;
-  return launch_pdl(k, grid, dim3(kThreads), 0, s, a);
+  static DeviceOnce once;
+  int sms = 0;
+  const cudaError_t err = once_per_device(once, &sms, [](int dev, int* v) {
+    return cudaDeviceGetAttribute(v, cudaDevAttrMultiProcessorCount, dev);
+  });
+  if (err != cudaSuccess) return err;
+  // units there may be, and the warps of two blocks an SM
+  const int64_t routes = (int64_t)a.N * a.K, warps = 2 * sms * kWarps;
+  const int64_t units = (routes < a.E ? routes : a.E) * (a.I / 16);
+  const int S = units * 8 <= warps ? 8 : units * 4 <= warps ? 4 : units * 2 <= warps ? 2 : 1;
+  return launch_pdl(w4_fc1_kernel<NT, GROUP>, dim3(2 * sms), dim3(kThreads), 0, s, a, S);
 }
 
 template <int NT>
+cudaError_t fc1(const W4Args& a, cudaStream_t s) {
+  return a.group == 128 ? fc1<NT, 128>(a, s) : a.group == 64 ? fc1<NT, 64>(a, s) : fc1<NT, 32>(a, s);
+}
+
+template <int NT, int GROUP, int W>
 cudaError_t fc2(const W4Args& a, cudaStream_t s) {
   const int tokens = a.N < 8 * NT ? a.N : 8 * NT;
   const int items = a.E < tokens * a.K ? a.E : tokens * a.K;
   const dim3 grid(a.H / 16, (a.N + 8 * NT - 1) / (8 * NT));
   // at most 256 x 32 x 5 bytes: within the 48 KB a kernel has without asking
   size_t smem = (size_t)items * 8 * NT * 5;
-  if (smem < (size_t)kWarps * 16 * 8 * NT * 4) smem = (size_t)kWarps * 16 * 8 * NT * 4;
-  auto* k = a.group == 128 ? w4_fc2_kernel<NT, 128>
-                           : a.group == 64 ? w4_fc2_kernel<NT, 64> : w4_fc2_kernel<NT, 32>;
-  return launch_pdl(k, grid, dim3(kThreads), smem, s, a);
+  if (smem < (size_t)W * 16 * 8 * NT * 4) smem = (size_t)W * 16 * 8 * NT * 4;
+  const int S = items * 8 <= W ? 8 : items * 4 <= W ? 4 : items * 2 <= W ? 2 : 1;
+  return launch_pdl(w4_fc2_kernel<NT, GROUP, W>, grid, dim3(W * 32), smem, s, a, S);
+}
+
+template <int NT, int GROUP>
+cudaError_t fc2(const W4Args& a, cudaStream_t s) {
+  // narrow outputs have fewer blocks than SMs to fill: more warps each
+  return (int64_t)(a.H / 16) * ((a.N + 8 * NT - 1) / (8 * NT)) <= 256 ? fc2<NT, GROUP, 16>(a, s)
+                                                                      : fc2<NT, GROUP, 8>(a, s);
+}
+
+template <int NT>
+cudaError_t fc2(const W4Args& a, cudaStream_t s) {
+  return a.group == 128 ? fc2<NT, 128>(a, s) : a.group == 64 ? fc2<NT, 64>(a, s) : fc2<NT, 32>(a, s);
 }
 
 }  // namespace
@@ -538,8 +672,7 @@ int launch_w4_matvec(const uint16_t* x, const uint8_t* q, const uint16_t* scale,
 
 int launch_w4_ffn(const W4Args& a, cudaStream_t s) {
   // tokens an expert serves at once: by the mean number of its routes
-  cudaError_t err = a.N <= 8 || a.N * a.K <= 4 * a.E ? fc1<1>(a, s)
-                                                     : a.N * a.K <= 12 * a.E ? fc1<2>(a, s) : fc1<4>(a, s);
+  cudaError_t err = a.N <= 8 || a.N * a.K <= 4 * a.E ? fc1<1>(a, s) : fc1<2>(a, s);
   if (err != cudaSuccess) return -(int)err;
   err = a.N <= 8 ? fc2<1>(a, s) : a.N <= 16 ? fc2<2>(a, s) : fc2<4>(a, s);
   return err != cudaSuccess ? -(int)err : 2;
