@@ -6,16 +6,17 @@
 //             y[t,:] = add[t,:] + sum_k p[t,k] W2[e] h[t,k,:]
 //
 // The time is that of reading the codes once, so the kernels are built around
-// that stream: a warp takes 16 rows and walks 128-column blocks of them, each
-// lane loading 16 bytes (32 codes) of its two rows straight into registers,
-// kAhead blocks ahead. The codes become the A operand of mma.sync m16n8k16 (the
-// products need 8 columns for 1 to 8 tokens, and the operands are already in
-// registers, which tcgen05.mma cannot read B or A from without a trip through
-// shared or tensor memory): a mask and an OR put four bits into the mantissa of
-// bf16 128 + code, one subtraction makes it code - 8, exactly. The order of the
-// columns within a block is free as long as x follows it, so no weight is
-// shuffled. The sums of one group are scaled in fp32 and added up in fp32. The
-// warps of a block split the columns and add their parts in a fixed order.
+// that stream. A warp takes 16 rows and walks blocks of their columns; the codes,
+// the scales and the same columns of x come through the warp's own ring of
+// shared-memory stages (cp.async, no barrier with other warps), so that neither
+// the codes' nor x's latency is waited for block by block. The codes become the A
+// operand of mma.sync m16n8k16: the products need 8 columns for 1 to 8 tokens, and
+// the opened codes are in registers, where tcgen05.mma takes no operand from. A
+// mask and an OR put four bits into the mantissa of bf16 128 + code, one
+// subtraction makes it code - 8, exactly. The order of the columns within a group
+// is free as long as x follows it, so no weight is moved between lanes. The sums
+// of one group are scaled in fp32 and added up in fp32. Warps that share a row
+// tile split its columns and add their parts in a fixed order.
 #include "act.cuh"
 #include "moe_internal.h"
 #include "ptx.cuh"
@@ -26,267 +27,352 @@ namespace {
 
 constexpr int kWarps = 8;
 constexpr int kThreads = kWarps * 32;
-constexpr int kBlock = 128;       // columns a warp takes at a time
+constexpr int kShare = 128;       // columns are dealt out to warps in multiples of these
 constexpr int kMaxRoutes = 1024;  // N*K, at most
+constexpr int kChunk = 32;        // tokens that a block of the second product serves
 
 __device__ __forceinline__ float bf(uint16_t v) { return __uint_as_float((uint32_t)v << 16); }
-
-// Within a block, lane t of a quad holds four words of eight codes; word j
-// covers columns word_col(t, j) .. + 7, so that the 16 columns of one MMA (two
-// MMAs a word) lie in one group.
-template <int GROUP>
-__device__ __forceinline__ int word_col(int t, int j) {
-  if (GROUP == 128) return 32 * t + 8 * j;
-  if (GROUP == 64) return 64 * (j >> 1) + 16 * t + 8 * (j & 1);
-  return 32 * j + 8 * t;
+__device__ __forceinline__ uint16_t to_bf(float v) {
+  return __bfloat16_as_ushort(__float2bfloat16_rn(v));
 }
 
-// The four words of block kb of a row; words past the last column stay 0 (their
-// x is 0).
-template <int GROUP>
-__device__ __forceinline__ uint4 load_codes(const uint8_t* row, int kb, int t, int cols) {
-  const uint8_t* at = row + kb * (kBlock / 2);
-  uint4 w = make_uint4(0u, 0u, 0u, 0u);
-  if constexpr (GROUP == 128) {
-    w = __ldg(reinterpret_cast<const uint4*>(at) + t);
-  } else if constexpr (GROUP == 64) {
-    const uint2 a = __ldg(reinterpret_cast<const uint2*>(at) + t);
-    w.x = a.x;
-    w.y = a.y;
-    if (kb * kBlock + 64 < cols) {
-      const uint2 b = __ldg(reinterpret_cast<const uint2*>(at) + 4 + t);
-      w.z = b.x;
-      w.w = b.y;
-    }
-  } else {
-    const uint32_t* p = reinterpret_cast<const uint32_t*>(at) + t;
-    const int left = cols - kb * kBlock;
-    w.x = __ldg(p);
-    if (left > 32) w.y = __ldg(p + 4);
-    if (left > 64) w.z = __ldg(p + 8);
-    if (left > 96) w.w = __ldg(p + 12);
-  }
-  return w;
-}
+// Where value i of h goes: each eight in the order 0 4 1 5 2 6 3 7, as the pairs
+// of open_codes lie.
+__device__ __forceinline__ int permuted(int i) { return (i & ~7) | ((i & 3) << 1) | ((i >> 2) & 1); }
 
 // Eight codes as four pairs of bf16 code - 8: columns (0,4), (1,5), (2,6), (3,7).
+// The mask and the OR are one instruction (the compiler makes two of them: 27 %
+// more ALU work, a 7168 x 7168 product 9.1 us instead of 7.7).
 __device__ __forceinline__ void open_codes(uint32_t w, uint32_t (&d)[4]) {
   const __nv_bfloat162 off = __floats2bfloat162_rn(136.0f, 136.0f);
 #pragma unroll
   for (int j = 0; j < 4; ++j) {
-    const uint32_t v = ((w >> (4 * j)) & 0x000F000Fu) | 0x43004300u;  // 128 + code
+    uint32_t v;  // 128 + code
+    asm("lop3.b32 %0, %1, %2, %3, 0xEA;"
+        : "=r"(v)
+        : "r"(w >> (4 * j)), "r"(0x000F000Fu), "r"(0x43004300u));
     const __nv_bfloat162 b = __hsub2(*reinterpret_cast<const __nv_bfloat162*>(&v), off);
     d[j] = *reinterpret_cast<const uint32_t*>(&b);
   }
 }
 
+// c = a b, or c += a b
+template <bool FIRST>
 __device__ __forceinline__ void mma16816(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2,
                                          uint32_t a3, uint32_t b0, uint32_t b1) {
-  asm volatile(
-      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
-      "{%0,%1,%2,%3};"
-      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+  if constexpr (FIRST)
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
+        "{%8,%9}, {%10,%10,%10,%10};"
+        : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.0f));
+  else
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
+        "{%8,%9}, {%0,%1,%2,%3};"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
-// Codes and scales of one block of MT tiles of 16 rows (this lane's rows g and
-// g + 8 of each).
-template <int MT, int GROUP>
-struct Block {
-  uint4 w[MT][2];
-  uint16_t s[MT][2][kBlock / GROUP];
+// Member m of S takes columns [share(m), share(m + 1)).
+__device__ __forceinline__ int share(int m, int S, int cols) {
+  return min(cols, (int)((int64_t)m * ((cols + kShare - 1) / kShare) / S) * kShare);
+}
 
-  // q, sc: this lane's row g of the first tile; row g + 8 is `eight` rows on (8,
-  // unless the matrix ends before it), the next tile `tile` rows
-  __device__ __forceinline__ void load(const uint8_t* q, const uint16_t* sc, int eight, int tile,
-                                       int kb, int t, int cols) {
-#pragma unroll
-    for (int m = 0; m < MT; ++m)
-#pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        const size_t rows = (size_t)(m * tile + i * eight);
-        w[m][i] = load_codes<GROUP>(q + rows * (cols / 2), kb, t, cols);
-#pragma unroll
-        for (int j = 0; j < kBlock / GROUP; ++j)
-          s[m][i][j] = (kb * kBlock + j * GROUP < cols)
-                           ? __ldg(sc + rows * (cols / GROUP) + kb * (kBlock / GROUP) + j)
-                           : (uint16_t)0;
-      }
+// A warp's stream of blocks: 16 rows (g and g + 8 of lane 4g + t, the second
+// anywhere in the matrix) by kCols columns, and the same columns of up to TOK
+// tokens. A stage holds
+//  - the codes, 16-byte piece c of row r at place c ^ swizzle(r), so that reads of
+//    4, 8 or 16 bytes a lane spread over the banks;
+//  - each row's scales, as the 4-byte words they lie in (a row of scales starts at
+//    any even address);
+//  - x, token by token, word j of lane t (8 columns, 16 bytes) of a group at
+//    place 4j + t of the group, odd tokens with bit 2 of the place flipped.
+// Lane 4g + t takes words of eight codes: word j < GROUP/32 of a group covers its
+// columns (GROUP/4) t + 8j .. + 7, so that the 16 columns of an MMA (two MMAs a
+// word) lie in one group.
+template <int GROUP, int TOK>
+struct Stream {
+  static constexpr int kCols = 128;
+  static constexpr int kAhead = TOK == 8 ? 3 : 2;    // stages
+  static constexpr int kNT = TOK / 8;                // tiles of 8 tokens
+  static constexpr int kG = kCols / GROUP;           // scales of a row in a block
+  static constexpr int kWords = GROUP / 32;          // words of a lane in a group
+  static constexpr int kScaleBytes = kG == 1 ? 4 : 2 * kG + 4;  // the words a row's scales touch
+  static constexpr int kCodes = 16 * kCols / 2;
+  static constexpr int kX = kCodes + 16 * kScaleBytes;
+  static constexpr int kStage = (kX + TOK * kCols * 2 + 127) / 128 * 128;
+  static constexpr int kBytes = kAhead * kStage;     // of a warp
+  static constexpr int kCopies = TOK / 2;            // x copies of a lane in a block
+
+  uint32_t base;           // the warp's ring
+  int fill = 0, take = 0;  // offsets of the stage filled and taken next
+  int lane, g, t;
+  const uint8_t* q;        // row g, at piece t of the block copied next
+  int64_t q8;              // bytes from there to the second row
+  const uint16_t* scales;  // of the whole matrix
+  int64_t si, s_end;       // this lane's scale (lanes 0-15: row lane), number of scales
+  int rs;                  // scales of a row
+  int left;                // columns of the share from the block copied next on
+  const uint16_t* x[kCopies];  // this lane's 8 columns of its tokens in that block
+  int tokens;
+
+  static __device__ __forceinline__ int swizzle(int r) { return (r >> 1) & 3; }
+
+  __device__ __forceinline__ void init(uint8_t* ring, int warp, int lane_, int64_t second, int cols,
+                                       const uint16_t* sc, int64_t rows) {
+    base = smem_u32(ring) + (uint32_t)(warp * kBytes);
+    lane = lane_;
+    g = lane >> 2;
+    t = lane & 3;
+    q8 = second * (cols / 2);
+    scales = sc;
+    rs = cols / GROUP;
+    s_end = rows * rs;
   }
 
-  // acc[m][n] += (rows of tile m) x (tokens of tile n); x[n]: this lane's token
-  // (column g of tile n) or null; tiles not in `live` (the same for all lanes)
-  // are left out. P: weights of the two token columns this lane holds of each tile.
-  template <int NT, bool P>
-  __device__ __forceinline__ void multiply(const uint16_t* const (&x)[NT], uint32_t live, int kb,
-                                           int t, int cols, const float (&p)[NT][2],
-                                           float (&acc)[MT][NT][4]) const {
-    constexpr int kGroups = kBlock / GROUP, kWords = 4 / kGroups;
+  // The token whose columns this lane copies with its i-th copy.
+  __device__ __forceinline__ int token(int i) const { return 2 * i + (lane >> 4); }
+  __device__ __forceinline__ int x_col() const { return (lane & (kCols / 8 - 1)) * 8; }
+
+  // Continues with columns [c0, c1) of the rows whose row g is `row` and whose row
+  // lane % 16 is `srow`, and of n tokens; the caller sets x[] (column c0 + x_col()).
+  __device__ __forceinline__ void seek(const uint8_t* codes, int64_t row, int64_t srow, int c0,
+                                       int c1, int cols, int n) {
+    q = codes + row * (cols / 2) + c0 / 2 + 16 * t;
+    si = srow * rs + c0 / GROUP;
+    left = c1 - c0;
+    tokens = n;
+  }
+
+  __device__ __forceinline__ void copy() {
+    const uint32_t st = base + (uint32_t)fill;
 #pragma unroll
-    for (int grp = 0; grp < kGroups; ++grp) {
-      if (kb * kBlock + grp * GROUP >= cols) break;
-      float part[MT][NT][4];
+    for (int i = 0; i < 2; ++i)
+      cp_async_16(st + (uint32_t)((g + 8 * i) * (kCols / 2) + ((t ^ swizzle(g)) << 4)),
+                  q + (i ? q8 : 0), GROUP == 128 || 32 * t < left ? 16u : 0u);
+    if (lane < 16) {
+      const int64_t w = si >> 1;
+      const uint16_t* src = scales + 2 * w;
+      const int n = (int)min(s_end - 2 * w, (int64_t)(kScaleBytes / 2));  // scales from there on
 #pragma unroll
-      for (int m = 0; m < MT; ++m)
+      for (int j = 0; j < kScaleBytes / 4; ++j)
+        cp_async_4(st + (uint32_t)(kCodes + lane * kScaleBytes + j * 4), n > 2 * j ? src + 2 * j : scales,
+                   n > 2 * j + 1 ? 4u : n > 2 * j ? 2u : 0u);
+    }
+    const int c = x_col() / 8, in = c % (GROUP / 8);
+    const int place = (c - in + (in % kWords) * 4 + in / kWords) ^ ((lane >> 4) << 2);
 #pragma unroll
-        for (int n = 0; n < NT; ++n)
+    for (int i = 0; i < kCopies; ++i) {
+      const bool there = token(i) < tokens && x_col() < left;
+      cp_async_16(st + (uint32_t)(kX + token(i) * kCols * 2 + place * 16), there ? x[i] : scales,
+                  there ? 16u : 0u);
+      x[i] += kCols;
+    }
+    q += kCols / 2;
+    si += kG;
+    left -= kCols;
+  }
+  __device__ __forceinline__ void commit() {
+    cp_async_commit();
+    fill = fill + kStage == kBytes ? 0 : fill + kStage;
+  }
+
+  // acc[n] += rows x (tokens of tile n) for the block taken next, of which `valid`
+  // columns and `n_tok` tokens count. PERMUTED: each eight values of x lie in the
+  // order 0 4 1 5 2 6 3 7. `odd`: whether the block's scales of this lane's rows
+  // start at an odd place of the matrix.
+  template <bool PERMUTED>
+  __device__ __forceinline__ void multiply(int odd, int valid, int n_tok, float (&acc)[kNT][4]) {
+    cp_async_wait<kAhead - 1>();
+    __syncwarp();
+    const uint32_t at = base + (uint32_t)take;
+    const uint32_t xt = at + (uint32_t)(kX + g * kCols * 2);
+    const uint32_t sc = at + (uint32_t)(kCodes + g * kScaleBytes + odd * 2);
 #pragma unroll
-          for (int i = 0; i < 4; ++i) part[m][n][i] = 0.0f;
+    for (int grp = 0; grp < kG; ++grp) {
+      if (grp > 0 && valid <= grp * GROUP) break;
+      uint32_t w[2][kWords];
 #pragma unroll
-      for (int jj = 0; jj < kWords; ++jj) {
-        const int j = grp * kWords + jj;
-        uint4 v[NT];
-#pragma unroll
-        for (int n = 0; n < NT; ++n) {
-          v[n] = make_uint4(0u, 0u, 0u, 0u);
-          if (x[n])
-            v[n] = *reinterpret_cast<const uint4*>(x[n] + kb * kBlock + word_col<GROUP>(t, j));
+      for (int i = 0; i < 2; ++i) {
+        const uint32_t row = at + (uint32_t)((g + 8 * i) * (kCols / 2));
+        if constexpr (GROUP == 128) {
+          asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];"
+                       : "=r"(w[i][0]), "=r"(w[i][1]), "=r"(w[i][2]), "=r"(w[i][3])
+                       : "r"(row + (uint32_t)(((4 * grp + t) ^ swizzle(g)) << 4))
+                       : "memory");
+        } else if constexpr (GROUP == 64) {
+          asm volatile("ld.shared.v2.u32 {%0,%1}, [%2];"
+                       : "=r"(w[i][0]), "=r"(w[i][1])
+                       : "r"(row + (uint32_t)((((2 * grp + (t >> 1)) ^ swizzle(g)) << 4) + (t & 1) * 8))
+                       : "memory");
+        } else {
+          asm volatile("ld.shared.u32 %0, [%1];"
+                       : "=r"(w[i][0])
+                       : "r"(row + (uint32_t)(((grp ^ swizzle(g)) << 4) + t * 4))
+                       : "memory");
         }
-        uint32_t a[MT][2][4];
+      }
+      float s[2];
 #pragma unroll
-        for (int m = 0; m < MT; ++m)
+      for (int i = 0; i < 2; ++i) {
+        uint16_t v;
+        asm volatile("ld.shared.u16 %0, [%1];"
+                     : "=h"(v)
+                     : "r"(sc + (uint32_t)(8 * i * kScaleBytes + 2 * grp))
+                     : "memory");
+        s[i] = bf(v);
+      }
+      float part[kNT][4];
 #pragma unroll
-          for (int i = 0; i < 2; ++i) {
-            const uint4& q = w[m][i];
-            open_codes(j == 0 ? q.x : j == 1 ? q.y : j == 2 ? q.z : q.w, a[m][i]);
-          }
+      for (int j = 0; j < kWords; ++j) {
+        uint32_t a[2][4];
+        open_codes(w[0][j], a[0]);
+        open_codes(w[1][j], a[1]);
 #pragma unroll
-        for (int n = 0; n < NT; ++n) {
-          if (NT > 1 && !((live >> n) & 1u)) continue;
-          const uint32_t b0 = __byte_perm(v[n].x, v[n].z, 0x5410), b1 = __byte_perm(v[n].x, v[n].z, 0x7632);
-          const uint32_t b2 = __byte_perm(v[n].y, v[n].w, 0x5410), b3 = __byte_perm(v[n].y, v[n].w, 0x7632);
-#pragma unroll
-          for (int m = 0; m < MT; ++m) {
-            mma16816(part[m][n], a[m][0][0], a[m][1][0], a[m][0][1], a[m][1][1], b0, b1);
-            mma16816(part[m][n], a[m][0][2], a[m][1][2], a[m][0][3], a[m][1][3], b2, b3);
-          }
+        for (int n = 0; n < kNT; ++n) {
+          if (n > 0 && 8 * n >= n_tok) break;
+          uint4 u;
+          asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];"
+                       : "=r"(u.x), "=r"(u.y), "=r"(u.z), "=r"(u.w)
+                       : "r"(xt + (uint32_t)(n * 8 * kCols * 2 +
+                                             (((grp * (GROUP / 8) + 4 * j + t) ^ ((g & 1) << 2)) << 4)))
+                       : "memory");
+          const uint32_t b0 = PERMUTED ? u.x : __byte_perm(u.x, u.z, 0x5410);
+          const uint32_t b1 = PERMUTED ? u.y : __byte_perm(u.x, u.z, 0x7632);
+          const uint32_t b2 = PERMUTED ? u.z : __byte_perm(u.y, u.w, 0x5410);
+          const uint32_t b3 = PERMUTED ? u.w : __byte_perm(u.y, u.w, 0x7632);
+          if (j == 0) mma16816<true>(part[n], a[0][0], a[1][0], a[0][1], a[1][1], b0, b1);
+          else mma16816<false>(part[n], a[0][0], a[1][0], a[0][1], a[1][1], b0, b1);
+          mma16816<false>(part[n], a[0][2], a[1][2], a[0][3], a[1][3], b2, b3);
         }
       }
 #pragma unroll
-      for (int m = 0; m < MT; ++m) {
-        const float s0 = bf(s[m][0][grp]), s1 = bf(s[m][1][grp]);
+      for (int n = 0; n < kNT; ++n) {
+        if (n > 0 && 8 * n >= n_tok) break;
 #pragma unroll
-        for (int n = 0; n < NT; ++n) {
-          if (NT > 1 && !((live >> n) & 1u)) continue;
-#pragma unroll
-          for (int i = 0; i < 2; ++i) {
-            acc[m][n][i] = fmaf(P ? s0 * p[n][i] : s0, part[m][n][i], acc[m][n][i]);
-            acc[m][n][2 + i] = fmaf(P ? s1 * p[n][i] : s1, part[m][n][2 + i], acc[m][n][2 + i]);
-          }
-        }
+        for (int i = 0; i < 4; ++i) acc[n][i] = fmaf(s[i >> 1], part[n][i], acc[n][i]);
       }
     }
+    __syncwarp();  // the stage may be filled again
+    take = take + kStage == kBytes ? 0 : take + kStage;
   }
 };
 
-// Every kWarps-th block of a row tile from this warp's own on, kAhead loads ahead.
-template <int NT, int GROUP, int kAhead>
-__device__ __forceinline__ void stream_rows(const uint8_t* q, const uint16_t* sc, int eight,
-                                            const uint16_t* const (&x)[NT], uint32_t live, int warp,
-                                            int t, int cols, float (&acc)[1][NT][4]) {
-  const int blocks = (cols + kBlock - 1) / kBlock;
-  const float none[NT][2] = {};
-  Block<1, GROUP> ring[kAhead];
+// A warp's sums of 16 rows x 8 NT tokens in shared memory: part[row * 8 NT + token].
+template <int NT>
+__device__ __forceinline__ void leave_part(float* part, int g, int t, const float (&acc)[NT][4]) {
 #pragma unroll
-  for (int d = 0; d < kAhead; ++d)
-    if (warp + d * kWarps < blocks) ring[d].load(q, sc, eight, 0, warp + d * kWarps, t, cols);
-  for (int kb = warp; kb < blocks; kb += kAhead * kWarps) {
-#pragma unroll
-    for (int d = 0; d < kAhead; ++d) {
-      const int at = kb + d * kWarps;
-      if (at < blocks) {
-        ring[d].template multiply<NT, false>(x, live, at, t, cols, none, acc);
-        if (at + kAhead * kWarps < blocks)
-          ring[d].load(q, sc, eight, 0, at + kAhead * kWarps, t, cols);
-      }
-    }
+  for (int n = 0; n < NT; ++n) {
+    float* at = part + g * 8 * NT + 8 * n + 2 * t;
+    *reinterpret_cast<float2*>(at) = make_float2(acc[n][0], acc[n][1]);
+    *reinterpret_cast<float2*>(at + 8 * 8 * NT) = make_float2(acc[n][2], acc[n][3]);
   }
 }
 
-// The warps' sums of MT x 16 rows x NT x 8 tokens side by side in shared memory:
-// part[((warp * MT + m) * 16 + row) * 8 NT + token].
-template <int MT, int NT>
-__device__ __forceinline__ void leave_parts(float* part, int warp, int g, int t,
-                                            const float (&acc)[MT][NT][4]) {
-#pragma unroll
-  for (int m = 0; m < MT; ++m)
-#pragma unroll
-    for (int n = 0; n < NT; ++n) {
-      float* at = part + ((warp * MT + m) * 16 + g) * 8 * NT + 8 * n + 2 * t;
-      *reinterpret_cast<float2*>(at) = make_float2(acc[m][n][0], acc[m][n][1]);
-      *reinterpret_cast<float2*>(at + 8 * 8 * NT) = make_float2(acc[m][n][2], acc[m][n][3]);
-    }
+__device__ __forceinline__ uint8_t* ring_of(uint8_t* dynamic) {
+  return dynamic + (-smem_u32(dynamic) & 127u);
 }
 
-template <int NT, int GROUP>
-__global__ void __launch_bounds__(kThreads) w4_matvec_kernel(const uint16_t* x, const uint8_t* q,
-                                                             const uint16_t* scale, int N, int rows,
-                                                             int cols, uint16_t* y) {
-  __shared__ __align__(16) float part[kWarps * 16 * 8 * NT];
+template <int GROUP, int TOK>
+__global__ void __launch_bounds__(kThreads, 2)
+    w4_matvec_kernel(const uint16_t* x, const uint8_t* q, const uint16_t* scale, int N, int rows,
+                     int cols, uint16_t* y) {
+  using St = Stream<GROUP, TOK>;
+  constexpr int kTok = 8 * St::kNT;
+  extern __shared__ __align__(16) uint8_t dynamic[];
+  __shared__ __align__(16) float part[kWarps * 16 * kTok];
   griddep_wait();
   griddep_launch_dependents();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
-  const int r0 = blockIdx.x * 16, t0 = blockIdx.y * 8 * NT;
+  const int r0 = blockIdx.x * 16, t0 = blockIdx.y * TOK, n = min(TOK, N - t0);
   const int row = min(r0 + g, rows - 1);  // a row past the last one reads the last one
-  const uint16_t* xt[NT];
-  uint32_t live = 0;
+  const int c0 = share(warp, kWarps, cols), c1 = share(warp + 1, kWarps, cols);
+  const int blocks = (c1 - c0 + St::kCols - 1) / St::kCols;
+  St st;
+  st.init(ring_of(dynamic), warp, lane, min(8, rows - 1 - row), cols, scale, rows);
+  st.seek(q, row, min(r0 + (lane & 15), rows - 1), c0, c1, cols, n);
 #pragma unroll
-  for (int n = 0; n < NT; ++n) {
-    const int tok = t0 + 8 * n + g;
-    xt[n] = tok < N ? x + (size_t)tok * cols : nullptr;
-    live |= (t0 + 8 * n < N) ? 1u << n : 0u;
+  for (int i = 0; i < St::kCopies; ++i)
+    st.x[i] = x + (size_t)(t0 + min(st.token(i), n - 1)) * cols + c0 + st.x_col();
+#pragma unroll
+  for (int d = 0; d < St::kAhead; ++d) {
+    if (d < blocks) st.copy();
+    st.commit();
   }
-  float acc[1][NT][4] = {};
-  stream_rows<NT, GROUP, NT == 1 ? 4 : 2>(q + (size_t)row * (cols / 2), scale + (size_t)row * (cols / GROUP),
-                                          min(8, rows - 1 - row), xt, live, warp, t, cols, acc);
-  leave_parts<1, NT>(part, warp, g, t, acc);
+  const int odd = ((row & 1) * st.rs + c0 / GROUP) & 1;
+  float acc[St::kNT][4] = {};
+  for (int b = 0; b < blocks; ++b) {
+    st.template multiply<false>((odd + b * St::kG) & 1, c1 - c0 - b * St::kCols, n, acc);
+    if (b + St::kAhead < blocks) st.copy();
+    st.commit();
+  }
+  leave_part<St::kNT>(part + warp * 16 * kTok, g, t, acc);
   __syncthreads();
-  for (int i = threadIdx.x; i < 16 * 8 * NT; i += kThreads) {
-    const int tok = t0 + (i >> 4), r = r0 + (i & 15);
-    if (tok >= N || r >= rows) continue;
+  for (int i = threadIdx.x; i < 16 * n; i += kThreads) {
+    const int r = r0 + (i & 15);
+    if (r >= rows) continue;
     float v = 0.0f;
 #pragma unroll
-    for (int w = 0; w < kWarps; ++w) v += part[(w * 16 + (i & 15)) * 8 * NT + (i >> 4)];
-    y[(size_t)tok * rows + r] = __bfloat16_as_ushort(__float2bfloat16_rn(v));
+    for (int w = 0; w < kWarps; ++w) v += part[(w * 16 + (i & 15)) * kTok + (i >> 4)];
+    y[(size_t)(t0 + (i >> 4)) * rows + r] = to_bf(v);
   }
 }
 
 // Routes grouped by expert, in shared memory, by the whole block: pieces of at
-// most `most` routes of one expert, experts ascending, routes in their order.
+// most `most` routes of one expert, experts ascending, routes in their order. A
+// route without an expert (an id outside 0..E-1), or to an expert that its token
+// has named before, is in none; p[] gets the token's whole probability of the
+// expert where the probabilities are given.
+template <int ROUTES>
 struct Groups {
-  int16_t order[kMaxRoutes];                          // routes, sorted by expert
-  int16_t expert[kMaxExperts + kMaxRoutes / 8];       // of each piece
-  int16_t first[kMaxExperts + kMaxRoutes / 8];        // its first place in `order`
-  int16_t count[kMaxExperts + kMaxRoutes / 8];
-  int16_t rank[kMaxRoutes];                           // of a route among its expert's
-  int16_t routes[kMaxExperts];                        // of each expert
-  int scan[2][kWarps];
+  static constexpr int kPieces = kMaxExperts + ROUTES / 8;
+  int16_t id[ROUTES];       // expert, or -1
+  int16_t rank[ROUTES];     // of a route among its expert's
+  int16_t order[ROUTES];    // routes, sorted by expert
+  int16_t routes[kMaxExperts];
+  int16_t expert[kPieces], first[kPieces], count[kPieces];  // first: its place in `order`
+  int scan[2][kMaxExperts / 32];
   int pieces;
 };
 
-__device__ __forceinline__ void group_routes(Groups& G, const int32_t* ids, int R, int E,
-                                             int most) {
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  static_assert(kThreads == kMaxExperts, "one thread per expert");
-  G.routes[threadIdx.x] = 0;
+template <int THREADS, int ROUTES>
+__device__ __forceinline__ void group_routes(Groups<ROUTES>& G, float* p, const int32_t* ids,
+                                             const float* probs, int R, int K, int E, int most) {
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, tid = threadIdx.x;
+  static_assert(THREADS >= kMaxExperts, "a thread for each expert");
+  if (tid < kMaxExperts) G.routes[tid] = 0;
+  for (int i = tid; i < R; i += THREADS) {
+    const int r0 = i / K * K;
+    int e = __ldcg(ids + i);
+    if (e < 0 || e >= E) e = -1;
+    for (int r = r0; r < i && e >= 0; ++r)
+      if (__ldcg(ids + r) == e) e = -1;
+    G.id[i] = (int16_t)e;
+    if (p && e >= 0) {
+      float v = __ldcg(probs + i);
+      for (int r = i + 1; r < r0 + K; ++r)
+        if (__ldcg(ids + r) == e) v += __ldcg(probs + r);
+      p[i] = v;
+    }
+  }
   __syncthreads();
   if (warp == 0) {  // 32 routes at a time, in order: each gets its rank within its expert
     for (int i0 = 0; i0 < R; i0 += 32) {
       const int i = i0 + lane;
-      const int id = i < R ? ids[i] : -1;
-      const int e = id >= 0 && id < E ? id : -1;
+      const int e = i < R ? G.id[i] : -1;
       const uint32_t same = __match_any_sync(0xFFFFFFFFu, e);
       const int before = __popc(same & ((1u << lane) - 1u));
-      const int base = e >= 0 ? G.routes[e] : 0;
+      const int from = e >= 0 ? G.routes[e] : 0;
       __syncwarp();
-      if (e >= 0 && before == 0) G.routes[e] = (int16_t)(base + __popc(same));
-      if (i < R) G.rank[i] = (int16_t)(base + before);
+      if (e >= 0 && before == 0) G.routes[e] = (int16_t)(from + __popc(same));
+      if (i < R) G.rank[i] = (int16_t)(from + before);
       __syncwarp();
     }
   }
   __syncthreads();
   // exclusive sums over the experts of their routes and of their pieces
-  const int n = G.routes[threadIdx.x], np = (n + most - 1) / most;
+  const int n = tid < kMaxExperts ? G.routes[tid] : 0, np = (n + most - 1) / most;
   int sn = n, sp = np;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
@@ -296,275 +382,476 @@ __device__ __forceinline__ void group_routes(Groups& G, const int32_t* ids, int 
       sp += vp;
     }
   }
-  if (lane == 31) {
+  if (lane == 31 && warp < kMaxExperts / 32) {
     G.scan[0][warp] = sn;
     G.scan[1][warp] = sp;
   }
   __syncthreads();
-  int on = sn - n, op = sp - np;
-  for (int w = 0; w < warp; ++w) {
-    on += G.scan[0][w];
-    op += G.scan[1][w];
+  if (tid < kMaxExperts) {
+    int on = sn - n, op = sp - np;
+    for (int w = 0; w < warp; ++w) {
+      on += G.scan[0][w];
+      op += G.scan[1][w];
+    }
+    G.routes[tid] = (int16_t)on;  // now: where the expert's routes begin
+    for (int j = 0; j < np; ++j) {
+      G.expert[op + j] = (int16_t)tid;
+      G.first[op + j] = (int16_t)(on + j * most);
+      G.count[op + j] = (int16_t)min(most, n - j * most);
+    }
+    if (tid == kMaxExperts - 1) G.pieces = op + np;
   }
-  G.routes[threadIdx.x] = (int16_t)on;  // now: where the expert's routes begin
-  for (int j = 0; j < np; ++j) {
-    G.expert[op + j] = (int16_t)threadIdx.x;
-    G.first[op + j] = (int16_t)(on + j * most);
-    G.count[op + j] = (int16_t)min(most, n - j * most);
-  }
-  if (threadIdx.x == kThreads - 1) G.pieces = op + np;
   __syncthreads();
-  for (int i = threadIdx.x; i < R; i += kThreads) {
-    const int e = ids[i];
-    if (e >= 0 && e < E) G.order[G.routes[e] + G.rank[i]] = (int16_t)i;
+  for (int i = tid; i < R; i += THREADS) {
+    const int e = G.id[i];
+    if (e >= 0) G.order[G.routes[e] + G.rank[i]] = (int16_t)i;
   }
   __syncthreads();
 }
 
-// First product. A unit is 16 features (their gate and up rows) of one expert's
-// piece of at most 8 NT routes; a team of S warps, which split the columns,
-// takes every teams-th unit, its loads running on from unit to unit. Teams of
-// a block take neighbouring features of the same expert.
-template <int NT, int GROUP>
+// First product. A unit is 8 features of one expert's piece of at most TOK
+// routes: rows g of the tile are their gate rows, rows g + 8 their up rows, so a
+// lane finds both sums of a feature in its own registers. A team of S warps,
+// which split the columns, takes every teams-th unit, its copies running on from
+// unit to unit.
+template <int GROUP, int TOK>
 __global__ void __launch_bounds__(kThreads, 2) w4_fc1_kernel(const W4Args a, const int S) {
-  constexpr int kAhead = 2, kPart = 2 * 16 * 8 * NT;
-  __shared__ Groups G;
+  using St = Stream<GROUP, TOK>;
+  constexpr int kTok = 8 * St::kNT, kPart = 16 * kTok;
+  extern __shared__ __align__(16) uint8_t dynamic[];
+  __shared__ Groups<kMaxRoutes> G;
   __shared__ __align__(16) float part[kWarps * kPart];
   griddep_wait();
   griddep_launch_dependents();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
-  group_routes(G, a.topk_ids, a.N * a.K, a.E, 8 * NT);
-  const int team = (blockIdx.x * kWarps + warp) / S, teams = gridDim.x * kWarps / S;
-  const int member = warp % S, i_tiles = a.I / 16, units = G.pieces * i_tiles;
-  const int blocks = (a.H + kBlock - 1) / kBlock;
+  group_routes<kThreads>(G, nullptr, a.topk_ids, nullptr, a.N * a.K, a.K, a.E, TOK);
+  // neighbouring units on different SMs, so that a few units fill them evenly
+  const int team = warp / S * gridDim.x + blockIdx.x, teams = gridDim.x * kWarps / S;
+  const int member = warp % S, i_tiles = a.I / 8, units = G.pieces * i_tiles;
+  const int c0 = share(member, S, a.H), c1 = share(member + 1, S, a.H);
+  const int blocks = (c1 - c0 + St::kCols - 1) / St::kCols;
 
-  Block<2, GROUP> ring[kAhead];
-  int unit_l = team, kb_l = member;  // what is loaded next
-  const uint8_t* q_l = nullptr;
-  const uint16_t* s_l = nullptr;
-  int have_l = -1;
-  auto load_next = [&](Block<2, GROUP>& b) {
-    while (kb_l >= blocks && unit_l < units) {
-      kb_l = member;
+  St st;
+  st.init(ring_of(dynamic), warp, lane, a.I, a.H, a.w13_scale, (int64_t)a.E * 2 * a.I);
+  int unit_l = team - teams, more_l = 0;  // what is copied next: blocks left of the unit
+  auto copy_next = [&]() {
+    if (more_l == 0 && blocks > 0 && unit_l < units) {
       unit_l += teams;
+      if (unit_l < units) {
+        const int piece = unit_l / i_tiles, i0 = (unit_l - piece * i_tiles) * 8;
+        const int first = G.first[piece], n = G.count[piece];
+        const int64_t row = (int64_t)G.expert[piece] * 2 * a.I + i0;
+        st.seek(a.w13, row + g, row + (lane & 7) + ((lane >> 3) & 1) * a.I, c0, c1, a.H, n);
+#pragma unroll
+        for (int i = 0; i < St::kCopies; ++i)
+          st.x[i] = a.x + (size_t)(G.order[first + min(st.token(i), n - 1)] / a.K) * a.H + c0 + st.x_col();
+        more_l = blocks;
+      }
     }
-    if (unit_l >= units) return;
-    if (unit_l != have_l) {
-      have_l = unit_l;
-      const int piece = unit_l / i_tiles, i0 = (unit_l - piece * i_tiles) * 16;
-      const size_t row = (size_t)G.expert[piece] * 2 * a.I + i0 + g;
-      q_l = a.w13 + row * (a.H / 2);
-      s_l = a.w13_scale + row * (a.H / GROUP);
+    if (more_l > 0) {
+      st.copy();
+      --more_l;
     }
-    b.load(q_l, s_l, 8, a.I, kb_l, t, a.H);
-    kb_l += S;
+    st.commit();
   };
 #pragma unroll
-  for (int d = 0; d < kAhead; ++d) load_next(ring[d]);
+  for (int d = 0; d < St::kAhead; ++d) copy_next();
 
-  const float none[NT][2] = {};
-  float acc[2][NT][4] = {};
-  const uint16_t* xt[NT];
-  uint32_t live = 0;
-  int unit = team, kb = member;
-  auto begin = [&]() {  // the tokens of the unit's piece
-    const int piece = unit / i_tiles, first = G.first[piece], n = G.count[piece];
-    live = 0;
-#pragma unroll
-    for (int j = 0; j < NT; ++j) {
-      const int at = 8 * j + g;
-      xt[j] = at < n ? a.x + (size_t)(G.order[first + at] / a.K) * a.H : nullptr;
-      live |= 8 * j < n ? 1u << j : 0u;
-    }
-#pragma unroll
-    for (int m = 0; m < 2; ++m)
-#pragma unroll
-      for (int j = 0; j < NT; ++j)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) acc[m][j][i] = 0.0f;
-  };
-  auto end = [&]() {  // h of the unit
-    const int piece = unit / i_tiles, i0 = (unit - piece * i_tiles) * 16;
+  const int odd = ((g & 1) * st.rs + c0 / GROUP) & 1;
+  for (int unit = team; unit < units; unit += teams) {
+    const int piece = unit / i_tiles, i0 = (unit - piece * i_tiles) * 8;
     const int first = G.first[piece], n = G.count[piece];
+    float acc[St::kNT][4] = {};
+    for (int b = 0; b < blocks; ++b) {
+      st.template multiply<false>((odd + b * St::kG) & 1, c1 - c0 - b * St::kCols, n, acc);
+      copy_next();
+    }
+    auto h_of = [&](int at, int i, float gate, float up) {
+      const float h = (a.activation ? act_fwd<1>(gate) : act_fwd<0>(gate)) * up;
+      a.h[(size_t)G.order[first + at] * a.I + i0 + permuted(i)] = to_bf(h);
+    };
     if (S > 1) {
-      float* mine = part + warp * kPart;
-      leave_parts<2, NT>(mine, 0, g, t, acc);
+      leave_part<St::kNT>(part + warp * kPart, g, t, acc);
       asm volatile("bar.sync %0, %1;" ::"r"(1 + warp / S), "r"(32 * S) : "memory");
       const float* all = part + (warp - member) * kPart;
-      for (int i = member * 32 + lane; i < 16 * 8 * NT; i += 32 * S) {
-        if ((i >> 4) >= n) break;
-        float gv = 0.0f, uv = 0.0f;
+      for (int i = member * 32 + lane; i < 8 * n; i += 32 * S) {
+        float gate = 0.0f, up = 0.0f;
         for (int w = 0; w < S; ++w) {
-          gv += all[w * kPart + (i & 15) * 8 * NT + (i >> 4)];
-          uv += all[w * kPart + (16 + (i & 15)) * 8 * NT + (i >> 4)];
+          gate += all[w * kPart + (i & 7) * kTok + (i >> 3)];
+          up += all[w * kPart + (8 + (i & 7)) * kTok + (i >> 3)];
         }
-        const float h = (a.activation ? act_fwd<1>(gv) : act_fwd<0>(gv)) * uv;
-        a.h[(size_t)G.order[first + (i >> 4)] * a.I + i0 + (i & 15)] =
-            __bfloat16_as_ushort(__float2bfloat16_rn(h));
+        h_of(i >> 3, i & 7, gate, up);
       }
       asm volatile("bar.sync %0, %1;" ::"r"(1 + warp / S), "r"(32 * S) : "memory");
     } else {
 #pragma unroll
-      for (int j = 0; j < NT; ++j)
+      for (int j = 0; j < St::kNT; ++j)
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const int at = 8 * j + 2 * t + (i & 1);
-          if (at >= n) continue;
-          const float gv = acc[0][j][i];
-          const float h = (a.activation ? act_fwd<1>(gv) : act_fwd<0>(gv)) * acc[1][j][i];
-          a.h[(size_t)G.order[first + at] * a.I + i0 + g + 8 * (i >> 1)] =
-              __bfloat16_as_ushort(__float2bfloat16_rn(h));
-        }
-    }
-  };
-  if (unit < units) begin();
-  while (unit < units) {
-#pragma unroll
-    for (int d = 0; d < kAhead; ++d) {
-      while (kb >= blocks && unit < units) {
-        end();
-        kb = member;
-        unit += teams;
-        if (unit < units) begin();
-      }
-      if (unit >= units) break;
-      ring[d].template multiply<NT, false>(xt, live, kb, t, a.H, none, acc);
-      load_next(ring[d]);
-      kb += S;
+        for (int i = 0; i < 2; ++i)
+          if (8 * j + 2 * t + i < n) h_of(8 * j + 2 * t + i, g, acc[j][i], acc[j][2 + i]);
     }
   }
 }
 
 // Second product and the sum over a token's routes: block (16 output columns,
-// 8 NT tokens) goes through the experts that its tokens chose, in ascending
-// order; a team of S warps, which split the columns, takes every teams-th
-// expert. A column of the products is a token, weighted by its probability for
-// the expert. Dynamic shared memory: prob [items][8 NT] f32, slot [items][8 NT]
-// i8; at the end the warps' sums.
-template <int NT, int GROUP, int W>
-__global__ void __launch_bounds__(W * 32, W == 16 ? 1 : 2) w4_fc2_kernel(const W4Args a, const int S) {
-  constexpr int kTok = 8 * NT;
-  extern __shared__ __align__(16) float prob[];
-  float* part = prob;
-  __shared__ int16_t item_of[kMaxExperts], expert_of[kMaxExperts];
-  __shared__ int warp_items[kMaxExperts / 32];
+// kChunk tokens) goes through the pieces of the experts that its tokens chose; a
+// team of S warps, which split the columns, takes every teams-th piece and adds
+// its products, weighted by the tokens' probabilities, to the warp's own sums
+// [token][16]. Dynamic shared memory: the rings, the sums, the probabilities.
+template <int GROUP, int TOK, int W>
+__global__ void __launch_bounds__(W * 32, 16 / W)
+    w4_fc2_kernel(const W4Args a, const int S) {
+  using St = Stream<GROUP, TOK>;
+  constexpr int kRoutes = kChunk * kMaxTopK;
+  extern __shared__ __align__(16) uint8_t dynamic[];
+  __shared__ Groups<kRoutes> G;
+  uint8_t* ring = ring_of(dynamic);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
-  const int r0 = blockIdx.x * 16, t0 = blockIdx.y * kTok;
-  const int tokens = min(kTok, a.N - t0), R = tokens * a.K;
-  const int32_t* ids = a.topk_ids + (size_t)t0 * a.K;
-  const float* ps = a.topk_p + (size_t)t0 * a.K;
+  const int r0 = blockIdx.x * 16, t0 = blockIdx.y * kChunk;
+  const int tokens = min(kChunk, a.N - t0);
+  float* sums = reinterpret_cast<float*>(ring + W * St::kBytes);
+  float* prob = sums + W * tokens * 16;
+  for (int i = threadIdx.x; i < W * tokens * 16; i += W * 32) sums[i] = 0.0f;
   // The first product's kernel let this one start after every earlier kernel had
   // finished, and writes neither the routes nor the weights: only h has to wait.
-  static_assert(W * 32 >= kMaxExperts, "a thread for each expert");
-  const int e_mine = threadIdx.x;
-  if (e_mine < kMaxExperts) item_of[e_mine] = -1;
-  __syncthreads();
-  for (int i = threadIdx.x; i < R; i += W * 32) {
-    const int e = __ldcg(ids + i);
-    if (e >= 0 && e < a.E) item_of[e] = 0;
-  }
-  __syncthreads();
-  const bool used = e_mine < kMaxExperts && item_of[e_mine] == 0;
-  const uint32_t ballot = __ballot_sync(0xFFFFFFFFu, used);
-  if (lane == 0 && e_mine < kMaxExperts) warp_items[warp] = __popc(ballot);
-  __syncthreads();
-  int before = 0, items = 0;
-#pragma unroll
-  for (int w = 0; w < kMaxExperts / 32; ++w) {
-    before += w < warp ? warp_items[w] : 0;
-    items += warp_items[w];
-  }
-  if (used) {
-    const int at = before + __popc(ballot & ((1u << lane) - 1u));
-    item_of[e_mine] = (int16_t)at;
-    expert_of[at] = (int16_t)e_mine;
-  }
-  int8_t* slot = reinterpret_cast<int8_t*>(prob + items * kTok);
-  for (int i = threadIdx.x; i < items * kTok; i += W * 32) {
-    prob[i] = 0.0f;
-    slot[i] = -1;
-  }
-  __syncthreads();
-  if ((int)threadIdx.x < tokens) {
-    // a token that names an expert twice gets both probabilities
-    for (int k = 0; k < a.K; ++k) {
-      const int e = __ldcg(ids + threadIdx.x * a.K + k);
-      if (e < 0 || e >= a.E) continue;
-      const int at = item_of[e] * kTok + threadIdx.x;
-      prob[at] += __ldcg(ps + threadIdx.x * a.K + k);
-      if (slot[at] < 0) slot[at] = (int8_t)k;
-    }
-  }
-  __syncthreads();
-
-  constexpr int kAhead = NT == 4 ? 2 : 4;
-  const int teams = W / S;
-  const int blocks = (a.I + kBlock - 1) / kBlock, member = warp % S;
-  Block<1, GROUP> ring[kAhead];
-  int item_l = warp / S, kb_l = member, have_l = -1;  // what is loaded next
-  const uint8_t* q_l = nullptr;
-  const uint16_t* s_l = nullptr;
-  auto load_next = [&](Block<1, GROUP>& b) {
-    while (kb_l >= blocks && item_l < items) {
-      kb_l = member;
-      item_l += teams;
-    }
-    if (item_l >= items) return;
-    if (item_l != have_l) {
-      have_l = item_l;
-      const size_t row = (size_t)expert_of[item_l] * a.H + r0 + g;
-      q_l = a.w2 + row * (a.I / 2);
-      s_l = a.w2_scale + row * (a.I / GROUP);
-    }
-    b.load(q_l, s_l, 8, 0, kb_l, t, a.I);
-    kb_l += S;
-  };
-#pragma unroll
-  for (int d = 0; d < kAhead; ++d) load_next(ring[d]);
+  group_routes<W * 32>(G, prob, a.topk_ids + (size_t)t0 * a.K, a.topk_p + (size_t)t0 * a.K,
+                       tokens * a.K, a.K, a.E, TOK);
+  const int teams = W / S, member = warp % S;
+  const int c0 = share(member, S, a.I), c1 = share(member + 1, S, a.I);
+  const int blocks = (c1 - c0 + St::kCols - 1) / St::kCols;
+  const int pieces = blocks > 0 ? G.pieces : 0;  // more warps than columns: nothing for this one
+  St st;
+  st.init(ring, warp, lane, 8, a.I, a.w2_scale, (int64_t)a.E * a.H);
   griddep_wait();
   griddep_launch_dependents();
-
-  float acc[1][NT][4] = {};
-  const uint16_t* ht[NT];
-  float p[NT][2];
-  uint32_t live = 0;
-  int item = warp / S, kb = member, have = -1;
-  while (item < items) {
+  int piece_l = warp / S - teams, more_l = 0;  // what is copied next
+  auto copy_next = [&]() {
+    if (more_l == 0 && piece_l < pieces) {
+      piece_l += teams;
+      if (piece_l < pieces) {
+        const int first = G.first[piece_l], n = G.count[piece_l];
+        const int64_t row = (int64_t)G.expert[piece_l] * a.H + r0;
+        st.seek(a.w2, row + g, row + (lane & 15), c0, c1, a.I, n);
 #pragma unroll
-    for (int d = 0; d < kAhead; ++d) {
-      while (kb >= blocks && item < items) {
-        kb = member;
-        item += teams;
+        for (int i = 0; i < St::kCopies; ++i)
+          st.x[i] = a.h + ((size_t)t0 * a.K + G.order[first + min(st.token(i), n - 1)]) * a.I + c0 + st.x_col();
+        more_l = blocks;
       }
-      if (item >= items) break;
-      if (item != have) {
-        have = item;
-        live = 0;
+    }
+    if (more_l > 0) {
+      st.copy();
+      --more_l;
+    }
+    st.commit();
+  };
 #pragma unroll
-        for (int n = 0; n < NT; ++n) {
-          const int k = slot[item * kTok + 8 * n + g];
-          ht[n] = k >= 0 ? a.h + ((size_t)(t0 + 8 * n + g) * a.K + k) * a.I : nullptr;
-          p[n][0] = prob[item * kTok + 8 * n + 2 * t];
-          p[n][1] = prob[item * kTok + 8 * n + 2 * t + 1];
-          live |= __any_sync(0xFFFFFFFFu, k >= 0) ? 1u << n : 0u;
+  for (int d = 0; d < St::kAhead; ++d) copy_next();
+
+  const int odd = ((g & 1) * st.rs + c0 / GROUP) & 1;
+  float* mine = sums + warp * tokens * 16;
+  for (int piece = warp / S; piece < pieces; piece += teams) {
+    const int first = G.first[piece], n = G.count[piece];
+    float acc[St::kNT][4] = {};
+    for (int b = 0; b < blocks; ++b) {
+      st.template multiply<true>((odd + b * St::kG) & 1, c1 - c0 - b * St::kCols, n, acc);
+      copy_next();
+    }
+#pragma unroll
+    for (int j = 0; j < St::kNT; ++j)
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const int at = 8 * j + 2 * t + i;
+        if (at < n) {  // a piece holds a token once: no two lanes meet
+          const int r = G.order[first + at];
+          float* to = mine + r / a.K * 16 + g;
+          to[0] = fmaf(prob[r], acc[j][i], to[0]);
+          to[8] = fmaf(prob[r], acc[j][2 + i], to[8]);
         }
       }
-      ring[d].template multiply<NT, true>(ht, live, kb, t, a.I, p, acc);
-      load_next(ring[d]);
-      kb += S;
-    }
+    __syncwarp();
   }
-  __syncthreads();  // every warp is done with prob and slot
-  leave_parts<1, NT>(part, warp, g, t, acc);
   __syncthreads();
-  for (int i = threadIdx.x; i < 16 * kTok; i += W * 32) {
-    const int tok = t0 + (i >> 4), c = r0 + (i & 15);
-    if (tok >= a.N) continue;
-    const size_t at = (size_t)tok * a.H + c;
+  for (int i = threadIdx.x; i < 16 * tokens; i += W * 32) {
+    const size_t at = (size_t)(t0 + (i >> 4)) * a.H + r0 + (i & 15);
     float v = a.add ? bf(a.add[at]) : 0.0f;
 #pragma unroll
-    for (int w = 0; w < W; ++w) v += part[(w * 16 + (i & 15)) * kTok + (i >> 4)];
-    a.y[at] = __bfloat16_as_ushort(__float2bfloat16_rn(v));
+    for (int w = 0; w < W; ++w) v += sums[w * tokens * 16 + i];
+    a.y[at] = to_bf(v);
+  }
+}
+
+// ------------------------------------------------------------------ one token
+// With one token the eight columns of an MMA are free, and they tell the groups
+// apart: lane t of a quad takes 16 bytes (32 columns) of its two rows of every
+// block of 128, and column n of B holds x only at the columns of the block's n-th
+// group (zeros elsewhere), so the sums of up to four groups come out side by side.
+// No code or scale passes through shared memory, the loads run kOneAhead blocks
+// ahead in registers, and each warp lays its own columns of x out once.
+constexpr int kOneAhead = 4;
+constexpr int kOneBlock = 128;
+
+__device__ __forceinline__ uint4 ld_codes(const uint8_t* p) {
+  uint4 v;
+  asm volatile("ld.global.nc.L1::no_allocate.L2::256B.v4.u32 {%0,%1,%2,%3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "l"(p));
+  return v;
+}
+
+// Sums of two rows (`q`, `s`: the lane's place in row g, `q8`, `s8`: on to the
+// second row) over n blocks, `cols` columns of which are there.
+template <int GROUP>
+struct OneRows {
+  static constexpr int kG = kOneBlock / GROUP;
+  static constexpr int kS = kG > 1 ? 2 : 1;  // groups whose sums this lane holds
+  const uint8_t* q;
+  const uint16_t* s;
+  int64_t q8, s8;
+  int n, cols, t;
+  bool mine;  // this lane's column of B takes x (of lane t's 32 columns)
+  uint4 w[kOneAhead][2];
+  uint16_t sc[kOneAhead][2][kS];
+
+  // Row g of the tile at column c0 (a multiple of 128), the second `second` rows on.
+  __device__ __forceinline__ void begin(const uint8_t* codes, const uint16_t* scales, int64_t row,
+                                        int64_t second, int row_cols, int c0, int c1, int lane) {
+    t = lane & 3;
+    const int g = lane >> 2;
+    mine = GROUP == 128 || t / (GROUP / 32) == g;
+    cols = c1 - c0;
+    n = (cols + kOneBlock - 1) / kOneBlock;
+    q = codes + row * (row_cols / 2) + c0 / 2 + 16 * t;
+    s = scales + row * (row_cols / GROUP) + c0 / GROUP + 2 * t;
+    if (kG == 1) s -= 2 * t;
+    q8 = second * (row_cols / 2);
+    s8 = second * (row_cols / GROUP);
+#pragma unroll
+    for (int d = 0; d < kOneAhead; ++d) fetch(d, d);
+  }
+  // Block b (b - d ahead of q) into place d.
+  __device__ __forceinline__ void fetch(int d, int b, int at = -1) {
+    if (at < 0) at = b;
+    if (at >= n) return;
+    const int left = cols - at * kOneBlock;
+    if (GROUP == 128 || 32 * t < left) {
+      w[d][0] = ld_codes(q + b * (kOneBlock / 2));
+      w[d][1] = ld_codes(q + q8 + b * (kOneBlock / 2));
+    }
+#pragma unroll
+    for (int j = 0; j < kS; ++j) {
+      const bool there = kG == 1 || (2 * t + j < kG && (2 * t + j) * GROUP < left);
+      sc[d][0][j] = there ? __ldg(s + b * kG + j) : (uint16_t)0;
+      sc[d][1][j] = there ? __ldg(s + s8 + b * kG + j) : (uint16_t)0;
+    }
+  }
+  // x: this lane's place in the laid-out columns from c0 on (lay_out)
+  __device__ __forceinline__ void run(uint32_t x, float& sum0, float& sum1) {
+    uint4 u[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) u[j] = make_uint4(0u, 0u, 0u, 0u);
+    for (int b = 0; b < n; b += kOneAhead) {
+#pragma unroll
+      for (int d = 0; d < kOneAhead; ++d) {
+        if (b + d >= n) break;
+        float p[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          // lanes whose column takes no x keep their zeros
+          asm volatile(
+              "{\n .reg .pred p;\n setp.ne.b32 p, %5, 0;\n"
+              " @p ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];\n}"
+              : "+r"(u[j].x), "+r"(u[j].y), "+r"(u[j].z), "+r"(u[j].w)
+              : "r"(x + (uint32_t)(d * 256 + j * 64)), "r"((int)mine)
+              : "memory");
+          uint32_t a0[4], a1[4];
+          open_codes(j == 0 ? w[d][0].x : j == 1 ? w[d][0].y : j == 2 ? w[d][0].z : w[d][0].w, a0);
+          open_codes(j == 0 ? w[d][1].x : j == 1 ? w[d][1].y : j == 2 ? w[d][1].z : w[d][1].w, a1);
+          if (j == 0) mma16816<true>(p, a0[0], a1[0], a0[1], a1[1], u[j].x, u[j].y);
+          else mma16816<false>(p, a0[0], a1[0], a0[1], a1[1], u[j].x, u[j].y);
+          mma16816<false>(p, a0[2], a1[2], a0[3], a1[3], u[j].z, u[j].w);
+        }
+        // columns 2t and 2t + 1 are this lane's; with one group only column 0 counts
+#pragma unroll
+        for (int j = 0; j < kS; ++j) {
+          if (kG > 1 && 2 * t + j >= kG) continue;
+          sum0 = fmaf(bf(sc[d][0][j]), p[j], sum0);
+          sum1 = fmaf(bf(sc[d][1][j]), p[2 + j], sum1);
+        }
+        fetch(d, d + kOneAhead, b + d + kOneAhead);
+      }
+      q += kOneAhead * (kOneBlock / 2);
+      s += kOneAhead * kG;
+      x += kOneAhead * 256;
+    }
+  }
+  // The sums of the quad's lanes, in lane t = 0.
+  static __device__ __forceinline__ float join(float v, int t) {
+    if (kG == 1) return v;
+    v = kG == 2 && t > 0 ? 0.0f : v;
+    return v + __shfl_xor_sync(0xFFFFFFFFu, v, 1);
+  }
+};
+
+// Columns [c0, c1) of x (c0 a multiple of 128), block by block in shared memory
+// (256 bytes from c0 on): word j of lane t at place 4j + t, its eight values in the
+// order of open_codes; zeros to the end of the last block. By one warp.
+template <bool PERMUTED>
+__device__ __forceinline__ void lay_out(uint32_t to, const uint16_t* x, int c0, int c1, int lane) {
+  for (int c = c0 / 8 + lane; c < (c1 + kOneBlock - 1) / kOneBlock * (kOneBlock / 8); c += 32) {
+    uint4 v = make_uint4(0u, 0u, 0u, 0u);
+    if (c * 8 < c1) v = __ldcg(reinterpret_cast<const uint4*>(x) + c);
+    const uint32_t at = to + (uint32_t)(((c & ~15) + (c & 3) * 4 + ((c & 15) >> 2)) * 16 - c0 * 2);
+    if (PERMUTED)
+      asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(at), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
+    else
+      asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(at), "r"(__byte_perm(v.x, v.z, 0x5410)),
+                   "r"(__byte_perm(v.x, v.z, 0x7632)), "r"(__byte_perm(v.y, v.w, 0x5410)),
+                   "r"(__byte_perm(v.y, v.w, 0x7632))
+                   : "memory");
+  }
+  __syncwarp();
+}
+
+constexpr int kOneWarps = 4;
+
+template <int GROUP>
+__global__ void __launch_bounds__(kOneWarps * 32, 6)
+    w4_matvec_one_kernel(const uint16_t* x, const uint8_t* q, const uint16_t* scale, int rows,
+                         int cols, uint16_t* y) {
+  extern __shared__ __align__(16) uint8_t dynamic[];
+  __shared__ float part[kOneWarps][16];
+  griddep_wait();
+  griddep_launch_dependents();
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+  const int r0 = blockIdx.x * 16, row = min(r0 + g, rows - 1);
+  const int c0 = share(warp, kOneWarps, cols), c1 = share(warp + 1, kOneWarps, cols);
+  OneRows<GROUP> o;
+  o.begin(q, scale, row, min(8, rows - 1 - row), cols, c0, c1, lane);
+  const uint32_t xs = smem_u32(dynamic) + (uint32_t)c0 * 2;
+  lay_out<false>(xs, x, c0, c1, lane);
+  float lo = 0.0f, hi = 0.0f;
+  o.run(xs + (uint32_t)t * 16, lo, hi);
+  lo = OneRows<GROUP>::join(lo, t);
+  hi = OneRows<GROUP>::join(hi, t);
+  if (t == 0) {
+    part[warp][g] = lo;
+    part[warp][g + 8] = hi;
+  }
+  __syncthreads();
+  if (threadIdx.x < 16 && r0 + (int)threadIdx.x < rows) {
+    float v = 0.0f;
+#pragma unroll
+    for (int w = 0; w < kOneWarps; ++w) v += part[w][threadIdx.x];
+    y[r0 + threadIdx.x] = to_bf(v);
+  }
+}
+
+// The token's route of this lane (lane < K): its expert, -1 for none or one named
+// before, and the token's whole probability of it.
+__device__ __forceinline__ int one_route(const W4Args& a, int lane, float* p) {
+  int e = lane < a.K ? __ldcg(a.topk_ids + lane) : -1;
+  if (e < 0 || e >= a.E) e = -1;
+  const uint32_t same = __match_any_sync(0xFFFFFFFFu, e);
+  if (p) {
+    const float mine = lane < a.K ? __ldcg(a.topk_p + lane) : 0.0f;
+    *p = 0.0f;
+    for (int k = 0; k < a.K; ++k) {
+      const float v = __shfl_sync(0xFFFFFFFFu, mine, k);
+      if ((same >> k) & 1u) *p += v;
+    }
+  }
+  return __ffs(same) - 1 == lane ? e : -1;
+}
+
+// Block (8 features, route): rows g of its tile are gate rows, rows g + 8 up rows.
+template <int GROUP>
+__global__ void __launch_bounds__(kOneWarps * 32, 6) w4_fc1_one_kernel(const W4Args a) {
+  extern __shared__ __align__(16) uint8_t dynamic[];
+  __shared__ float part[kOneWarps][16];
+  griddep_wait();
+  griddep_launch_dependents();
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+  const int e = __shfl_sync(0xFFFFFFFFu, one_route(a, lane, nullptr), blockIdx.y);
+  if (e < 0) return;
+  const int i0 = blockIdx.x * 8;
+  const int c0 = share(warp, kOneWarps, a.H), c1 = share(warp + 1, kOneWarps, a.H);
+  OneRows<GROUP> o;
+  o.begin(a.w13, a.w13_scale, (int64_t)e * 2 * a.I + i0 + g, a.I, a.H, c0, c1, lane);
+  const uint32_t xs = smem_u32(dynamic) + (uint32_t)c0 * 2;
+  lay_out<false>(xs, a.x, c0, c1, lane);
+  float lo = 0.0f, hi = 0.0f;
+  o.run(xs + (uint32_t)t * 16, lo, hi);
+  lo = OneRows<GROUP>::join(lo, t);
+  hi = OneRows<GROUP>::join(hi, t);
+  if (t == 0) {
+    part[warp][g] = lo;
+    part[warp][g + 8] = hi;
+  }
+  __syncthreads();
+  if (threadIdx.x < 8) {
+    float gate = 0.0f, up = 0.0f;
+#pragma unroll
+    for (int w = 0; w < kOneWarps; ++w) {
+      gate += part[w][threadIdx.x];
+      up += part[w][8 + threadIdx.x];
+    }
+    const float h = (a.activation ? act_fwd<1>(gate) : act_fwd<0>(gate)) * up;
+    a.h[(size_t)blockIdx.y * a.I + i0 + permuted(threadIdx.x)] = to_bf(h);
+  }
+}
+
+// Block (16 output columns): the 128-column blocks of the token's experts, one
+// expert after the other, are dealt out to the warps in runs.
+template <int GROUP>
+__global__ void __launch_bounds__(kThreads, 3) w4_fc2_one_kernel(const W4Args a) {
+  extern __shared__ __align__(16) uint8_t dynamic[];
+  __shared__ float part[kWarps][16];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+  // The first product's kernel let this one start after every earlier kernel had
+  // finished, and writes neither the routes nor the weights: only h has to wait.
+  float p_lane;
+  const int e_lane = one_route(a, lane, &p_lane);
+  uint32_t routes = __ballot_sync(0xFFFFFFFFu, e_lane >= 0);
+  const int r0 = blockIdx.x * 16, per = (a.I + kOneBlock - 1) / kOneBlock;
+  const int total = __popc(routes) * per;
+  int at = warp * total / kWarps;
+  const int end = (warp + 1) * total / kWarps;
+  for (int skip = at / per; skip > 0; --skip) routes &= routes - 1;
+  float lo = 0.0f, hi = 0.0f;
+  bool waited = false;
+  while (at < end) {  // the run's part of one expert
+    const int r = __ffs(routes) - 1, b0 = at % per, b1 = min(per, b0 + end - at);
+    const int e = __shfl_sync(0xFFFFFFFFu, e_lane, r);
+    const float p = __shfl_sync(0xFFFFFFFFu, p_lane, r);
+    const int c0 = b0 * kOneBlock, c1 = min(a.I, b1 * kOneBlock);
+    OneRows<GROUP> o;
+    o.begin(a.w2, a.w2_scale, (int64_t)e * a.H + r0 + g, 8, a.I, c0, c1, lane);
+    if (!waited) griddep_wait();
+    waited = true;
+    const uint32_t hs = smem_u32(dynamic) + (uint32_t)(r * per + b0) * 256u;
+    lay_out<true>(hs, a.h + (size_t)r * a.I, c0, c1, lane);
+    float lo_e = 0.0f, hi_e = 0.0f;
+    o.run(hs + (uint32_t)t * 16, lo_e, hi_e);
+    lo = fmaf(p, lo_e, lo);
+    hi = fmaf(p, hi_e, hi);
+    at += b1 - b0;
+    routes &= routes - 1;
+  }
+  if (!waited) griddep_wait();
+  griddep_launch_dependents();
+  lo = OneRows<GROUP>::join(lo, t);
+  hi = OneRows<GROUP>::join(hi, t);
+  if (t == 0) {
+    part[warp][g] = lo;
+    part[warp][g + 8] = hi;
+  }
+  __syncthreads();
+  if (threadIdx.x < 16) {
+    const int c = r0 + threadIdx.x;
+    float v = a.add ? bf(a.add[c]) : 0.0f;
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) v += part[w][threadIdx.x];
+    a.y[c] = to_bf(v);
   }
 }
 
@@ -607,74 +894,147 @@ __global__ void __launch_bounds__(kWarps * 32) w4_quantize_kernel(const uint16_t
 
 namespace {
 
-template <int NT>
-cudaError_t matvec(const uint16_t* x, const uint8_t* q, const uint16_t* scale, int N, int rows,
-                   int cols, int group, uint16_t* y, cudaStream_t s) {
-  const dim3 grid((rows + 15) / 16, (N + 8 * NT - 1) / (8 * NT));
-  auto* k = group == 128 ? w4_matvec_kernel<NT, 128>
-                         : group == 64 ? w4_matvec_kernel<NT, 64> : w4_matvec_kernel<NT, 32>;
-  return launch_pdl(k, grid, dim3(kThreads), 0, s, x, q, scale, N, rows, cols, y);
+// A launch whose kernel takes up to `most` bytes of dynamic shared memory (asked
+// for once per device).
+template <typename... KArgs, typename... Args>
+cudaError_t launch_ring(DeviceOnce& once, void (*kernel)(KArgs...), size_t most, dim3 grid,
+                        dim3 block, size_t smem, cudaStream_t s, Args... args) {
+  const cudaError_t err = once_per_device(once, nullptr, [&](int, int* v) {
+    *v = 1;
+    return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)most);
+  });
+  return err != cudaSuccess ? err : launch_pdl(kernel, grid, block, smem, s, args...);
 }
 
-template <int NT, int GROUP>
-cudaError_t fc1(const W4Args& a, cudaStream_t s) {
+template <int GROUP, int TOK>
+cudaError_t matvec(const uint16_t* x, const uint8_t* q, const uint16_t* scale, int N, int rows,
+                   int cols, uint16_t* y, cudaStream_t s) {
   static DeviceOnce once;
+  constexpr size_t smem = kWarps * Stream<GROUP, TOK>::kBytes + 128;
+  return launch_ring(once, w4_matvec_kernel<GROUP, TOK>, smem,
+                     dim3((rows + 15) / 16, (N + TOK - 1) / TOK), dim3(kThreads), smem, s, x, q, scale,
+                     N, rows, cols, y);
+}
+
+template <int TOK>
+cudaError_t matvec(const uint16_t* x, const uint8_t* q, const uint16_t* scale, int N, int rows,
+                   int cols, int group, uint16_t* y, cudaStream_t s) {
+  return group == 128  ? matvec<128, TOK>(x, q, scale, N, rows, cols, y, s)
+         : group == 64 ? matvec<64, TOK>(x, q, scale, N, rows, cols, y, s)
+                       : matvec<32, TOK>(x, q, scale, N, rows, cols, y, s);
+}
+
+// Warps that share a unit's columns: the count (1, 2, 4, 8) with the fewest
+// blocks on the longest warp, as long as each keeps four blocks of a unit.
+int split_of(int64_t units, int64_t warps, int blocks) {
+  int best = 1;
+  double least = 0;
+  for (int S = 1; S <= 8; S *= 2) {
+    if (S > 1 && blocks / S < 4) break;
+    const int64_t teams = warps / S;
+    const double rounds = (double)((units + teams - 1) / teams) / S;
+    if (S == 1 || rounds < 0.98 * least) {
+      best = S;
+      least = rounds;
+    }
+  }
+  return best;
+}
+
+template <int GROUP, int TOK>
+cudaError_t fc1(const W4Args& a, cudaStream_t s) {
+  using St = Stream<GROUP, TOK>;
+  static DeviceOnce once, count;
+  constexpr int kBlocks = 2;  // an SM
+  constexpr size_t smem = kWarps * St::kBytes + 128;
   int sms = 0;
-  const cudaError_t err = once_per_device(once, &sms, [](int dev, int* v) {
+  const cudaError_t err = once_per_device(count, &sms, [](int dev, int* v) {
     return cudaDeviceGetAttribute(v, cudaDevAttrMultiProcessorCount, dev);
   });
   if (err != cudaSuccess) return err;
-  // units there may be, and the warps of two blocks an SM
-  const int64_t routes = (int64_t)a.N * a.K, warps = 2 * sms * kWarps;
-  const int64_t units = (routes < a.E ? routes : a.E) * (a.I / 16);
-  const int S = units * 8 <= warps ? 8 : units * 4 <= warps ? 4 : units * 2 <= warps ? 2 : 1;
-  return launch_pdl(w4_fc1_kernel<NT, GROUP>, dim3(2 * sms), dim3(kThreads), 0, s, a, S);
+  const int64_t routes = (int64_t)a.N * a.K;
+  const int S = split_of((routes < a.E ? routes : a.E) * (a.I / 8), (int64_t)kBlocks * sms * kWarps,
+                         a.H / St::kCols);
+  return launch_ring(once, w4_fc1_kernel<GROUP, TOK>, smem, dim3(kBlocks * sms), dim3(kThreads), smem, s, a, S);
 }
 
-template <int NT>
+template <int TOK>
 cudaError_t fc1(const W4Args& a, cudaStream_t s) {
-  return a.group == 128 ? fc1<NT, 128>(a, s) : a.group == 64 ? fc1<NT, 64>(a, s) : fc1<NT, 32>(a, s);
+  return a.group == 128 ? fc1<128, TOK>(a, s) : a.group == 64 ? fc1<64, TOK>(a, s) : fc1<32, TOK>(a, s);
 }
 
-template <int NT, int GROUP, int W>
+template <int GROUP, int TOK, int W>
 cudaError_t fc2(const W4Args& a, cudaStream_t s) {
-  const int tokens = a.N < 8 * NT ? a.N : 8 * NT;
+  using St = Stream<GROUP, TOK>;
+  static DeviceOnce once;
+  const int tokens = a.N < kChunk ? a.N : kChunk;
   const int items = a.E < tokens * a.K ? a.E : tokens * a.K;
-  const dim3 grid(a.H / 16, (a.N + 8 * NT - 1) / (8 * NT));
-  // at most 256 x 32 x 5 bytes: within the 48 KB a kernel has without asking
-  size_t smem = (size_t)items * 8 * NT * 5;
-  if (smem < (size_t)W * 16 * 8 * NT * 4) smem = (size_t)W * 16 * 8 * NT * 4;
+  const dim3 grid(a.H / 16, (a.N + kChunk - 1) / kChunk);
+  constexpr size_t ring = W * St::kBytes + 128;
+  const size_t smem = ring + (size_t)tokens * (W * 16 + a.K) * 4;
+  constexpr size_t most = ring + (size_t)kChunk * (W * 16 + kMaxTopK) * 4;
   const int S = items * 8 <= W ? 8 : items * 4 <= W ? 4 : items * 2 <= W ? 2 : 1;
-  return launch_pdl(w4_fc2_kernel<NT, GROUP, W>, grid, dim3(W * 32), smem, s, a, S);
+  return launch_ring(once, w4_fc2_kernel<GROUP, TOK, W>, most, grid, dim3(W * 32), smem, s, a, S);
 }
 
-template <int NT, int GROUP>
+template <int GROUP, int TOK>
 cudaError_t fc2(const W4Args& a, cudaStream_t s) {
   // narrow outputs have fewer blocks than SMs to fill: more warps each
-  return (int64_t)(a.H / 16) * ((a.N + 8 * NT - 1) / (8 * NT)) <= 256 ? fc2<NT, GROUP, 16>(a, s)
-                                                                      : fc2<NT, GROUP, 8>(a, s);
+  return (int64_t)(a.H / 16) * ((a.N + kChunk - 1) / kChunk) <= 256 ? fc2<GROUP, TOK, 16>(a, s)
+                                                                    : fc2<GROUP, TOK, 8>(a, s);
 }
 
-template <int NT>
+template <int TOK>
 cudaError_t fc2(const W4Args& a, cudaStream_t s) {
-  return a.group == 128 ? fc2<NT, 128>(a, s) : a.group == 64 ? fc2<NT, 64>(a, s) : fc2<NT, 32>(a, s);
+  return a.group == 128 ? fc2<128, TOK>(a, s) : a.group == 64 ? fc2<64, TOK>(a, s) : fc2<32, TOK>(a, s);
+}
+
+// One token: x, or h of its routes, has to fit the block's shared memory next to
+// six (three) more blocks on the SM.
+constexpr size_t kOneBytes = 36 << 10;
+
+template <int GROUP>
+cudaError_t matvec_one(const uint16_t* x, const uint8_t* q, const uint16_t* scale, int rows, int cols,
+                       uint16_t* y, cudaStream_t s) {
+  return launch_pdl(w4_matvec_one_kernel<GROUP>, dim3((rows + 15) / 16), dim3(kOneWarps * 32),
+                    (size_t)(cols + 127) / 128 * 256, s, x, q, scale, rows, cols, y);
+}
+
+template <int GROUP>
+cudaError_t ffn_one(const W4Args& a, cudaStream_t s) {
+  const cudaError_t err = launch_pdl(w4_fc1_one_kernel<GROUP>, dim3(a.I / 8, a.K), dim3(kOneWarps * 32),
+                                     (size_t)(a.H + 127) / 128 * 256, s, a);
+  if (err != cudaSuccess) return err;
+  return launch_pdl(w4_fc2_one_kernel<GROUP>, dim3(a.H / 16), dim3(kThreads),
+                    (size_t)a.K * ((a.I + 127) / 128) * 256, s, a);
 }
 
 }  // namespace
 
 int launch_w4_matvec(const uint16_t* x, const uint8_t* q, const uint16_t* scale, int N, int rows,
                      int cols, int group, uint16_t* y, cudaStream_t s) {
-  const cudaError_t err = N <= 8 ? matvec<1>(x, q, scale, N, rows, cols, group, y, s)
-                                 : N <= 16 ? matvec<2>(x, q, scale, N, rows, cols, group, y, s)
-                                           : matvec<4>(x, q, scale, N, rows, cols, group, y, s);
+  cudaError_t err;
+  if (N == 1 && (size_t)cols * 2 <= kOneBytes)
+    err = group == 128  ? matvec_one<128>(x, q, scale, rows, cols, y, s)
+          : group == 64 ? matvec_one<64>(x, q, scale, rows, cols, y, s)
+                        : matvec_one<32>(x, q, scale, rows, cols, y, s);
+  else
+    err = N <= 8 ? matvec<8>(x, q, scale, N, rows, cols, group, y, s)
+                 : matvec<16>(x, q, scale, N, rows, cols, group, y, s);
   return err != cudaSuccess ? -(int)err : 1;
 }
 
 int launch_w4_ffn(const W4Args& a, cudaStream_t s) {
-  // tokens an expert serves at once: by the mean number of its routes
-  cudaError_t err = a.N <= 8 || a.N * a.K <= 4 * a.E ? fc1<1>(a, s) : fc1<2>(a, s);
+  // routes an expert serves at once: by their mean number
+  cudaError_t err;
+  if (a.N == 1 && (size_t)a.H * 2 <= kOneBytes && (size_t)a.K * ((a.I + 127) / 128) * 256 <= kOneBytes) {
+    err = a.group == 128 ? ffn_one<128>(a, s) : a.group == 64 ? ffn_one<64>(a, s) : ffn_one<32>(a, s);
+    return err != cudaSuccess ? -(int)err : 2;
+  }
+  const bool few = a.N <= 8 || a.N * a.K <= 6 * a.E;
+  err = few ? fc1<8>(a, s) : fc1<16>(a, s);
   if (err != cudaSuccess) return -(int)err;
-  err = a.N <= 8 ? fc2<1>(a, s) : a.N <= 16 ? fc2<2>(a, s) : fc2<4>(a, s);
+  err = few ? fc2<8>(a, s) : fc2<16>(a, s);
   return err != cudaSuccess ? -(int)err : 2;
 }
 
