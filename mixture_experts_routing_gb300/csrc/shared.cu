@@ -495,6 +495,7 @@ cudaError_t launch(const CUtensorMap& a, const CUtensorMap& b, const CUtensorMap
 }  // namespace
 
 int launch_shared_forward(const SharedArgs& a, cudaStream_t s) {
+  if (a.N <= 256) return launch_shared_forward_few(a, s);
   CUtensorMap x, w13, w2, h_in, h_out, y, add{};
   if (!operand_map(&x, a.x, a.H, a.N, false) || !operand_map(&w13, a.w13, a.H, 2 * a.I, false) ||
       !operand_map(&h_in, a.h, a.I, a.N, false) || !operand_map(&w2, a.w2, a.I, a.H, false) ||

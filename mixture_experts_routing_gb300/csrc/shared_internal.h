@@ -27,6 +27,7 @@ struct SharedArgs {
 
 // Each returns the number of kernels launched (>= 0) or a negative cudaError_t.
 int launch_shared_forward(const SharedArgs& a, cudaStream_t s);
+int launch_shared_forward_few(const SharedArgs& a, cudaStream_t s);  // shared_few.cu
 int launch_shared_backward(const SharedArgs& a, cudaStream_t s);
 
 struct W4Args {
