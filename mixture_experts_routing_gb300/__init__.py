@@ -246,10 +246,22 @@ def _ptr(t) -> Optional[int]:
     return None if t is None else t.data_ptr()
 
 
+_current = None  # (device) -> handle of its current stream, and () -> current device
+
+
 def _stream(stream) -> int:
-    import torch
-    s = torch.cuda.current_stream() if stream is None else stream
-    return s.cuda_stream
+    """The stream's handle; by default that of the current device's current
+    stream, asked for without building a torch.cuda.Stream (3 us a call)."""
+    global _current
+    if stream is not None:
+        return stream.cuda_stream
+    if _current is None:
+        import torch
+        raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+        if raw is None:
+            raw = lambda d: torch.cuda.current_stream(d).cuda_stream  # noqa: E731
+        _current = (raw, torch.cuda.current_device)
+    return _current[0](_current[1]())
 
 
 def alloc_routes(cfg: Config, device) -> Routes:
@@ -512,12 +524,17 @@ def forward(cfg: Config, x, w_router, bias, w13, w2, routes: Routes, workspace, 
 
 
 # ------------------------------------------------------------------ shared expert
-def _need(fn: str, dtype, **named) -> None:
-    """Refuses a tensor of another shape or type, one in host memory, or one
-    whose rows do not lie one after another (the library is given addresses
-    only). Each keyword is (tensor, shape)."""
-    for name, (t, shape) in named.items():
-        if t.dtype != dtype or t.shape != shape or not t.is_contiguous() or not t.is_cuda:
+def _is(t, dtype, *shape) -> bool:
+    """The tensor has this type and shape, its rows lie one after another and it
+    is in device memory (the library is given addresses only)."""
+    return t.dtype is dtype and t.shape == shape and t.is_contiguous() and t.is_cuda
+
+
+def _refuse(fn: str, **named) -> None:
+    """Names the first argument that is not what the call needs; each keyword is
+    (tensor, type, shape...)."""
+    for name, (t, dtype, *shape) in named.items():
+        if not _is(t, dtype, *shape):
             raise ValueError("%s: %s must be a contiguous %s CUDA tensor of shape %s, got %s %s on %s%s" % (
                 fn, name, str(dtype).replace("torch.", ""), tuple(shape),
                 str(t.dtype).replace("torch.", ""), tuple(t.shape), t.device,
@@ -550,24 +567,19 @@ def alloc_shared_backward_workspace(cfg: SharedConfig, device):
                        device=device)
 
 
-def _shared_operands(fn, cfg, x, w13, w2, add, add_name):
-    import torch
-    N, H, I = cfg.n_tokens, cfg.hidden, cfg.inter
-    _need(fn, torch.bfloat16, x=(x, (N, H)), w13=(w13, (2 * I, H)), w2=(w2, (H, I)))
-    if add is not None:
-        _need(fn, torch.bfloat16, **{add_name: (add, (N, H))})
-
-
 def shared_forward(cfg: SharedConfig, x, w13, w2, h, y, add=None, stream=None) -> None:
     """y = (act(x W_gate) * (x W_up)) W_down (+ add): w13 [2I,H] and w2 [H,I] bf16
     (one expert of pack_w13 / pack_w2), h [N,I] scratch; add may be y."""
     import torch
-    _shared_operands("shared_forward", cfg, x, w13, w2, add, "add")
-    _need("shared_forward", torch.bfloat16, h=(h, (cfg.n_tokens, cfg.inter)),
-          y=(y, (cfg.n_tokens, cfg.hidden)))
-    _check("moe_shared_forward",
-           lib().moe_shared_forward(ctypes.byref(cfg), _ptr(x), _ptr(w13), _ptr(w2), _ptr(add),
-                                    _ptr(h), _ptr(y), _stream(stream)))
+    bf, N, H, I = torch.bfloat16, cfg.n_tokens, cfg.hidden, cfg.inter
+    if not (_is(x, bf, N, H) and _is(w13, bf, 2 * I, H) and _is(w2, bf, H, I) and _is(h, bf, N, I)
+            and _is(y, bf, N, H) and (add is None or _is(add, bf, N, H))):
+        _refuse("shared_forward", x=(x, bf, N, H), w13=(w13, bf, 2 * I, H), w2=(w2, bf, H, I),
+                h=(h, bf, N, I), y=(y, bf, N, H), add=(x if add is None else add, bf, N, H))
+    rc = lib().moe_shared_forward(ctypes.byref(cfg), x.data_ptr(), w13.data_ptr(), w2.data_ptr(),
+                                  _ptr(add), h.data_ptr(), y.data_ptr(), _stream(stream))
+    if rc:
+        raise MoEError("moe_shared_forward", rc)
 
 
 def shared_forward_train(cfg: SharedConfig, x, w13, w2, h, y, ck, ck_sf, add=None,
@@ -575,14 +587,19 @@ def shared_forward_train(cfg: SharedConfig, x, w13, w2, h, y, ck, ck_sf, add=Non
     """shared_forward that also keeps the pre-activations [g | u] in 8 bits
     (alloc_shared_checkpoint) for shared_backward."""
     import torch
-    _shared_operands("shared_forward_train", cfg, x, w13, w2, add, "add")
-    N, H, I = cfg.n_tokens, cfg.hidden, cfg.inter
-    _need("shared_forward_train", torch.bfloat16, h=(h, (N, I)), y=(y, (N, H)))
-    _need("shared_forward_train", torch.uint8, ck=(ck, (N, 2 * I)), ck_sf=(ck_sf, (N, I // 16)))
-    _check("moe_shared_forward_train",
-           lib().moe_shared_forward_train(ctypes.byref(cfg), _ptr(x), _ptr(w13), _ptr(w2),
-                                          _ptr(add), _ptr(h), _ptr(y), _ptr(ck), _ptr(ck_sf),
-                                          _stream(stream)))
+    bf, u8, N, H, I = torch.bfloat16, torch.uint8, cfg.n_tokens, cfg.hidden, cfg.inter
+    if not (_is(x, bf, N, H) and _is(w13, bf, 2 * I, H) and _is(w2, bf, H, I) and _is(h, bf, N, I)
+            and _is(y, bf, N, H) and (add is None or _is(add, bf, N, H))
+            and _is(ck, u8, N, 2 * I) and _is(ck_sf, u8, N, I // 16)):
+        _refuse("shared_forward_train", x=(x, bf, N, H), w13=(w13, bf, 2 * I, H),
+                w2=(w2, bf, H, I), h=(h, bf, N, I), y=(y, bf, N, H),
+                add=(x if add is None else add, bf, N, H), ck=(ck, u8, N, 2 * I),
+                ck_sf=(ck_sf, u8, N, I // 16))
+    rc = lib().moe_shared_forward_train(ctypes.byref(cfg), x.data_ptr(), w13.data_ptr(),
+                                        w2.data_ptr(), _ptr(add), h.data_ptr(), y.data_ptr(),
+                                        ck.data_ptr(), ck_sf.data_ptr(), _stream(stream))
+    if rc:
+        raise MoEError("moe_shared_forward_train", rc)
 
 
 def shared_backward(cfg: SharedConfig, x, w13, w2, ck, ck_sf, dy, dx, dw13, dw2, workspace,
@@ -590,18 +607,23 @@ def shared_backward(cfg: SharedConfig, x, w13, w2, ck, ck_sf, dy, dx, dw13, dw2,
     """Gradients from the 8-bit checkpoint: dx [N,H] bf16 (+ dx_add, which may be
     dx), dw13 [2I,H] and dw2 [H,I] (bf16, or f32 with cfg.grad_f32; overwritten)."""
     import torch
-    _shared_operands("shared_backward", cfg, x, w13, w2, dx_add, "dx_add")
-    N, H, I = cfg.n_tokens, cfg.hidden, cfg.inter
-    _need("shared_backward", torch.bfloat16, dy=(dy, (N, H)), dx=(dx, (N, H)))
-    _need("shared_backward", torch.uint8, ck=(ck, (N, 2 * I)), ck_sf=(ck_sf, (N, I // 16)))
-    _need("shared_backward", torch.float32 if cfg.grad_f32 else torch.bfloat16,
-          dw13=(dw13, (2 * I, H)), dw2=(dw2, (H, I)))
-    _check("moe_shared_backward",
-           lib().moe_shared_backward(ctypes.byref(cfg), _ptr(x), _ptr(w13), _ptr(w2), _ptr(ck),
-                                     _ptr(ck_sf), _ptr(dy), _ptr(dx_add), _ptr(dx), _ptr(dw13),
-                                     _ptr(dw2), _ptr(workspace),
-                                     workspace.numel() * workspace.element_size(),
-                                     _stream(stream)))
+    bf, u8, N, H, I = torch.bfloat16, torch.uint8, cfg.n_tokens, cfg.hidden, cfg.inter
+    gt = torch.float32 if cfg.grad_f32 else bf
+    if not (_is(x, bf, N, H) and _is(w13, bf, 2 * I, H) and _is(w2, bf, H, I)
+            and _is(ck, u8, N, 2 * I) and _is(ck_sf, u8, N, I // 16) and _is(dy, bf, N, H)
+            and _is(dx, bf, N, H) and (dx_add is None or _is(dx_add, bf, N, H))
+            and _is(dw13, gt, 2 * I, H) and _is(dw2, gt, H, I) and workspace.is_cuda):
+        _refuse("shared_backward", x=(x, bf, N, H), w13=(w13, bf, 2 * I, H), w2=(w2, bf, H, I),
+                ck=(ck, u8, N, 2 * I), ck_sf=(ck_sf, u8, N, I // 16), dy=(dy, bf, N, H),
+                dx=(dx, bf, N, H), dx_add=(x if dx_add is None else dx_add, bf, N, H),
+                dw13=(dw13, gt, 2 * I, H), dw2=(dw2, gt, H, I),
+                workspace=(workspace, workspace.dtype, *workspace.shape))
+    rc = lib().moe_shared_backward(ctypes.byref(cfg), x.data_ptr(), w13.data_ptr(), w2.data_ptr(),
+                                   ck.data_ptr(), ck_sf.data_ptr(), dy.data_ptr(), _ptr(dx_add),
+                                   dx.data_ptr(), dw13.data_ptr(), dw2.data_ptr(),
+                                   workspace.data_ptr(), workspace.nbytes, _stream(stream))
+    if rc:
+        raise MoEError("moe_shared_backward", rc)
 
 
 # ------------------------------------------------------------------ 4-bit weights
@@ -610,8 +632,8 @@ def w4_quantize(m, group: int, q, scale, stream=None) -> None:
     bf16 matrix m [rows, cols]."""
     import torch
     rows, cols = m.shape
-    _need("w4_quantize", torch.bfloat16, m=(m, (rows, cols)), scale=(scale, (rows, cols // group)))
-    _need("w4_quantize", torch.uint8, q=(q, (rows, cols // 2)))
+    _refuse("w4_quantize", m=(m, torch.bfloat16, rows, cols), q=(q, torch.uint8, rows, cols // 2),
+            scale=(scale, torch.bfloat16, rows, cols // group))
     _check("moe_w4_quantize", lib().moe_w4_quantize(_ptr(m), int(rows), int(cols), int(group),
                                                     _ptr(q), _ptr(scale), _stream(stream)))
 
@@ -648,16 +670,18 @@ def w4_matvec(x, q, scale, y, stream=None) -> None:
     """y [n, rows] = x [n, cols] . w^T for a 4-bit matrix: q [rows, cols/2] u8,
     scale [rows, cols/group] bf16."""
     import torch
-    n, cols = x.shape
-    rows, groups = scale.shape
+    bf, (n, cols), (rows, groups) = torch.bfloat16, x.shape, scale.shape
     group = cols // groups if groups else 0
-    _need("w4_matvec", torch.bfloat16, x=(x, (n, cols)), scale=(scale, (rows, groups)),
-          y=(y, (n, rows)))
-    _need("w4_matvec", torch.uint8, q=(q, (rows, cols // 2)))
+    if not (_is(x, bf, n, cols) and _is(q, torch.uint8, rows, cols // 2)
+            and _is(scale, bf, rows, groups) and _is(y, bf, n, rows)):
+        _refuse("w4_matvec", x=(x, bf, n, cols), q=(q, torch.uint8, rows, cols // 2),
+                scale=(scale, bf, rows, groups), y=(y, bf, n, rows))
     if group * groups != cols:
         raise ValueError("w4_matvec: %d scales a row do not divide %d columns" % (groups, cols))
-    _check("moe_w4_matvec", lib().moe_w4_matvec(_ptr(x), _ptr(q), _ptr(scale), n, rows, cols, group,
-                                                _ptr(y), _stream(stream)))
+    rc = lib().moe_w4_matvec(x.data_ptr(), q.data_ptr(), scale.data_ptr(), n, rows, cols, group,
+                             y.data_ptr(), _stream(stream))
+    if rc:
+        raise MoEError("moe_w4_matvec", rc)
 
 
 def w4_ffn_forward(cfg: W4Config, topk_ids, topk_p, x, w13q, w13_scale, w2q, w2_scale, y,
@@ -667,22 +691,25 @@ def w4_ffn_forward(cfg: W4Config, topk_ids, topk_p, x, w13q, w13_scale, w2q, w2_
     -1 is no route."""
     import torch
     N, H, E, K, I, g = cfg.n_tokens, cfg.hidden, cfg.n_experts, cfg.top_k, cfg.inter, cfg.group
-    fn = "w4_ffn_forward"
+    bf, u8 = torch.bfloat16, torch.uint8
     if g <= 0:
         raise MoEError("moe_w4_ffn_forward", MOE_ERR_INVALID_ARG)
-    _need(fn, torch.int32, topk_ids=(topk_ids, (N, K)))
-    _need(fn, torch.float32, topk_p=(topk_p, (N, K)))
-    _need(fn, torch.uint8, w13q=(w13q, (E, 2 * I, H // 2)), w2q=(w2q, (E, H, I // 2)))
-    _need(fn, torch.bfloat16, x=(x, (N, H)), y=(y, (N, H)),
-          w13_scale=(w13_scale, (E, 2 * I, H // g)), w2_scale=(w2_scale, (E, H, I // g)))
-    if add is not None:
-        _need(fn, torch.bfloat16, add=(add, (N, H)))
-    _check("moe_w4_ffn_forward",
-           lib().moe_w4_ffn_forward(ctypes.byref(cfg), _ptr(topk_ids), _ptr(topk_p), _ptr(x),
-                                    _ptr(w13q), _ptr(w13_scale), _ptr(w2q), _ptr(w2_scale),
-                                    _ptr(add), _ptr(y), _ptr(workspace),
-                                    workspace.numel() * workspace.element_size(),
-                                    _stream(stream)))
+    if not (_is(topk_ids, torch.int32, N, K) and _is(topk_p, torch.float32, N, K) and _is(x, bf, N, H)
+            and _is(w13q, u8, E, 2 * I, H // 2) and _is(w13_scale, bf, E, 2 * I, H // g)
+            and _is(w2q, u8, E, H, I // 2) and _is(w2_scale, bf, E, H, I // g) and _is(y, bf, N, H)
+            and (add is None or _is(add, bf, N, H)) and workspace.is_cuda):
+        _refuse("w4_ffn_forward", topk_ids=(topk_ids, torch.int32, N, K),
+                topk_p=(topk_p, torch.float32, N, K), x=(x, bf, N, H),
+                w13q=(w13q, u8, E, 2 * I, H // 2), w13_scale=(w13_scale, bf, E, 2 * I, H // g),
+                w2q=(w2q, u8, E, H, I // 2), w2_scale=(w2_scale, bf, E, H, I // g),
+                y=(y, bf, N, H), add=(x if add is None else add, bf, N, H),
+                workspace=(workspace, workspace.dtype, *workspace.shape))
+    rc = lib().moe_w4_ffn_forward(ctypes.byref(cfg), topk_ids.data_ptr(), topk_p.data_ptr(),
+                                  x.data_ptr(), w13q.data_ptr(), w13_scale.data_ptr(),
+                                  w2q.data_ptr(), w2_scale.data_ptr(), _ptr(add), y.data_ptr(),
+                                  workspace.data_ptr(), workspace.nbytes, _stream(stream))
+    if rc:
+        raise MoEError("moe_w4_ffn_forward", rc)
 
 
 def launch_count() -> int:
