@@ -1,10 +1,12 @@
 // The shared expert's contractions on the 5th-generation tensor cores.
 //
-// D[m, n] = sum_k A[m, k] B[n, k], one launch per contraction:
+// D[m, n] = sum_k A[m, k] B[n, k]; the launches:
 //   gated      D = x W13^T      epilogue h = act(g) u, 8-bit checkpoint of g, u
-//   out        D = h W2^T, or [dg du] W13   epilogue (+ add), bf16
+//   out        D = h W2^T       epilogue (+ add)
 //   gated bwd  D = dy W2        epilogue dg, du and h from the checkpoint
-//   grad       D = [dg du]^T x, or dy^T h   bf16 or f32
+//   out        D = [dg du] W13 (+ add), [dg du]^T x and dy^T h in one launch: they
+//              need nothing of one another, and one list of their tiles leaves one
+//              partly filled turn of the SMs instead of three
 // A and B are read as they lie in memory: K-major, or MN-major where the
 // contraction index is the row of the matrix (no transposed copy is written).
 //
@@ -44,19 +46,38 @@ constexpr uint32_t kEpiBytes = 4096;              // per epilogue warp
 constexpr uint32_t kSmemBytes = kStages * kStageBytes + kEpiWarps * kEpiBytes + 1024;
 constexpr int kBand = 8;              // M tiles walked together before the next N tile
 
-enum Epi { kGated = 0, kOut = 1, kGatedBwd = 2, kGradF32 = 3 };
+enum Epi { kGated = 0, kOut = 1, kGatedBwd = 2, kGrads = 3 };
 
-struct MmaParams {
+constexpr int kMaxProblems = 3;
+
+// One contraction of a launch.
+struct Problem {
   int M, N;              // output rows and columns (gated: columns of h)
   int k_tiles;
   int m_tiles, n_tiles;  // tiles of 256 rows; of 256 columns (gated: 128 features)
-  int b_pair_off;        // rows of B between the CTAs' halves: 128, or I (gated)
-  int has_add;           // kOut
+  int full;              // tiles taken whole; the others as two halves of their columns
+  int begin;             // of its tiles in the launch's list
+  int amn;               // kGrads: A read MN-major
+  int has_add;           // kOut, kGrads
+  int f32;               // kGrads: f32 output
+};
+
+struct MmaParams {
+  Problem pr[kMaxProblems];
+  int problems, tiles;
+  int up;                // kGated: rows of B from a feature's gate row to its up row
   const uint8_t* ck_in;  // kGatedBwd: [M,2N] codes, [M,2N/32] bytes
   const uint8_t* sf_in;
   uint8_t* ck;           // kGated: the same as outputs, or null
   uint8_t* sf;
   uint32_t* err;
+};
+
+// Of each problem: A, B, the output, what is added (kOut); kGatedBwd (one problem):
+// the outputs dg, du and h in o[0], x[0] and o[1].
+struct Maps {
+  CUtensorMap a[kMaxProblems], b[kMaxProblems], o[kMaxProblems], x[kMaxProblems];
+  CUtensorMap b_half;  // B of the one problem whose B is K-major, in boxes of 64 rows
 };
 
 __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
@@ -146,22 +167,45 @@ __device__ __forceinline__ void tma_load_2d_pair(uint32_t dst, const CUtensorMap
       : "memory");
 }
 
-// Tile t: M tiles in bands of kBand, walked M first within a band.
-__device__ __forceinline__ void tile_of(const MmaParams& p, int t, int& m, int& n) {
-  const int per = kBand * p.n_tiles;
+struct Tile {
+  int pr;    // problem
+  int m, n;  // first row of the pair, first column (gated: first feature)
+  int half;  // half the columns of a whole tile
+};
+
+// Tile t of the list: the problems one after another, M tiles in bands of kBand,
+// walked M first within a band; halves last.
+template <int EPI>
+__device__ __forceinline__ Tile tile_of(const MmaParams& p, int t) {
+  Tile T;
+  T.pr = 0;
+#pragma unroll
+  for (int i = 1; i < kMaxProblems; ++i)
+    if (i < p.problems && t >= p.pr[i].begin) T.pr = i;
+  const Problem& P = p.pr[T.pr];
+  t -= P.begin;
+  T.half = t >= P.full;
+  const int second = T.half ? (t - P.full) & 1 : 0;
+  if (T.half) t = P.full + ((t - P.full) >> 1);
+  const int per = kBand * P.n_tiles;
   const int band = t / per, r = t - band * per;
-  const int rows = min(kBand, p.m_tiles - band * kBand);
-  n = r / rows;
-  m = band * kBand + (r - n * rows);
+  const int rows = min(kBand, P.m_tiles - band * kBand);
+  const int n = r / rows;
+  constexpr int kWide = EPI == kGated ? kBM : 2 * kBM;
+  T.m = (band * kBand + (r - n * rows)) * 2 * kBM;
+  T.n = n * kWide + second * (kWide / 2);
+  return T;
 }
 
-template <int EPI, int ACT, bool AMN, bool BMN>
+// Which operands are read MN-major: the launch's kind tells, but for the gradients.
+template <int EPI>
+__device__ __forceinline__ bool kAMn(const Problem& P) { return EPI == kGrads && P.amn; }
+template <int EPI>
+__device__ __forceinline__ bool kBMn(const Problem& P) { return EPI == kGatedBwd || EPI == kGrads; }
+
+template <int EPI, int ACT>
 __global__ void __launch_bounds__(kThreads, 1)
-    shared_mma_kernel(const __grid_constant__ CUtensorMap tmA,
-                      const __grid_constant__ CUtensorMap tmB,
-                      const __grid_constant__ CUtensorMap tmO,
-                      const __grid_constant__ CUtensorMap tmO2,
-                      const __grid_constant__ CUtensorMap tmO3, const MmaParams p) {
+    shared_mma_kernel(const __grid_constant__ Maps maps, const __grid_constant__ MmaParams p) {
   extern __shared__ uint8_t smem_raw[];
   __shared__ __align__(8) uint64_t full_bar[kStages];
   __shared__ __align__(8) uint64_t empty_bar[kStages];
@@ -173,7 +217,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t crank = cluster_ctarank();
   const uint32_t sbase = (smem_u32(smem_raw) + 1023u) & ~1023u;
-  const int tiles = p.m_tiles * p.n_tiles;
+  const int tiles = p.tiles;
   const int pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
 
   if (threadIdx.x == 0) {
@@ -189,9 +233,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int b = 0; b < 2; ++b) mbar_init(smem_u32(&add_bar[w][b]), 1);
     mbar_fence_init();
   }
-  if (warp == 0 && lane == 0) {
-    tma_prefetch_desc(&tmA);
-    tma_prefetch_desc(&tmB);
+  if (warp == 0 && lane < p.problems) {
+    tma_prefetch_desc(&maps.a[lane]);
+    tma_prefetch_desc(&maps.b[lane]);
   }
   if (warp == 1) tmem_alloc_pair(smem_u32(&tmem_base_s), 512);
   tc_fence_before();
@@ -207,11 +251,19 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint32_t g = 0;
     bool ok = true;
     for (int t = pair; ok && t < tiles; t += pairs) {
-      int m, n;
-      tile_of(p, t, m, n);
-      const int am = m * 2 * kBM + (int)crank * kBM;
-      const int bn = n * (EPI == kGated ? kBM : 2 * kBM) + (int)crank * p.b_pair_off;
-      for (int kt = 0; kt < p.k_tiles; ++kt, ++g) {
+      const Tile T = tile_of<EPI>(p, t);
+      const Problem& P = p.pr[T.pr];
+      // what the loop needs, in registers: a read of the parameters by problem in
+      // every step made the launch 9 % slower
+      const CUtensorMap *ma = &maps.a[T.pr], *mb = !T.half || kBMn<EPI>(P) ? &maps.b[T.pr] : &maps.b_half;
+      const bool amn = kAMn<EPI>(P), bmn = kBMn<EPI>(P);
+      const int k_tiles = P.k_tiles;
+      const uint32_t bar0 = mapa_shared(smem_u32(&full_bar[0]), 0);
+      const int am = T.m + (int)crank * kBM;
+      // the odd CTA's rows of B: the second half of the tile's columns (gated: the up rows)
+      const int bn = T.n + (int)crank * (EPI == kGated ? p.up : T.half ? kBM / 2 : kBM);
+      const uint32_t bytes = 2 * kOpBytes + (T.half ? kOpBytes : 2 * kOpBytes);  // of both CTAs
+      for (int kt = 0; kt < k_tiles; ++kt, ++g) {
         const uint32_t s = g % kStages, u = g / kStages;
         if (u > 0 && !mbar_wait_cluster_warp(smem_u32(&empty_bar[s]), (u - 1u) & 1u, p.err,
                                              kErrWaitEmpty)) {
@@ -219,21 +271,22 @@ __global__ void __launch_bounds__(kThreads, 1)
           break;
         }
         if (lane == 0) {
-          const uint32_t bar = mapa_shared(smem_u32(&full_bar[s]), 0);
-          if (crank == 0) mbar_arrive_expect_tx(smem_u32(&full_bar[s]), 2 * kStageBytes);
+          const uint32_t bar = bar0 + 8u * s;
+          if (crank == 0) mbar_arrive_expect_tx(smem_u32(&full_bar[s]), bytes);
           const uint32_t a = sbase + s * kStageBytes, b = a + kOpBytes;
           const int k = kt * kBK;
-          if (AMN) {
-            tma_load_2d_pair(a, &tmA, am, k, bar);
-            tma_load_2d_pair(a + kOpBytes / 2, &tmA, am + 64, k, bar);
+          // K-major: one box of all rows; MN-major: boxes of 64 columns
+          if (amn) {
+            tma_load_2d_pair(a, ma, am, k, bar);
+            tma_load_2d_pair(a + kOpBytes / 2, ma, am + 64, k, bar);
           } else {
-            tma_load_2d_pair(a, &tmA, k, am, bar);
+            tma_load_2d_pair(a, ma, k, am, bar);
           }
-          if (BMN) {
-            tma_load_2d_pair(b, &tmB, bn, k, bar);
-            tma_load_2d_pair(b + kOpBytes / 2, &tmB, bn + 64, k, bar);
+          if (bmn) {
+            tma_load_2d_pair(b, mb, bn, k, bar);
+            if (!T.half) tma_load_2d_pair(b + kOpBytes / 2, mb, bn + 64, k, bar);
           } else {
-            tma_load_2d_pair(b, &tmB, k, bn, bar);
+            tma_load_2d_pair(b, mb, k, bn, bar);
           }
         }
         __syncwarp();
@@ -242,19 +295,26 @@ __global__ void __launch_bounds__(kThreads, 1)
   } else if (warp == 1) {
     // ------------------------------------------------------------ MMA issuer
     if (crank == 0) {
-      constexpr uint32_t idesc = idesc_bf16_f32(2 * kBM, 2 * kBM) | (AMN ? kIdescAMnMajor : 0u) |
-                                 (BMN ? kIdescBMnMajor : 0u);
-      // 16 contraction values: 32 bytes along a K-major row, 16 rows of an MN-major tile
-      constexpr uint32_t a_step = AMN ? 2048u : 32u, b_step = BMN ? 2048u : 32u;
       uint32_t g = 0, tc = 0;
       bool ok = true;
       for (int t = pair; ok && t < tiles; t += pairs, ++tc) {
+        const Tile T = tile_of<EPI>(p, t);
+        const Problem& P = p.pr[T.pr];
+        const bool amn = kAMn<EPI>(P), bmn = kBMn<EPI>(P);
+        const int k_tiles = P.k_tiles;
+        const uint32_t idesc = idesc_bf16_f32(2 * kBM, T.half ? kBM : 2 * kBM) |
+                               (amn ? kIdescAMnMajor : 0u) | (bmn ? kIdescBMnMajor : 0u);
+        // 16 contraction values: 32 bytes along a K-major row, 16 rows of an MN-major
+        // tile (descriptors count in 16 bytes)
+        const uint64_t a_step = amn ? 128u : 2u, b_step = bmn ? 128u : 2u;
+        const uint64_t a_base = amn ? sdesc_sw128_mn(sbase) : sdesc_sw128(sbase);
+        const uint64_t b_base = bmn ? sdesc_sw128_mn(sbase + kOpBytes) : sdesc_sw128(sbase + kOpBytes);
         const uint32_t b = tc & 1u, bu = tc >> 1;
         if (bu > 0 && !mbar_wait_cluster_warp(smem_u32(&tmem_empty_bar[b]), (bu - 1u) & 1u, p.err,
                                               kErrWaitAccum))
           break;
         tc_fence_after();
-        for (int kt = 0; kt < p.k_tiles; ++kt, ++g) {
+        for (int kt = 0; kt < k_tiles; ++kt, ++g) {
           const uint32_t s = g % kStages, u = g / kStages;
           if (!mbar_wait_cluster_warp(smem_u32(&full_bar[s]), u & 1u, p.err, kErrWaitFull)) {
             ok = false;
@@ -262,13 +322,11 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           tc_fence_after();
           if (lane == 0) {
-            const uint32_t a0 = sbase + s * kStageBytes, b0 = a0 + kOpBytes;
+            const uint64_t at = (uint64_t)(s * (kStageBytes >> 4));
 #pragma unroll
             for (uint32_t kk = 0; kk < kBK / 16; ++kk)
-              umma_bf16_pair(tmem + b * 256u,
-                             AMN ? sdesc_sw128_mn(a0 + kk * a_step) : sdesc_sw128(a0 + kk * a_step),
-                             BMN ? sdesc_sw128_mn(b0 + kk * b_step) : sdesc_sw128(b0 + kk * b_step),
-                             idesc, (kt | (int)kk) != 0);
+              umma_bf16_pair(tmem + b * 256u, a_base + at + kk * a_step, b_base + at + kk * b_step, idesc,
+                             (kt | (int)kk) != 0);
             umma_commit_pair(smem_u32(&empty_bar[s]), 3);
           }
           __syncwarp();
@@ -283,21 +341,22 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t buf0 = sbase + kStages * kStageBytes + (uint32_t)ew * kEpiBytes;
     uint32_t tc = 0, adds[2] = {0, 0};  // adds: phases of this warp's add barriers so far
     for (int t = pair; t < tiles; t += pairs, ++tc) {
-      int m, n;
-      tile_of(p, t, m, n);
+      const Tile T = tile_of<EPI>(p, t);
+      const Problem& P = p.pr[T.pr];
+      const CUtensorMap *mo = &maps.o[T.pr], *mx = &maps.x[T.pr];
       const uint32_t b = tc & 1u, bu = tc >> 1;
-      const int row0 = m * 2 * kBM + (int)crank * kBM + q * 32, row = row0 + lane;
-      const int col0 = n * (EPI == kGated ? kBM : 2 * kBM) + half * (EPI == kGated ? kBM / 2 : kBM);
-      const uint32_t tl = tmem + b * 256u + ((uint32_t)(q * 32) << 16) +
-                          (uint32_t)(half * (EPI == kGated ? kBM / 2 : kBM));
+      const int row0 = T.m + (int)crank * kBM + q * 32, row = row0 + lane;
+      const int wide = (EPI == kGated ? kBM / 2 : kBM) >> T.half;  // columns of this warp
+      const int col0 = T.n + half * wide;
+      const uint32_t tl = tmem + b * 256u + ((uint32_t)(q * 32) << 16) + (uint32_t)(half * wide);
       // 32-column chunks of this warp that hold output values
-      const int nch = row0 < p.M ? max(0, min(EPI == kGated ? 2 : 4, (p.N - col0 + 31) / 32)) : 0;
-      const bool add = EPI == kOut && p.has_add;
+      const int nch = row0 < P.M ? max(0, min(wide / 32, (P.N - col0 + 31) / 32)) : 0;
+      const bool add = (EPI == kOut || EPI == kGrads) && P.has_add;
       auto load_add = [&](int c) {
         if (lane == 0) {
           const uint32_t bar = smem_u32(&add_bar[ew][c & 1]);
           mbar_arrive_expect_tx(bar, 2048);
-          tma_load_2d_pair(buf0 + (uint32_t)(c & 1) * 2048u, &tmO2, col0 + 32 * c, row0, bar);
+          tma_load_2d_pair(buf0 + (uint32_t)(c & 1) * 2048u, mx, col0 + 32 * c, row0, bar);
         }
       };
       if (add && nch > 0) {  // under the tile's MMAs: the first two chunks of what is added
@@ -314,7 +373,16 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint32_t buf = buf0 + (uint32_t)(c & 1) * 2048u;
         float v[32];
         tmem_row32(tl + 32u * (uint32_t)c, v);
-        if constexpr (EPI == kOut) {
+        if (EPI == kGrads && P.f32) {
+          if (lane == 0) bulk_wait_read<0>();
+          __syncwarp();
+#pragma unroll
+          for (int j = 0; j < 8; ++j)  // 128-byte rows, 128-byte swizzle
+            st_shared_v4(buf0 + (uint32_t)(lane * 128 + ((j ^ (lane & 7)) << 4)),
+                         __float_as_uint(v[4 * j]), __float_as_uint(v[4 * j + 1]),
+                         __float_as_uint(v[4 * j + 2]), __float_as_uint(v[4 * j + 3]));
+          store_box(mo, buf0, col, row0, lane);
+        } else if constexpr (EPI == kOut || EPI == kGrads) {
           if (add) {
             const uint32_t use = adds[c & 1]++;
             if (!mbar_wait_warp(smem_u32(&add_bar[ew][c & 1]), use & 1u, p.err, kErrWaitAccum)) break;
@@ -333,46 +401,37 @@ __global__ void __launch_bounds__(kThreads, 1)
             __syncwarp();
           }
           stage_row(buf, lane, v);
-          store_box(&tmO, buf, col, row0, lane);
+          store_box(mo, buf, col, row0, lane);
           if (add && c + 2 < nch) {
             if (lane == 0) bulk_wait_read<0>();
             __syncwarp();
             load_add(c + 2);
           }
-        } else if constexpr (EPI == kGradF32) {
-          if (lane == 0) bulk_wait_read<0>();
-          __syncwarp();
-#pragma unroll
-          for (int j = 0; j < 8; ++j)  // 128-byte rows, 128-byte swizzle
-            st_shared_v4(buf0 + (uint32_t)(lane * 128 + ((j ^ (lane & 7)) << 4)),
-                         __float_as_uint(v[4 * j]), __float_as_uint(v[4 * j + 1]),
-                         __float_as_uint(v[4 * j + 2]), __float_as_uint(v[4 * j + 3]));
-          store_box(&tmO, buf0, col, row0, lane);
         } else if constexpr (EPI == kGated) {
           float u[32];
-          tmem_row32(tl + (uint32_t)kBM + 32u * (uint32_t)c, u);
-          if (p.ck && row < p.M) {
-            const size_t at = (size_t)row * 2 * p.N + col, sa = (size_t)row * (p.N / 16) + col / 32;
+          tmem_row32(tl + (uint32_t)(kBM >> T.half) + 32u * (uint32_t)c, u);
+          if (p.ck && row < P.M) {
+            const size_t at = (size_t)row * 2 * P.N + col, sa = (size_t)row * (P.N / 16) + col / 32;
             keep_block(v, p.ck + at, p.sf + sa);
-            keep_block(u, p.ck + at + p.N, p.sf + sa + p.N / 32);
+            keep_block(u, p.ck + at + P.N, p.sf + sa + P.N / 32);
           }
 #pragma unroll
           for (int j = 0; j < 32; ++j) v[j] = act_fwd<ACT>(v[j]) * u[j];
           if (lane == 0) bulk_wait_read<1>();
           __syncwarp();
           stage_row(buf, lane, v);
-          store_box(&tmO, buf, col, row0, lane);
+          store_box(mo, buf, col, row0, lane);
         } else {  // kGatedBwd
           uint4 gc[2] = {}, uc[2] = {};
           float fg = 0.0f, fu = 0.0f;
-          if (row < p.M) {
-            const size_t at = (size_t)row * 2 * p.N + col, sa = (size_t)row * (p.N / 16) + col / 32;
+          if (row < P.M) {
+            const size_t at = (size_t)row * 2 * P.N + col, sa = (size_t)row * (P.N / 16) + col / 32;
             gc[0] = reinterpret_cast<const uint4*>(p.ck_in + at)[0];
             gc[1] = reinterpret_cast<const uint4*>(p.ck_in + at)[1];
-            uc[0] = reinterpret_cast<const uint4*>(p.ck_in + at + p.N)[0];
-            uc[1] = reinterpret_cast<const uint4*>(p.ck_in + at + p.N)[1];
+            uc[0] = reinterpret_cast<const uint4*>(p.ck_in + at + P.N)[0];
+            uc[1] = reinterpret_cast<const uint4*>(p.ck_in + at + P.N)[1];
             fg = e8m0_value(p.sf_in[sa]);
-            fu = e8m0_value(p.sf_in[sa + p.N / 32]);
+            fu = e8m0_value(p.sf_in[sa + P.N / 32]);
           }
           const uint32_t gw[8] = {gc[0].x, gc[0].y, gc[0].z, gc[0].w, gc[1].x, gc[1].y, gc[1].z, gc[1].w};
           const uint32_t uw[8] = {uc[0].x, uc[0].y, uc[0].z, uc[0].w, uc[1].x, uc[1].y, uc[1].z, uc[1].w};
@@ -396,13 +455,13 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (lane == 0) bulk_wait_read<0>();
           __syncwarp();
           stage_row(buf0, lane, v);
-          store_box(&tmO, buf0, col, row0, lane);
+          store_box(mo, buf0, col, row0, lane);
           stage_row(buf0 + 2048u, lane, du);
-          store_box(&tmO2, buf0 + 2048u, col, row0, lane);
+          store_box(mx, buf0 + 2048u, col, row0, lane);
           if (lane == 0) bulk_wait_read<1>();
           __syncwarp();
           stage_row(buf0, lane, h);
-          store_box(&tmO3, buf0, col, row0, lane);
+          store_box(&maps.o[1], buf0, col, row0, lane);
         }
       }
       tc_fence_before();
@@ -440,10 +499,11 @@ bool map2d(CUtensorMap* m, const void* base, int64_t cols, int64_t rows, int64_t
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-// An operand [rows, cols]: K-major boxes of 64 k x 128 rows, or (mn) MN-major
-// boxes of 64 columns x 64 k.
-bool operand_map(CUtensorMap* m, const void* base, int64_t cols, int64_t rows, bool mn) {
-  return map2d(m, base, cols, rows, cols, 64, mn ? 64 : 128, CU_TENSOR_MAP_SWIZZLE_128B);
+// An operand [rows, cols]: K-major boxes of 64 contraction values x `box_rows`
+// rows, or (mn) MN-major boxes of 64 columns x 64 contraction values.
+bool operand_map(CUtensorMap* m, const void* base, int64_t cols, int64_t rows, bool mn,
+                 uint32_t box_rows = kBM) {
+  return map2d(m, base, cols, rows, cols, 64, mn ? 64 : box_rows, CU_TENSOR_MAP_SWIZZLE_128B);
 }
 
 bool out_map(CUtensorMap* m, const void* base, int64_t cols, int64_t rows, int64_t pitch) {
@@ -451,12 +511,12 @@ bool out_map(CUtensorMap* m, const void* base, int64_t cols, int64_t rows, int64
 }
 
 // Pairs resident at once, and the kernel's shared-memory opt-in, once per device.
-template <int EPI, int ACT, bool AMN, bool BMN>
+template <int EPI, int ACT>
 int max_pairs(cudaError_t* err) {
   static DeviceOnce once;
   int n = 0;
   *err = once_per_device(once, &n, [](int, int* v) {
-    auto* k = shared_mma_kernel<EPI, ACT, AMN, BMN>;
+    auto* k = shared_mma_kernel<EPI, ACT>;
     cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                          (int)kSmemBytes);
     if (e != cudaSuccess) return e;
@@ -475,94 +535,117 @@ int max_pairs(cudaError_t* err) {
   return *err == cudaSuccess ? n : 0;
 }
 
-template <int EPI, int ACT, bool AMN, bool BMN>
-cudaError_t launch(const CUtensorMap& a, const CUtensorMap& b, const CUtensorMap& o,
-                   const CUtensorMap& o2, const CUtensorMap& o3, MmaParams p, int64_t K,
-                   cudaStream_t s) {
-  p.k_tiles = (int)((K + kBK - 1) / kBK);
-  p.m_tiles = (p.M + 2 * kBM - 1) / (2 * kBM);
-  const int bn = EPI == kGated ? kBM : 2 * kBM;
-  p.n_tiles = (p.N + bn - 1) / bn;
-  if ((int64_t)p.m_tiles * p.n_tiles > INT32_MAX / 2) return cudaErrorInvalidValue;
+Problem problem(int M, int N, int64_t K, bool amn = false) {
+  Problem P{};
+  P.M = M;
+  P.N = N;
+  P.k_tiles = (int)((K + kBK - 1) / kBK);
+  P.amn = amn;
+  return P;
+}
+
+// The problems come longest contraction first: the pairs take tiles in turn, so the
+// short ones even the pairs out.
+template <int EPI, int ACT>
+cudaError_t launch(const Maps& maps, MmaParams p, cudaStream_t s) {
   cudaError_t err = cudaSuccess;
-  const int pairs = max_pairs<EPI, ACT, AMN, BMN>(&err);
+  const int pairs = max_pairs<EPI, ACT>(&err);
   if (pairs <= 0) return err != cudaSuccess ? err : cudaErrorUnknown;
-  const int n = p.m_tiles * p.n_tiles < pairs ? p.m_tiles * p.n_tiles : pairs;
-  return launch_pdl_pairs(shared_mma_kernel<EPI, ACT, AMN, BMN>, dim3(2 * n), dim3(kThreads),
-                          kSmemBytes, s, a, b, o, o2, o3, p);
+  int64_t tiles = 0;
+  for (int i = 0; i < p.problems; ++i) {
+    Problem& P = p.pr[i];
+    P.m_tiles = (P.M + 2 * kBM - 1) / (2 * kBM);
+    const int wide = EPI == kGated ? kBM : 2 * kBM;
+    P.n_tiles = (P.N + wide - 1) / wide;
+    const int64_t n = (int64_t)P.m_tiles * P.n_tiles;
+    P.begin = (int)tiles;
+    P.full = (int)n;
+    // the last, partly filled turn in halves where that fills it: a half costs
+    // about 0.6 of a whole tile, a turn that is at most half full costs a whole one
+    if (i == p.problems - 1) {
+      const int rest = (int)((tiles + n) % pairs);
+      if (rest <= pairs / 2 && rest <= n) P.full = (int)n - rest;
+    }
+    tiles += P.full + 2 * (n - P.full);
+    if (tiles > INT32_MAX / 4) return cudaErrorInvalidValue;
+  }
+  p.tiles = (int)tiles;
+  const int n = p.tiles < pairs ? p.tiles : pairs;
+  return launch_pdl_pairs(shared_mma_kernel<EPI, ACT>, dim3(2 * n), dim3(kThreads), kSmemBytes, s, maps, p);
 }
 
 }  // namespace
 
 int launch_shared_forward(const SharedArgs& a, cudaStream_t s) {
   if (a.N <= 256) return launch_shared_forward_few(a, s);
-  CUtensorMap x, w13, w2, h_in, h_out, y, add{};
-  if (!operand_map(&x, a.x, a.H, a.N, false) || !operand_map(&w13, a.w13, a.H, 2 * a.I, false) ||
-      !operand_map(&h_in, a.h, a.I, a.N, false) || !operand_map(&w2, a.w2, a.I, a.H, false) ||
-      !out_map(&h_out, a.h, a.I, a.N, a.I) || !out_map(&y, a.y, a.H, a.N, a.H) ||
-      (a.add && !out_map(&add, a.add, a.H, a.N, a.H)))
+  Maps m{};
+  if (!operand_map(&m.a[0], a.x, a.H, a.N, false) || !operand_map(&m.b[0], a.w13, a.H, 2 * a.I, false) ||
+      !operand_map(&m.b_half, a.w13, a.H, 2 * a.I, false, 64) ||
+      !out_map(&m.o[0], a.h, a.I, a.N, a.I))
     return -1;
   MmaParams p{};
   p.err = a.err;
-  p.M = a.N;
-  p.N = a.I;
-  p.b_pair_off = a.I;
+  p.problems = 1;
+  p.pr[0] = problem(a.N, a.I, a.H);
+  p.up = a.I;
   p.ck = a.ck;
   p.sf = a.ck_sf;
-  cudaError_t err = a.activation ? launch<kGated, 1, false, false>(x, w13, h_out, h_out, h_out, p, a.H, s)
-                                 : launch<kGated, 0, false, false>(x, w13, h_out, h_out, h_out, p, a.H, s);
+  cudaError_t err = a.activation ? launch<kGated, 1>(m, p, s) : launch<kGated, 0>(m, p, s);
   if (err != cudaSuccess) return -(int)err;
+  if (!operand_map(&m.a[0], a.h, a.I, a.N, false) || !operand_map(&m.b[0], a.w2, a.I, a.H, false) ||
+      !operand_map(&m.b_half, a.w2, a.I, a.H, false, 64) ||
+      !out_map(&m.o[0], a.y, a.H, a.N, a.H) || (a.add && !out_map(&m.x[0], a.add, a.H, a.N, a.H)))
+    return -1;
   p = MmaParams{};
   p.err = a.err;
-  p.M = a.N;
-  p.N = a.H;
-  p.b_pair_off = kBM;
-  p.has_add = a.add != nullptr;
-  err = launch<kOut, 0, false, false>(h_in, w2, y, a.add ? add : y, y, p, a.I, s);
+  p.problems = 1;
+  p.pr[0] = problem(a.N, a.H, a.I);
+  p.pr[0].has_add = a.add != nullptr;
+  err = launch<kOut, 0>(m, p, s);
   return err != cudaSuccess ? -(int)err : 2;
 }
 
 int launch_shared_backward(const SharedArgs& a, cudaStream_t s) {
-  CUtensorMap dy, w2, dg, du, h, dpre, w13, dx, add{}, dpre_t, x_t, dy_t, h_t, dw13, dw2;
-  const CUtensorMapDataType f32 = CU_TENSOR_MAP_DATA_TYPE_FLOAT32;
-  const bool f = a.grad_f32 != 0;
-  if (!operand_map(&dy, a.dy, a.H, a.N, false) || !operand_map(&w2, a.w2, a.I, a.H, true) ||
-      !out_map(&dg, a.dpre, a.I, a.N, 2 * a.I) || !out_map(&du, a.dpre + a.I, a.I, a.N, 2 * a.I) ||
-      !out_map(&h, a.h, a.I, a.N, a.I) || !operand_map(&dpre, a.dpre, 2 * a.I, a.N, false) ||
-      !operand_map(&w13, a.w13, a.H, 2 * a.I, true) || !out_map(&dx, a.dx, a.H, a.N, a.H) ||
-      (a.add && !out_map(&add, a.add, a.H, a.N, a.H)) ||
-      !operand_map(&dpre_t, a.dpre, 2 * a.I, a.N, true) || !operand_map(&x_t, a.x, a.H, a.N, true) ||
-      !operand_map(&dy_t, a.dy, a.H, a.N, true) || !operand_map(&h_t, a.h, a.I, a.N, true) ||
-      !(f ? map2d(&dw13, a.dw13, a.H, 2 * a.I, a.H, 32, 32, CU_TENSOR_MAP_SWIZZLE_128B, f32, 4)
-          : out_map(&dw13, a.dw13, a.H, 2 * a.I, a.H)) ||
-      !(f ? map2d(&dw2, a.dw2, a.I, a.H, a.I, 32, 32, CU_TENSOR_MAP_SWIZZLE_128B, f32, 4)
-          : out_map(&dw2, a.dw2, a.I, a.H, a.I)))
+  Maps m{};
+  // da = dy W2; dg, du and h from the checkpoint
+  if (!operand_map(&m.a[0], a.dy, a.H, a.N, false) || !operand_map(&m.b[0], a.w2, a.I, a.H, true) ||
+      !out_map(&m.o[0], a.dpre, a.I, a.N, 2 * (int64_t)a.I) ||
+      !out_map(&m.x[0], a.dpre + a.I, a.I, a.N, 2 * (int64_t)a.I) || !out_map(&m.o[1], a.h, a.I, a.N, a.I))
     return -1;
-  MmaParams p{};  // da = dy W2; dg, du and h from the checkpoint
+  MmaParams p{};
   p.err = a.err;
-  p.M = a.N;
-  p.N = a.I;
-  p.b_pair_off = kBM;
+  p.problems = 1;
+  p.pr[0] = problem(a.N, a.I, a.H);
   p.ck_in = a.ck;
   p.sf_in = a.ck_sf;
-  cudaError_t err = a.activation ? launch<kGatedBwd, 1, false, true>(dy, w2, dg, du, h, p, a.H, s)
-                                 : launch<kGatedBwd, 0, false, true>(dy, w2, dg, du, h, p, a.H, s);
+  cudaError_t err = a.activation ? launch<kGatedBwd, 1>(m, p, s) : launch<kGatedBwd, 0>(m, p, s);
   if (err != cudaSuccess) return -(int)err;
-  p.ck_in = p.sf_in = nullptr;
-  p.N = a.H;  // dx = [dg du] W13
-  p.has_add = a.add != nullptr;
-  err = launch<kOut, 0, false, true>(dpre, w13, dx, a.add ? add : dx, dx, p, 2 * (int64_t)a.I, s);
-  if (err != cudaSuccess) return -(int)err;
-  p.has_add = 0;
-  p.M = 2 * a.I;  // dW13 = [dg du]^T x
-  err = f ? launch<kGradF32, 0, true, true>(dpre_t, x_t, dw13, dw13, dw13, p, a.N, s)
-          : launch<kOut, 0, true, true>(dpre_t, x_t, dw13, dw13, dw13, p, a.N, s);
-  if (err != cudaSuccess) return -(int)err;
-  p.M = a.H;  // dW2 = dy^T h
-  p.N = a.I;
-  err = f ? launch<kGradF32, 0, true, true>(dy_t, h_t, dw2, dw2, dw2, p, a.N, s)
-          : launch<kOut, 0, true, true>(dy_t, h_t, dw2, dw2, dw2, p, a.N, s);
-  return err != cudaSuccess ? -(int)err : 4;
+  // dx = [dg du] W13, dW13 = [dg du]^T x and dW2 = dy^T h in one launch
+  m = Maps{};
+  p = MmaParams{};
+  p.err = a.err;
+  p.problems = 3;
+  const bool dx_first = 2 * (int64_t)a.I >= a.N;
+  const int ix = dx_first ? 0 : 2, i13 = dx_first ? 1 : 0, i2 = dx_first ? 2 : 1;
+  auto grad_map = [&](CUtensorMap* t, void* d, int64_t cols, int64_t rows) {
+    return a.grad_f32 ? map2d(t, d, cols, rows, cols, 32, 32, CU_TENSOR_MAP_SWIZZLE_128B,
+                              CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 4)
+                      : out_map(t, d, cols, rows, cols);
+  };
+  if (!operand_map(&m.a[ix], a.dpre, 2 * (int64_t)a.I, a.N, false) ||
+      !operand_map(&m.b[ix], a.w13, a.H, 2 * (int64_t)a.I, true) ||
+      !out_map(&m.o[ix], a.dx, a.H, a.N, a.H) || (a.add && !out_map(&m.x[ix], a.add, a.H, a.N, a.H)) ||
+      !operand_map(&m.a[i13], a.dpre, 2 * (int64_t)a.I, a.N, true) || !operand_map(&m.b[i13], a.x, a.H, a.N, true) ||
+      !grad_map(&m.o[i13], a.dw13, a.H, 2 * (int64_t)a.I) || !operand_map(&m.a[i2], a.dy, a.H, a.N, true) ||
+      !operand_map(&m.b[i2], a.h, a.I, a.N, true) || !grad_map(&m.o[i2], a.dw2, a.I, a.H))
+    return -1;
+  p.pr[ix] = problem(a.N, a.H, 2 * (int64_t)a.I);
+  p.pr[ix].has_add = a.add != nullptr;
+  p.pr[i13] = problem(2 * a.I, a.H, a.N, true);
+  p.pr[i2] = problem(a.H, a.I, a.N, true);
+  p.pr[i13].f32 = p.pr[i2].f32 = a.grad_f32;
+  err = launch<kGrads, 0>(m, p, s);
+  return err != cudaSuccess ? -(int)err : 2;
 }
 
 }  // namespace moe
