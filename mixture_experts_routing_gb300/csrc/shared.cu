@@ -54,8 +54,8 @@ constexpr int kMaxProblems = 3;
 struct Problem {
   int M, N;              // output rows and columns (gated: columns of h)
   int k_tiles;
-  int m_tiles, n_tiles;  // tiles of 256 rows; of 256 columns (gated: 128 features)
-  int full;              // tiles taken whole; the others as two halves of their columns
+  int w;                 // rows of B that a CTA stages: a tile has 2w columns (gated: w features)
+  int m_tiles, n_tiles;
   int begin;             // of its tiles in the launch's list
   int amn;               // kGrads: A read MN-major
   int has_add;           // kOut, kGrads
@@ -77,7 +77,7 @@ struct MmaParams {
 // the outputs dg, du and h in o[0], x[0] and o[1].
 struct Maps {
   CUtensorMap a[kMaxProblems], b[kMaxProblems], o[kMaxProblems], x[kMaxProblems];
-  CUtensorMap b_half;  // B of the one problem whose B is K-major, in boxes of 64 rows
+  CUtensorMap o16;  // kGated: the output in boxes of 16 columns
 };
 
 __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
@@ -106,13 +106,17 @@ __device__ __forceinline__ uint32_t at64(int r, int c) {
   return (uint32_t)(r * 64 + ((c ^ ((r >> 1) & 3)) << 4));
 }
 
-// This lane's row of 32 bf16 values into a staged box.
-__device__ __forceinline__ void stage_row(uint32_t buf, int lane, const float (&v)[32]) {
+// This lane's row of 32 bf16 values, as pairs or to be rounded, into a staged box.
+__device__ __forceinline__ void stage_pairs(uint32_t buf, int lane, const uint32_t (&v)[16]) {
 #pragma unroll
   for (int c = 0; c < 4; ++c)
-    st_shared_v4(buf + at64(lane, c), pack_bf16(v[8 * c], v[8 * c + 1]),
-                 pack_bf16(v[8 * c + 2], v[8 * c + 3]), pack_bf16(v[8 * c + 4], v[8 * c + 5]),
-                 pack_bf16(v[8 * c + 6], v[8 * c + 7]));
+    st_shared_v4(buf + at64(lane, c), v[4 * c], v[4 * c + 1], v[4 * c + 2], v[4 * c + 3]);
+}
+__device__ __forceinline__ void stage_row(uint32_t buf, int lane, const float (&v)[32]) {
+  uint32_t w[16];
+#pragma unroll
+  for (int j = 0; j < 16; ++j) w[j] = pack_bf16(v[2 * j], v[2 * j + 1]);
+  stage_pairs(buf, lane, w);
 }
 
 __device__ __forceinline__ void store_box(const CUtensorMap* m, uint32_t buf, int x, int y,
@@ -170,11 +174,10 @@ __device__ __forceinline__ void tma_load_2d_pair(uint32_t dst, const CUtensorMap
 struct Tile {
   int pr;    // problem
   int m, n;  // first row of the pair, first column (gated: first feature)
-  int half;  // half the columns of a whole tile
 };
 
 // Tile t of the list: the problems one after another, M tiles in bands of kBand,
-// walked M first within a band; halves last.
+// walked M first within a band.
 template <int EPI>
 __device__ __forceinline__ Tile tile_of(const MmaParams& p, int t) {
   Tile T;
@@ -184,16 +187,12 @@ __device__ __forceinline__ Tile tile_of(const MmaParams& p, int t) {
     if (i < p.problems && t >= p.pr[i].begin) T.pr = i;
   const Problem& P = p.pr[T.pr];
   t -= P.begin;
-  T.half = t >= P.full;
-  const int second = T.half ? (t - P.full) & 1 : 0;
-  if (T.half) t = P.full + ((t - P.full) >> 1);
   const int per = kBand * P.n_tiles;
   const int band = t / per, r = t - band * per;
   const int rows = min(kBand, P.m_tiles - band * kBand);
   const int n = r / rows;
-  constexpr int kWide = EPI == kGated ? kBM : 2 * kBM;
   T.m = (band * kBand + (r - n * rows)) * 2 * kBM;
-  T.n = n * kWide + second * (kWide / 2);
+  T.n = n * (EPI == kGated ? P.w : 2 * P.w);
   return T;
 }
 
@@ -255,14 +254,15 @@ __global__ void __launch_bounds__(kThreads, 1)
       const Problem& P = p.pr[T.pr];
       // what the loop needs, in registers: a read of the parameters by problem in
       // every step made the launch 9 % slower
-      const CUtensorMap *ma = &maps.a[T.pr], *mb = !T.half || kBMn<EPI>(P) ? &maps.b[T.pr] : &maps.b_half;
+      const CUtensorMap *ma = &maps.a[T.pr], *mb = &maps.b[T.pr];
       const bool amn = kAMn<EPI>(P), bmn = kBMn<EPI>(P);
-      const int k_tiles = P.k_tiles;
+      const int k_tiles = P.k_tiles, w = P.w;
       const uint32_t bar0 = mapa_shared(smem_u32(&full_bar[0]), 0);
       const int am = T.m + (int)crank * kBM;
       // the odd CTA's rows of B: the second half of the tile's columns (gated: the up rows)
-      const int bn = T.n + (int)crank * (EPI == kGated ? p.up : T.half ? kBM / 2 : kBM);
-      const uint32_t bytes = 2 * kOpBytes + (T.half ? kOpBytes : 2 * kOpBytes);  // of both CTAs
+      const int bn = T.n + (int)crank * (EPI == kGated ? p.up : w);
+      // of both CTAs: K-major boxes of w rows, MN-major ones of 64 columns
+      const uint32_t bytes = 2 * (kOpBytes + (bmn ? (w > 64 ? kOpBytes : kOpBytes / 2) : (uint32_t)w * 128u));
       for (int kt = 0; kt < k_tiles; ++kt, ++g) {
         const uint32_t s = g % kStages, u = g / kStages;
         if (u > 0 && !mbar_wait_cluster_warp(smem_u32(&empty_bar[s]), (u - 1u) & 1u, p.err,
@@ -284,7 +284,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           if (bmn) {
             tma_load_2d_pair(b, mb, bn, k, bar);
-            if (!T.half) tma_load_2d_pair(b + kOpBytes / 2, mb, bn + 64, k, bar);
+            if (w > 64) tma_load_2d_pair(b + kOpBytes / 2, mb, bn + 64, k, bar);
           } else {
             tma_load_2d_pair(b, mb, k, bn, bar);
           }
@@ -302,7 +302,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const Problem& P = p.pr[T.pr];
         const bool amn = kAMn<EPI>(P), bmn = kBMn<EPI>(P);
         const int k_tiles = P.k_tiles;
-        const uint32_t idesc = idesc_bf16_f32(2 * kBM, T.half ? kBM : 2 * kBM) |
+        const uint32_t idesc = idesc_bf16_f32(2 * kBM, 2 * P.w) |
                                (amn ? kIdescAMnMajor : 0u) | (bmn ? kIdescBMnMajor : 0u);
         // 16 contraction values: 32 bytes along a K-major row, 16 rows of an MN-major
         // tile (descriptors count in 16 bytes)
@@ -346,31 +346,45 @@ __global__ void __launch_bounds__(kThreads, 1)
       const CUtensorMap *mo = &maps.o[T.pr], *mx = &maps.x[T.pr];
       const uint32_t b = tc & 1u, bu = tc >> 1;
       const int row0 = T.m + (int)crank * kBM + q * 32, row = row0 + lane;
-      const int wide = (EPI == kGated ? kBM / 2 : kBM) >> T.half;  // columns of this warp
-      const int col0 = T.n + half * wide;
-      const uint32_t tl = tmem + b * 256u + ((uint32_t)(q * 32) << 16) + (uint32_t)(half * wide);
-      // 32-column chunks of this warp that hold output values
-      const int nch = row0 < P.M ? max(0, min(wide / 32, (P.N - col0 + 31) / 32)) : 0;
+      const uint32_t tl = tmem + b * 256u + ((uint32_t)(q * 32) << 16);
+      const int M = P.M, N = P.N, w = P.w;
+      // 32-column chunks of the tile that hold output values; this warp takes every second
+      const int cols = min(EPI == kGated ? w : 2 * w, N - T.n);
+      const int chunks = row0 < M ? (cols + 31) / 32 : 0;
       const bool add = (EPI == kOut || EPI == kGrads) && P.has_add;
       auto load_add = [&](int c) {
-        if (lane == 0) {
-          const uint32_t bar = smem_u32(&add_bar[ew][c & 1]);
+        if (c < chunks && lane == 0) {
+          const uint32_t bar = smem_u32(&add_bar[ew][(c >> 1) & 1]);
           mbar_arrive_expect_tx(bar, 2048);
-          tma_load_2d_pair(buf0 + (uint32_t)(c & 1) * 2048u, mx, col0 + 32 * c, row0, bar);
+          tma_load_2d_pair(buf0 + (uint32_t)((c >> 1) & 1) * 2048u, mx, T.n + 32 * c, row0, bar);
         }
       };
-      if (add && nch > 0) {  // under the tile's MMAs: the first two chunks of what is added
+      if (add && half < chunks) {  // under the tile's MMAs: the first two chunks of what is added
         if (lane == 0) bulk_wait_read<0>();
         __syncwarp();
-        load_add(0);
-        if (nch > 1) load_add(1);
+        load_add(half);
+        load_add(half + 2);
       }
+      // the checkpoint of a chunk is loaded a chunk ahead, the first under the tile's MMAs
+      uint4 nx[4] = {};
+      uint32_t nsf = 0;
+      auto load_kept = [&](int c) {
+        if (EPI == kGatedBwd && c < chunks && row < M) {
+          const uint8_t* from = p.ck_in + (size_t)row * 2 * N + T.n + 32 * c;
+          const uint8_t* sf = p.sf_in + (size_t)row * (N / 16) + T.n / 32 + c;
+          nx[0] = reinterpret_cast<const uint4*>(from)[0];
+          nx[1] = reinterpret_cast<const uint4*>(from)[1];
+          nx[2] = reinterpret_cast<const uint4*>(from + N)[0];
+          nx[3] = reinterpret_cast<const uint4*>(from + N)[1];
+          nsf = (uint32_t)sf[0] | ((uint32_t)sf[N / 32] << 8);
+        }
+      };
+      load_kept(half);
       if (!mbar_wait_cluster_warp(smem_u32(&tmem_full_bar[b]), bu & 1u, p.err, kErrWaitAccum)) break;
       tc_fence_after();
-#pragma unroll 2
-      for (int c = 0; c < nch; ++c) {
-        const int col = col0 + 32 * c;
-        const uint32_t buf = buf0 + (uint32_t)(c & 1) * 2048u;
+      for (int c = half; c < chunks; c += 2) {
+        const int col = T.n + 32 * c, odd = (c >> 1) & 1;
+        const uint32_t buf = buf0 + (uint32_t)odd * 2048u;
         float v[32];
         tmem_row32(tl + 32u * (uint32_t)c, v);
         if (EPI == kGrads && P.f32) {
@@ -384,8 +398,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           store_box(mo, buf0, col, row0, lane);
         } else if constexpr (EPI == kOut || EPI == kGrads) {
           if (add) {
-            const uint32_t use = adds[c & 1]++;
-            if (!mbar_wait_warp(smem_u32(&add_bar[ew][c & 1]), use & 1u, p.err, kErrWaitAccum)) break;
+            const uint32_t use = adds[odd]++;
+            if (!mbar_wait_warp(smem_u32(&add_bar[ew][odd]), use & 1u, p.err, kErrWaitAccum)) break;
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
               const uint4 w = ld_shared_v4(buf + at64(lane, j));
@@ -402,65 +416,67 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           stage_row(buf, lane, v);
           store_box(mo, buf, col, row0, lane);
-          if (add && c + 2 < nch) {
+          if (add && c + 4 < chunks) {
             if (lane == 0) bulk_wait_read<0>();
             __syncwarp();
-            load_add(c + 2);
+            load_add(c + 4);
           }
         } else if constexpr (EPI == kGated) {
           float u[32];
-          tmem_row32(tl + (uint32_t)(kBM >> T.half) + 32u * (uint32_t)c, u);
-          if (p.ck && row < P.M) {
-            const size_t at = (size_t)row * 2 * P.N + col, sa = (size_t)row * (P.N / 16) + col / 32;
+          tmem_row32(tl + (uint32_t)w + 32u * (uint32_t)c, u);
+          if (p.ck && row < M) {
+            const size_t at = (size_t)row * 2 * N + col, sa = (size_t)row * (N / 16) + col / 32;
             keep_block(v, p.ck + at, p.sf + sa);
-            keep_block(u, p.ck + at + P.N, p.sf + sa + P.N / 32);
+            keep_block(u, p.ck + at + N, p.sf + sa + N / 32);
           }
 #pragma unroll
           for (int j = 0; j < 32; ++j) v[j] = act_fwd<ACT>(v[j]) * u[j];
           if (lane == 0) bulk_wait_read<1>();
           __syncwarp();
-          stage_row(buf, lane, v);
-          store_box(mo, buf, col, row0, lane);
-        } else {  // kGatedBwd
-          uint4 gc[2] = {}, uc[2] = {};
-          float fg = 0.0f, fu = 0.0f;
-          if (row < P.M) {
-            const size_t at = (size_t)row * 2 * P.N + col, sa = (size_t)row * (P.N / 16) + col / 32;
-            gc[0] = reinterpret_cast<const uint4*>(p.ck_in + at)[0];
-            gc[1] = reinterpret_cast<const uint4*>(p.ck_in + at)[1];
-            uc[0] = reinterpret_cast<const uint4*>(p.ck_in + at + P.N)[0];
-            uc[1] = reinterpret_cast<const uint4*>(p.ck_in + at + P.N)[1];
-            fg = e8m0_value(p.sf_in[sa]);
-            fu = e8m0_value(p.sf_in[sa + P.N / 32]);
+          if (32 * c + 32 <= w) {
+            stage_row(buf, lane, v);
+            store_box(mo, buf, col, row0, lane);
+          } else {  // the tile ends after 16 columns
+#pragma unroll
+            for (int j = 0; j < 2; ++j)
+              st_shared_v4(buf + (uint32_t)(lane * 32 + j * 16), pack_bf16(v[8 * j], v[8 * j + 1]),
+                           pack_bf16(v[8 * j + 2], v[8 * j + 3]), pack_bf16(v[8 * j + 4], v[8 * j + 5]),
+                           pack_bf16(v[8 * j + 6], v[8 * j + 7]));
+            store_box(&maps.o16, buf, col, row0, lane);
           }
-          const uint32_t gw[8] = {gc[0].x, gc[0].y, gc[0].z, gc[0].w, gc[1].x, gc[1].y, gc[1].z, gc[1].w};
-          const uint32_t uw[8] = {uc[0].x, uc[0].y, uc[0].z, uc[0].w, uc[1].x, uc[1].y, uc[1].z, uc[1].w};
-          float du[32], h[32];
+        } else {  // kGatedBwd
+          const uint32_t gw[8] = {nx[0].x, nx[0].y, nx[0].z, nx[0].w, nx[1].x, nx[1].y, nx[1].z, nx[1].w};
+          const uint32_t uw[8] = {nx[2].x, nx[2].y, nx[2].z, nx[2].w, nx[3].x, nx[3].y, nx[3].z, nx[3].w};
+          const float fg = e8m0_value(nsf & 255u), fu = e8m0_value(nsf >> 8);
+          load_kept(c + 2);
+          uint32_t dg[16], du[16], h[16];  // pairs of bf16
 #pragma unroll
           for (int j = 0; j < 16; ++j) {
             const uint32_t sh = (j & 1) * 16;
             const float2 g2 = e4m3x2_value((gw[j >> 1] >> sh) & 0xFFFFu);
             const float2 u2 = e4m3x2_value((uw[j >> 1] >> sh) & 0xFFFFu);
+            float a[2], d[2], e[2];
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
               const float g = (i ? g2.y : g2.x) * fg, u = (i ? u2.y : u2.x) * fu;
-              const float da = v[2 * j + i];
-              const float k = act_core<ACT>(g);
-              const float a = g * k;
-              v[2 * j + i] = da * u * act_grad_core<ACT>(g, k);
-              du[2 * j + i] = da * a;
-              h[2 * j + i] = a * u;
+              const float da = v[2 * j + i], k = act_core<ACT>(g), act = g * k;
+              d[i] = da * u * act_grad_core<ACT>(g, k);
+              e[i] = da * act;
+              a[i] = act * u;
             }
+            dg[j] = pack_bf16(d[0], d[1]);
+            du[j] = pack_bf16(e[0], e[1]);
+            h[j] = pack_bf16(a[0], a[1]);
           }
           if (lane == 0) bulk_wait_read<0>();
           __syncwarp();
-          stage_row(buf0, lane, v);
+          stage_pairs(buf0, lane, dg);
           store_box(mo, buf0, col, row0, lane);
-          stage_row(buf0 + 2048u, lane, du);
+          stage_pairs(buf0 + 2048u, lane, du);
           store_box(mx, buf0 + 2048u, col, row0, lane);
           if (lane == 0) bulk_wait_read<1>();
           __syncwarp();
-          stage_row(buf0, lane, h);
+          stage_pairs(buf0, lane, h);
           store_box(&maps.o[1], buf0, col, row0, lane);
         }
       }
@@ -544,29 +560,59 @@ Problem problem(int M, int N, int64_t K, bool amn = false) {
   return P;
 }
 
+// How long a tile of width w takes, in k-tiles of the widest: its MMAs, or its
+// operands' way into shared memory (128 + w rows a CTA; the widest tile's operands
+// take 0.82 of its MMAs' time), and what a tile costs beside its contraction.
+double tile_cost(int w, int k_tiles) {
+  const double mma = w / 128.0, operands = 0.82 * (128 + w) / 256.0;
+  return k_tiles * (mma > operands ? mma : operands) + 1.5;
+}
+
+void set_width(Problem& P, int w, bool gated) {
+  P.w = w;
+  P.m_tiles = (P.M + 2 * kBM - 1) / (2 * kBM);
+  const int wide = gated ? w : 2 * w;
+  P.n_tiles = (P.N + wide - 1) / wide;
+}
+
+// The width of the launch's tiles (one for all its problems) whose longest pair ends
+// first: pair p takes tiles p, p + pairs, ... of the list, so a last turn that few
+// tiles fill costs as much as a full one. 8192 x 2048 x 768, the gated product: 128
+// -> 96 features, 2.5 turns that cost 3 become 3.4 that cost 2.9.
+void pick_width(Problem* pr, int n, int pairs, bool gated, int step) {
+  double least = 0;
+  int best = 128;
+  for (int w = 128; w >= 64; w -= step) {
+    double cost[kMaxProblems];
+    int64_t begin[kMaxProblems + 1] = {0};
+    for (int i = 0; i < n; ++i) {
+      set_width(pr[i], w, gated);
+      cost[i] = tile_cost(w, pr[i].k_tiles);
+      begin[i + 1] = begin[i] + (int64_t)pr[i].m_tiles * pr[i].n_tiles;
+    }
+    double longest = 0;
+    for (int p = 0; p < pairs; ++p) {
+      double sum = 0;
+      for (int i = 0; i < n; ++i)
+        sum += cost[i] * (double)((begin[i + 1] - p + pairs - 1) / pairs - (begin[i] - p + pairs - 1) / pairs);
+      longest = sum > longest ? sum : longest;
+    }
+    if (w == 128 || longest < 0.97 * least) {
+      least = longest;
+      best = w;
+    }
+  }
+  for (int i = 0; i < n; ++i) set_width(pr[i], best, gated);
+}
+
 // The problems come longest contraction first: the pairs take tiles in turn, so the
 // short ones even the pairs out.
 template <int EPI, int ACT>
-cudaError_t launch(const Maps& maps, MmaParams p, cudaStream_t s) {
-  cudaError_t err = cudaSuccess;
-  const int pairs = max_pairs<EPI, ACT>(&err);
-  if (pairs <= 0) return err != cudaSuccess ? err : cudaErrorUnknown;
+cudaError_t launch(const Maps& maps, MmaParams p, int pairs, cudaStream_t s) {
   int64_t tiles = 0;
   for (int i = 0; i < p.problems; ++i) {
-    Problem& P = p.pr[i];
-    P.m_tiles = (P.M + 2 * kBM - 1) / (2 * kBM);
-    const int wide = EPI == kGated ? kBM : 2 * kBM;
-    P.n_tiles = (P.N + wide - 1) / wide;
-    const int64_t n = (int64_t)P.m_tiles * P.n_tiles;
-    P.begin = (int)tiles;
-    P.full = (int)n;
-    // the last, partly filled turn in halves where that fills it: a half costs
-    // about 0.6 of a whole tile, a turn that is at most half full costs a whole one
-    if (i == p.problems - 1) {
-      const int rest = (int)((tiles + n) % pairs);
-      if (rest <= pairs / 2 && rest <= n) P.full = (int)n - rest;
-    }
-    tiles += P.full + 2 * (n - P.full);
+    p.pr[i].begin = (int)tiles;
+    tiles += (int64_t)p.pr[i].m_tiles * p.pr[i].n_tiles;
     if (tiles > INT32_MAX / 4) return cudaErrorInvalidValue;
   }
   p.tiles = (int)tiles;
@@ -574,77 +620,104 @@ cudaError_t launch(const Maps& maps, MmaParams p, cudaStream_t s) {
   return launch_pdl_pairs(shared_mma_kernel<EPI, ACT>, dim3(2 * n), dim3(kThreads), kSmemBytes, s, maps, p);
 }
 
-}  // namespace
-
-int launch_shared_forward(const SharedArgs& a, cudaStream_t s) {
-  if (a.N <= 256) return launch_shared_forward_few(a, s);
+template <int ACT>
+cudaError_t forward(const SharedArgs& a, cudaStream_t s) {
+  cudaError_t err = cudaSuccess;
+  int pairs = max_pairs<kGated, ACT>(&err);
+  if (pairs <= 0) return err != cudaSuccess ? err : cudaErrorUnknown;
   Maps m{};
-  if (!operand_map(&m.a[0], a.x, a.H, a.N, false) || !operand_map(&m.b[0], a.w13, a.H, 2 * a.I, false) ||
-      !operand_map(&m.b_half, a.w13, a.H, 2 * a.I, false, 64) ||
-      !out_map(&m.o[0], a.h, a.I, a.N, a.I))
-    return -1;
   MmaParams p{};
   p.err = a.err;
   p.problems = 1;
   p.pr[0] = problem(a.N, a.I, a.H);
+  // a checkpoint block of 32 features lies in one tile
+  pick_width(p.pr, 1, pairs, true, a.ck ? 32 : 16);
   p.up = a.I;
   p.ck = a.ck;
   p.sf = a.ck_sf;
-  cudaError_t err = a.activation ? launch<kGated, 1>(m, p, s) : launch<kGated, 0>(m, p, s);
-  if (err != cudaSuccess) return -(int)err;
-  if (!operand_map(&m.a[0], a.h, a.I, a.N, false) || !operand_map(&m.b[0], a.w2, a.I, a.H, false) ||
-      !operand_map(&m.b_half, a.w2, a.I, a.H, false, 64) ||
-      !out_map(&m.o[0], a.y, a.H, a.N, a.H) || (a.add && !out_map(&m.x[0], a.add, a.H, a.N, a.H)))
-    return -1;
+  if (!operand_map(&m.a[0], a.x, a.H, a.N, false) ||
+      !operand_map(&m.b[0], a.w13, a.H, 2 * (int64_t)a.I, false, (uint32_t)p.pr[0].w) ||
+      !out_map(&m.o[0], a.h, a.I, a.N, a.I) ||
+      !map2d(&m.o16, a.h, a.I, a.N, a.I, 16, 32, CU_TENSOR_MAP_SWIZZLE_NONE))
+    return cudaErrorInvalidValue;
+  err = launch<kGated, ACT>(m, p, pairs, s);
+  if (err != cudaSuccess) return err;
+  pairs = max_pairs<kOut, 0>(&err);
+  if (pairs <= 0) return err != cudaSuccess ? err : cudaErrorUnknown;
   p = MmaParams{};
   p.err = a.err;
   p.problems = 1;
   p.pr[0] = problem(a.N, a.H, a.I);
   p.pr[0].has_add = a.add != nullptr;
-  err = launch<kOut, 0>(m, p, s);
-  return err != cudaSuccess ? -(int)err : 2;
+  pick_width(p.pr, 1, pairs, false, 16);
+  if (!operand_map(&m.a[0], a.h, a.I, a.N, false) ||
+      !operand_map(&m.b[0], a.w2, a.I, a.H, false, (uint32_t)p.pr[0].w) ||
+      !out_map(&m.o[0], a.y, a.H, a.N, a.H) || (a.add && !out_map(&m.x[0], a.add, a.H, a.N, a.H)))
+    return cudaErrorInvalidValue;
+  return launch<kOut, 0>(m, p, pairs, s);
 }
 
-int launch_shared_backward(const SharedArgs& a, cudaStream_t s) {
-  Maps m{};
+template <int ACT>
+cudaError_t backward(const SharedArgs& a, cudaStream_t s) {
+  cudaError_t err = cudaSuccess;
+  int pairs = max_pairs<kGatedBwd, ACT>(&err);
+  if (pairs <= 0) return err != cudaSuccess ? err : cudaErrorUnknown;
   // da = dy W2; dg, du and h from the checkpoint
-  if (!operand_map(&m.a[0], a.dy, a.H, a.N, false) || !operand_map(&m.b[0], a.w2, a.I, a.H, true) ||
-      !out_map(&m.o[0], a.dpre, a.I, a.N, 2 * (int64_t)a.I) ||
-      !out_map(&m.x[0], a.dpre + a.I, a.I, a.N, 2 * (int64_t)a.I) || !out_map(&m.o[1], a.h, a.I, a.N, a.I))
-    return -1;
+  Maps m{};
   MmaParams p{};
   p.err = a.err;
   p.problems = 1;
   p.pr[0] = problem(a.N, a.I, a.H);
+  pick_width(p.pr, 1, pairs, false, 16);
   p.ck_in = a.ck;
   p.sf_in = a.ck_sf;
-  cudaError_t err = a.activation ? launch<kGatedBwd, 1>(m, p, s) : launch<kGatedBwd, 0>(m, p, s);
-  if (err != cudaSuccess) return -(int)err;
+  if (!operand_map(&m.a[0], a.dy, a.H, a.N, false) || !operand_map(&m.b[0], a.w2, a.I, a.H, true) ||
+      !out_map(&m.o[0], a.dpre, a.I, a.N, 2 * (int64_t)a.I) ||
+      !out_map(&m.x[0], a.dpre + a.I, a.I, a.N, 2 * (int64_t)a.I) || !out_map(&m.o[1], a.h, a.I, a.N, a.I))
+    return cudaErrorInvalidValue;
+  err = launch<kGatedBwd, ACT>(m, p, pairs, s);
+  if (err != cudaSuccess) return err;
   // dx = [dg du] W13, dW13 = [dg du]^T x and dW2 = dy^T h in one launch
+  pairs = max_pairs<kGrads, 0>(&err);
+  if (pairs <= 0) return err != cudaSuccess ? err : cudaErrorUnknown;
   m = Maps{};
   p = MmaParams{};
   p.err = a.err;
   p.problems = 3;
   const bool dx_first = 2 * (int64_t)a.I >= a.N;
   const int ix = dx_first ? 0 : 2, i13 = dx_first ? 1 : 0, i2 = dx_first ? 2 : 1;
+  p.pr[ix] = problem(a.N, a.H, 2 * (int64_t)a.I);
+  p.pr[ix].has_add = a.add != nullptr;
+  p.pr[i13] = problem(2 * a.I, a.H, a.N, true);
+  p.pr[i2] = problem(a.H, a.I, a.N, true);
+  p.pr[i13].f32 = p.pr[i2].f32 = a.grad_f32;
+  pick_width(p.pr, 3, pairs, false, 32);
   auto grad_map = [&](CUtensorMap* t, void* d, int64_t cols, int64_t rows) {
     return a.grad_f32 ? map2d(t, d, cols, rows, cols, 32, 32, CU_TENSOR_MAP_SWIZZLE_128B,
                               CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 4)
                       : out_map(t, d, cols, rows, cols);
   };
   if (!operand_map(&m.a[ix], a.dpre, 2 * (int64_t)a.I, a.N, false) ||
-      !operand_map(&m.b[ix], a.w13, a.H, 2 * (int64_t)a.I, true) ||
-      !out_map(&m.o[ix], a.dx, a.H, a.N, a.H) || (a.add && !out_map(&m.x[ix], a.add, a.H, a.N, a.H)) ||
-      !operand_map(&m.a[i13], a.dpre, 2 * (int64_t)a.I, a.N, true) || !operand_map(&m.b[i13], a.x, a.H, a.N, true) ||
-      !grad_map(&m.o[i13], a.dw13, a.H, 2 * (int64_t)a.I) || !operand_map(&m.a[i2], a.dy, a.H, a.N, true) ||
-      !operand_map(&m.b[i2], a.h, a.I, a.N, true) || !grad_map(&m.o[i2], a.dw2, a.I, a.H))
-    return -1;
-  p.pr[ix] = problem(a.N, a.H, 2 * (int64_t)a.I);
-  p.pr[ix].has_add = a.add != nullptr;
-  p.pr[i13] = problem(2 * a.I, a.H, a.N, true);
-  p.pr[i2] = problem(a.H, a.I, a.N, true);
-  p.pr[i13].f32 = p.pr[i2].f32 = a.grad_f32;
-  err = launch<kGrads, 0>(m, p, s);
+      !operand_map(&m.b[ix], a.w13, a.H, 2 * (int64_t)a.I, true) || !out_map(&m.o[ix], a.dx, a.H, a.N, a.H) ||
+      (a.add && !out_map(&m.x[ix], a.add, a.H, a.N, a.H)) ||
+      !operand_map(&m.a[i13], a.dpre, 2 * (int64_t)a.I, a.N, true) ||
+      !operand_map(&m.b[i13], a.x, a.H, a.N, true) || !grad_map(&m.o[i13], a.dw13, a.H, 2 * (int64_t)a.I) ||
+      !operand_map(&m.a[i2], a.dy, a.H, a.N, true) || !operand_map(&m.b[i2], a.h, a.I, a.N, true) ||
+      !grad_map(&m.o[i2], a.dw2, a.I, a.H))
+    return cudaErrorInvalidValue;
+  return launch<kGrads, 0>(m, p, pairs, s);
+}
+
+}  // namespace
+
+int launch_shared_forward(const SharedArgs& a, cudaStream_t s) {
+  if (a.N <= 256) return launch_shared_forward_few(a, s);
+  const cudaError_t err = a.activation ? forward<1>(a, s) : forward<0>(a, s);
+  return err != cudaSuccess ? -(int)err : 2;
+}
+
+int launch_shared_backward(const SharedArgs& a, cudaStream_t s) {
+  const cudaError_t err = a.activation ? backward<1>(a, s) : backward<0>(a, s);
   return err != cudaSuccess ? -(int)err : 2;
 }
 
