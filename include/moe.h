@@ -506,7 +506,7 @@ int moe_w4_matvec(const void* x, const void* q, const void* scale, int n, int ro
 
 /* Shape of a decode batch through 4-bit experts.
  *  n_tokens N, hidden H, n_experts E (1..256), top_k K (1..16), inter I;
- *  group divides H and I; N*K at most 1024. */
+ *  group divides H and I, both at most 16384; N*K at most 1024. */
 typedef struct moe_w4_config {
   int32_t n_tokens;
   int32_t hidden;
@@ -517,7 +517,8 @@ typedef struct moe_w4_config {
   int32_t activation;
 } moe_w4_config_t;
 
-/* Bytes of scratch moe_w4_ffn_forward needs (h of every route). */
+/* Bytes of scratch moe_w4_ffn_forward needs: the routes by expert, h of every
+ * route (bf16) and its weighted products (f32). */
 int64_t moe_w4_workspace_bytes(const moe_w4_config_t* cfg);
 
 /* The experts of a decode batch, from the router's choice to the layer's output:

@@ -825,7 +825,7 @@ static int check_w4(const moe_w4_config_t* c) {
       (c->activation != MOE_ACT_SWIGLU && c->activation != MOE_ACT_GEGLU))
     return MOE_ERR_INVALID_ARG;
   if (c->n_experts > moe::kMaxExperts || c->top_k > moe::kMaxTopK || c->hidden % c->group != 0 ||
-      c->inter % c->group != 0 || c->hidden > (1 << 24) || c->inter > (1 << 23) ||
+      c->inter % c->group != 0 || c->hidden > (1 << 14) || c->inter > (1 << 14) ||
       (int64_t)c->n_tokens * c->top_k > kW4MaxRoutes)
     return MOE_ERR_UNSUPPORTED_SHAPE;
   return MOE_OK;
@@ -833,7 +833,7 @@ static int check_w4(const moe_w4_config_t* c) {
 
 int64_t moe_w4_workspace_bytes(const moe_w4_config_t* cfg) {
   const int rc = check_w4(cfg);
-  return rc != MOE_OK ? rc : roundup((int64_t)cfg->n_tokens * cfg->top_k * cfg->inter * 2, 256);
+  return rc != MOE_OK ? rc : moe::w4_workspace_bytes(cfg->n_tokens, cfg->top_k, cfg->hidden, cfg->inter);
 }
 
 int moe_w4_ffn_forward(const moe_w4_config_t* cfg, const int32_t* topk_ids, const float* topk_p,
@@ -865,7 +865,7 @@ int moe_w4_ffn_forward(const moe_w4_config_t* cfg, const int32_t* topk_ids, cons
   a.w2 = static_cast<const uint8_t*>(w2q);
   a.w2_scale = static_cast<const uint16_t*>(w2_scale);
   a.add = static_cast<const uint16_t*>(add);
-  a.h = static_cast<uint16_t*>(workspace);
+  a.ws = static_cast<uint8_t*>(workspace);
   a.y = static_cast<uint16_t*>(y);
   return finish(moe::launch_w4_ffn(a, stream));
 }

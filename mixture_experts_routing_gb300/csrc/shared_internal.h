@@ -40,9 +40,12 @@ struct W4Args {
   const uint8_t* w2;        // [E,H,I/2]
   const uint16_t* w2_scale;  // [E,H,I/group] bf16
   const uint16_t* add;      // [N,H] or null
-  uint16_t* h;              // [N*K,I] workspace
+  uint8_t* ws;              // w4_workspace_bytes
+  uint16_t* h;              // [N*K,I] in the workspace (set by launch_w4_ffn)
   uint16_t* y;              // [N,H]
 };
+
+int64_t w4_workspace_bytes(int N, int K, int H, int I);
 
 int launch_w4_ffn(const W4Args& a, cudaStream_t s);
 int launch_w4_matvec(const uint16_t* x, const uint8_t* q, const uint16_t* scale, int N, int rows,

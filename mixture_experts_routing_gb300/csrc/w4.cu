@@ -6,17 +6,23 @@
 //             y[t,:] = add[t,:] + sum_k p[t,k] W2[e] h[t,k,:]
 //
 // The time is that of reading the codes once, so the kernels are built around
-// that stream. A warp takes 16 rows and walks blocks of their columns; the codes,
-// the scales and the same columns of x come through the warp's own ring of
-// shared-memory stages (cp.async, no barrier with other warps), so that neither
-// the codes' nor x's latency is waited for block by block. The codes become the A
-// operand of mma.sync m16n8k16: the products need 8 columns for 1 to 8 tokens, and
-// the opened codes are in registers, where tcgen05.mma takes no operand from. A
-// mask and an OR put four bits into the mantissa of bf16 128 + code, one
-// subtraction makes it code - 8, exactly. The order of the columns within a group
-// is free as long as x follows it, so no weight is moved between lanes. The sums
-// of one group are scaled in fp32 and added up in fp32. Warps that share a row
-// tile split its columns and add their parts in a fixed order.
+// that stream. A warp takes 16 rows. The codes become the A operand of mma.sync
+// m16n8k16: the products need 8 columns for 1 to 8 tokens, and the opened codes are
+// in registers, where tcgen05.mma takes no operand from. A mask and an OR put four
+// bits into the mantissa of bf16 128 + code, one subtraction makes it code - 8,
+// exactly. The order of the columns within a group is free as long as x follows
+// it, so no weight is moved between lanes. The sums of one group are scaled in
+// fp32 and added up in fp32. Warps that share a row tile split its columns and add
+// their parts in a fixed order.
+//
+// Experts, and one token's matvec (Rows): a lane loads 16 bytes of its two rows
+// straight into registers, four blocks of 128 columns ahead; x is laid out in shared
+// memory once per block of threads. Several tokens: one small kernel groups the
+// routes by expert, a block of the products takes some rows of one expert and its
+// routes (so an expert's weights are read once for all of them), and a last kernel
+// adds up each token's routes.
+// Several tokens' matvec (Stream): codes, scales and x come through each warp's own
+// ring of shared-memory stages.
 #include "act.cuh"
 #include "moe_internal.h"
 #include "ptx.cuh"
@@ -319,276 +325,14 @@ __global__ void __launch_bounds__(kThreads, 2)
   }
 }
 
-// Routes grouped by expert, in shared memory, by the whole block: pieces of at
-// most `most` routes of one expert, experts ascending, routes in their order. A
-// route without an expert (an id outside 0..E-1), or to an expert that its token
-// has named before, is in none; p[] gets the token's whole probability of the
-// expert where the probabilities are given.
-template <int ROUTES>
-struct Groups {
-  static constexpr int kPieces = kMaxExperts + ROUTES / 8;
-  int16_t id[ROUTES];       // expert, or -1
-  int16_t rank[ROUTES];     // of a route among its expert's
-  int16_t order[ROUTES];    // routes, sorted by expert
-  int16_t routes[kMaxExperts];
-  int16_t expert[kPieces], first[kPieces], count[kPieces];  // first: its place in `order`
-  int scan[2][kMaxExperts / 32];
-  int pieces;
-};
-
-template <int THREADS, int ROUTES>
-__device__ __forceinline__ void group_routes(Groups<ROUTES>& G, float* p, const int32_t* ids,
-                                             const float* probs, int R, int K, int E, int most) {
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, tid = threadIdx.x;
-  static_assert(THREADS >= kMaxExperts, "a thread for each expert");
-  if (tid < kMaxExperts) G.routes[tid] = 0;
-  for (int i = tid; i < R; i += THREADS) {
-    const int r0 = i / K * K;
-    int e = __ldcg(ids + i);
-    if (e < 0 || e >= E) e = -1;
-    for (int r = r0; r < i && e >= 0; ++r)
-      if (__ldcg(ids + r) == e) e = -1;
-    G.id[i] = (int16_t)e;
-    if (p && e >= 0) {
-      float v = __ldcg(probs + i);
-      for (int r = i + 1; r < r0 + K; ++r)
-        if (__ldcg(ids + r) == e) v += __ldcg(probs + r);
-      p[i] = v;
-    }
-  }
-  __syncthreads();
-  if (warp == 0) {  // 32 routes at a time, in order: each gets its rank within its expert
-    for (int i0 = 0; i0 < R; i0 += 32) {
-      const int i = i0 + lane;
-      const int e = i < R ? G.id[i] : -1;
-      const uint32_t same = __match_any_sync(0xFFFFFFFFu, e);
-      const int before = __popc(same & ((1u << lane) - 1u));
-      const int from = e >= 0 ? G.routes[e] : 0;
-      __syncwarp();
-      if (e >= 0 && before == 0) G.routes[e] = (int16_t)(from + __popc(same));
-      if (i < R) G.rank[i] = (int16_t)(from + before);
-      __syncwarp();
-    }
-  }
-  __syncthreads();
-  // exclusive sums over the experts of their routes and of their pieces
-  const int n = tid < kMaxExperts ? G.routes[tid] : 0, np = (n + most - 1) / most;
-  int sn = n, sp = np;
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const int vn = __shfl_up_sync(0xFFFFFFFFu, sn, o), vp = __shfl_up_sync(0xFFFFFFFFu, sp, o);
-    if (lane >= o) {
-      sn += vn;
-      sp += vp;
-    }
-  }
-  if (lane == 31 && warp < kMaxExperts / 32) {
-    G.scan[0][warp] = sn;
-    G.scan[1][warp] = sp;
-  }
-  __syncthreads();
-  if (tid < kMaxExperts) {
-    int on = sn - n, op = sp - np;
-    for (int w = 0; w < warp; ++w) {
-      on += G.scan[0][w];
-      op += G.scan[1][w];
-    }
-    G.routes[tid] = (int16_t)on;  // now: where the expert's routes begin
-    for (int j = 0; j < np; ++j) {
-      G.expert[op + j] = (int16_t)tid;
-      G.first[op + j] = (int16_t)(on + j * most);
-      G.count[op + j] = (int16_t)min(most, n - j * most);
-    }
-    if (tid == kMaxExperts - 1) G.pieces = op + np;
-  }
-  __syncthreads();
-  for (int i = tid; i < R; i += THREADS) {
-    const int e = G.id[i];
-    if (e >= 0) G.order[G.routes[e] + G.rank[i]] = (int16_t)i;
-  }
-  __syncthreads();
-}
-
-// First product. A unit is 8 features of one expert's piece of at most TOK
-// routes: rows g of the tile are their gate rows, rows g + 8 their up rows, so a
-// lane finds both sums of a feature in its own registers. A team of S warps,
-// which split the columns, takes every teams-th unit, its copies running on from
-// unit to unit.
-template <int GROUP, int TOK>
-__global__ void __launch_bounds__(kThreads, 2) w4_fc1_kernel(const W4Args a, const int S) {
-  using St = Stream<GROUP, TOK>;
-  constexpr int kTok = 8 * St::kNT, kPart = 16 * kTok;
-  extern __shared__ __align__(16) uint8_t dynamic[];
-  __shared__ Groups<kMaxRoutes> G;
-  __shared__ __align__(16) float part[kWarps * kPart];
-  griddep_wait();
-  griddep_launch_dependents();
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
-  group_routes<kThreads>(G, nullptr, a.topk_ids, nullptr, a.N * a.K, a.K, a.E, TOK);
-  // neighbouring units on different SMs, so that a few units fill them evenly
-  const int team = warp / S * gridDim.x + blockIdx.x, teams = gridDim.x * kWarps / S;
-  const int member = warp % S, i_tiles = a.I / 8, units = G.pieces * i_tiles;
-  const int c0 = share(member, S, a.H), c1 = share(member + 1, S, a.H);
-  const int blocks = (c1 - c0 + St::kCols - 1) / St::kCols;
-
-  St st;
-  st.init(ring_of(dynamic), warp, lane, a.I, a.H, a.w13_scale, (int64_t)a.E * 2 * a.I);
-  int unit_l = team - teams, more_l = 0;  // what is copied next: blocks left of the unit
-  auto copy_next = [&]() {
-    if (more_l == 0 && blocks > 0 && unit_l < units) {
-      unit_l += teams;
-      if (unit_l < units) {
-        const int piece = unit_l / i_tiles, i0 = (unit_l - piece * i_tiles) * 8;
-        const int first = G.first[piece], n = G.count[piece];
-        const int64_t row = (int64_t)G.expert[piece] * 2 * a.I + i0;
-        st.seek(a.w13, row + g, row + (lane & 7) + ((lane >> 3) & 1) * a.I, c0, c1, a.H, n);
-#pragma unroll
-        for (int i = 0; i < St::kCopies; ++i)
-          st.x[i] = a.x + (size_t)(G.order[first + min(st.token(i), n - 1)] / a.K) * a.H + c0 + st.x_col();
-        more_l = blocks;
-      }
-    }
-    if (more_l > 0) {
-      st.copy();
-      --more_l;
-    }
-    st.commit();
-  };
-#pragma unroll
-  for (int d = 0; d < St::kAhead; ++d) copy_next();
-
-  const int odd = ((g & 1) * st.rs + c0 / GROUP) & 1;
-  for (int unit = team; unit < units; unit += teams) {
-    const int piece = unit / i_tiles, i0 = (unit - piece * i_tiles) * 8;
-    const int first = G.first[piece], n = G.count[piece];
-    float acc[St::kNT][4] = {};
-    for (int b = 0; b < blocks; ++b) {
-      st.template multiply<false>((odd + b * St::kG) & 1, c1 - c0 - b * St::kCols, n, acc);
-      copy_next();
-    }
-    auto h_of = [&](int at, int i, float gate, float up) {
-      const float h = (a.activation ? act_fwd<1>(gate) : act_fwd<0>(gate)) * up;
-      a.h[(size_t)G.order[first + at] * a.I + i0 + permuted(i)] = to_bf(h);
-    };
-    if (S > 1) {
-      leave_part<St::kNT>(part + warp * kPart, g, t, acc);
-      asm volatile("bar.sync %0, %1;" ::"r"(1 + warp / S), "r"(32 * S) : "memory");
-      const float* all = part + (warp - member) * kPart;
-      for (int i = member * 32 + lane; i < 8 * n; i += 32 * S) {
-        float gate = 0.0f, up = 0.0f;
-        for (int w = 0; w < S; ++w) {
-          gate += all[w * kPart + (i & 7) * kTok + (i >> 3)];
-          up += all[w * kPart + (8 + (i & 7)) * kTok + (i >> 3)];
-        }
-        h_of(i >> 3, i & 7, gate, up);
-      }
-      asm volatile("bar.sync %0, %1;" ::"r"(1 + warp / S), "r"(32 * S) : "memory");
-    } else {
-#pragma unroll
-      for (int j = 0; j < St::kNT; ++j)
-#pragma unroll
-        for (int i = 0; i < 2; ++i)
-          if (8 * j + 2 * t + i < n) h_of(8 * j + 2 * t + i, g, acc[j][i], acc[j][2 + i]);
-    }
-  }
-}
-
-// Second product and the sum over a token's routes: block (16 output columns,
-// kChunk tokens) goes through the pieces of the experts that its tokens chose; a
-// team of S warps, which split the columns, takes every teams-th piece and adds
-// its products, weighted by the tokens' probabilities, to the warp's own sums
-// [token][16]. Dynamic shared memory: the rings, the sums, the probabilities.
-template <int GROUP, int TOK, int W>
-__global__ void __launch_bounds__(W * 32, 16 / W)
-    w4_fc2_kernel(const W4Args a, const int S) {
-  using St = Stream<GROUP, TOK>;
-  constexpr int kRoutes = kChunk * kMaxTopK;
-  extern __shared__ __align__(16) uint8_t dynamic[];
-  __shared__ Groups<kRoutes> G;
-  uint8_t* ring = ring_of(dynamic);
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
-  const int r0 = blockIdx.x * 16, t0 = blockIdx.y * kChunk;
-  const int tokens = min(kChunk, a.N - t0);
-  float* sums = reinterpret_cast<float*>(ring + W * St::kBytes);
-  float* prob = sums + W * tokens * 16;
-  for (int i = threadIdx.x; i < W * tokens * 16; i += W * 32) sums[i] = 0.0f;
-  // The first product's kernel let this one start after every earlier kernel had
-  // finished, and writes neither the routes nor the weights: only h has to wait.
-  group_routes<W * 32>(G, prob, a.topk_ids + (size_t)t0 * a.K, a.topk_p + (size_t)t0 * a.K,
-                       tokens * a.K, a.K, a.E, TOK);
-  const int teams = W / S, member = warp % S;
-  const int c0 = share(member, S, a.I), c1 = share(member + 1, S, a.I);
-  const int blocks = (c1 - c0 + St::kCols - 1) / St::kCols;
-  const int pieces = blocks > 0 ? G.pieces : 0;  // more warps than columns: nothing for this one
-  St st;
-  st.init(ring, warp, lane, 8, a.I, a.w2_scale, (int64_t)a.E * a.H);
-  griddep_wait();
-  griddep_launch_dependents();
-  int piece_l = warp / S - teams, more_l = 0;  // what is copied next
-  auto copy_next = [&]() {
-    if (more_l == 0 && piece_l < pieces) {
-      piece_l += teams;
-      if (piece_l < pieces) {
-        const int first = G.first[piece_l], n = G.count[piece_l];
-        const int64_t row = (int64_t)G.expert[piece_l] * a.H + r0;
-        st.seek(a.w2, row + g, row + (lane & 15), c0, c1, a.I, n);
-#pragma unroll
-        for (int i = 0; i < St::kCopies; ++i)
-          st.x[i] = a.h + ((size_t)t0 * a.K + G.order[first + min(st.token(i), n - 1)]) * a.I + c0 + st.x_col();
-        more_l = blocks;
-      }
-    }
-    if (more_l > 0) {
-      st.copy();
-      --more_l;
-    }
-    st.commit();
-  };
-#pragma unroll
-  for (int d = 0; d < St::kAhead; ++d) copy_next();
-
-  const int odd = ((g & 1) * st.rs + c0 / GROUP) & 1;
-  float* mine = sums + warp * tokens * 16;
-  for (int piece = warp / S; piece < pieces; piece += teams) {
-    const int first = G.first[piece], n = G.count[piece];
-    float acc[St::kNT][4] = {};
-    for (int b = 0; b < blocks; ++b) {
-      st.template multiply<true>((odd + b * St::kG) & 1, c1 - c0 - b * St::kCols, n, acc);
-      copy_next();
-    }
-#pragma unroll
-    for (int j = 0; j < St::kNT; ++j)
-#pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        const int at = 8 * j + 2 * t + i;
-        if (at < n) {  // a piece holds a token once: no two lanes meet
-          const int r = G.order[first + at];
-          float* to = mine + r / a.K * 16 + g;
-          to[0] = fmaf(prob[r], acc[j][i], to[0]);
-          to[8] = fmaf(prob[r], acc[j][2 + i], to[8]);
-        }
-      }
-    __syncwarp();
-  }
-  __syncthreads();
-  for (int i = threadIdx.x; i < 16 * tokens; i += W * 32) {
-    const size_t at = (size_t)(t0 + (i >> 4)) * a.H + r0 + (i & 15);
-    float v = a.add ? bf(a.add[at]) : 0.0f;
-#pragma unroll
-    for (int w = 0; w < W; ++w) v += sums[w * tokens * 16 + i];
-    a.y[at] = to_bf(v);
-  }
-}
-
-// ------------------------------------------------------------------ one token
-// With one token the eight columns of an MMA are free, and they tell the groups
-// apart: lane t of a quad takes 16 bytes (32 columns) of its two rows of every
-// block of 128, and column n of B holds x only at the columns of the block's n-th
-// group (zeros elsewhere), so the sums of up to four groups come out side by side.
-// No code or scale passes through shared memory, the loads run kOneAhead blocks
-// ahead in registers, and each warp lays its own columns of x out once.
-constexpr int kOneAhead = 4;
-constexpr int kOneBlock = 128;
+// ------------------------------------------------------------------ rows in registers
+// Lane 4g + t takes 16 bytes (32 columns) of its two rows of every block of 128
+// columns. A block may hold kG groups, whose sums must not mix: the MMA's columns
+// tell them apart. Column c of B is token c / kG and takes x only at the columns of
+// the block's group c % kG (zeros elsewhere), so one MMA gives the sums of kG groups
+// for 8 / kG tokens side by side, and P of them those of P times as many.
+constexpr int kRowsAhead = 4;
+constexpr int kRowsBlock = 128;
 
 __device__ __forceinline__ uint4 ld_codes(const uint8_t* p) {
   uint4 v;
@@ -598,97 +342,128 @@ __device__ __forceinline__ uint4 ld_codes(const uint8_t* p) {
   return v;
 }
 
-// Sums of two rows (`q`, `s`: the lane's place in row g, `q8`, `s8`: on to the
-// second row) over n blocks, `cols` columns of which are there.
-template <int GROUP>
-struct OneRows {
-  static constexpr int kG = kOneBlock / GROUP;
-  static constexpr int kS = kG > 1 ? 2 : 1;  // groups whose sums this lane holds
-  const uint8_t* q;
+template <int GROUP, int P>
+struct Rows {
+  static constexpr int kG = kRowsBlock / GROUP;
+  static constexpr int kTok = 8 / kG;         // tokens of an MMA
+  static constexpr int kS = kG > 1 ? 2 : 1;   // groups whose sums a lane holds
+  static constexpr int kHeld = kG > 1 ? 1 : 2;  // tokens whose sums a lane holds, an MMA
+  const uint8_t* q;   // row g, this lane's place in the block fetched next
   const uint16_t* s;
-  int64_t q8, s8;
-  int n, cols, t;
-  bool mine;  // this lane's column of B takes x (of lane t's 32 columns)
-  uint4 w[kOneAhead][2];
-  uint16_t sc[kOneAhead][2][kS];
+  int64_t q8, s8;     // on to the second row
+  int n, cols, t, g;  // blocks, columns
+  uint4 w[kRowsAhead][2];
+  uint16_t sc[kRowsAhead][2][kS];
+  float sum[P][2][kHeld];
 
-  // Row g of the tile at column c0 (a multiple of 128), the second `second` rows on.
+  // Row g at `row`, the second `second` rows on, columns [c0, c1), c0 a multiple of 128.
   __device__ __forceinline__ void begin(const uint8_t* codes, const uint16_t* scales, int64_t row,
                                         int64_t second, int row_cols, int c0, int c1, int lane) {
     t = lane & 3;
-    const int g = lane >> 2;
-    mine = GROUP == 128 || t / (GROUP / 32) == g;
+    g = lane >> 2;
     cols = c1 - c0;
-    n = (cols + kOneBlock - 1) / kOneBlock;
+    n = (cols + kRowsBlock - 1) / kRowsBlock;
     q = codes + row * (row_cols / 2) + c0 / 2 + 16 * t;
-    s = scales + row * (row_cols / GROUP) + c0 / GROUP + 2 * t;
-    if (kG == 1) s -= 2 * t;
+    s = scales + row * (row_cols / GROUP) + c0 / GROUP + first_group();
     q8 = second * (row_cols / 2);
     s8 = second * (row_cols / GROUP);
 #pragma unroll
-    for (int d = 0; d < kOneAhead; ++d) fetch(d, d);
+    for (int i = 0; i < P; ++i)
+#pragma unroll
+      for (int j = 0; j < kHeld; ++j) sum[i][0][j] = sum[i][1][j] = 0.0f;
+#pragma unroll
+    for (int d = 0; d < kRowsAhead; ++d) fetch(d, d, d);
   }
-  // Block b (b - d ahead of q) into place d.
-  __device__ __forceinline__ void fetch(int d, int b, int at = -1) {
-    if (at < 0) at = b;
+  // the first group of a block whose sums this lane holds
+  __device__ __forceinline__ int first_group() const { return kG == 4 ? 2 * (t & 1) : 0; }
+  // Block `at`, b blocks from q on, into place d.
+  __device__ __forceinline__ void fetch(int d, int b, int at) {
     if (at >= n) return;
-    const int left = cols - at * kOneBlock;
+    const int left = cols - at * kRowsBlock;
     if (GROUP == 128 || 32 * t < left) {
-      w[d][0] = ld_codes(q + b * (kOneBlock / 2));
-      w[d][1] = ld_codes(q + q8 + b * (kOneBlock / 2));
+      w[d][0] = ld_codes(q + b * (kRowsBlock / 2));
+      w[d][1] = ld_codes(q + q8 + b * (kRowsBlock / 2));
     }
 #pragma unroll
     for (int j = 0; j < kS; ++j) {
-      const bool there = kG == 1 || (2 * t + j < kG && (2 * t + j) * GROUP < left);
+      const bool there = kG == 1 || (first_group() + j) * GROUP < left;
       sc[d][0][j] = there ? __ldg(s + b * kG + j) : (uint16_t)0;
       sc[d][1][j] = there ? __ldg(s + s8 + b * kG + j) : (uint16_t)0;
     }
   }
-  // x: this lane's place in the laid-out columns from c0 on (lay_out)
-  __device__ __forceinline__ void run(uint32_t x, float& sum0, float& sum1) {
+  // x: the laid-out columns from c0 on of the first token, `stride` bytes on to the
+  // next; `tokens` of them (columns without a token take another's, and their sums are
+  // not used).
+  __device__ __forceinline__ void run(uint32_t x, uint32_t stride, int tokens) {
+    const bool mine = kG == 1 || t / (GROUP / 32) == g % kG;  // this lane's column takes x of its columns
+    const int live = P == 1 ? 1 : (tokens + kTok - 1) / kTok;
+    uint32_t xp[P];
+#pragma unroll
+    for (int i = 0; i < P; ++i) xp[i] = x + (uint32_t)min(g / kG + i * kTok, tokens - 1) * stride + (uint32_t)t * 16u;
     uint4 u[4];
 #pragma unroll
     for (int j = 0; j < 4; ++j) u[j] = make_uint4(0u, 0u, 0u, 0u);
-    for (int b = 0; b < n; b += kOneAhead) {
+    for (int b = 0; b < n; b += kRowsAhead) {
 #pragma unroll
-      for (int d = 0; d < kOneAhead; ++d) {
+      for (int d = 0; d < kRowsAhead; ++d) {
         if (b + d >= n) break;
-        float p[4];
+        float p[P][4];
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-          // lanes whose column takes no x keep their zeros
-          asm volatile(
-              "{\n .reg .pred p;\n setp.ne.b32 p, %5, 0;\n"
-              " @p ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];\n}"
-              : "+r"(u[j].x), "+r"(u[j].y), "+r"(u[j].z), "+r"(u[j].w)
-              : "r"(x + (uint32_t)(d * 256 + j * 64)), "r"((int)mine)
-              : "memory");
           uint32_t a0[4], a1[4];
           open_codes(j == 0 ? w[d][0].x : j == 1 ? w[d][0].y : j == 2 ? w[d][0].z : w[d][0].w, a0);
           open_codes(j == 0 ? w[d][1].x : j == 1 ? w[d][1].y : j == 2 ? w[d][1].z : w[d][1].w, a1);
-          if (j == 0) mma16816<true>(p, a0[0], a1[0], a0[1], a1[1], u[j].x, u[j].y);
-          else mma16816<false>(p, a0[0], a1[0], a0[1], a1[1], u[j].x, u[j].y);
-          mma16816<false>(p, a0[2], a1[2], a0[3], a1[3], u[j].z, u[j].w);
-        }
-        // columns 2t and 2t + 1 are this lane's; with one group only column 0 counts
 #pragma unroll
-        for (int j = 0; j < kS; ++j) {
-          if (kG > 1 && 2 * t + j >= kG) continue;
-          sum0 = fmaf(bf(sc[d][0][j]), p[j], sum0);
-          sum1 = fmaf(bf(sc[d][1][j]), p[2 + j], sum1);
+          for (int i = 0; i < P; ++i) {
+            if (i > 0 && i >= live) break;
+            // lanes whose column takes no x keep their zeros
+            asm volatile(
+                "{\n .reg .pred p;\n setp.ne.b32 p, %5, 0;\n"
+                " @p ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];\n}"
+                : "+r"(u[j].x), "+r"(u[j].y), "+r"(u[j].z), "+r"(u[j].w)
+                : "r"(xp[i] + (uint32_t)(d * 256 + j * 64)), "r"((int)mine)
+                : "memory");
+            if (j == 0) mma16816<true>(p[i], a0[0], a1[0], a0[1], a1[1], u[j].x, u[j].y);
+            else mma16816<false>(p[i], a0[0], a1[0], a0[1], a1[1], u[j].x, u[j].y);
+            mma16816<false>(p[i], a0[2], a1[2], a0[3], a1[3], u[j].z, u[j].w);
+          }
         }
-        fetch(d, d + kOneAhead, b + d + kOneAhead);
+        // columns 2t and 2t + 1 are this lane's: two tokens, or two groups of one
+#pragma unroll
+        for (int i = 0; i < P; ++i) {
+          if (i > 0 && i >= live) break;
+#pragma unroll
+          for (int r = 0; r < 2; ++r)
+#pragma unroll
+            for (int j = 0; j < 2; ++j)
+              sum[i][r][kG == 1 ? j : 0] =
+                  fmaf(bf(sc[d][r][kG == 1 ? 0 : j]), p[i][2 * r + j], sum[i][r][kG == 1 ? j : 0]);
+        }
+        fetch(d, d + kRowsAhead, b + d + kRowsAhead);
       }
-      q += kOneAhead * (kOneBlock / 2);
-      s += kOneAhead * kG;
-      x += kOneAhead * 256;
+      q += kRowsAhead * (kRowsBlock / 2);
+      s += kRowsAhead * kG;
+#pragma unroll
+      for (int i = 0; i < P; ++i) xp[i] += kRowsAhead * 256;
     }
+    if (kG == 4)  // two lanes hold the four groups of a token
+#pragma unroll
+      for (int i = 0; i < P; ++i)
+#pragma unroll
+        for (int r = 0; r < 2; ++r) sum[i][r][0] += __shfl_xor_sync(0xFFFFFFFFu, sum[i][r][0], 1);
   }
-  // The sums of the quad's lanes, in lane t = 0.
-  static __device__ __forceinline__ float join(float v, int t) {
-    if (kG == 1) return v;
-    v = kG == 2 && t > 0 ? 0.0f : v;
-    return v + __shfl_xor_sync(0xFFFFFFFFu, v, 1);
+  // Where the sums go: to(row of the tile, token, value), for the tokens below n.
+  template <class F>
+  __device__ __forceinline__ void give(int tokens, F to) const {
+#pragma unroll
+    for (int i = 0; i < P; ++i)
+#pragma unroll
+      for (int j = 0; j < kHeld; ++j) {
+        const int tok = i * kTok + (kG == 1 ? 2 * t + j : kG == 2 ? t : t >> 1);
+        if (tok >= tokens || (kG == 4 && (t & 1))) continue;
+        to(g, tok, sum[i][0][j]);
+        to(g + 8, tok, sum[i][1][j]);
+      }
   }
 };
 
@@ -697,7 +472,7 @@ struct OneRows {
 // order of open_codes; zeros to the end of the last block. By one warp.
 template <bool PERMUTED>
 __device__ __forceinline__ void lay_out(uint32_t to, const uint16_t* x, int c0, int c1, int lane) {
-  for (int c = c0 / 8 + lane; c < (c1 + kOneBlock - 1) / kOneBlock * (kOneBlock / 8); c += 32) {
+  for (int c = c0 / 8 + lane; c < (c1 + kRowsBlock - 1) / kRowsBlock * (kRowsBlock / 8); c += 32) {
     uint4 v = make_uint4(0u, 0u, 0u, 0u);
     if (c * 8 < c1) v = __ldcg(reinterpret_cast<const uint4*>(x) + c);
     const uint32_t at = to + (uint32_t)(((c & ~15) + (c & 3) * 4 + ((c & 15) >> 2)) * 16 - c0 * 2);
@@ -722,21 +497,15 @@ __global__ void __launch_bounds__(kOneWarps * 32, 6)
   __shared__ float part[kOneWarps][16];
   griddep_wait();
   griddep_launch_dependents();
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2;
   const int r0 = blockIdx.x * 16, row = min(r0 + g, rows - 1);
   const int c0 = share(warp, kOneWarps, cols), c1 = share(warp + 1, kOneWarps, cols);
-  OneRows<GROUP> o;
+  Rows<GROUP, 1> o;
   o.begin(q, scale, row, min(8, rows - 1 - row), cols, c0, c1, lane);
   const uint32_t xs = smem_u32(dynamic) + (uint32_t)c0 * 2;
   lay_out<false>(xs, x, c0, c1, lane);
-  float lo = 0.0f, hi = 0.0f;
-  o.run(xs + (uint32_t)t * 16, lo, hi);
-  lo = OneRows<GROUP>::join(lo, t);
-  hi = OneRows<GROUP>::join(hi, t);
-  if (t == 0) {
-    part[warp][g] = lo;
-    part[warp][g + 8] = hi;
-  }
+  o.run(xs, 0, 1);
+  o.give(1, [&](int r, int, float v) { part[warp][r] = v; });
   __syncthreads();
   if (threadIdx.x < 16 && r0 + (int)threadIdx.x < rows) {
     float v = 0.0f;
@@ -770,23 +539,17 @@ __global__ void __launch_bounds__(kOneWarps * 32, 6) w4_fc1_one_kernel(const W4A
   __shared__ float part[kOneWarps][16];
   griddep_wait();
   griddep_launch_dependents();
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2;
   const int e = __shfl_sync(0xFFFFFFFFu, one_route(a, lane, nullptr), blockIdx.y);
   if (e < 0) return;
   const int i0 = blockIdx.x * 8;
   const int c0 = share(warp, kOneWarps, a.H), c1 = share(warp + 1, kOneWarps, a.H);
-  OneRows<GROUP> o;
+  Rows<GROUP, 1> o;
   o.begin(a.w13, a.w13_scale, (int64_t)e * 2 * a.I + i0 + g, a.I, a.H, c0, c1, lane);
   const uint32_t xs = smem_u32(dynamic) + (uint32_t)c0 * 2;
   lay_out<false>(xs, a.x, c0, c1, lane);
-  float lo = 0.0f, hi = 0.0f;
-  o.run(xs + (uint32_t)t * 16, lo, hi);
-  lo = OneRows<GROUP>::join(lo, t);
-  hi = OneRows<GROUP>::join(hi, t);
-  if (t == 0) {
-    part[warp][g] = lo;
-    part[warp][g + 8] = hi;
-  }
+  o.run(xs, 0, 1);
+  o.give(1, [&](int r, int, float v) { part[warp][r] = v; });
   __syncthreads();
   if (threadIdx.x < 8) {
     float gate = 0.0f, up = 0.0f;
@@ -812,7 +575,7 @@ __global__ void __launch_bounds__(kThreads, 3) w4_fc2_one_kernel(const W4Args a)
   float p_lane;
   const int e_lane = one_route(a, lane, &p_lane);
   uint32_t routes = __ballot_sync(0xFFFFFFFFu, e_lane >= 0);
-  const int r0 = blockIdx.x * 16, per = (a.I + kOneBlock - 1) / kOneBlock;
+  const int r0 = blockIdx.x * 16, per = (a.I + kRowsBlock - 1) / kRowsBlock;
   const int total = __popc(routes) * per;
   int at = warp * total / kWarps;
   const int end = (warp + 1) * total / kWarps;
@@ -823,24 +586,21 @@ __global__ void __launch_bounds__(kThreads, 3) w4_fc2_one_kernel(const W4Args a)
     const int r = __ffs(routes) - 1, b0 = at % per, b1 = min(per, b0 + end - at);
     const int e = __shfl_sync(0xFFFFFFFFu, e_lane, r);
     const float p = __shfl_sync(0xFFFFFFFFu, p_lane, r);
-    const int c0 = b0 * kOneBlock, c1 = min(a.I, b1 * kOneBlock);
-    OneRows<GROUP> o;
+    const int c0 = b0 * kRowsBlock, c1 = min(a.I, b1 * kRowsBlock);
+    Rows<GROUP, 1> o;
     o.begin(a.w2, a.w2_scale, (int64_t)e * a.H + r0 + g, 8, a.I, c0, c1, lane);
     if (!waited) griddep_wait();
     waited = true;
     const uint32_t hs = smem_u32(dynamic) + (uint32_t)(r * per + b0) * 256u;
     lay_out<true>(hs, a.h + (size_t)r * a.I, c0, c1, lane);
-    float lo_e = 0.0f, hi_e = 0.0f;
-    o.run(hs + (uint32_t)t * 16, lo_e, hi_e);
-    lo = fmaf(p, lo_e, lo);
-    hi = fmaf(p, hi_e, hi);
+    o.run(hs, 0, 1);
+    lo = fmaf(p, o.sum[0][0][0], lo);  // of the token in lane t = 0
+    hi = fmaf(p, o.sum[0][1][0], hi);
     at += b1 - b0;
     routes &= routes - 1;
   }
   if (!waited) griddep_wait();
   griddep_launch_dependents();
-  lo = OneRows<GROUP>::join(lo, t);
-  hi = OneRows<GROUP>::join(hi, t);
   if (t == 0) {
     part[warp][g] = lo;
     part[warp][g + 8] = hi;
@@ -853,6 +613,173 @@ __global__ void __launch_bounds__(kThreads, 3) w4_fc2_one_kernel(const W4Args a)
     for (int w = 0; w < kWarps; ++w) v += part[w][threadIdx.x];
     a.y[c] = to_bf(v);
   }
+}
+
+// ------------------------------------------------------------------ several tokens
+// What the grouping kernel leaves in the workspace: pieces of at most `most` routes
+// of one expert, experts ascending, routes in their order. A route without an
+// expert (an id outside 0..E-1), or to an expert that its token has named before,
+// is in none.
+constexpr int kMaxPieces = kMaxExperts + kMaxRoutes;
+struct W4Groups {
+  int32_t pieces;
+  int32_t expert[kMaxPieces], first[kMaxPieces], count[kMaxPieces];  // first: its place in `order`
+  int32_t order[kMaxRoutes];  // routes, sorted by expert
+  int32_t used[kMaxRoutes];   // of each route: whether it is in a piece
+  float prob[kMaxRoutes];     // the token's whole probability of the route's expert
+};
+
+__global__ void __launch_bounds__(kMaxExperts) w4_group_kernel(const int32_t* ids, const float* probs,
+                                                               int R, int K, int E, int most, W4Groups* G) {
+  __shared__ int16_t id[kMaxRoutes], rank[kMaxRoutes];
+  __shared__ int routes[kMaxExperts], scan[2][kMaxExperts / 32];
+  griddep_wait();
+  griddep_launch_dependents();
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, tid = threadIdx.x;
+  routes[tid] = 0;
+  for (int i = tid; i < R; i += kMaxExperts) {
+    const int r0 = i / K * K;
+    int e = ids[i];
+    if (e < 0 || e >= E) e = -1;
+    float p = e >= 0 ? probs[i] : 0.0f;
+    for (int r = r0; r < r0 + K && e >= 0; ++r) {
+      if (r == i || ids[r] != e) continue;
+      if (r < i) e = -1;
+      else p += probs[r];
+    }
+    id[i] = (int16_t)e;
+    G->used[i] = e >= 0;
+    G->prob[i] = p;
+  }
+  __syncthreads();
+  if (warp == 0) {  // 32 routes at a time, in order: each gets its rank within its expert
+    for (int i0 = 0; i0 < R; i0 += 32) {
+      const int i = i0 + lane;
+      const int e = i < R ? id[i] : -1;
+      const uint32_t same = __match_any_sync(0xFFFFFFFFu, e);
+      const int before = __popc(same & ((1u << lane) - 1u));
+      const int from = e >= 0 ? routes[e] : 0;
+      __syncwarp();
+      if (e >= 0 && before == 0) routes[e] = from + __popc(same);
+      if (i < R) rank[i] = (int16_t)(from + before);
+      __syncwarp();
+    }
+  }
+  __syncthreads();
+  // exclusive sums over the experts of their routes and of their pieces
+  const int n = routes[tid], np = (n + most - 1) / most;
+  int sn = n, sp = np;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int vn = __shfl_up_sync(0xFFFFFFFFu, sn, o), vp = __shfl_up_sync(0xFFFFFFFFu, sp, o);
+    if (lane >= o) {
+      sn += vn;
+      sp += vp;
+    }
+  }
+  if (lane == 31) {
+    scan[0][warp] = sn;
+    scan[1][warp] = sp;
+  }
+  __syncthreads();
+  int on = sn - n, op = sp - np;
+  for (int w = 0; w < warp; ++w) {
+    on += scan[0][w];
+    op += scan[1][w];
+  }
+  routes[tid] = on;  // now: where the expert's routes begin
+  for (int j = 0; j < np; ++j) {
+    G->expert[op + j] = tid;
+    G->first[op + j] = on + j * most;
+    G->count[op + j] = min(most, n - j * most);
+  }
+  if (tid == kMaxExperts - 1) G->pieces = op + np;
+  __syncthreads();
+  for (int i = tid; i < R; i += kMaxExperts)
+    if (id[i] >= 0) G->order[routes[id[i]] + rank[i]] = i;
+}
+
+// Block (rows, piece): kWarps / S tiles of 16 rows, S warps a tile, which split its
+// columns. Gated: 8 features a tile, rows g their gate rows, rows g + 8 their up
+// rows; h of each route, in the order of open_codes. Else 16 columns of the output
+// a tile; each route's products, times its probability, in fp32.
+template <bool GATED, int GROUP, int P>
+__global__ void __launch_bounds__(kThreads, P == 1 ? 3 : 2)
+    w4_piece_kernel(const W4Args a, const W4Groups* G, float* o, const int S, const uint32_t stride) {
+  using R = Rows<GROUP, P>;
+  constexpr int kMost = R::kTok * P;
+  extern __shared__ __align__(16) uint8_t dynamic[];
+  __shared__ float part[kWarps][16][kMost];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2;
+  const int cols = GATED ? a.H : a.I, rows = GATED ? a.I : a.H, step = GATED ? 8 : 16;
+  // The second product's piece and weights were there before the first one began
+  // (its kernel started after the grouping's had finished): only h has to wait.
+  if (GATED) griddep_wait();
+  griddep_launch_dependents();
+  const int piece = blockIdx.y;
+  if (piece >= __ldcg(&G->pieces)) {
+    if (!GATED) griddep_wait();
+    return;
+  }
+  const int e = __ldcg(&G->expert[piece]), first = __ldcg(&G->first[piece]), n = __ldcg(&G->count[piece]);
+  const int row0 = (blockIdx.x * (kWarps / S) + warp / S) * step, member = warp % S;
+  const int c0 = share(member, S, cols), c1 = row0 < rows ? share(member + 1, S, cols) : c0;
+  R r;
+  r.begin(GATED ? a.w13 : a.w2, GATED ? a.w13_scale : a.w2_scale,
+          GATED ? (int64_t)e * 2 * a.I + row0 + g : (int64_t)e * a.H + row0 + g, GATED ? a.I : 8, cols, c0, c1,
+          lane);
+  if (!GATED) griddep_wait();
+  // the piece's tokens (second product: their h), a warp a token at a time
+  for (int k = warp; k < n; k += kWarps) {
+    const int route = __ldcg(&G->order[first + k]);
+    const uint16_t* x = GATED ? a.x + (size_t)(route / a.K) * cols : a.h + (size_t)route * cols;
+    lay_out<!GATED>(smem_u32(dynamic) + (uint32_t)k * stride, x, 0, cols, lane);
+  }
+  __syncthreads();
+  r.run(smem_u32(dynamic) + (uint32_t)c0 * 2u, stride, n);
+  r.give(n, [&](int row, int tok, float v) { part[warp][row][tok] = v; });
+  __syncthreads();
+  const int per = kWarps / S * step;  // rows of the block
+  for (int i = threadIdx.x; i < per * n; i += kThreads) {
+    const int at = i % per, tok = i / per, row = blockIdx.x * per + at;
+    if (row >= rows) continue;
+    const int route = __ldcg(&G->order[first + tok]), w0 = at / step * S, in = at % step;
+    float v = 0.0f, u = 0.0f;
+    for (int w = w0; w < w0 + S; ++w) {
+      v += part[w][in][tok];
+      if (GATED) u += part[w][8 + in][tok];
+    }
+    if (GATED)
+      a.h[(size_t)route * a.I + permuted(row)] = to_bf((a.activation ? act_fwd<1>(v) : act_fwd<0>(v)) * u);
+    else
+      o[(size_t)route * a.H + row] = __ldcg(&G->prob[route]) * v;
+  }
+}
+
+// y[t] = add[t] + the products of t's routes, in their order: four columns a thread.
+__global__ void __launch_bounds__(256) w4_sum_kernel(const W4Args a, const W4Groups* G, const float* o) {
+  griddep_wait();
+  griddep_launch_dependents();
+  const int c = (blockIdx.x * 256 + threadIdx.x) * 4, t = blockIdx.y;
+  if (c >= a.H) return;
+  const size_t at = (size_t)t * a.H + c;
+  float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+  if (a.add) {
+    const uint2 b = *reinterpret_cast<const uint2*>(a.add + at);
+    v = make_float4(__uint_as_float(b.x << 16), __uint_as_float(b.x & 0xFFFF0000u), __uint_as_float(b.y << 16),
+                    __uint_as_float(b.y & 0xFFFF0000u));
+  }
+  for (int k = 0; k < a.K; ++k) {
+    const int r = t * a.K + k;
+    if (!G->used[r]) continue;
+    const float4 b = *reinterpret_cast<const float4*>(o + (size_t)r * a.H + c);
+    v.x += b.x;
+    v.y += b.y;
+    v.z += b.z;
+    v.w += b.w;
+  }
+  *reinterpret_cast<uint2*>(a.y + at) =
+      make_uint2((uint32_t)to_bf(v.x) | ((uint32_t)to_bf(v.y) << 16), (uint32_t)to_bf(v.z) | ((uint32_t)to_bf(v.w) << 16));
 }
 
 // One warp per group of a row: scale = bf16(max|w| / 7) (1 for a group of
@@ -924,69 +851,78 @@ cudaError_t matvec(const uint16_t* x, const uint8_t* q, const uint16_t* scale, i
                        : matvec<32, TOK>(x, q, scale, N, rows, cols, y, s);
 }
 
-// Warps that share a unit's columns: the count (1, 2, 4, 8) with the fewest
-// blocks on the longest warp, as long as each keeps four blocks of a unit.
-int split_of(int64_t units, int64_t warps, int blocks) {
-  int best = 1;
-  double least = 0;
-  for (int S = 1; S <= 8; S *= 2) {
-    if (S > 1 && blocks / S < 4) break;
-    const int64_t teams = warps / S;
-    const double rounds = (double)((units + teams - 1) / teams) / S;
-    if (S == 1 || rounds < 0.98 * least) {
-      best = S;
-      least = rounds;
-    }
-  }
-  return best;
+// Several tokens. Routes of a piece: what x leaves room for in a third of an SM's
+// shared memory, at most 8. Warps a row tile: more where the blocks would not fill
+// the SMs twice.
+constexpr size_t kPieceBytes = 64 << 10;
+
+struct W4Layout {
+  size_t groups, o, h, total;
+};
+
+W4Layout w4_layout(int N, int K, int H, int I) {
+  W4Layout L{};
+  const size_t R = (size_t)N * K;
+  L.h = (sizeof(W4Groups) + 255) / 256 * 256;
+  L.o = L.h + (R * I * 2 + 255) / 256 * 256;
+  L.total = L.o + (R * H * 4 + 255) / 256 * 256;
+  return L;
 }
 
-template <int GROUP, int TOK>
-cudaError_t fc1(const W4Args& a, cudaStream_t s) {
-  using St = Stream<GROUP, TOK>;
-  static DeviceOnce once, count;
-  constexpr int kBlocks = 2;  // an SM
-  constexpr size_t smem = kWarps * St::kBytes + 128;
+template <bool GATED, int GROUP, int P>
+cudaError_t piece(const W4Args& a, const W4Groups* G, float* o, int most, int pieces, int sms, cudaStream_t s) {
+  static DeviceOnce once;
+  const int cols = GATED ? a.H : a.I, rows = GATED ? a.I / 8 : a.H / 16;
+  // 64 bytes over a multiple of 128: two tokens' words in different banks
+  const uint32_t stride = (uint32_t)((cols + 127) / 128 * 256 + 64);
+  int S = 1;
+  while (S < 8 && (int64_t)((rows + 8 / S - 1) / (8 / S)) * pieces < 4 * (int64_t)sms && cols / 128 >= 8 * S) S *= 2;
+  return launch_ring(once, w4_piece_kernel<GATED, GROUP, P>, kPieceBytes + 1024,
+                     dim3((rows + 8 / S - 1) / (8 / S), pieces), dim3(kThreads), (size_t)most * stride, s, a, G, o, S,
+                     stride);
+}
+
+template <bool GATED, int GROUP>
+cudaError_t piece(const W4Args& a, const W4Groups* G, float* o, int most, int pieces, int sms, cudaStream_t s) {
+  constexpr int kTok = 8 / (128 / GROUP);
+  if (most <= kTok) return piece<GATED, GROUP, 1>(a, G, o, most, pieces, sms, s);
+  if constexpr (kTok < 4)
+    if (most > 2 * kTok) return piece<GATED, GROUP, 4>(a, G, o, most, pieces, sms, s);
+  if constexpr (kTok < 8) return piece<GATED, GROUP, 2>(a, G, o, most, pieces, sms, s);
+  return cudaErrorInvalidValue;
+}
+
+template <bool GATED>
+cudaError_t piece(const W4Args& a, const W4Groups* G, float* o, int most, int pieces, int sms, cudaStream_t s) {
+  return a.group == 128  ? piece<GATED, 128>(a, G, o, most, pieces, sms, s)
+         : a.group == 64 ? piece<GATED, 64>(a, G, o, most, pieces, sms, s)
+                         : piece<GATED, 32>(a, G, o, most, pieces, sms, s);
+}
+
+cudaError_t ffn_many(const W4Args& a, cudaStream_t s) {
+  static DeviceOnce count;
   int sms = 0;
-  const cudaError_t err = once_per_device(count, &sms, [](int dev, int* v) {
+  cudaError_t err = once_per_device(count, &sms, [](int dev, int* v) {
     return cudaDeviceGetAttribute(v, cudaDevAttrMultiProcessorCount, dev);
   });
   if (err != cudaSuccess) return err;
-  const int64_t routes = (int64_t)a.N * a.K;
-  const int S = split_of((routes < a.E ? routes : a.E) * (a.I / 8), (int64_t)kBlocks * sms * kWarps,
-                         a.H / St::kCols);
-  return launch_ring(once, w4_fc1_kernel<GROUP, TOK>, smem, dim3(kBlocks * sms), dim3(kThreads), smem, s, a, S);
-}
-
-template <int TOK>
-cudaError_t fc1(const W4Args& a, cudaStream_t s) {
-  return a.group == 128 ? fc1<128, TOK>(a, s) : a.group == 64 ? fc1<64, TOK>(a, s) : fc1<32, TOK>(a, s);
-}
-
-template <int GROUP, int TOK, int W>
-cudaError_t fc2(const W4Args& a, cudaStream_t s) {
-  using St = Stream<GROUP, TOK>;
-  static DeviceOnce once;
-  const int tokens = a.N < kChunk ? a.N : kChunk;
-  const int items = a.E < tokens * a.K ? a.E : tokens * a.K;
-  const dim3 grid(a.H / 16, (a.N + kChunk - 1) / kChunk);
-  constexpr size_t ring = W * St::kBytes + 128;
-  const size_t smem = ring + (size_t)tokens * (W * 16 + a.K) * 4;
-  constexpr size_t most = ring + (size_t)kChunk * (W * 16 + kMaxTopK) * 4;
-  const int S = items * 8 <= W ? 8 : items * 4 <= W ? 4 : items * 2 <= W ? 2 : 1;
-  return launch_ring(once, w4_fc2_kernel<GROUP, TOK, W>, most, grid, dim3(W * 32), smem, s, a, S);
-}
-
-template <int GROUP, int TOK>
-cudaError_t fc2(const W4Args& a, cudaStream_t s) {
-  // narrow outputs have fewer blocks than SMs to fill: more warps each
-  return (int64_t)(a.H / 16) * ((a.N + kChunk - 1) / kChunk) <= 256 ? fc2<GROUP, TOK, 16>(a, s)
-                                                                    : fc2<GROUP, TOK, 8>(a, s);
-}
-
-template <int TOK>
-cudaError_t fc2(const W4Args& a, cudaStream_t s) {
-  return a.group == 128 ? fc2<128, TOK>(a, s) : a.group == 64 ? fc2<64, TOK>(a, s) : fc2<32, TOK>(a, s);
+  const int wide = a.H > a.I ? a.H : a.I, R = a.N * a.K;
+  int most = (int)(kPieceBytes / ((size_t)(wide + 127) / 128 * 256 + 64));
+  if (most > 8) most = 8;
+  if (most > a.N) most = a.N;
+  // pieces there may be: one more for every `most` routes beyond an expert's first
+  const int experts = R < a.E ? R : a.E, pieces = experts + (R - experts) / most;
+  const W4Layout L = w4_layout(a.N, a.K, a.H, a.I);
+  uint8_t* ws = a.ws;
+  W4Groups* G = reinterpret_cast<W4Groups*>(ws);
+  float* o = reinterpret_cast<float*>(ws + L.o);
+  err = launch_pdl(w4_group_kernel, dim3(1), dim3(kMaxExperts), 0, s, a.topk_ids, a.topk_p, R, a.K, a.E, most, G);
+  if (err != cudaSuccess) return err;
+  err = piece<true>(a, G, o, most, pieces, sms, s);
+  if (err != cudaSuccess) return err;
+  err = piece<false>(a, G, o, most, pieces, sms, s);
+  if (err != cudaSuccess) return err;
+  return launch_pdl(w4_sum_kernel, dim3((a.H + 1023) / 1024, a.N), dim3(256), 0, s, a, G, o);
 }
 
 // One token: x, or h of its routes, has to fit the block's shared memory next to
@@ -1024,18 +960,18 @@ int launch_w4_matvec(const uint16_t* x, const uint8_t* q, const uint16_t* scale,
   return err != cudaSuccess ? -(int)err : 1;
 }
 
-int launch_w4_ffn(const W4Args& a, cudaStream_t s) {
-  // routes an expert serves at once: by their mean number
+int64_t w4_workspace_bytes(int N, int K, int H, int I) { return (int64_t)w4_layout(N, K, H, I).total; }
+
+int launch_w4_ffn(const W4Args& args, cudaStream_t s) {
+  W4Args a = args;
+  a.h = reinterpret_cast<uint16_t*>(a.ws + w4_layout(a.N, a.K, a.H, a.I).h);
   cudaError_t err;
   if (a.N == 1 && (size_t)a.H * 2 <= kOneBytes && (size_t)a.K * ((a.I + 127) / 128) * 256 <= kOneBytes) {
     err = a.group == 128 ? ffn_one<128>(a, s) : a.group == 64 ? ffn_one<64>(a, s) : ffn_one<32>(a, s);
     return err != cudaSuccess ? -(int)err : 2;
   }
-  const bool few = a.N <= 8 || a.N * a.K <= 6 * a.E;
-  err = few ? fc1<8>(a, s) : fc1<16>(a, s);
-  if (err != cudaSuccess) return -(int)err;
-  err = few ? fc2<8>(a, s) : fc2<16>(a, s);
-  return err != cudaSuccess ? -(int)err : 2;
+  err = ffn_many(a, s);
+  return err != cudaSuccess ? -(int)err : 4;
 }
 
 int launch_w4_quantize(const uint16_t* m, int64_t rows, int cols, int group, uint8_t* q,
