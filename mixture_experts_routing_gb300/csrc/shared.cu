@@ -339,7 +339,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     // ------------------------------------------------------------ epilogue
     const int q = warp & 3, half = (warp - 2) >> 2, ew = warp - 2;
     const uint32_t buf0 = sbase + kStages * kStageBytes + (uint32_t)ew * kEpiBytes;
-    uint32_t tc = 0, adds[2] = {0, 0};  // adds: phases of this warp's add barriers so far
+    // adds: phases of this warp's add barriers so far; turn: which of its two boxes the
+    // next chunk uses (they alternate from tile to tile too: a store may still read the
+    // last one)
+    uint32_t tc = 0, adds[2] = {0, 0}, turn = 0;
     for (int t = pair; t < tiles; t += pairs, ++tc) {
       const Tile T = tile_of<EPI>(p, t);
       const Problem& P = p.pr[T.pr];
@@ -354,9 +357,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       const bool add = (EPI == kOut || EPI == kGrads) && P.has_add;
       auto load_add = [&](int c) {
         if (c < chunks && lane == 0) {
-          const uint32_t bar = smem_u32(&add_bar[ew][(c >> 1) & 1]);
+          const uint32_t box = (turn + (uint32_t)(c >> 1)) & 1u, bar = smem_u32(&add_bar[ew][box]);
           mbar_arrive_expect_tx(bar, 2048);
-          tma_load_2d_pair(buf0 + (uint32_t)((c >> 1) & 1) * 2048u, mx, T.n + 32 * c, row0, bar);
+          tma_load_2d_pair(buf0 + box * 2048u, mx, T.n + 32 * c, row0, bar);
         }
       };
       if (add && half < chunks) {  // under the tile's MMAs: the first two chunks of what is added
@@ -383,8 +386,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (!mbar_wait_cluster_warp(smem_u32(&tmem_full_bar[b]), bu & 1u, p.err, kErrWaitAccum)) break;
       tc_fence_after();
       for (int c = half; c < chunks; c += 2) {
-        const int col = T.n + 32 * c, odd = (c >> 1) & 1;
-        const uint32_t buf = buf0 + (uint32_t)odd * 2048u;
+        const int col = T.n + 32 * c;
+        const uint32_t odd = (turn + (uint32_t)(c >> 1)) & 1u, buf = buf0 + odd * 2048u;
         float v[32];
         tmem_row32(tl + 32u * (uint32_t)c, v);
         if (EPI == kGrads && P.f32) {
@@ -480,6 +483,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           store_box(&maps.o[1], buf0, col, row0, lane);
         }
       }
+      if (chunks > half) turn += (uint32_t)(chunks - half + 1) >> 1;
       tc_fence_before();
       __syncwarp();
       if (lane == 0) {
@@ -711,7 +715,10 @@ cudaError_t backward(const SharedArgs& a, cudaStream_t s) {
 }  // namespace
 
 int launch_shared_forward(const SharedArgs& a, cudaStream_t s) {
-  if (a.N <= 256) return launch_shared_forward_few(a, s);
+  // up to 512 tokens the pairs' tiles of 256 rows are too few to fill the SMs: 400
+  // tokens, 7168 x 2048: 55 us against 60; 2048 x 768: 19 against 23; from 700 on
+  // the pairs are faster on wide layers (71 against 97)
+  if (a.N <= 512) return launch_shared_forward_few(a, s);
   const cudaError_t err = a.activation ? forward<1>(a, s) : forward<0>(a, s);
   return err != cudaSuccess ? -(int)err : 2;
 }

@@ -346,14 +346,14 @@ template <int GROUP, int P>
 struct Rows {
   static constexpr int kG = kRowsBlock / GROUP;
   static constexpr int kTok = 8 / kG;         // tokens of an MMA
-  static constexpr int kS = kG > 1 ? 2 : 1;   // groups whose sums a lane holds
   static constexpr int kHeld = kG > 1 ? 1 : 2;  // tokens whose sums a lane holds, an MMA
   const uint8_t* q;   // row g, this lane's place in the block fetched next
   const uint16_t* s;
   int64_t q8, s8;     // on to the second row
   int n, cols, t, g;  // blocks, columns
   uint4 w[kRowsAhead][2];
-  uint16_t sc[kRowsAhead][2][kS];
+  uint32_t sc[kRowsAhead][2];  // the scales of this lane's one or two groups
+  bool pairs;  // rows of scales start at even places: two make an aligned word
   float sum[P][2][kHeld];
 
   // Row g at `row`, the second `second` rows on, columns [c0, c1), c0 a multiple of 128.
@@ -367,6 +367,7 @@ struct Rows {
     s = scales + row * (row_cols / GROUP) + c0 / GROUP + first_group();
     q8 = second * (row_cols / 2);
     s8 = second * (row_cols / GROUP);
+    pairs = row_cols / GROUP % 2 == 0;
 #pragma unroll
     for (int i = 0; i < P; ++i)
 #pragma unroll
@@ -384,11 +385,21 @@ struct Rows {
       w[d][0] = ld_codes(q + b * (kRowsBlock / 2));
       w[d][1] = ld_codes(q + q8 + b * (kRowsBlock / 2));
     }
-#pragma unroll
-    for (int j = 0; j < kS; ++j) {
-      const bool there = kG == 1 || (first_group() + j) * GROUP < left;
-      sc[d][0][j] = there ? __ldg(s + b * kG + j) : (uint16_t)0;
-      sc[d][1][j] = there ? __ldg(s + s8 + b * kG + j) : (uint16_t)0;
+    const uint16_t* s0 = s + b * kG;
+    if (kG == 1) {
+      sc[d][0] = __ldg(s0);
+      sc[d][1] = __ldg(s0 + s8);
+    } else if (first_group() * GROUP < left) {
+      if (pairs) {
+        sc[d][0] = __ldg(reinterpret_cast<const uint32_t*>(s0));
+        sc[d][1] = __ldg(reinterpret_cast<const uint32_t*>(s0 + s8));
+      } else {
+        const bool both = (first_group() + 1) * GROUP < left;
+        sc[d][0] = __ldg(s0) | (both ? (uint32_t)__ldg(s0 + 1) << 16 : 0u);
+        sc[d][1] = __ldg(s0 + s8) | (both ? (uint32_t)__ldg(s0 + s8 + 1) << 16 : 0u);
+      }
+    } else {
+      sc[d][0] = sc[d][1] = 0u;
     }
   }
   // x: the laid-out columns from c0 on of the first token, `stride` bytes on to the
@@ -437,7 +448,8 @@ struct Rows {
 #pragma unroll
             for (int j = 0; j < 2; ++j)
               sum[i][r][kG == 1 ? j : 0] =
-                  fmaf(bf(sc[d][r][kG == 1 ? 0 : j]), p[i][2 * r + j], sum[i][r][kG == 1 ? j : 0]);
+                  fmaf(__uint_as_float(kG == 1 || j == 0 ? sc[d][r] << 16 : sc[d][r] & 0xFFFF0000u), p[i][2 * r + j],
+                       sum[i][r][kG == 1 ? j : 0]);
         }
         fetch(d, d + kRowsAhead, b + d + kRowsAhead);
       }
@@ -631,19 +643,24 @@ struct W4Groups {
 
 __global__ void __launch_bounds__(kMaxExperts) w4_group_kernel(const int32_t* ids, const float* probs,
                                                                int R, int K, int E, int most, W4Groups* G) {
-  __shared__ int16_t id[kMaxRoutes], rank[kMaxRoutes];
+  __shared__ int16_t named[kMaxRoutes], id[kMaxRoutes], rank[kMaxRoutes];
   __shared__ int routes[kMaxExperts], scan[2][kMaxExperts / 32];
+  __shared__ int16_t of_warp[kWarps][kMaxExperts];  // routes of an expert in a warp's share, then before it
   griddep_wait();
   griddep_launch_dependents();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, tid = threadIdx.x;
-  routes[tid] = 0;
+  for (int w = 0; w < kWarps; ++w) of_warp[w][tid] = 0;
+  for (int i = tid; i < R; i += kMaxExperts) {
+    const int e = ids[i];
+    named[i] = (int16_t)(e < 0 || e >= E ? -1 : e);
+  }
+  __syncthreads();
   for (int i = tid; i < R; i += kMaxExperts) {
     const int r0 = i / K * K;
-    int e = ids[i];
-    if (e < 0 || e >= E) e = -1;
+    int e = named[i];
     float p = e >= 0 ? probs[i] : 0.0f;
     for (int r = r0; r < r0 + K && e >= 0; ++r) {
-      if (r == i || ids[r] != e) continue;
+      if (r == i || named[r] != e) continue;
       if (r < i) e = -1;
       else p += probs[r];
     }
@@ -652,22 +669,28 @@ __global__ void __launch_bounds__(kMaxExperts) w4_group_kernel(const int32_t* id
     G->prob[i] = p;
   }
   __syncthreads();
-  if (warp == 0) {  // 32 routes at a time, in order: each gets its rank within its expert
-    for (int i0 = 0; i0 < R; i0 += 32) {
-      const int i = i0 + lane;
-      const int e = i < R ? id[i] : -1;
-      const uint32_t same = __match_any_sync(0xFFFFFFFFu, e);
-      const int before = __popc(same & ((1u << lane) - 1u));
-      const int from = e >= 0 ? routes[e] : 0;
-      __syncwarp();
-      if (e >= 0 && before == 0) routes[e] = from + __popc(same);
-      if (i < R) rank[i] = (int16_t)(from + before);
-      __syncwarp();
-    }
+  // each warp ranks its share of the routes within their experts, 32 at a time, in order
+  const int part = ((R + kWarps - 1) / kWarps + 31) / 32 * 32, from = warp * part, to = min(R, from + part);
+  for (int i0 = from; i0 < to; i0 += 32) {
+    const int i = i0 + lane;
+    const int e = i < to ? id[i] : -1;
+    const uint32_t same = __match_any_sync(0xFFFFFFFFu, e);
+    const int before = __popc(same & ((1u << lane) - 1u));
+    const int had = e >= 0 ? of_warp[warp][e] : 0;
+    __syncwarp();
+    if (e >= 0 && before == 0) of_warp[warp][e] = (int16_t)(had + __popc(same));
+    if (i < to) rank[i] = (int16_t)(had + before);
+    __syncwarp();
   }
   __syncthreads();
+  int n = 0;
+  for (int w = 0; w < kWarps; ++w) {
+    const int v = of_warp[w][tid];
+    of_warp[w][tid] = (int16_t)n;
+    n += v;
+  }
   // exclusive sums over the experts of their routes and of their pieces
-  const int n = routes[tid], np = (n + most - 1) / most;
+  const int np = (n + most - 1) / most;
   int sn = n, sp = np;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
@@ -687,7 +710,7 @@ __global__ void __launch_bounds__(kMaxExperts) w4_group_kernel(const int32_t* id
     on += scan[0][w];
     op += scan[1][w];
   }
-  routes[tid] = on;  // now: where the expert's routes begin
+  routes[tid] = on;  // where the expert's routes begin
   for (int j = 0; j < np; ++j) {
     G->expert[op + j] = tid;
     G->first[op + j] = on + j * most;
@@ -696,7 +719,7 @@ __global__ void __launch_bounds__(kMaxExperts) w4_group_kernel(const int32_t* id
   if (tid == kMaxExperts - 1) G->pieces = op + np;
   __syncthreads();
   for (int i = tid; i < R; i += kMaxExperts)
-    if (id[i] >= 0) G->order[routes[id[i]] + rank[i]] = i;
+    if (id[i] >= 0) G->order[routes[id[i]] + of_warp[i / part][id[i]] + rank[i]] = i;
 }
 
 // Block (rows, piece): kWarps / S tiles of 16 rows, S warps a tile, which split its
@@ -908,10 +931,14 @@ cudaError_t ffn_many(const W4Args& a, cudaStream_t s) {
   if (err != cudaSuccess) return err;
   const int wide = a.H > a.I ? a.H : a.I, R = a.N * a.K;
   int most = (int)(kPieceBytes / ((size_t)(wide + 127) / 128 * 256 + 64));
+  const int experts = R < a.E ? R : a.E, one = 8 / (128 / a.group);  // routes of one MMA
+  // where experts have few routes each, pieces that one MMA takes: fewer registers,
+  // more blocks an SM
   if (most > 8) most = 8;
+  if (most > one && R <= experts * one / 2) most = one;
   if (most > a.N) most = a.N;
   // pieces there may be: one more for every `most` routes beyond an expert's first
-  const int experts = R < a.E ? R : a.E, pieces = experts + (R - experts) / most;
+  const int pieces = experts + (R - experts) / most;
   const W4Layout L = w4_layout(a.N, a.K, a.H, a.I);
   uint8_t* ws = a.ws;
   W4Groups* G = reinterpret_cast<W4Groups*>(ws);
