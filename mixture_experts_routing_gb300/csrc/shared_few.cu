@@ -29,6 +29,9 @@ constexpr int kThreads = 192;
 constexpr uint32_t kABytes = kBM * kBK * 2;
 constexpr int kMaxStages = 12;
 constexpr int kMaxTok = 128;  // of a tile
+// A ring of about 100 KB leaves room for a second block on the SM, of this kernel or of
+// the next, which fills its own while this one runs.
+constexpr uint32_t kRing = 104u << 10;
 
 struct FewParams {
   int N, M;          // tokens; output columns (gated: features)
@@ -71,7 +74,16 @@ __device__ __forceinline__ float4 sum_ranks(uint32_t at) {
   return a[0];
 }
 __device__ __forceinline__ float4 sum_ranks(uint32_t at, uint32_t S) {
-  return S == 8 ? sum_ranks<8>(at) : S == 4 ? sum_ranks<4>(at) : S == 2 ? sum_ranks<2>(at) : sum_ranks<1>(at);
+  switch (S) {
+    case 8: return sum_ranks<8>(at);
+    case 7: return sum_ranks<7>(at);
+    case 6: return sum_ranks<6>(at);
+    case 5: return sum_ranks<5>(at);
+    case 4: return sum_ranks<4>(at);
+    case 3: return sum_ranks<3>(at);
+    case 2: return sum_ranks<2>(at);
+    default: return sum_ranks<1>(at);
+  }
 }
 
 __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
@@ -261,6 +273,31 @@ __global__ void __launch_bounds__(kThreads)
   }
 }
 
+// Clusters of S CTAs of this kernel that run at once, once per device: two CTAs an SM
+// (the query counts one, since the kernel allocates tensor memory).
+template <bool GATED, int ACT>
+int max_clusters(int S, cudaError_t* err) {
+  static DeviceOnce once[9];
+  int n = 0;
+  *err = once_per_device(once[S], &n, [&](int, int* v) {
+    auto* k = shared_few_kernel<GATED, ACT>;
+    cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, kRing + 1024);
+    if (e != cudaSuccess) return e;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)S);
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = kRing + 1024;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = (unsigned)S;
+    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaOccupancyMaxActiveClusters(v, k, &cfg);
+  });
+  return *err == cudaSuccess ? 2 * n : 0;
+}
+
 template <bool GATED, int ACT>
 cudaError_t launch(const void* w, int64_t w_rows, const void* x, int K, FewParams p, cudaStream_t s) {
   p.m_tiles = (p.M + (GATED ? 63 : 127)) / (GATED ? 64 : 128);
@@ -274,23 +311,23 @@ cudaError_t launch(const void* w, int64_t w_rows, const void* x, int K, FewParam
   p.k_tiles = (K + kBK - 1) / kBK;
   p.tmem_cols = 32;
   while ((int)p.tmem_cols < p.n_tok) p.tmem_cols *= 2;
-  static DeviceOnce once;
-  int sms = 0;
-  cudaError_t err = once_per_device(once, &sms, [](int dev, int* v) {
-    cudaError_t e = cudaDeviceGetAttribute(v, cudaDevAttrMultiProcessorCount, dev);
-    if (e != cudaSuccess) return e;
-    return cudaFuncSetAttribute(shared_few_kernel<GATED, ACT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                110 << 10);
-  });
-  if (err != cudaSuccess) return err;
   const int tiles = p.m_tiles * n_tiles;
-  // a ring of about 100 KB leaves room for a second block on the SM, of this kernel
-  // or of the next, which fills its own while this one runs
+  // CTAs a tile: the most whose clusters all run at once, with three stages each at
+  // least (500 tokens, 4096 x 1408, gated: two 39 us, three 37, four 46: a second turn)
+  int S = 1;
+  for (int s2 = 2; s2 <= 8 && p.k_tiles >= 3 * s2; ++s2) {
+    cudaError_t err = cudaSuccess;
+    const int most = max_clusters<GATED, ACT>(s2, &err);
+    if (err != cudaSuccess) return err;
+    if (tiles <= most) S = s2;
+  }
+  if (S == 1) {  // the shared-memory opt-in
+    cudaError_t err = cudaSuccess;
+    max_clusters<GATED, ACT>(1, &err);
+    if (err != cudaSuccess) return err;
+  }
   const uint32_t stage = kABytes + (uint32_t)p.n_tok * 128u, sums = (uint32_t)p.n_tok * kBM * 4u;
-  const uint32_t budget = 104u << 10;
-  int S = 1;  // CTAs a tile: as many as fill the SMs twice, with four stages each at least
-  while (S < 8 && tiles * S * 2 <= 2 * sms && p.k_tiles >= 8 * S) S *= 2;
-  p.stages = (int)(budget / stage);
+  p.stages = (int)(kRing / stage);
   if (p.stages > kMaxStages) p.stages = kMaxStages;
   uint32_t bytes = (uint32_t)p.stages * stage;
   if (bytes < sums) bytes = sums;
