@@ -18,9 +18,9 @@
 // Experts, and one token's matvec (Rows): a lane loads 16 bytes of its two rows
 // straight into registers, four blocks of 128 columns ahead; x is laid out in shared
 // memory once per block of threads. Several tokens: one small kernel groups the
-// routes by expert, a block of the products takes some rows of one expert and its
-// routes (so an expert's weights are read once for all of them), and a last kernel
-// adds up each token's routes.
+// routes by expert, the blocks of the products share out the rows of the experts and
+// multiply each by all its routes, or 2 to 8 of them at a time (an expert's weights
+// come from HBM once), and a last kernel adds up each token's routes.
 // Several tokens' matvec (Stream): codes, scales and x come through each warp's own
 // ring of shared-memory stages.
 #include "act.cuh"
@@ -331,7 +331,7 @@ __global__ void __launch_bounds__(kThreads, 2)
 // tell them apart. Column c of B is token c / kG and takes x only at the columns of
 // the block's group c % kG (zeros elsewhere), so one MMA gives the sums of kG groups
 // for 8 / kG tokens side by side, and P of them those of P times as many.
-constexpr int kRowsAhead = 4;
+constexpr int kRowsAhead = 4;  // six: 4 to 5 % slower
 constexpr int kRowsBlock = 128;
 
 __device__ __forceinline__ uint4 ld_codes(const uint8_t* p) {
@@ -368,24 +368,20 @@ struct Rows {
     q8 = second * (row_cols / 2);
     s8 = second * (row_cols / GROUP);
     pairs = row_cols / GROUP % 2 == 0;
+    clear();
 #pragma unroll
-    for (int i = 0; i < P; ++i)
-#pragma unroll
-      for (int j = 0; j < kHeld; ++j) sum[i][0][j] = sum[i][1][j] = 0.0f;
-#pragma unroll
-    for (int d = 0; d < kRowsAhead; ++d) fetch(d, d, d);
+    for (int d = 0; d < kRowsAhead; ++d) fetch(d, q + d * (kRowsBlock / 2), s + d * kG, d);
   }
   // the first group of a block whose sums this lane holds
   __device__ __forceinline__ int first_group() const { return kG == 4 ? 2 * (t & 1) : 0; }
-  // Block `at`, b blocks from q on, into place d.
-  __device__ __forceinline__ void fetch(int d, int b, int at) {
+  // Block `at` of a tile, its codes and scales at qa and s0, into place d.
+  __device__ __forceinline__ void fetch(int d, const uint8_t* qa, const uint16_t* s0, int at) {
     if (at >= n) return;
     const int left = cols - at * kRowsBlock;
     if (GROUP == 128 || 32 * t < left) {
-      w[d][0] = ld_codes(q + b * (kRowsBlock / 2));
-      w[d][1] = ld_codes(q + q8 + b * (kRowsBlock / 2));
+      w[d][0] = ld_codes(qa);
+      w[d][1] = ld_codes(qa + q8);
     }
-    const uint16_t* s0 = s + b * kG;
     if (kG == 1) {
       sc[d][0] = __ldg(s0);
       sc[d][1] = __ldg(s0 + s8);
@@ -404,8 +400,11 @@ struct Rows {
   }
   // x: the laid-out columns from c0 on of the first token, `stride` bytes on to the
   // next; `tokens` of them (columns without a token take another's, and their sums are
-  // not used).
-  __device__ __forceinline__ void run(uint32_t x, uint32_t stride, int tokens) {
+  // not used). STREAM: with `more`, another tile follows, `next` rows on: a place that
+  // this tile is through with takes that one's block.
+  template <bool STREAM = false>
+  __device__ __forceinline__ void run(uint32_t x, uint32_t stride, int tokens, bool more = false, int next = 0,
+                                      int row_cols = 0) {
     const bool mine = kG == 1 || t / (GROUP / 32) == g % kG;  // this lane's column takes x of its columns
     const int live = P == 1 ? 1 : (tokens + kTok - 1) / kTok;
     uint32_t xp[P];
@@ -414,6 +413,8 @@ struct Rows {
     uint4 u[4];
 #pragma unroll
     for (int j = 0; j < 4; ++j) u[j] = make_uint4(0u, 0u, 0u, 0u);
+    const uint8_t* qn = q + (int64_t)next * (row_cols / 2);
+    const uint16_t* sn = s + (int64_t)next * (row_cols / GROUP);
     for (int b = 0; b < n; b += kRowsAhead) {
 #pragma unroll
       for (int d = 0; d < kRowsAhead; ++d) {
@@ -451,12 +452,22 @@ struct Rows {
                   fmaf(__uint_as_float(kG == 1 || j == 0 ? sc[d][r] << 16 : sc[d][r] & 0xFFFF0000u), p[i][2 * r + j],
                        sum[i][r][kG == 1 ? j : 0]);
         }
-        fetch(d, d + kRowsAhead, b + d + kRowsAhead);
+        if constexpr (STREAM) {
+          const bool here = b + d + kRowsAhead < n;
+          fetch(d, (here ? q + kRowsAhead * (kRowsBlock / 2) : qn) + d * (kRowsBlock / 2),
+                (here ? s + kRowsAhead * kG : sn) + d * kG, here ? b + d + kRowsAhead : more ? d : n);
+        } else {
+          fetch(d, q + (d + kRowsAhead) * (kRowsBlock / 2), s + (d + kRowsAhead) * kG, b + d + kRowsAhead);
+        }
       }
       q += kRowsAhead * (kRowsBlock / 2);
       s += kRowsAhead * kG;
 #pragma unroll
       for (int i = 0; i < P; ++i) xp[i] += kRowsAhead * 256;
+    }
+    if (STREAM) {
+      q = qn;
+      s = sn;
     }
     if (kG == 4)  // two lanes hold the four groups of a token
 #pragma unroll
@@ -464,17 +475,30 @@ struct Rows {
 #pragma unroll
         for (int r = 0; r < 2; ++r) sum[i][r][0] += __shfl_xor_sync(0xFFFFFFFFu, sum[i][r][0], 1);
   }
+  __device__ __forceinline__ void clear() {
+#pragma unroll
+    for (int i = 0; i < P; ++i)
+#pragma unroll
+      for (int j = 0; j < kHeld; ++j) sum[i][0][j] = sum[i][1][j] = 0.0f;
+  }
   // Where the sums go: to(row of the tile, token, value), for the tokens below n.
   template <class F>
   __device__ __forceinline__ void give(int tokens, F to) const {
+    each(tokens, [&](int tok, float v0, float v1) {
+      to(g, tok, v0);
+      to(g + 8, tok, v1);
+    });
+  }
+  // to(token, row g's, row g + 8's)
+  template <class F>
+  __device__ __forceinline__ void each(int tokens, F to) const {
 #pragma unroll
     for (int i = 0; i < P; ++i)
 #pragma unroll
       for (int j = 0; j < kHeld; ++j) {
         const int tok = i * kTok + (kG == 1 ? 2 * t + j : kG == 2 ? t : t >> 1);
         if (tok >= tokens || (kG == 4 && (t & 1))) continue;
-        to(g, tok, sum[i][0][j]);
-        to(g + 8, tok, sum[i][1][j]);
+        to(tok, sum[i][0][j], sum[i][1][j]);
       }
   }
 };
@@ -501,8 +525,14 @@ __device__ __forceinline__ void lay_out(uint32_t to, const uint16_t* x, int c0, 
 
 constexpr int kOneWarps = 4;
 
+// Blocks an SM that the registers allow without spills: groups told apart by the
+// MMA's columns take more. 7168 x 7168, group 64: 4 blocks 9.8 us, 6 12.9 us (some
+// registers spilled); group 128: 9.2 and 8.1 us. One token's experts of 7168 x 2048,
+// group 64: 48 us, 57.7 us.
+constexpr int one_blocks(int group) { return group == 128 ? 6 : 4; }
+
 template <int GROUP>
-__global__ void __launch_bounds__(kOneWarps * 32, 6)
+__global__ void __launch_bounds__(kOneWarps * 32, one_blocks(GROUP))
     w4_matvec_one_kernel(const uint16_t* x, const uint8_t* q, const uint16_t* scale, int rows,
                          int cols, uint16_t* y) {
   extern __shared__ __align__(16) uint8_t dynamic[];
@@ -546,7 +576,7 @@ __device__ __forceinline__ int one_route(const W4Args& a, int lane, float* p) {
 
 // Block (8 features, route): rows g of its tile are gate rows, rows g + 8 up rows.
 template <int GROUP>
-__global__ void __launch_bounds__(kOneWarps * 32, 6) w4_fc1_one_kernel(const W4Args a) {
+__global__ void __launch_bounds__(kOneWarps * 32, one_blocks(GROUP)) w4_fc1_one_kernel(const W4Args a) {
   extern __shared__ __align__(16) uint8_t dynamic[];
   __shared__ float part[kOneWarps][16];
   griddep_wait();
@@ -578,7 +608,7 @@ __global__ void __launch_bounds__(kOneWarps * 32, 6) w4_fc1_one_kernel(const W4A
 // Block (16 output columns): the 128-column blocks of the token's experts, one
 // expert after the other, are dealt out to the warps in runs.
 template <int GROUP>
-__global__ void __launch_bounds__(kThreads, 3) w4_fc2_one_kernel(const W4Args a) {
+__global__ void __launch_bounds__(kThreads, one_blocks(GROUP) / 2) w4_fc2_one_kernel(const W4Args a) {
   extern __shared__ __align__(16) uint8_t dynamic[];
   __shared__ float part[kWarps][16];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
@@ -722,61 +752,102 @@ __global__ void __launch_bounds__(kMaxExperts) w4_group_kernel(const int32_t* id
     if (id[i] >= 0) G->order[routes[id[i]] + of_warp[i / part][id[i]] + rank[i]] = i;
 }
 
-// Block (rows, piece): kWarps / S tiles of 16 rows, S warps a tile, which split its
-// columns. Gated: 8 features a tile, rows g their gate rows, rows g + 8 their up
-// rows; h of each route, in the order of open_codes. Else 16 columns of the output
-// a tile; each route's products, times its probability, in fp32.
+// The work is a list of items, those of the first piece, of the second, ...: kWarps / S
+// tiles of 16 rows, S warps a tile, which split its columns. A block takes a run of
+// the list, and a warp's stream of codes goes on from tile to tile of a piece. Gated:
+// 8 features a tile, rows g their gate rows, rows g + 8 their up rows; h of each
+// route, in the order of open_codes. Else 16 columns of the output a tile; each
+// route's products, times its probability, in fp32.
 template <bool GATED, int GROUP, int P>
-__global__ void __launch_bounds__(kThreads, P == 1 ? 3 : 2)
+__global__ void __launch_bounds__(kThreads, 2)
     w4_piece_kernel(const W4Args a, const W4Groups* G, float* o, const int S, const uint32_t stride) {
   using R = Rows<GROUP, P>;
   constexpr int kMost = R::kTok * P;
   extern __shared__ __align__(16) uint8_t dynamic[];
-  __shared__ float part[kWarps][16][kMost];
+  __shared__ float part[2][kWarps][16][kMost];
+  __shared__ int route_s[kMost];
+  __shared__ float prob_s[kMost];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2;
   const int cols = GATED ? a.H : a.I, rows = GATED ? a.I : a.H, step = GATED ? 8 : 16;
-  // The second product's piece and weights were there before the first one began
+  const int per = kWarps / S * step, items = (rows + per - 1) / per;  // rows of an item, items of a piece
+  // The second product's pieces and weights were there before the first one began
   // (its kernel started after the grouping's had finished): only h has to wait.
   if (GATED) griddep_wait();
   griddep_launch_dependents();
-  const int piece = blockIdx.y;
-  if (piece >= __ldcg(&G->pieces)) {
-    if (!GATED) griddep_wait();
-    return;
-  }
-  const int e = __ldcg(&G->expert[piece]), first = __ldcg(&G->first[piece]), n = __ldcg(&G->count[piece]);
-  const int row0 = (blockIdx.x * (kWarps / S) + warp / S) * step, member = warp % S;
-  const int c0 = share(member, S, cols), c1 = row0 < rows ? share(member + 1, S, cols) : c0;
-  R r;
-  r.begin(GATED ? a.w13 : a.w2, GATED ? a.w13_scale : a.w2_scale,
-          GATED ? (int64_t)e * 2 * a.I + row0 + g : (int64_t)e * a.H + row0 + g, GATED ? a.I : 8, cols, c0, c1,
-          lane);
-  if (!GATED) griddep_wait();
-  // the piece's tokens (second product: their h), a warp a token at a time
-  for (int k = warp; k < n; k += kWarps) {
-    const int route = __ldcg(&G->order[first + k]);
-    const uint16_t* x = GATED ? a.x + (size_t)(route / a.K) * cols : a.h + (size_t)route * cols;
-    lay_out<!GATED>(smem_u32(dynamic) + (uint32_t)k * stride, x, 0, cols, lane);
-  }
-  __syncthreads();
-  r.run(smem_u32(dynamic) + (uint32_t)c0 * 2u, stride, n);
-  r.give(n, [&](int row, int tok, float v) { part[warp][row][tok] = v; });
-  __syncthreads();
-  const int per = kWarps / S * step;  // rows of the block
-  for (int i = threadIdx.x; i < per * n; i += kThreads) {
-    const int at = i % per, tok = i / per, row = blockIdx.x * per + at;
-    if (row >= rows) continue;
-    const int route = __ldcg(&G->order[first + tok]), w0 = at / step * S, in = at % step;
-    float v = 0.0f, u = 0.0f;
-    for (int w = w0; w < w0 + S; ++w) {
-      v += part[w][in][tok];
-      if (GATED) u += part[w][8 + in][tok];
+  bool waited = GATED;
+  const int64_t all = (int64_t)__ldcg(&G->pieces) * items;
+  int at = (int)(all * blockIdx.x / gridDim.x);
+  const int end = (int)(all * (blockIdx.x + 1) / gridDim.x);
+  const int member = warp % S, c0 = share(member, S, cols), c1 = share(member + 1, S, cols);
+  const uint32_t xs = smem_u32(dynamic) + (uint32_t)c0 * 2u;
+  while (at < end) {
+    const int piece = at / items, from = at - piece * items, to = min(items, from + end - at);
+    at += to - from;
+    const int e = __ldcg(&G->expert[piece]), first = __ldcg(&G->first[piece]), n = __ldcg(&G->count[piece]);
+    const int row0 = from * per + warp / S * step;
+    int tiles = to - from;  // this warp's: the last item may have fewer
+    if (row0 + (tiles - 1) * per >= rows) --tiles;
+    R r;  // not set up, and not used, in a warp without a tile
+    if (tiles > 0)
+      r.begin(GATED ? a.w13 : a.w2, GATED ? a.w13_scale : a.w2_scale,
+              GATED ? (int64_t)e * 2 * a.I + row0 + g : (int64_t)e * a.H + row0 + g, GATED ? a.I : 8, cols, c0,
+              c1, lane);
+    if (!waited) {
+      griddep_wait();
+      waited = true;
     }
-    if (GATED)
-      a.h[(size_t)route * a.I + permuted(row)] = to_bf((a.activation ? act_fwd<1>(v) : act_fwd<0>(v)) * u);
-    else
-      o[(size_t)route * a.H + row] = __ldcg(&G->prob[route]) * v;
+    // the piece's tokens (second product: their h), a warp a token at a time
+    for (int k = warp; k < n; k += kWarps) {
+      const int route = __ldcg(&G->order[first + k]);
+      if (lane == 0) {
+        route_s[k] = route;
+        prob_s[k] = __ldcg(&G->prob[route]);
+      }
+      const uint16_t* x = GATED ? a.x + (size_t)(route / a.K) * cols : a.h + (size_t)route * cols;
+      lay_out<!GATED>(smem_u32(dynamic) + (uint32_t)k * stride, x, 0, cols, lane);
+    }
+    __syncthreads();
+    const auto put = [&](int tok, int row, float v, float u) {
+      const int route = route_s[tok];
+      if (GATED)
+        a.h[(size_t)route * a.I + permuted(row)] = to_bf((a.activation ? act_fwd<1>(v) : act_fwd<0>(v)) * u);
+      else
+        o[(size_t)route * a.H + row] = prob_s[tok] * v;
+    };
+    for (int i = 0; i < to - from; ++i) {
+      if (i < tiles) r.template run<true>(xs, stride, n, i + 1 < tiles, per, cols);
+      if (S == 1) {
+        if (i < tiles)
+          r.each(n, [&](int tok, float v0, float v1) {
+            const int row = row0 + i * per + g;
+            put(tok, row, v0, v1);
+            if (!GATED) put(tok, row + 8, v1, 0.0f);
+          });
+      } else {
+        float(*mine)[16][kMost] = part[i & 1];
+        if (i < tiles)
+          r.each(n, [&](int tok, float v0, float v1) {
+            mine[warp][g][tok] = v0;
+            mine[warp][g + 8][tok] = v1;
+          });
+        __syncthreads();
+        for (int j = threadIdx.x; j < per * n; j += kThreads) {
+          const int in_item = j % per, tok = j / per, row = (from + i) * per + in_item;
+          if (row >= rows) continue;
+          const int w0 = in_item / step * S, in = in_item % step;
+          float v = 0.0f, u = 0.0f;
+          for (int w = w0; w < w0 + S; ++w) {
+            v += mine[w][in][tok];
+            if (GATED) u += mine[w][8 + in][tok];
+          }
+          put(tok, row, v, u);
+        }
+      }
+      if (i < tiles) r.clear();
+    }
+    __syncthreads();  // before the next piece's x is laid out
   }
+  if (!waited) griddep_wait();
 }
 
 // y[t] = add[t] + the products of t's routes, in their order: four columns a thread.
@@ -874,10 +945,12 @@ cudaError_t matvec(const uint16_t* x, const uint8_t* q, const uint16_t* scale, i
                        : matvec<32, TOK>(x, q, scale, N, rows, cols, y, s);
 }
 
-// Several tokens. Routes of a piece: what x leaves room for in a third of an SM's
-// shared memory, at most 8. Warps a row tile: more where the blocks would not fill
-// the SMs twice.
-constexpr size_t kPieceBytes = 64 << 10;
+// Several tokens. Routes of a piece: what x leaves room for in half of an SM's shared
+// memory, at most 8. Warps a row tile: more where there are few items for the blocks
+// (2 an SM) to share evenly, while a warp keeps eight blocks of columns: four tokens'
+// experts of 7168 x 2048 145 us with kFill 4, 154 us with 2.
+constexpr size_t kPieceBytes = 96 << 10;
+constexpr int kFill = 4;
 
 struct W4Layout {
   size_t groups, o, h, total;
@@ -898,19 +971,19 @@ cudaError_t piece(const W4Args& a, const W4Groups* G, float* o, int most, int pi
   const int cols = GATED ? a.H : a.I, rows = GATED ? a.I / 8 : a.H / 16;
   // 64 bytes over a multiple of 128: two tokens' words in different banks
   const uint32_t stride = (uint32_t)((cols + 127) / 128 * 256 + 64);
+  const int blocks = 2 * sms;
   int S = 1;
-  while (S < 8 && (int64_t)((rows + 8 / S - 1) / (8 / S)) * pieces < 4 * (int64_t)sms && cols / 128 >= 8 * S) S *= 2;
+  while (S < 8 && (int64_t)((rows + 8 / S - 1) / (8 / S)) * pieces < kFill * (int64_t)blocks && cols / 128 >= 8 * S) S *= 2;
+  const int64_t items = (int64_t)((rows + 8 / S - 1) / (8 / S)) * pieces;
   return launch_ring(once, w4_piece_kernel<GATED, GROUP, P>, kPieceBytes + 1024,
-                     dim3((rows + 8 / S - 1) / (8 / S), pieces), dim3(kThreads), (size_t)most * stride, s, a, G, o, S,
-                     stride);
+                     dim3((unsigned)(items < blocks ? items : blocks)), dim3(kThreads), (size_t)most * stride, s, a, G,
+                     o, S, stride);
 }
 
 template <bool GATED, int GROUP>
 cudaError_t piece(const W4Args& a, const W4Groups* G, float* o, int most, int pieces, int sms, cudaStream_t s) {
   constexpr int kTok = 8 / (128 / GROUP);
   if (most <= kTok) return piece<GATED, GROUP, 1>(a, G, o, most, pieces, sms, s);
-  if constexpr (kTok < 4)
-    if (most > 2 * kTok) return piece<GATED, GROUP, 4>(a, G, o, most, pieces, sms, s);
   if constexpr (kTok < 8) return piece<GATED, GROUP, 2>(a, G, o, most, pieces, sms, s);
   return cudaErrorInvalidValue;
 }
@@ -932,10 +1005,12 @@ cudaError_t ffn_many(const W4Args& a, cudaStream_t s) {
   const int wide = a.H > a.I ? a.H : a.I, R = a.N * a.K;
   int most = (int)(kPieceBytes / ((size_t)(wide + 127) / 128 * 256 + 64));
   const int experts = R < a.E ? R : a.E, one = 8 / (128 / a.group);  // routes of one MMA
-  // where experts have few routes each, pieces that one MMA takes: fewer registers,
-  // more blocks an SM
-  if (most > 8) most = 8;
-  if (most > one && R <= experts * one / 2) most = one;
+  // Pieces of what one MMA takes: the second piece of an expert finds its weights in
+  // L2. Of two MMAs' routes where experts have that many each: 16 experts of 4096 x
+  // 1408, group 32, 2 routes an expert 54 us and 60, 4 83 and 80, 16 247 and 195; four
+  // MMAs' 66, 82 and 213.
+  const int take = one < 8 && R >= 2 * one * experts ? 2 * one : one;
+  if (most > take) most = take;
   if (most > a.N) most = a.N;
   // pieces there may be: one more for every `most` routes beyond an expert's first
   const int pieces = experts + (R - experts) / most;

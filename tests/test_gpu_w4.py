@@ -158,6 +158,19 @@ def test_experts(n, h, e, k, i, group, act):
     b.check()
 
 
+@pytest.mark.parametrize("idle", [0, 3])
+@pytest.mark.parametrize("n,h,e,k,i,group", [
+    (24, 2080, 40, 4, 1056, 32), (32, 1056, 20, 8, 2080, 32), (32, 1088, 24, 8, 1088, 64), (25, 2112, 70, 3, 1088, 64), (32, 1152, 60, 4, 1280, 128),
+])
+def test_blocks_that_take_rows_of_several_experts(n, h, e, k, i, group, idle):
+    """More items than blocks: runs that begin and end inside an expert's rows,
+    last items with fewer tiles than warps, and experts without a route."""
+    b = Batch(n, h, e, k, i, group, moe.ACT_SWIGLU, add=True)
+    b.ids[n - idle:] = -1
+    b.run()
+    b.check()
+
+
 def test_routes_without_an_expert_contribute_nothing():
     for add in (True, False):
         b = Batch(21, 256, 8, 3, 128, 64, add=add)
