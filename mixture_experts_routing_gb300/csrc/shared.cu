@@ -594,11 +594,20 @@ void pick_width(Problem* pr, int n, int pairs, bool gated, int step) {
       cost[i] = tile_cost(w, pr[i].k_tiles);
       begin[i + 1] = begin[i] + (int64_t)pr[i].m_tiles * pr[i].n_tiles;
     }
+    // pair p has begin / pairs + (p < begin % pairs) tiles of those before `begin`, so
+    // its load changes only at the p that are such remainders
+    int64_t turns[kMaxProblems + 1];
+    int rest[kMaxProblems + 1];
+    for (int i = 0; i <= n; ++i) {
+      turns[i] = begin[i] / pairs;
+      rest[i] = (int)(begin[i] - turns[i] * pairs);
+    }
     double longest = 0;
-    for (int p = 0; p < pairs; ++p) {
+    for (int c = 0; c <= n; ++c) {
+      const int p = rest[c];  // the first is 0
       double sum = 0;
       for (int i = 0; i < n; ++i)
-        sum += cost[i] * (double)((begin[i + 1] - p + pairs - 1) / pairs - (begin[i] - p + pairs - 1) / pairs);
+        sum += cost[i] * (double)(turns[i + 1] + (p < rest[i + 1]) - turns[i] - (p < rest[i]));
       longest = sum > longest ? sum : longest;
     }
     if (w == 128 || longest < 0.97 * least) {
