@@ -65,6 +65,7 @@ struct Problem {
 struct MmaParams {
   Problem pr[kMaxProblems];
   int problems, tiles;
+  int split;             // pairs of a cluster, which share a tile's contraction (below)
   int up;                // kGated: rows of B from a feature's gate row to its up row
   const uint8_t* ck_in;  // kGatedBwd: [M,2N] codes, [M,2N/32] bytes
   const uint8_t* sf_in;
@@ -95,6 +96,15 @@ __device__ __forceinline__ uint4 ld_shared_v4(uint32_t at) {
   uint4 v;
   asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];"
                : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "r"(at)
+               : "memory");
+  return v;
+}
+
+__device__ __forceinline__ float4 ld_cluster_v4(uint32_t at) {
+  float4 v;
+  asm volatile("ld.shared::cluster.v4.f32 {%0,%1,%2,%3}, [%4];"
+               : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
                : "r"(at)
                : "memory");
   return v;
@@ -202,7 +212,9 @@ __device__ __forceinline__ bool kAMn(const Problem& P) { return EPI == kGrads &&
 template <int EPI>
 __device__ __forceinline__ bool kBMn(const Problem& P) { return EPI == kGatedBwd || EPI == kGrads; }
 
-template <int EPI, int ACT>
+// SHARED: the cluster's p.split pairs share the contraction of its only tile. A
+// kernel of its own: with the split read at run time every launch took 0.5 us more.
+template <int EPI, int ACT, bool SHARED>
 __global__ void __launch_bounds__(kThreads, 1)
     shared_mma_kernel(const __grid_constant__ Maps maps, const __grid_constant__ MmaParams p) {
   extern __shared__ uint8_t smem_raw[];
@@ -214,10 +226,12 @@ __global__ void __launch_bounds__(kThreads, 1)
   __shared__ uint32_t tmem_base_s;
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const uint32_t crank = cluster_ctarank();
+  const int split = SHARED ? p.split : 1;
+  const uint32_t rank = cluster_ctarank(), crank = rank & 1u, even = SHARED ? rank & ~1u : 0u;
+  const int part = SHARED ? (int)(rank >> 1) : 0;
   const uint32_t sbase = (smem_u32(smem_raw) + 1023u) & ~1023u;
   const int tiles = p.tiles;
-  const int pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
+  const int pair = blockIdx.x / (2 * split), pairs = gridDim.x / (2 * split);
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < kStages; ++s) {
@@ -256,14 +270,14 @@ __global__ void __launch_bounds__(kThreads, 1)
       // every step made the launch 9 % slower
       const CUtensorMap *ma = &maps.a[T.pr], *mb = &maps.b[T.pr];
       const bool amn = kAMn<EPI>(P), bmn = kBMn<EPI>(P);
-      const int k_tiles = P.k_tiles, w = P.w;
-      const uint32_t bar0 = mapa_shared(smem_u32(&full_bar[0]), 0);
+      const int k0 = P.k_tiles * part / split, k1 = P.k_tiles * (part + 1) / split, w = P.w;
+      const uint32_t bar0 = mapa_shared(smem_u32(&full_bar[0]), even);
       const int am = T.m + (int)crank * kBM;
       // the odd CTA's rows of B: the second half of the tile's columns (gated: the up rows)
       const int bn = T.n + (int)crank * (EPI == kGated ? p.up : w);
       // of both CTAs: K-major boxes of w rows, MN-major ones of 64 columns
       const uint32_t bytes = 2 * (kOpBytes + (bmn ? (w > 64 ? kOpBytes : kOpBytes / 2) : (uint32_t)w * 128u));
-      for (int kt = 0; kt < k_tiles; ++kt, ++g) {
+      for (int kt = k0; kt < k1; ++kt, ++g) {
         const uint32_t s = g % kStages, u = g / kStages;
         if (u > 0 && !mbar_wait_cluster_warp(smem_u32(&empty_bar[s]), (u - 1u) & 1u, p.err,
                                              kErrWaitEmpty)) {
@@ -292,6 +306,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         __syncwarp();
       }
     }
+    __syncwarp();
+    if (SHARED) cluster_sync_all();
   } else if (warp == 1) {
     // ------------------------------------------------------------ MMA issuer
     if (crank == 0) {
@@ -301,7 +317,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const Tile T = tile_of<EPI>(p, t);
         const Problem& P = p.pr[T.pr];
         const bool amn = kAMn<EPI>(P), bmn = kBMn<EPI>(P);
-        const int k_tiles = P.k_tiles;
+        const int k0 = P.k_tiles * part / split, k1 = P.k_tiles * (part + 1) / split;
         const uint32_t idesc = idesc_bf16_f32(2 * kBM, 2 * P.w) |
                                (amn ? kIdescAMnMajor : 0u) | (bmn ? kIdescBMnMajor : 0u);
         // 16 contraction values: 32 bytes along a K-major row, 16 rows of an MN-major
@@ -314,7 +330,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                                               kErrWaitAccum))
           break;
         tc_fence_after();
-        for (int kt = 0; kt < k_tiles; ++kt, ++g) {
+        for (int kt = k0; kt < k1; ++kt, ++g) {
           const uint32_t s = g % kStages, u = g / kStages;
           if (!mbar_wait_cluster_warp(smem_u32(&full_bar[s]), u & 1u, p.err, kErrWaitFull)) {
             ok = false;
@@ -326,15 +342,17 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
             for (uint32_t kk = 0; kk < kBK / 16; ++kk)
               umma_bf16_pair(tmem + b * 256u, a_base + at + kk * a_step, b_base + at + kk * b_step, idesc,
-                             (kt | (int)kk) != 0);
-            umma_commit_pair(smem_u32(&empty_bar[s]), 3);
+                             ((kt - k0) | (int)kk) != 0);
+            umma_commit_pair(smem_u32(&empty_bar[s]), (uint16_t)(3u << even));
           }
           __syncwarp();
         }
-        if (lane == 0) umma_commit_pair(smem_u32(&tmem_full_bar[b]), 3);  // also after an abort
+        if (lane == 0) umma_commit_pair(smem_u32(&tmem_full_bar[b]), (uint16_t)(3u << even));  // also after an abort
         __syncwarp();
       }
     }
+    __syncwarp();
+    if (SHARED) cluster_sync_all();
   } else {
     // ------------------------------------------------------------ epilogue
     const int q = warp & 3, half = (warp - 2) >> 2, ew = warp - 2;
@@ -343,6 +361,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     // next chunk uses (they alternate from tile to tile too: a store may still read the
     // last one)
     uint32_t tc = 0, adds[2] = {0, 0}, turn = 0;
+    // this warp's chunks of a tile: of a shared one, the pair's
+    const int first = half + 2 * part, step = 2 * split;
+    bool met = !SHARED;
     for (int t = pair; t < tiles; t += pairs, ++tc) {
       const Tile T = tile_of<EPI>(p, t);
       const Problem& P = p.pr[T.pr];
@@ -355,18 +376,18 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int cols = min(EPI == kGated ? w : 2 * w, N - T.n);
       const int chunks = row0 < M ? (cols + 31) / 32 : 0;
       const bool add = (EPI == kOut || EPI == kGrads) && P.has_add;
-      auto load_add = [&](int c) {
+      auto load_add = [&](int c, uint32_t i) {  // the tile's i-th chunk of this warp
         if (c < chunks && lane == 0) {
-          const uint32_t box = (turn + (uint32_t)(c >> 1)) & 1u, bar = smem_u32(&add_bar[ew][box]);
+          const uint32_t box = (turn + i) & 1u, bar = smem_u32(&add_bar[ew][box]);
           mbar_arrive_expect_tx(bar, 2048);
           tma_load_2d_pair(buf0 + box * 2048u, mx, T.n + 32 * c, row0, bar);
         }
       };
-      if (add && half < chunks) {  // under the tile's MMAs: the first two chunks of what is added
+      if (add && first < chunks) {  // under the tile's MMAs: the first two chunks of what is added
         if (lane == 0) bulk_wait_read<0>();
         __syncwarp();
-        load_add(half);
-        load_add(half + 2);
+        load_add(first, 0);
+        load_add(first + step, 1);
       }
       // the checkpoint of a chunk is loaded a chunk ahead, the first under the tile's MMAs
       uint4 nx[4] = {};
@@ -382,14 +403,54 @@ __global__ void __launch_bounds__(kThreads, 1)
           nsf = (uint32_t)sf[0] | ((uint32_t)sf[N / 32] << 8);
         }
       };
-      load_kept(half);
+      load_kept(first);
       if (!mbar_wait_cluster_warp(smem_u32(&tmem_full_bar[b]), bu & 1u, p.err, kErrWaitAccum)) break;
       tc_fence_after();
-      for (int c = half; c < chunks; c += 2) {
+      if (SHARED) {
+        // the other pairs' chunks to where they read them: the stages, whose last MMA is done
+        for (int c = half; c < chunks; c += 2) {
+          if ((c >> 1) % split == part) continue;
+          float v[32];
+          tmem_row32(tl + 32u * (uint32_t)c, v);
+          const uint32_t at = sbase + (uint32_t)(c * kBM + q * 32 + lane) * 128u;
+#pragma unroll
+          for (int j = 0; j < 8; ++j)
+            st_shared_v4(at + (uint32_t)((j ^ (lane & 7)) << 4), __float_as_uint(v[4 * j]),
+                         __float_as_uint(v[4 * j + 1]), __float_as_uint(v[4 * j + 2]),
+                         __float_as_uint(v[4 * j + 3]));
+        }
+        __syncwarp();
+        cluster_sync_all();
+        met = true;
+      }
+      uint32_t nth = 0;
+      for (int c = first; c < chunks; c += step, ++nth) {
         const int col = T.n + 32 * c;
-        const uint32_t odd = (turn + (uint32_t)(c >> 1)) & 1u, buf = buf0 + odd * 2048u;
+        const uint32_t odd = (turn + nth) & 1u, buf = buf0 + odd * 2048u;
         float v[32];
         tmem_row32(tl + 32u * (uint32_t)c, v);
+        if (SHARED) {  // the pairs' sums, in their order
+          float sum[32] = {};
+          const uint32_t at = sbase + (uint32_t)(c * kBM + q * 32 + lane) * 128u;
+          for (int r = 0; r < split; ++r) {
+            if (r == part) {
+#pragma unroll
+              for (int j = 0; j < 32; ++j) sum[j] += v[j];
+              continue;
+            }
+            const uint32_t from = mapa_shared(at, 2u * (uint32_t)r + crank);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+              const float4 o = ld_cluster_v4(from + (uint32_t)((j ^ (lane & 7)) << 4));
+              sum[4 * j] += o.x;
+              sum[4 * j + 1] += o.y;
+              sum[4 * j + 2] += o.z;
+              sum[4 * j + 3] += o.w;
+            }
+          }
+#pragma unroll
+          for (int j = 0; j < 32; ++j) v[j] = sum[j];
+        }
         if (EPI == kGrads && P.f32) {
           if (lane == 0) bulk_wait_read<0>();
           __syncwarp();
@@ -419,10 +480,10 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           stage_row(buf, lane, v);
           store_box(mo, buf, col, row0, lane);
-          if (add && c + 4 < chunks) {
+          if (add && c + 2 * step < chunks) {
             if (lane == 0) bulk_wait_read<0>();
             __syncwarp();
-            load_add(c + 4);
+            load_add(c + 2 * step, nth + 2);
           }
         } else if constexpr (EPI == kGated) {
           float u[32];
@@ -451,7 +512,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           const uint32_t gw[8] = {nx[0].x, nx[0].y, nx[0].z, nx[0].w, nx[1].x, nx[1].y, nx[1].z, nx[1].w};
           const uint32_t uw[8] = {nx[2].x, nx[2].y, nx[2].z, nx[2].w, nx[3].x, nx[3].y, nx[3].z, nx[3].w};
           const float fg = e8m0_value(nsf & 255u), fu = e8m0_value(nsf >> 8);
-          load_kept(c + 2);
+          load_kept(c + step);
           uint32_t dg[16], du[16], h[16];  // pairs of bf16
 #pragma unroll
           for (int j = 0; j < 16; ++j) {
@@ -483,17 +544,19 @@ __global__ void __launch_bounds__(kThreads, 1)
           store_box(&maps.o[1], buf0, col, row0, lane);
         }
       }
-      if (chunks > half) turn += (uint32_t)(chunks - half + 1) >> 1;
+      turn += nth;
       tc_fence_before();
       __syncwarp();
       if (lane == 0) {
         if (crank == 0)
           mbar_arrive(smem_u32(&tmem_empty_bar[b]));
         else
-          mbar_arrive_remote_relaxed(mapa_shared(smem_u32(&tmem_empty_bar[b]), 0));
+          mbar_arrive_remote_relaxed(mapa_shared(smem_u32(&tmem_empty_bar[b]), even));
       }
     }
     if (lane == 0) bulk_wait_all();
+    __syncwarp();
+    if (!met) cluster_sync_all();  // after an abort
   }
   tc_fence_before();
   __syncthreads();
@@ -530,24 +593,31 @@ bool out_map(CUtensorMap* m, const void* base, int64_t cols, int64_t rows, int64
   return map2d(m, base, cols, rows, pitch, 32, 32, CU_TENSOR_MAP_SWIZZLE_64B);
 }
 
-// Pairs resident at once, and the kernel's shared-memory opt-in, once per device.
-template <int EPI, int ACT>
-int max_pairs(cudaError_t* err) {
-  static DeviceOnce once;
+constexpr int kMaxSplit = 4;
+
+void set_cluster(cudaLaunchAttribute& a, int ctas) {
+  a.id = cudaLaunchAttributeClusterDimension;
+  a.val.clusterDim.x = (unsigned)ctas;
+  a.val.clusterDim.y = a.val.clusterDim.z = 1;
+}
+
+// Clusters of `split` pairs resident at once, and the kernel's shared-memory opt-in,
+// once per device.
+template <int EPI, int ACT, bool SHARED>
+int max_clusters(int split, cudaError_t* err) {
+  static DeviceOnce once[kMaxSplit + 1];
   int n = 0;
-  *err = once_per_device(once, &n, [](int, int* v) {
-    auto* k = shared_mma_kernel<EPI, ACT>;
+  *err = once_per_device(once[split], &n, [&](int, int* v) {
+    auto* k = shared_mma_kernel<EPI, ACT, SHARED>;
     cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                          (int)kSmemBytes);
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(2);
+    cfg.gridDim = dim3((unsigned)(2 * split));
     cfg.blockDim = dim3(kThreads);
     cfg.dynamicSmemBytes = kSmemBytes;
     cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = 2;
-    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    set_cluster(attr[0], 2 * split);
     cfg.attrs = attr;
     cfg.numAttrs = 1;
     return cudaOccupancyMaxActiveClusters(v, k, &cfg);
@@ -564,11 +634,16 @@ Problem problem(int M, int N, int64_t K, bool amn = false) {
   return P;
 }
 
+// In k-tiles of the widest tile, as tile_cost below.
+constexpr double kShareCost = 5;   // for each pair more that shares a tile
+constexpr double kLaunchCost = 8;  // of a launch more (4 and 13: the same choices but for few)
+
 // How long a tile of width w takes, in k-tiles of the widest: its MMAs, or its
-// operands' way into shared memory (128 + w rows a CTA; the widest tile's operands
-// take 0.82 of its MMAs' time), and what a tile costs beside its contraction.
-double tile_cost(int w, int k_tiles) {
-  const double mma = w / 128.0, operands = 0.82 * (128 + w) / 256.0;
+// operands' way into shared memory (128 + w rows a CTA, MN-major B in boxes of 64; the
+// widest tile's operands take 0.82 of its MMAs' time), and what a tile costs beside its
+// contraction.
+double tile_cost(int w, int k_tiles, bool mn) {
+  const double mma = w / 128.0, operands = 0.82 * (128 + (mn ? (w > 64 ? 128 : 64) : w)) / 256.0;
   return k_tiles * (mma > operands ? mma : operands) + 1.5;
 }
 
@@ -583,7 +658,7 @@ void set_width(Problem& P, int w, bool gated) {
 // first: pair p takes tiles p, p + pairs, ... of the list, so a last turn that few
 // tiles fill costs as much as a full one. 8192 x 2048 x 768, the gated product: 128
 // -> 96 features, 2.5 turns that cost 3 become 3.4 that cost 2.9.
-void pick_width(Problem* pr, int n, int pairs, bool gated, int step) {
+double pick_width(Problem* pr, int n, int pairs, bool gated, bool mn, int step) {
   double least = 0;
   int best = 128;
   for (int w = 128; w >= 64; w -= step) {
@@ -591,7 +666,7 @@ void pick_width(Problem* pr, int n, int pairs, bool gated, int step) {
     int64_t begin[kMaxProblems + 1] = {0};
     for (int i = 0; i < n; ++i) {
       set_width(pr[i], w, gated);
-      cost[i] = tile_cost(w, pr[i].k_tiles);
+      cost[i] = tile_cost(w, pr[i].k_tiles, mn);
       begin[i + 1] = begin[i] + (int64_t)pr[i].m_tiles * pr[i].n_tiles;
     }
     // pair p has begin / pairs + (p < begin % pairs) tiles of those before `begin`, so
@@ -616,6 +691,37 @@ void pick_width(Problem* pr, int n, int pairs, bool gated, int step) {
     }
   }
   for (int i = 0; i < n; ++i) set_width(pr[i], best, gated);
+  return least;
+}
+
+// One contraction whose tiles are too few for the SMs: the pairs of a cluster share a
+// tile, each a part of the contraction, and each adds up some of its columns from all
+// (a tile for each cluster then, not a list for each pair). Sets the width and returns
+// the pairs of a cluster. Backward, 64 tokens: 7168 x 2048 96 us without, 65 with;
+// 1024 x 352 18.7 and 17.9; 1000 tokens, 4096 x 1408 75 and 70.
+template <int EPI, int ACT>
+int pick_split(Problem& P, double* cost, cudaError_t* err) {
+  int pairs = max_clusters<EPI, ACT, false>(1, err), best = 1, w = 128;
+  if (pairs <= 0) return 0;
+  *cost = pick_width(&P, 1, pairs, false, true, 16);
+  w = P.w;
+  if ((int64_t)P.m_tiles * P.n_tiles < pairs)
+    for (int split = 2; split <= kMaxSplit && split <= P.k_tiles; ++split) {
+      const int clusters = max_clusters<EPI, ACT, true>(split, err);
+      if (*err != cudaSuccess) return 0;
+      for (int v = 128; v >= 64; v -= 16) {
+        set_width(P, v, false);
+        if ((int64_t)P.m_tiles * P.n_tiles > clusters) continue;
+        const double c = tile_cost(v, (P.k_tiles + split - 1) / split, true) + kShareCost * (split - 1);
+        if (c < 0.97 * *cost) {
+          *cost = c;
+          best = split;
+          w = v;
+        }
+      }
+    }
+  set_width(P, w, false);
+  return best;
 }
 
 // The problems come longest contraction first: the pairs take tiles in turn, so the
@@ -629,14 +735,28 @@ cudaError_t launch(const Maps& maps, MmaParams p, int pairs, cudaStream_t s) {
     if (tiles > INT32_MAX / 4) return cudaErrorInvalidValue;
   }
   p.tiles = (int)tiles;
-  const int n = p.tiles < pairs ? p.tiles : pairs;
-  return launch_pdl_pairs(shared_mma_kernel<EPI, ACT>, dim3(2 * n), dim3(kThreads), kSmemBytes, s, maps, p);
+  if (p.split < 1) p.split = 1;
+  const int n = p.split > 1 || p.tiles < pairs ? p.tiles : pairs;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)(2 * p.split * n));
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = kSmemBytes;
+  cfg.stream = s;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  set_cluster(attr[1], 2 * p.split);
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
+  if constexpr (EPI == kGatedBwd || EPI == kGrads)
+    if (p.split > 1) return cudaLaunchKernelEx(&cfg, shared_mma_kernel<EPI, ACT, true>, maps, p);
+  return cudaLaunchKernelEx(&cfg, shared_mma_kernel<EPI, ACT, false>, maps, p);
 }
 
 template <int ACT>
 cudaError_t forward(const SharedArgs& a, cudaStream_t s) {
   cudaError_t err = cudaSuccess;
-  int pairs = max_pairs<kGated, ACT>(&err);
+  int pairs = max_clusters<kGated, ACT, false>(1, &err);
   if (pairs <= 0) return err != cudaSuccess ? err : cudaErrorUnknown;
   Maps m{};
   MmaParams p{};
@@ -644,7 +764,7 @@ cudaError_t forward(const SharedArgs& a, cudaStream_t s) {
   p.problems = 1;
   p.pr[0] = problem(a.N, a.I, a.H);
   // a checkpoint block of 32 features lies in one tile
-  pick_width(p.pr, 1, pairs, true, a.ck ? 32 : 16);
+  pick_width(p.pr, 1, pairs, true, false, a.ck ? 32 : 16);
   p.up = a.I;
   p.ck = a.ck;
   p.sf = a.ck_sf;
@@ -655,14 +775,14 @@ cudaError_t forward(const SharedArgs& a, cudaStream_t s) {
     return cudaErrorInvalidValue;
   err = launch<kGated, ACT>(m, p, pairs, s);
   if (err != cudaSuccess) return err;
-  pairs = max_pairs<kOut, 0>(&err);
+  pairs = max_clusters<kOut, 0, false>(1, &err);
   if (pairs <= 0) return err != cudaSuccess ? err : cudaErrorUnknown;
   p = MmaParams{};
   p.err = a.err;
   p.problems = 1;
   p.pr[0] = problem(a.N, a.H, a.I);
   p.pr[0].has_add = a.add != nullptr;
-  pick_width(p.pr, 1, pairs, false, 16);
+  pick_width(p.pr, 1, pairs, false, false, 16);
   if (!operand_map(&m.a[0], a.h, a.I, a.N, false) ||
       !operand_map(&m.b[0], a.w2, a.I, a.H, false, (uint32_t)p.pr[0].w) ||
       !out_map(&m.o[0], a.y, a.H, a.N, a.H) || (a.add && !out_map(&m.x[0], a.add, a.H, a.N, a.H)))
@@ -671,17 +791,18 @@ cudaError_t forward(const SharedArgs& a, cudaStream_t s) {
 }
 
 template <int ACT>
-cudaError_t backward(const SharedArgs& a, cudaStream_t s) {
+cudaError_t backward(const SharedArgs& a, cudaStream_t s, int* launches) {
   cudaError_t err = cudaSuccess;
-  int pairs = max_pairs<kGatedBwd, ACT>(&err);
-  if (pairs <= 0) return err != cudaSuccess ? err : cudaErrorUnknown;
   // da = dy W2; dg, du and h from the checkpoint
   Maps m{};
   MmaParams p{};
   p.err = a.err;
   p.problems = 1;
   p.pr[0] = problem(a.N, a.I, a.H);
-  pick_width(p.pr, 1, pairs, false, 16);
+  double cost;
+  p.split = pick_split<kGatedBwd, ACT>(p.pr[0], &cost, &err);
+  if (p.split <= 0) return err != cudaSuccess ? err : cudaErrorUnknown;
+  int pairs = max_clusters<kGatedBwd, ACT, false>(1, &err);
   p.ck_in = a.ck;
   p.sf_in = a.ck_sf;
   if (!operand_map(&m.a[0], a.dy, a.H, a.N, false) || !operand_map(&m.b[0], a.w2, a.I, a.H, true) ||
@@ -691,29 +812,58 @@ cudaError_t backward(const SharedArgs& a, cudaStream_t s) {
   err = launch<kGatedBwd, ACT>(m, p, pairs, s);
   if (err != cudaSuccess) return err;
   // dx = [dg du] W13, dW13 = [dg du]^T x and dW2 = dy^T h in one launch
-  pairs = max_pairs<kGrads, 0>(&err);
+  pairs = max_clusters<kGrads, 0, false>(1, &err);
   if (pairs <= 0) return err != cudaSuccess ? err : cudaErrorUnknown;
   m = Maps{};
   p = MmaParams{};
   p.err = a.err;
-  p.problems = 3;
+  Problem dx = problem(a.N, a.H, 2 * (int64_t)a.I);
+  dx.has_add = a.add != nullptr;
+  Problem dw[2] = {problem(2 * a.I, a.H, a.N, true), problem(a.H, a.I, a.N, true)};
+  dw[0].f32 = dw[1].f32 = a.grad_f32;
   const bool dx_first = 2 * (int64_t)a.I >= a.N;
-  const int ix = dx_first ? 0 : 2, i13 = dx_first ? 1 : 0, i2 = dx_first ? 2 : 1;
-  p.pr[ix] = problem(a.N, a.H, 2 * (int64_t)a.I);
-  p.pr[ix].has_add = a.add != nullptr;
-  p.pr[i13] = problem(2 * a.I, a.H, a.N, true);
-  p.pr[i2] = problem(a.H, a.I, a.N, true);
-  p.pr[i13].f32 = p.pr[i2].f32 = a.grad_f32;
-  pick_width(p.pr, 3, pairs, false, 32);
+  int ix = dx_first ? 0 : 2, i13 = dx_first ? 1 : 0, i2 = dx_first ? 2 : 1;
+  p.pr[ix] = dx;
+  p.pr[i13] = dw[0];
+  p.pr[i2] = dw[1];
+  p.problems = 3;
+  cost = pick_width(p.pr, 3, pairs, false, true, 32);
+  // few tokens: dx's few tiles of a long contraction would outlast all others, so they
+  // are shared out in a launch of their own
+  double alone = 0;
+  const int split = pick_split<kGrads, 0>(dx, &alone, &err);
+  if (split <= 0) return err != cudaSuccess ? err : cudaErrorUnknown;
+  if (split > 1 && alone + kLaunchCost + pick_width(dw, 2, pairs, false, true, 32) < cost) {
+    MmaParams o{};
+    o.err = a.err;
+    o.problems = 1;
+    o.pr[0] = dx;
+    o.split = split;
+    if (!operand_map(&m.a[0], a.dpre, 2 * (int64_t)a.I, a.N, false) ||
+        !operand_map(&m.b[0], a.w13, a.H, 2 * (int64_t)a.I, true) || !out_map(&m.o[0], a.dx, a.H, a.N, a.H) ||
+        (a.add && !out_map(&m.x[0], a.add, a.H, a.N, a.H)))
+      return cudaErrorInvalidValue;
+    err = launch<kGrads, 0>(m, o, pairs, s);
+    if (err != cudaSuccess) return err;
+    ++*launches;
+    m = Maps{};
+    p.pr[0] = dw[0];
+    p.pr[1] = dw[1];
+    p.problems = 2;
+    ix = -1;
+    i13 = 0;
+    i2 = 1;
+  }
   auto grad_map = [&](CUtensorMap* t, void* d, int64_t cols, int64_t rows) {
     return a.grad_f32 ? map2d(t, d, cols, rows, cols, 32, 32, CU_TENSOR_MAP_SWIZZLE_128B,
                               CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 4)
                       : out_map(t, d, cols, rows, cols);
   };
-  if (!operand_map(&m.a[ix], a.dpre, 2 * (int64_t)a.I, a.N, false) ||
-      !operand_map(&m.b[ix], a.w13, a.H, 2 * (int64_t)a.I, true) || !out_map(&m.o[ix], a.dx, a.H, a.N, a.H) ||
-      (a.add && !out_map(&m.x[ix], a.add, a.H, a.N, a.H)) ||
-      !operand_map(&m.a[i13], a.dpre, 2 * (int64_t)a.I, a.N, true) ||
+  if (ix >= 0 && (!operand_map(&m.a[ix], a.dpre, 2 * (int64_t)a.I, a.N, false) ||
+                  !operand_map(&m.b[ix], a.w13, a.H, 2 * (int64_t)a.I, true) ||
+                  !out_map(&m.o[ix], a.dx, a.H, a.N, a.H) || (a.add && !out_map(&m.x[ix], a.add, a.H, a.N, a.H))))
+    return cudaErrorInvalidValue;
+  if (!operand_map(&m.a[i13], a.dpre, 2 * (int64_t)a.I, a.N, true) ||
       !operand_map(&m.b[i13], a.x, a.H, a.N, true) || !grad_map(&m.o[i13], a.dw13, a.H, 2 * (int64_t)a.I) ||
       !operand_map(&m.a[i2], a.dy, a.H, a.N, true) || !operand_map(&m.b[i2], a.h, a.I, a.N, true) ||
       !grad_map(&m.o[i2], a.dw2, a.I, a.H))
@@ -733,8 +883,9 @@ int launch_shared_forward(const SharedArgs& a, cudaStream_t s) {
 }
 
 int launch_shared_backward(const SharedArgs& a, cudaStream_t s) {
-  const cudaError_t err = a.activation ? backward<1>(a, s) : backward<0>(a, s);
-  return err != cudaSuccess ? -(int)err : 2;
+  int launches = 2;
+  const cudaError_t err = a.activation ? backward<1>(a, s, &launches) : backward<0>(a, s, &launches);
+  return err != cudaSuccess ? -(int)err : launches;
 }
 
 }  // namespace moe

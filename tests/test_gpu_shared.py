@@ -175,6 +175,28 @@ def test_backward(n, h, i, act):
         fro(got, ref, 5e-3, name)
 
 
+@pytest.mark.parametrize("grad_f32", [0, 1])
+@pytest.mark.parametrize("n,h,i", [
+    (1, 5120, 896), (5, 7168, 64), (64, 4096, 2048), (77, 2056, 160), (130, 1032, 1408), (300, 4096, 1408), (1000, 4096, 1408), (700, 264, 2048),
+])
+def test_backward_of_long_contractions(n, h, i, grad_f32):
+    """Tiles too few for the SMs: a cluster's pairs share their contractions."""
+    b = Block(n, h, i, moe.ACT_SWIGLU, add=n % 2 == 0, grad_f32=grad_f32)
+    b.forward()
+    b.backward()
+    ok()
+    for name, got, (ref, bound) in zip(("dx", "dw13", "dw2"), (b.dx, b.dw13, b.dw2), reference_backward(b)):
+        within(got, ref, bound, name)
+        fro(got, ref, 5e-3, name)
+    first = [t.clone() for t in (b.dx, b.dw13, b.dw2)]
+    for _ in range(3):
+        for t in (b.dx, b.dw13, b.dw2):
+            t.fill_(math.nan)
+        b.backward()
+        ok()
+        assert all(torch.equal(t, f) for t, f in zip((b.dx, b.dw13, b.dw2), first))
+
+
 @pytest.mark.parametrize("act", [moe.ACT_SWIGLU, moe.ACT_GEGLU])
 def test_gradients_against_differences(act):
     """Inputs whose pre-activations are whole 8-bit values (few significant
