@@ -17,7 +17,7 @@
 //
 // Experts, and one token's matvec (Rows): a lane loads 16 bytes of its two rows
 // straight into registers, four blocks of 128 columns ahead; x is laid out in shared
-// memory once per block of threads. Several tokens: one small kernel groups the
+// memory once per block of threads. Several tokens that share experts: one small kernel groups the
 // routes by expert, the blocks of the products share out the rows of the experts and
 // multiply each by all its routes, or 2 to 8 of them at a time (an expert's weights
 // come from HBM once), and a last kernel adds up each token's routes.
@@ -565,12 +565,12 @@ __global__ void __launch_bounds__(kOneWarps * 32, one_blocks(GROUP))
 
 // The token's route of this lane (lane < K): its expert, -1 for none or one named
 // before, and the token's whole probability of it.
-__device__ __forceinline__ int one_route(const W4Args& a, int lane, float* p) {
-  int e = lane < a.K ? __ldcg(a.topk_ids + lane) : -1;
+__device__ __forceinline__ int one_route(const W4Args& a, int token, int lane, float* p) {
+  int e = lane < a.K ? __ldcg(a.topk_ids + token * a.K + lane) : -1;
   if (e < 0 || e >= a.E) e = -1;
   const uint32_t same = __match_any_sync(0xFFFFFFFFu, e);
   if (p) {
-    const float mine = lane < a.K ? __ldcg(a.topk_p + lane) : 0.0f;
+    const float mine = lane < a.K ? __ldcg(a.topk_p + token * a.K + lane) : 0.0f;
     *p = 0.0f;
     for (int k = 0; k < a.K; ++k) {
       const float v = __shfl_sync(0xFFFFFFFFu, mine, k);
@@ -588,14 +588,15 @@ __global__ void __launch_bounds__(kOneWarps * 32, one_blocks(GROUP)) w4_fc1_one_
   griddep_wait();
   griddep_launch_dependents();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2;
-  const int e = __shfl_sync(0xFFFFFFFFu, one_route(a, lane, nullptr), blockIdx.y);
+  const int token = blockIdx.z;
+  const int e = __shfl_sync(0xFFFFFFFFu, one_route(a, token, lane, nullptr), blockIdx.y);
   if (e < 0) return;
   const int i0 = blockIdx.x * 8;
   const int c0 = share(warp, kOneWarps, a.H), c1 = share(warp + 1, kOneWarps, a.H);
   Rows<GROUP, 1> o;
   o.begin(a.w13, a.w13_scale, (int64_t)e * 2 * a.I + i0 + g, a.I, a.H, c0, c1, lane);
   const uint32_t xs = smem_u32(dynamic) + (uint32_t)c0 * 2;
-  lay_out<false>(xs, a.x, c0, c1, lane);
+  lay_out<false>(xs, a.x + (size_t)token * a.H, c0, c1, lane);
   o.run(xs, 0, 1);
   o.give(1, [&](int r, int, float v) { part[warp][r] = v; });
   __syncthreads();
@@ -607,7 +608,7 @@ __global__ void __launch_bounds__(kOneWarps * 32, one_blocks(GROUP)) w4_fc1_one_
       up += part[w][8 + threadIdx.x];
     }
     const float h = (a.activation ? act_fwd<1>(gate) : act_fwd<0>(gate)) * up;
-    a.h[(size_t)blockIdx.y * a.I + i0 + permuted(threadIdx.x)] = to_bf(h);
+    a.h[(size_t)(token * a.K + blockIdx.y) * a.I + i0 + permuted(threadIdx.x)] = to_bf(h);
   }
 }
 
@@ -621,7 +622,8 @@ __global__ void __launch_bounds__(kThreads, one_blocks(GROUP) / 2) w4_fc2_one_ke
   // The first product's kernel let this one start after every earlier kernel had
   // finished, and writes neither the routes nor the weights: only h has to wait.
   float p_lane;
-  const int e_lane = one_route(a, lane, &p_lane);
+  const int token = blockIdx.y;
+  const int e_lane = one_route(a, token, lane, &p_lane);
   uint32_t routes = __ballot_sync(0xFFFFFFFFu, e_lane >= 0);
   const int r0 = blockIdx.x * 16, per = (a.I + kRowsBlock - 1) / kRowsBlock;
   const int total = __popc(routes) * per;
@@ -640,7 +642,7 @@ __global__ void __launch_bounds__(kThreads, one_blocks(GROUP) / 2) w4_fc2_one_ke
     if (!waited) griddep_wait();
     waited = true;
     const uint32_t hs = smem_u32(dynamic) + (uint32_t)(r * per + b0) * 256u;
-    lay_out<true>(hs, a.h + (size_t)r * a.I, c0, c1, lane);
+    lay_out<true>(hs, a.h + (size_t)(token * a.K + r) * a.I, c0, c1, lane);
     o.run(hs, 0, 1);
     lo = fmaf(p, o.sum[0][0][0], lo);  // of the token in lane t = 0
     hi = fmaf(p, o.sum[0][1][0], hi);
@@ -655,7 +657,7 @@ __global__ void __launch_bounds__(kThreads, one_blocks(GROUP) / 2) w4_fc2_one_ke
   }
   __syncthreads();
   if (threadIdx.x < 16) {
-    const int c = r0 + threadIdx.x;
+    const size_t c = (size_t)token * a.H + r0 + threadIdx.x;
     float v = a.add ? bf(a.add[c]) : 0.0f;
 #pragma unroll
     for (int w = 0; w < kWarps; ++w) v += part[w][threadIdx.x];
@@ -1050,10 +1052,10 @@ cudaError_t matvec_one(const uint16_t* x, const uint8_t* q, const uint16_t* scal
 
 template <int GROUP>
 cudaError_t ffn_one(const W4Args& a, cudaStream_t s) {
-  const cudaError_t err = launch_pdl(w4_fc1_one_kernel<GROUP>, dim3(a.I / 8, a.K), dim3(kOneWarps * 32),
+  const cudaError_t err = launch_pdl(w4_fc1_one_kernel<GROUP>, dim3(a.I / 8, a.K, a.N), dim3(kOneWarps * 32),
                                      (size_t)(a.H + 127) / 128 * 256, s, a);
   if (err != cudaSuccess) return err;
-  return launch_pdl(w4_fc2_one_kernel<GROUP>, dim3(a.H / 16), dim3(kThreads),
+  return launch_pdl(w4_fc2_one_kernel<GROUP>, dim3(a.H / 16, a.N), dim3(kThreads),
                     (size_t)a.K * ((a.I + 127) / 128) * 256, s, a);
 }
 
@@ -1081,11 +1083,28 @@ int launch_w4_matvec(const uint16_t* x, const uint8_t* q, const uint16_t* scale,
 
 int64_t w4_workspace_bytes(int N, int K, int H, int I) { return (int64_t)w4_layout(N, K, H, I).total; }
 
+// Each token for itself, as if it were the only one: two launches instead of four, but
+// an expert's weights are read for each token that names it. Where few routes share an
+// expert (as many as E experts chosen evenly would give), or experts are small: 2 tokens
+// of 128 experts of 2048 x 768, group 64, 15 us against 22, 6 (16.5 MB read again) 37.5
+// and 39.8, 8 (30 MB) 47 and 44.5; 16 of 8 experts of 512 x 352 10 and 12.7.
+constexpr int kAloneTokens = 32;
+constexpr double kAloneBytes = 16 << 20;
+
+static bool token_by_token(const W4Args& a) {
+  if (a.N == 1) return true;
+  if (a.N > kAloneTokens) return false;
+  double none = 1.0;  // that no token names an expert
+  for (int t = 0; t < a.N; ++t) none *= 1.0 - (double)a.K / a.E;
+  const double again = (double)a.N * a.K - a.E * (1.0 - none);
+  return again * 3.0 * a.H * a.I * (0.5 + 2.0 / a.group) <= kAloneBytes;
+}
+
 int launch_w4_ffn(const W4Args& args, cudaStream_t s) {
   W4Args a = args;
   a.h = reinterpret_cast<uint16_t*>(a.ws + w4_layout(a.N, a.K, a.H, a.I).h);
   cudaError_t err;
-  if (a.N == 1 && (size_t)a.H * 2 <= kOneBytes && (size_t)a.K * ((a.I + 127) / 128) * 256 <= kOneBytes) {
+  if (token_by_token(a) && (size_t)a.H * 2 <= kOneBytes && (size_t)a.K * ((a.I + 127) / 128) * 256 <= kOneBytes) {
     err = a.group == 128 ? ffn_one<128>(a, s) : a.group == 64 ? ffn_one<64>(a, s) : ffn_one<32>(a, s);
     return err != cudaSuccess ? -(int)err : 2;
   }

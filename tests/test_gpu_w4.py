@@ -202,6 +202,21 @@ def test_one_expert_twice_for_a_token_and_one_for_all():
     b.check()
 
 
+@pytest.mark.parametrize("n", [3, 7, 40])
+def test_routes_of_all_kinds_in_one_batch(n):
+    """Tokens with an expert twice or three times, an id out of range (and a
+    probability that must not count), no expert at all, and all the same one."""
+    b = Batch(n, 256, 6, 4, 192, 64)
+    b.ids[0] = torch.tensor([2, 5, 2, 2], dtype=torch.int32, device=DEV)
+    b.ids[1] = torch.tensor([-1, 3, 6, 3], dtype=torch.int32, device=DEV)
+    b.p[1, 0], b.p[1, 2] = math.nan, math.inf
+    b.ids[2] = -1
+    b.ids[4:] = torch.tensor([5, 5, 0, 1], dtype=torch.int32, device=DEV)
+    b.run()
+    b.check()
+    assert torch.equal(b.y[2], b.add[2])
+
+
 @pytest.mark.parametrize("n", [1, 6, 50])
 def test_same_result_every_time_on_another_stream_and_in_place(n):
     b = Batch(n, 512, 16, 4, 256, 64)
