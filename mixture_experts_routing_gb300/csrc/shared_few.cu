@@ -301,14 +301,18 @@ int max_clusters(int S, cudaError_t* err) {
 template <bool GATED, int ACT>
 cudaError_t launch(const void* w, int64_t w_rows, const void* x, int K, FewParams p, cudaStream_t s) {
   p.m_tiles = (p.M + (GATED ? 63 : 127)) / (GATED ? 64 : 128);
-  // tiles of 64 tokens while few enough that clusters still split each: their sums
-  // pass through shared memory in half the time (128 tokens, 2048 x 768: 17.4 ->
-  // 14.9 us); else each further tile reads the weights again (200 tokens, 7168 x
-  // 2048: 45.5 us in tiles of 64, 35.3 in tiles of 128)
-  int n_tiles = (p.N + 63) / 64;
-  if (p.m_tiles * n_tiles > 60) n_tiles = (p.N + kMaxTok - 1) / kMaxTok;
-  p.n_tok = ((p.N + n_tiles - 1) / n_tiles + 15) / 16 * 16;
   p.k_tiles = (K + kBK - 1) / kBK;
+  // Tokens of a tile: 64 while the tiles are few enough that clusters still split each:
+  // their sums pass through shared memory in half the time (128 tokens, 2048 x 768: 17.4
+  // -> 14.9 us); else each further tile reads the weights again (200 tokens, 7168 x 2048:
+  // 45.5 us in tiles of 64, 35.3 in tiles of 128). Short contractions, which are not
+  // split: fewer tokens instead (100 tokens, 304 x 256: 11.6 us in tiles of 64, 8.6 of 16;
+  // 64 tokens, 2048 x 768: 11.3 and 13.0).
+  const int parts = p.k_tiles < 6 ? 1 : p.k_tiles < 15 ? p.k_tiles / 3 : 5;
+  int tok = parts == 1 ? 16 : parts < 4 ? 32 : 64;
+  while (tok < kMaxTok && p.m_tiles * ((p.N + tok - 1) / tok) > 300 / parts) tok *= 2;
+  const int n_tiles = (p.N + tok - 1) / tok;
+  p.n_tok = ((p.N + n_tiles - 1) / n_tiles + 15) / 16 * 16;
   p.tmem_cols = 32;
   while ((int)p.tmem_cols < p.n_tok) p.tmem_cols *= 2;
   const int tiles = p.m_tiles * n_tiles;
