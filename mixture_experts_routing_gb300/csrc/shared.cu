@@ -4,9 +4,11 @@
 //   gated      D = x W13^T      epilogue h = act(g) u, 8-bit checkpoint of g, u
 //   out        D = h W2^T       epilogue (+ add)
 //   gated bwd  D = dy W2        epilogue dg, du and h from the checkpoint
-//   out        D = [dg du] W13 (+ add), [dg du]^T x and dy^T h in one launch: they
+//   gradients  D = [dg du] W13 (+ add), [dg du]^T x and dy^T h in one launch: they
 //              need nothing of one another, and one list of their tiles leaves one
 //              partly filled turn of the SMs instead of three
+// Where the backward's tiles are too few for the SMs, the pairs of a cluster share a
+// tile's contraction (SHARED).
 // A and B are read as they lie in memory: K-major, or MN-major where the
 // contraction index is the row of the matrix (no transposed copy is written).
 //
