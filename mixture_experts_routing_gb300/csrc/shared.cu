@@ -696,25 +696,38 @@ double pick_width(Problem* pr, int n, int pairs, bool gated, bool mn, int step) 
   return least;
 }
 
-// One contraction whose tiles are too few for the SMs: the pairs of a cluster share a
+// Contractions whose tiles are too few for the SMs: the pairs of a cluster share a
 // tile, each a part of the contraction, and each adds up some of its columns from all
 // (a tile for each cluster then, not a list for each pair). Sets the width and returns
 // the pairs of a cluster. Backward, 64 tokens: 7168 x 2048 96 us without, 65 with;
-// 1024 x 352 18.7 and 17.9; 1000 tokens, 4096 x 1408 75 and 70.
+// 1024 x 352 18.7 and 17.9; 1000 tokens, 4096 x 1408 75 and 70; 4000 tokens, 256 x 128,
+// whose weight gradients are a few long contractions, 32 and 25.
 template <int EPI, int ACT>
-int pick_split(Problem& P, double* cost, cudaError_t* err) {
-  int pairs = max_clusters<EPI, ACT, false>(1, err), best = 1, w = 128;
+int pick_split(Problem* pr, int n, int step, double* cost, cudaError_t* err) {
+  const int pairs = max_clusters<EPI, ACT, false>(1, err);
   if (pairs <= 0) return 0;
-  *cost = pick_width(&P, 1, pairs, false, true, 16);
-  w = P.w;
-  if ((int64_t)P.m_tiles * P.n_tiles < pairs)
-    for (int split = 2; split <= kMaxSplit && split <= P.k_tiles; ++split) {
+  *cost = pick_width(pr, n, pairs, false, true, step);
+  int best = 1, w = pr[0].w, shortest = pr[0].k_tiles;
+  int64_t tiles = 0;
+  for (int i = 0; i < n; ++i) {
+    tiles += (int64_t)pr[i].m_tiles * pr[i].n_tiles;
+    shortest = pr[i].k_tiles < shortest ? pr[i].k_tiles : shortest;
+  }
+  if (tiles < pairs)
+    for (int split = 2; split <= kMaxSplit && split <= shortest; ++split) {
       const int clusters = max_clusters<EPI, ACT, true>(split, err);
       if (*err != cudaSuccess) return 0;
-      for (int v = 128; v >= 64; v -= 16) {
-        set_width(P, v, false);
-        if ((int64_t)P.m_tiles * P.n_tiles > clusters) continue;
-        const double c = tile_cost(v, (P.k_tiles + split - 1) / split, true) + kShareCost * (split - 1);
+      for (int v = 128; v >= 64; v -= step) {
+        double longest = 0;
+        tiles = 0;
+        for (int i = 0; i < n; ++i) {
+          set_width(pr[i], v, false);
+          tiles += (int64_t)pr[i].m_tiles * pr[i].n_tiles;
+          const double c = tile_cost(v, (pr[i].k_tiles + split - 1) / split, true);
+          longest = c > longest ? c : longest;
+        }
+        if (tiles > clusters) continue;
+        const double c = longest + kShareCost * (split - 1);
         if (c < 0.97 * *cost) {
           *cost = c;
           best = split;
@@ -722,7 +735,7 @@ int pick_split(Problem& P, double* cost, cudaError_t* err) {
         }
       }
     }
-  set_width(P, w, false);
+  for (int i = 0; i < n; ++i) set_width(pr[i], w, false);
   return best;
 }
 
@@ -802,7 +815,7 @@ cudaError_t backward(const SharedArgs& a, cudaStream_t s, int* launches) {
   p.problems = 1;
   p.pr[0] = problem(a.N, a.I, a.H);
   double cost;
-  p.split = pick_split<kGatedBwd, ACT>(p.pr[0], &cost, &err);
+  p.split = pick_split<kGatedBwd, ACT>(p.pr, 1, 16, &cost, &err);
   if (p.split <= 0) return err != cudaSuccess ? err : cudaErrorUnknown;
   int pairs = max_clusters<kGatedBwd, ACT, false>(1, &err);
   p.ck_in = a.ck;
@@ -829,11 +842,12 @@ cudaError_t backward(const SharedArgs& a, cudaStream_t s, int* launches) {
   p.pr[i13] = dw[0];
   p.pr[i2] = dw[1];
   p.problems = 3;
-  cost = pick_width(p.pr, 3, pairs, false, true, 32);
+  p.split = pick_split<kGrads, 0>(p.pr, 3, 32, &cost, &err);
+  if (p.split <= 0) return err != cudaSuccess ? err : cudaErrorUnknown;
   // few tokens: dx's few tiles of a long contraction would outlast all others, so they
   // are shared out in a launch of their own
   double alone = 0;
-  const int split = pick_split<kGrads, 0>(dx, &alone, &err);
+  const int split = pick_split<kGrads, 0>(&dx, 1, 16, &alone, &err);
   if (split <= 0) return err != cudaSuccess ? err : cudaErrorUnknown;
   if (split > 1 && alone + kLaunchCost + pick_width(dw, 2, pairs, false, true, 32) < cost) {
     MmaParams o{};
@@ -852,6 +866,7 @@ cudaError_t backward(const SharedArgs& a, cudaStream_t s, int* launches) {
     p.pr[0] = dw[0];
     p.pr[1] = dw[1];
     p.problems = 2;
+    p.split = 1;
     ix = -1;
     i13 = 0;
     i2 = 1;

@@ -318,17 +318,13 @@ cudaError_t launch(const void* w, int64_t w_rows, const void* x, int K, FewParam
   const int tiles = p.m_tiles * n_tiles;
   // CTAs a tile: the most whose clusters all run at once, with three stages each at
   // least (500 tokens, 4096 x 1408, gated: two 39 us, three 37, four 46: a second turn)
-  int S = 1;
-  for (int s2 = 2; s2 <= 8 && p.k_tiles >= 3 * s2; ++s2) {
+  int S = p.k_tiles / 3 < 8 ? p.k_tiles / 3 : 8;
+  if (S < 1) S = 1;
+  for (;; --S) {  // the query also asks for the shared memory
     cudaError_t err = cudaSuccess;
-    const int most = max_clusters<GATED, ACT>(s2, &err);
+    const int most = max_clusters<GATED, ACT>(S, &err);
     if (err != cudaSuccess) return err;
-    if (tiles <= most) S = s2;
-  }
-  if (S == 1) {  // the shared-memory opt-in
-    cudaError_t err = cudaSuccess;
-    max_clusters<GATED, ACT>(1, &err);
-    if (err != cudaSuccess) return err;
+    if (S == 1 || tiles <= most) break;
   }
   const uint32_t stage = kABytes + (uint32_t)p.n_tok * 128u, sums = (uint32_t)p.n_tok * kBM * 4u;
   p.stages = (int)(kRing / stage);

@@ -178,6 +178,7 @@ def test_backward(n, h, i, act):
 @pytest.mark.parametrize("grad_f32", [0, 1])
 @pytest.mark.parametrize("n,h,i", [
     (1, 5120, 896), (5, 7168, 64), (64, 4096, 2048), (77, 2056, 160), (130, 1032, 1408), (300, 4096, 1408), (1000, 4096, 1408), (700, 264, 2048),
+    (1935, 304, 256), (4000, 256, 128), (2001, 520, 512),
 ])
 def test_backward_of_long_contractions(n, h, i, grad_f32):
     """Tiles too few for the SMs: a cluster's pairs share their contractions."""
