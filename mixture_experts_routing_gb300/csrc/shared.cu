@@ -554,7 +554,11 @@ __global__ void __launch_bounds__(kThreads, 1)
           mbar_arrive(smem_u32(&tmem_empty_bar[b]));
         else
           mbar_arrive_remote_relaxed(mapa_shared(smem_u32(&tmem_empty_bar[b]), even));
+        // the store of an f32 chunk reads both boxes, and a bf16 chunk of the next tile
+        // waits for all stores but the newest only
+        if (EPI == kGrads && P.f32) bulk_wait_read<0>();
       }
+      __syncwarp();
     }
     if (lane == 0) bulk_wait_all();
     __syncwarp();
