@@ -1094,9 +1094,10 @@ constexpr double kAloneBytes = 16 << 20;
 static bool token_by_token(const W4Args& a) {
   if (a.N == 1) return true;
   if (a.N > kAloneTokens) return false;
+  const int chosen = a.K < a.E ? a.K : a.E;  // experts of a token: it reads one named again once
   double none = 1.0;  // that no token names an expert
-  for (int t = 0; t < a.N; ++t) none *= 1.0 - (double)a.K / a.E;
-  const double again = (double)a.N * a.K - a.E * (1.0 - none);
+  for (int t = 0; t < a.N; ++t) none *= 1.0 - (double)chosen / a.E;
+  const double again = (double)a.N * chosen - a.E * (1.0 - none);
   return again * 3.0 * a.H * a.I * (0.5 + 2.0 / a.group) <= kAloneBytes;
 }
 
