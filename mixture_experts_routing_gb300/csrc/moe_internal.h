@@ -41,6 +41,20 @@ inline cudaError_t once_per_device(DeviceOnce& o, int* value, Fn fn) {
   return cudaSuccess;
 }
 
+// The same for a count that may be 0 (clusters resident at once): kept plus one, so
+// that 0 stays 0 and is not asked for again.
+template <class Fn>
+inline cudaError_t count_per_device(DeviceOnce& o, int* count, Fn fn) {
+  int v = 0;
+  const cudaError_t err = once_per_device(o, &v, [&](int dev, int* n) {
+    const cudaError_t e = fn(dev, n);
+    ++*n;
+    return e;
+  });
+  *count = err == cudaSuccess ? v - 1 : 0;
+  return err;
+}
+
 // Launch of a forward-path kernel with programmatic stream serialization: it
 // may start (setup, then griddep_wait) while the previous kernel in the
 // stream finishes, which hides the launch gap between the six kernels of a

@@ -607,13 +607,13 @@ void set_cluster(cudaLaunchAttribute& a, int ctas) {
   a.val.clusterDim.y = a.val.clusterDim.z = 1;
 }
 
-// Clusters of `split` pairs resident at once, and the kernel's shared-memory opt-in,
-// once per device.
+// Clusters of `split` pairs resident at once (0 where one does not fit), and the kernel's
+// shared-memory opt-in, once per device.
 template <int EPI, int ACT, bool SHARED>
 int max_clusters(int split, cudaError_t* err) {
   static DeviceOnce once[kMaxSplit + 1];
   int n = 0;
-  *err = once_per_device(once[split], &n, [&](int, int* v) {
+  *err = count_per_device(once[split], &n, [&](int, int* v) {
     auto* k = shared_mma_kernel<EPI, ACT, SHARED>;
     cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                          (int)kSmemBytes);
@@ -628,7 +628,7 @@ int max_clusters(int split, cudaError_t* err) {
     cfg.numAttrs = 1;
     return cudaOccupancyMaxActiveClusters(v, k, &cfg);
   });
-  return *err == cudaSuccess ? n : 0;
+  return n;
 }
 
 Problem problem(int M, int N, int64_t K, bool amn = false) {

@@ -273,13 +273,13 @@ __global__ void __launch_bounds__(kThreads)
   }
 }
 
-// Clusters of S CTAs of this kernel that run at once, once per device: two CTAs an SM
-// (the query counts one, since the kernel allocates tensor memory).
+// Clusters of S CTAs of this kernel that run at once (0 where one does not fit), once per
+// device: two CTAs an SM (the query counts one, since the kernel allocates tensor memory).
 template <bool GATED, int ACT>
 int max_clusters(int S, cudaError_t* err) {
   static DeviceOnce once[9];
   int n = 0;
-  *err = once_per_device(once[S], &n, [&](int, int* v) {
+  *err = count_per_device(once[S], &n, [&](int, int* v) {
     auto* k = shared_few_kernel<GATED, ACT>;
     cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, kRing + 1024);
     if (e != cudaSuccess) return e;
@@ -295,7 +295,7 @@ int max_clusters(int S, cudaError_t* err) {
     cfg.numAttrs = 1;
     return cudaOccupancyMaxActiveClusters(v, k, &cfg);
   });
-  return *err == cudaSuccess ? 2 * n : 0;
+  return 2 * n;
 }
 
 template <bool GATED, int ACT>
