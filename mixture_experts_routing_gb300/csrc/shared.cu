@@ -308,6 +308,12 @@ __global__ void __launch_bounds__(kThreads, 1)
         __syncwarp();
       }
     }
+    // neither CTA leaves with a copy under way, after a wait that ran out too: both CTAs'
+    // signal the even one's barriers
+    if (crank == 0)
+      for (uint32_t j = g > kStages ? g - kStages : 0; j < g; ++j)
+        if (!mbar_wait_cluster_warp(smem_u32(&full_bar[j % kStages]), (j / kStages) & 1u, p.err, kErrWaitFull))
+          break;
     __syncwarp();
     if (SHARED) cluster_sync_all();
   } else if (warp == 1) {
@@ -385,6 +391,10 @@ __global__ void __launch_bounds__(kThreads, 1)
           tma_load_2d_pair(buf0 + box * 2048u, mx, T.n + 32 * c, row0, bar);
         }
       };
+      auto added = [&](uint32_t i) {  // waits for that load
+        const uint32_t box = (turn + i) & 1u, use = adds[box]++;
+        return mbar_wait_warp(smem_u32(&add_bar[ew][box]), use & 1u, p.err, kErrWaitAccum);
+      };
       if (add && first < chunks) {  // under the tile's MMAs: the first two chunks of what is added
         if (lane == 0) bulk_wait_read<0>();
         __syncwarp();
@@ -406,7 +416,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       };
       load_kept(first);
-      if (!mbar_wait_cluster_warp(smem_u32(&tmem_full_bar[b]), bu & 1u, p.err, kErrWaitAccum)) break;
+      if (!mbar_wait_cluster_warp(smem_u32(&tmem_full_bar[b]), bu & 1u, p.err, kErrWaitAccum)) {
+        if (add && first < chunks) added(0);
+        if (add && first + step < chunks) added(1);
+        break;
+      }
       tc_fence_after();
       if (SHARED) {
         // the other pairs' chunks to where they read them: the stages, whose last MMA is done
@@ -464,8 +478,11 @@ __global__ void __launch_bounds__(kThreads, 1)
           store_box(mo, buf0, col, row0, lane);
         } else if constexpr (EPI == kOut || EPI == kGrads) {
           if (add) {
-            const uint32_t use = adds[odd]++;
-            if (!mbar_wait_warp(smem_u32(&add_bar[ew][odd]), use & 1u, p.err, kErrWaitAccum)) break;
+            if (!added(nth)) {
+              if (c + step < chunks) added(nth + 1);
+              t = tiles;  // the last tile of this warp
+              break;
+            }
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
               const uint4 w = ld_shared_v4(buf + at64(lane, j));

@@ -176,7 +176,8 @@ __global__ void __launch_bounds__(kThreads)
       if (!p.early) load_w(i);
       load_x(i);
     }
-    for (int i = ahead; i < kt; ++i) {
+    int i = ahead;
+    for (; i < kt; ++i) {
       if (!mbar_wait_warp(smem_u32(&empty_bar[i % p.stages]), (uint32_t)(i / p.stages - 1) & 1u, p.err,
                           kErrWaitEmpty))
         break;
@@ -184,6 +185,10 @@ __global__ void __launch_bounds__(kThreads)
       load_x(i);
       __syncwarp();
     }
+    // the block leaves with no copy under way, after a wait that ran out too
+    for (int j = max(0, i - p.stages); j < i; ++j)
+      if (!mbar_wait_warp(smem_u32(&full_bar[j % p.stages]), (uint32_t)(j / p.stages) & 1u, p.err, kErrWaitFull))
+        break;
   } else if (warp == 1) {
     // ------------------------------------------------------------ MMA issuer
     const uint32_t idesc = idesc_bf16_f32(kBM, p.n_tok);
