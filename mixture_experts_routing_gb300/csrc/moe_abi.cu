@@ -789,8 +789,6 @@ int moe_shared_backward(const moe_shared_config_t* cfg, const void* x, const voi
 // ---------------------------------------------------------------- 4-bit weights
 static bool w4_group_ok(int group) { return group == 32 || group == 64 || group == 128; }
 
-static constexpr int kW4MaxRoutes = 1024;
-
 int moe_w4_quantize(const void* m, int64_t rows, int cols, int group, void* q, void* scale,
                     cudaStream_t stream) {
   if (rows < 0 || cols <= 0 || !w4_group_ok(group) || cols % group != 0 ||
@@ -808,7 +806,7 @@ int moe_w4_matvec(const void* x, const void* q, const void* scale, int n, int ro
                   int group, void* y, cudaStream_t stream) {
   if (n < 0 || rows <= 0 || cols <= 0 || !w4_group_ok(group) || cols % group != 0)
     return MOE_ERR_INVALID_ARG;
-  if (n > kW4MaxRoutes || rows > (1 << 24) || cols > (1 << 24)) return MOE_ERR_UNSUPPORTED_SHAPE;
+  if (n > moe::kW4MaxRoutes || rows > (1 << 24) || cols > (1 << 24)) return MOE_ERR_UNSUPPORTED_SHAPE;
   if (n == 0) return MOE_OK;
   if (!x || !q || !scale || !y || !aligned16(x) || !aligned16(q) || !aligned16(scale) ||
       !aligned16(y))
@@ -826,7 +824,7 @@ static int check_w4(const moe_w4_config_t* c) {
     return MOE_ERR_INVALID_ARG;
   if (c->n_experts > moe::kMaxExperts || c->top_k > moe::kMaxTopK || c->hidden % c->group != 0 ||
       c->inter % c->group != 0 || c->hidden > (1 << 14) || c->inter > (1 << 14) ||
-      (int64_t)c->n_tokens * c->top_k > kW4MaxRoutes)
+      (int64_t)c->n_tokens * c->top_k > moe::kW4MaxRoutes)
     return MOE_ERR_UNSUPPORTED_SHAPE;
   return MOE_OK;
 }

@@ -30,6 +30,8 @@ int launch_shared_forward(const SharedArgs& a, cudaStream_t s);
 int launch_shared_forward_few(const SharedArgs& a, cudaStream_t s);  // shared_few.cu
 int launch_shared_backward(const SharedArgs& a, cudaStream_t s);
 
+constexpr int kW4MaxRoutes = 1024;  // routes of a decode batch, rows of a product
+
 struct W4Args {
   int N, H, E, K, I, group, activation;
   const int32_t* topk_ids;  // [N,K], -1: no route

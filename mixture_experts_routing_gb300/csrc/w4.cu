@@ -34,8 +34,7 @@ namespace {
 constexpr int kWarps = 8;
 constexpr int kThreads = kWarps * 32;
 constexpr int kShare = 128;       // columns are dealt out to warps in multiples of these
-constexpr int kMaxRoutes = 1024;  // N*K, at most
-constexpr int kChunk = 32;        // tokens that a block of the second product serves
+constexpr int kMaxRoutes = kW4MaxRoutes;  // N*K, at most: the grouping kernel's shared arrays
 
 __device__ __forceinline__ float bf(uint16_t v) { return __uint_as_float((uint32_t)v << 16); }
 __device__ __forceinline__ uint16_t to_bf(float v) {
