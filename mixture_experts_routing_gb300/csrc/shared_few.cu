@@ -27,11 +27,13 @@ namespace {
 constexpr int kBM = 128, kBK = 64;
 constexpr int kThreads = 192;
 constexpr uint32_t kABytes = kBM * kBK * 2;
-constexpr int kMaxStages = 12;
 constexpr int kMaxTok = 128;  // of a tile
 // A ring of about 100 KB leaves room for a second block on the SM, of this kernel or of
 // the next, which fills its own while this one runs.
 constexpr uint32_t kRing = 104u << 10;
+constexpr int kMaxStages = kRing / (kABytes + 16 * kBK * 2);  // of the fewest tokens
+// the sums of a tile take the place of its stages
+static_assert(kRing - (kABytes + kMaxTok * kBK * 2) >= kMaxTok * kBM * 4, "the ring holds the sums");
 
 struct FewParams {
   int N, M;          // tokens; output columns (gated: features)
@@ -116,7 +118,6 @@ __global__ void __launch_bounds__(kThreads)
   __shared__ __align__(8) uint64_t empty_bar[kMaxStages];
   __shared__ __align__(8) uint64_t done_bar;
   __shared__ uint32_t tmem_base_s;
-  __shared__ int failed;
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   uint32_t S;
@@ -135,7 +136,6 @@ __global__ void __launch_bounds__(kThreads)
       mbar_init(smem_u32(&empty_bar[s]), 1);
     }
     mbar_init(smem_u32(&done_bar), 1);
-    failed = 0;
     mbar_fence_init();
   }
   if (warp == 0 && lane == 0) {
@@ -192,13 +192,9 @@ __global__ void __launch_bounds__(kThreads)
   } else if (warp == 1) {
     // ------------------------------------------------------------ MMA issuer
     const uint32_t idesc = idesc_bf16_f32(kBM, p.n_tok);
-    bool ok = true;
     for (int i = 0; i < kt; ++i) {
       const uint32_t s = (uint32_t)(i % p.stages);
-      if (!mbar_wait_warp(smem_u32(&full_bar[s]), (uint32_t)(i / p.stages) & 1u, p.err, kErrWaitFull)) {
-        ok = false;
-        break;
-      }
+      if (!mbar_wait_warp(smem_u32(&full_bar[s]), (uint32_t)(i / p.stages) & 1u, p.err, kErrWaitFull)) break;
       tc_fence_after();
       if (lane == 0) {
         const uint32_t a0 = sbase + s * stage_bytes, b0 = a0 + kABytes;
@@ -209,8 +205,8 @@ __global__ void __launch_bounds__(kThreads)
       }
       __syncwarp();
     }
-    if (!ok && lane == 0) failed = 1;
-    if (lane == 0) umma_commit(smem_u32(&done_bar));  // also after an abort
+    // also after an abort: the outputs are then of no use, and the error word says so
+    if (lane == 0) umma_commit(smem_u32(&done_bar));
     __syncwarp();
     griddep_wait();
   } else {
@@ -331,11 +327,8 @@ cudaError_t launch(const void* w, int64_t w_rows, const void* x, int K, FewParam
     if (err != cudaSuccess) return err;
     if (S == 1 || tiles <= most) break;
   }
-  const uint32_t stage = kABytes + (uint32_t)p.n_tok * 128u, sums = (uint32_t)p.n_tok * kBM * 4u;
+  const uint32_t stage = kABytes + (uint32_t)p.n_tok * 128u;
   p.stages = (int)(kRing / stage);
-  if (p.stages > kMaxStages) p.stages = kMaxStages;
-  uint32_t bytes = (uint32_t)p.stages * stage;
-  if (bytes < sums) bytes = sums;
   CUtensorMap tw, tx;
   if (!make_map(&tw, w, (uint64_t)K, (uint64_t)w_rows, 64, 64) ||
       !make_map(&tx, x, (uint64_t)K, (uint64_t)p.N, 64, (uint32_t)p.n_tok))
@@ -343,7 +336,7 @@ cudaError_t launch(const void* w, int64_t w_rows, const void* x, int K, FewParam
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)(tiles * S));
   cfg.blockDim = dim3(kThreads);
-  cfg.dynamicSmemBytes = bytes + 1024;
+  cfg.dynamicSmemBytes = (uint32_t)p.stages * stage + 1024;
   cfg.stream = s;
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
