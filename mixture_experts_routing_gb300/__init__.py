@@ -632,6 +632,8 @@ def w4_quantize(m, group: int, q, scale, stream=None) -> None:
     bf16 matrix m [rows, cols]."""
     import torch
     rows, cols = m.shape
+    if group <= 0:
+        raise MoEError("moe_w4_quantize", MOE_ERR_INVALID_ARG)
     _refuse("w4_quantize", m=(m, torch.bfloat16, rows, cols), q=(q, torch.uint8, rows, cols // 2),
             scale=(scale, torch.bfloat16, rows, cols // group))
     _check("moe_w4_quantize", lib().moe_w4_quantize(_ptr(m), int(rows), int(cols), int(group),
@@ -643,6 +645,8 @@ class W4Weights:
 
     def __init__(self, w13, w2, group: int = 128, stream=None):
         import torch
+        if group <= 0:
+            raise MoEError("moe_w4_quantize", MOE_ERR_INVALID_ARG)
         E, I2, H = w13.shape
         I = w2.shape[2]
         dev = w13.device
