@@ -41,7 +41,9 @@
  *  - The forward-path kernels are launched with programmatic stream
  *    serialization: each may start its on-chip setup while the previous
  *    kernel in the stream drains, and waits for that kernel to complete
- *    before its first global-memory access, so stream order semantics hold.
+ *    before its first global-memory access (the second kernel of a call may
+ *    read weights and routes earlier: the first one, which waited, writes
+ *    neither), so stream order semantics hold.
  *    Stream capture records these as programmatic edges.
  */
 #ifndef MOE_GB300_H
@@ -460,7 +462,7 @@ int moe_shared_forward(const moe_shared_config_t* cfg, const void* x, const void
 
 /* moe_shared_forward that also writes the checkpoint.
  *  ck    [N,2I] u8 E4M3 codes of g (columns [0,I)) and u (columns [I,2I))
- *  ck_sf [N,2I/32] u8 E8M0 bytes */
+ *  ck_sf [N,2I/32] u8 E8M0 bytes; both 16-byte aligned */
 int moe_shared_forward_train(const moe_shared_config_t* cfg, const void* x, const void* w13,
                              const void* w2, const void* add, void* h, void* y, void* ck,
                              void* ck_sf, cudaStream_t stream);
@@ -476,7 +478,8 @@ int64_t moe_shared_backward_workspace_bytes(const moe_shared_config_t* cfg);
  *         may be dx itself
  *  dx     [N,H] bf16 output
  *  dw13   [2I,H], dw2 [H,I] outputs, bf16 or f32 (cfg->grad_f32), overwritten
- *  workspace/ws_bytes  moe_shared_backward_workspace_bytes, 16-byte aligned
+ *  workspace/ws_bytes  moe_shared_backward_workspace_bytes, 16-byte aligned, as
+ *         all matrices
  * fp32 sums; dg, du and a are rounded to bf16 as operands of the products.
  * Deterministic. */
 int moe_shared_backward(const moe_shared_config_t* cfg, const void* x, const void* w13,
@@ -495,12 +498,13 @@ int moe_shared_backward(const moe_shared_config_t* cfg, const void* x, const voi
 /* Codes and scales of a bf16 matrix of finite values: scale = bf16(max|w| / 7)
  * of the group (1 where that is 0), code = w / scale rounded to nearest even,
  * within -8..7, plus 8.
- *  m [rows, cols] bf16; q [rows, cols/2] u8; scale [rows, cols/group] bf16 */
+ *  m [rows, cols] bf16; q [rows, cols/2] u8; scale [rows, cols/group] bf16; all
+ *  16-byte aligned */
 int moe_w4_quantize(const void* m, int64_t rows, int cols, int group, void* q, void* scale,
                     cudaStream_t stream);
 
 /* y[t,:] = w x[t,:] for n tokens: x [n, cols] bf16, q/scale [rows, cols], y
- * [n, rows] bf16; fp32 sums, rounded once. n 0..1024. x and q 16-byte aligned. */
+ * [n, rows] bf16; fp32 sums, rounded once. n 0..1024. All 16-byte aligned. */
 int moe_w4_matvec(const void* x, const void* q, const void* scale, int n, int rows, int cols,
                   int group, void* y, cudaStream_t stream);
 
@@ -532,7 +536,8 @@ int64_t moe_w4_workspace_bytes(const moe_w4_config_t* cfg);
  *  w2q       [E,H,I/2] u8, w2_scale [E,H,I/group] bf16 (packed w2 rows)
  *  add       [N,H] bf16, or NULL; may be y itself
  *  y         [N,H] bf16 output (add, or 0, for a token without routes)
- *  workspace/ws_bytes  moe_w4_workspace_bytes, 16-byte aligned
+ *  workspace/ws_bytes  moe_w4_workspace_bytes, 16-byte aligned, as all but
+ *            topk_ids and topk_p
  * fp32 sums; the activations are rounded to bf16 between the two products.
  * Deterministic: routes are summed in a fixed order. */
 int moe_w4_ffn_forward(const moe_w4_config_t* cfg, const int32_t* topk_ids, const float* topk_p,

@@ -29,8 +29,10 @@ __device__ __forceinline__ uint64_t globaltimer_ns() {
 // the previous kernel in the stream is still running. griddep_wait() blocks
 // until that kernel has completed and its memory is visible; every kernel of
 // this library that is launched so calls it before its first global-memory
-// access (in every CTA, also in CTAs that leave early). It is a no-op for an
-// ordinary launch. griddep_launch_dependents() lets the next such kernel
+// access (in every CTA, also in CTAs that leave early), but for the second kernels
+// of the shared expert (few tokens) and of the 4-bit experts: these read weights and
+// routes before it, which the first kernel, having waited itself before it let them
+// launch, does not write. It is a no-op for an ordinary launch. griddep_launch_dependents() lets the next such kernel
 // launch; a dependent grid starts only after every CTA of this one has
 // issued it or exited.
 __device__ __forceinline__ void griddep_wait() {
