@@ -545,6 +545,170 @@ int moe_w4_ffn_forward(const moe_w4_config_t* cfg, const int32_t* topk_ids, cons
                        const void* w2_scale, const void* add, void* y, void* workspace,
                        size_t ws_bytes, cudaStream_t stream);
 
+/* ---- The whole layer for a few tokens -----------------------------------------
+ * Router, top-K, experts and combine of a decode step in bf16 (an extension beyond
+ * the pages, whose layer is made for thousands of tokens): dropless, every chosen
+ * expert's weights read once, no slots and no padding. Two launches. */
+
+/* Shape of the layer.
+ *  n_tokens   N  0..64
+ *  hidden     H  multiple of 64, at most 16384
+ *  n_experts  E  1..256
+ *  top_k      K  1..min(E,16)
+ *  inter      I  multiple of 64, at most 16384
+ *  renorm     1 = the K probabilities are divided by their sum, 0 = kept as they are
+ *  activation MOE_ACT_SWIGLU or MOE_ACT_GEGLU */
+typedef struct moe_few_config {
+  int32_t n_tokens;
+  int32_t hidden;
+  int32_t n_experts;
+  int32_t top_k;
+  int32_t inter;
+  int32_t renorm;
+  int32_t activation;
+} moe_few_config_t;
+
+/* Bytes of scratch moe_few_forward needs: logits, h of every route (bf16), its
+ * products (f32), work counters. */
+int64_t moe_few_workspace_bytes(const moe_few_config_t* cfg);
+
+/* y[t] = add[t] + sum_k p'[t,k] W2[e] (act(W_gate[e] x_t) * (W_up[e] x_t)), e the
+ * K experts of the largest probabilities (ties to the lower id), p' as in
+ * moe_route_align.
+ *  x        [N,H] bf16
+ *  w_router [H,E] f32; bias [E] f32 or NULL. A logit of -inf (a bias of -inf) shuts
+ *           an expert out: its probability is 0, and where it is chosen all the same,
+ *           for want of others, its weights are not read. A token whose logits are
+ *           all -inf, or hold a NaN or +inf, has NaN probabilities and a NaN row.
+ *  w13      [E,2I,H] bf16 packed (moe_pack_w13); w2 [E,H,I] bf16 (moe_pack_w2)
+ *  add      [N,H] bf16, or NULL; may be y itself
+ *  n_valid  NULL, or a DEVICE int32 with the number of live tokens n (clamped to
+ *           0..N), read when the kernels run: rows n and up of x and add are not
+ *           read, those of y, topk_ids and topk_p stay as they are. One captured
+ *           graph serves every batch up to N
+ *  y        [N,H] bf16 output
+ *  topk_ids [N,K] i32, topk_p [N,K] f32: the choice, or NULL each
+ *  workspace/ws_bytes  moe_few_workspace_bytes, 16-byte aligned, as all but the
+ *           f32 and i32 arguments. Calls that share it must not overlap
+ * The logits are sums of the products that moe_route_align sums, in fp32 and in
+ * another order: a token whose K-th and next logits are closer than that rounding
+ * may choose another expert than there. fp32 sums; h is rounded to bf16 between the
+ * two products, y once. Deterministic: the order of every sum is fixed by the shape
+ * and the routes. */
+int moe_few_forward(const moe_few_config_t* cfg, const void* x, const float* w_router,
+                    const float* bias, const void* w13, const void* w2, const void* add,
+                    const int32_t* n_valid, void* y, int32_t* topk_ids, float* topk_p,
+                    void* workspace, size_t ws_bytes, cudaStream_t stream);
+
+/* ---- Layer norm --------------------------------------------------------------
+ * What stands in front of the router (an extension beyond the pages): the residual
+ * sum, the norm over a row, and the backward of both.
+ *   s = bf16(x + add); mean, var over the row; r = 1/sqrt(var + eps)
+ *   y = (s - mean) r w + b           kind MOE_NORM_LAYER
+ *   y = s r w + b, var = mean(s^2)   kind MOE_NORM_RMS */
+#define MOE_NORM_LAYER 0
+#define MOE_NORM_RMS 1
+
+/*  n_tokens N  0 or more (N*H may pass 2^31)
+ *  hidden   H  multiple of 8, at most 16384
+ *  eps         at least 0, finite */
+typedef struct moe_norm_config {
+  int32_t n_tokens;
+  int32_t hidden;
+  int32_t kind;
+  float eps;
+} moe_norm_config_t;
+
+/*  x      [N,H] bf16
+ *  add    [N,H] bf16 added to x, or NULL
+ *  weight [H] f32, bias [H] f32 or NULL
+ *  sum    [N,H] bf16 output s, the rows that the backward reads; required with add
+ *         (NULL without); may be x or add
+ *  y      [N,H] bf16 output; may be x or add (not with sum there)
+ *  mean   [N] f32 output (LAYER only), rstd [N] f32 output r: for the backward, or
+ *         NULL each
+ * All 16-byte aligned but mean and rstd. The row stays in registers: mean and var
+ * are two sums over it in fp32, var from the differences to the mean. */
+int moe_norm_forward(const moe_norm_config_t* cfg, const void* x, const void* add,
+                     const float* weight, const float* bias, void* sum, void* y, float* mean,
+                     float* rstd, cudaStream_t stream);
+
+/* Bytes of scratch moe_norm_backward needs: partial sums of dweight and dbias. */
+int64_t moe_norm_backward_workspace_bytes(const moe_norm_config_t* cfg);
+
+/* With z = (s - mean) r and g = dy w:
+ *   dx = r (g - z mean(g z) - mean(g)) (+ dx_add)   (RMS: z = s r, no mean(g))
+ *   dweight = sum over rows of dy z, dbias = sum of dy
+ *  x       [N,H] bf16: the rows that were normed (sum, where there was an add)
+ *  mean    [N] f32 (LAYER; NULL for RMS), rstd [N] f32, from the forward
+ *  dy      [N,H] bf16
+ *  dx_add  [N,H] bf16 added to dx (the residual's gradient), or NULL; may be dx
+ *  dx      [N,H] bf16 output, may be dy; it is the gradient of x and of add alike
+ *  dweight [H] f32 output; dbias [H] f32 output or NULL; overwritten (0 for N = 0)
+ *  workspace/ws_bytes  moe_norm_backward_workspace_bytes; all 16-byte aligned but
+ *          mean and rstd
+ * fp32 sums in an order that the shape and the GPU's number of SMs fix, no atomics.
+ * Deterministic. */
+int moe_norm_backward(const moe_norm_config_t* cfg, const void* x, const float* weight,
+                      const float* mean, const float* rstd, const void* dy, const void* dx_add,
+                      void* dx, float* dweight, float* dbias, void* workspace, size_t ws_bytes,
+                      cudaStream_t stream);
+
+/* ---- AdamW over many tensors ---------------------------------------------------
+ * The step that consumes the gradients of the calls above (an extension beyond the
+ * pages), over any number of tensors in one launch per 240 of them:
+ *   g = grad_scale * grad; m = b1 m + (1-b1) g; v = b2 v + (1-b2) g^2
+ *   p -= lr (m/(1-b1^t) / (sqrt(v/(1-b2^t)) + eps) + weight_decay p)
+ * in fp32. A bf16 weight is the rounding of its f32 master, which the step keeps.
+ *
+ * States in 8 bits: m and sqrt(v) as E4M3 codes, one f32 scale per 256 consecutive
+ * values of a tensor (the last block may be shorter): scale = max|value| / 448,
+ * value = decode(code) * scale. The step computes with the new states before they
+ * are rounded. They are rounded at random, to one of the two nearest codes, with
+ * the probabilities that keep the mean: v changes by 1-b2 of itself a step, far
+ * less than half a code, and would never decay if rounded to the nearest. The
+ * random bits are a hash of (seed, t, first + index), so a step can be repeated.
+ * A block whose largest value is under 2^-100 is stored as zeros; one that holds an
+ * infinity or a NaN gets a NaN scale and reads as NaN. */
+typedef struct moe_adamw_tensor {
+  void* param;       /* f32 without master, bf16 with one; updated */
+  float* master;     /* f32 master of a bf16 param, updated; NULL: param is f32 */
+  const void* grad;  /* f32, or bf16 with grad_bf16 */
+  void* m;           /* f32, or u8 codes with state_bits 8; updated */
+  void* v;
+  float* m_scale;    /* [ceil(n/256)] f32 with state_bits 8, else NULL */
+  float* v_scale;
+  int64_t n;         /* values, 0 or more */
+  int64_t first;     /* index of the first value in the hash (0 or more) */
+  float weight_decay;
+  int32_t grad_bf16;
+} moe_adamw_tensor_t;
+
+/*  lr, beta1, beta2 (0 up to, not including, 1), eps (over 0): finite, the betas in 64
+ *  bits since 1-beta of an f32 beta near 1 has few digits left; state_bits 32 or 8;
+ *  seed of the rounding (8 bits) */
+typedef struct moe_adamw_config {
+  double beta1;
+  double beta2;
+  float lr;
+  float eps;
+  int32_t state_bits;
+  uint32_t seed;
+} moe_adamw_config_t;
+
+/*  tensors    [n_tensors] HOST array, read during the call (at most 2^20)
+ *  lr_dev     NULL, or a DEVICE f32 used instead of cfg->lr (captured graphs)
+ *  grad_scale NULL (1), or a DEVICE f32 (a clipping factor, one over a loss scale).
+ *             Where it holds a NaN or an infinity the step is skipped: nothing is
+ *             written and t does not advance
+ *  steps      DEVICE i32[2], 4-byte aligned: steps[0] = t-1, the steps taken so far,
+ *             advanced by the call; steps[1] is the call's, 0 between calls. Both 0
+ *             at first. Calls that share it must not overlap
+ * param, master, grad, m, v 16-byte aligned. Tensors must not overlap. */
+int moe_adamw_step(const moe_adamw_config_t* cfg, const moe_adamw_tensor_t* tensors,
+                   int n_tensors, const float* lr_dev, const float* grad_scale, int32_t* steps,
+                   cudaStream_t stream);
+
 /* Where moe_route_align leaves the router logits l [N,E] f32 (before the
  * softmax, bias included) inside its workspace; NULL for an invalid config or
  * workspace. Host-side pointer arithmetic only. */

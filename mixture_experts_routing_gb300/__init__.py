@@ -36,6 +36,10 @@ __all__ = [
     "shared_forward_train", "shared_backward",
     "W4Config", "W4Weights", "w4_quantize", "w4_workspace_bytes", "alloc_w4_workspace",
     "w4_matvec", "w4_ffn_forward",
+    "FewConfig", "few_workspace_bytes", "alloc_few_workspace", "few_forward",
+    "NORM_LAYER", "NORM_RMS", "NormConfig", "norm_forward", "norm_backward_workspace_bytes",
+    "alloc_norm_backward_workspace", "norm_backward",
+    "AdamWConfig", "AdamW",
 ]
 
 _PKG = os.path.dirname(os.path.abspath(__file__))
@@ -98,6 +102,40 @@ class W4Config(ctypes.Structure):
     def __init__(self, n_tokens, hidden, n_experts, top_k, inter, group=128,
                  activation=ACT_SWIGLU):
         super().__init__(n_tokens, hidden, n_experts, top_k, inter, group, activation)
+
+
+class FewConfig(ctypes.Structure):
+    """Mirror of moe_few_config_t: the whole layer for at most 64 tokens."""
+    _fields_ = [(n, ctypes.c_int32) for n in ("n_tokens", "hidden", "n_experts", "top_k", "inter",
+                                              "renorm", "activation")]
+
+    def __init__(self, n_tokens, hidden, n_experts, top_k, inter, renorm=1, activation=ACT_SWIGLU):
+        super().__init__(n_tokens, hidden, n_experts, top_k, inter, int(bool(renorm)), activation)
+
+
+NORM_LAYER, NORM_RMS = 0, 1
+
+
+class NormConfig(ctypes.Structure):
+    """Mirror of moe_norm_config_t: rows of a layer norm (NORM_LAYER) or of its form
+    without a mean (NORM_RMS)."""
+    _fields_ = [("n_tokens", ctypes.c_int32), ("hidden", ctypes.c_int32), ("kind", ctypes.c_int32),
+                ("eps", ctypes.c_float)]
+
+    def __init__(self, n_tokens, hidden, kind=NORM_LAYER, eps=1e-5):
+        super().__init__(n_tokens, hidden, kind, eps)
+
+
+class AdamWConfig(ctypes.Structure):
+    """Mirror of moe_adamw_config_t."""
+    _fields_ = [("beta1", ctypes.c_double), ("beta2", ctypes.c_double), ("lr", ctypes.c_float),
+                ("eps", ctypes.c_float), ("state_bits", ctypes.c_int32), ("seed", ctypes.c_uint32)]
+
+
+class _AdamWTensorC(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_void_p) for n in ("param", "master", "grad", "m", "v", "m_scale", "v_scale")] + [
+        ("n", ctypes.c_int64), ("first", ctypes.c_int64), ("weight_decay", ctypes.c_float),
+        ("grad_bf16", ctypes.c_int32)]
 
 
 class _RoutesC(ctypes.Structure):
@@ -177,6 +215,17 @@ def lib():
             getattr(L, name).restype = I64
         for name in ("moe_shared_forward", "moe_shared_forward_train", "moe_shared_backward",
                      "moe_w4_quantize", "moe_w4_matvec", "moe_w4_ffn_forward"):
+            getattr(L, name).restype = I32
+        FP, NP = ctypes.POINTER(FewConfig), ctypes.POINTER(NormConfig)
+        L.moe_few_workspace_bytes.argtypes = [FP]
+        L.moe_few_forward.argtypes = [FP] + [P] * 11 + [SZ, P]
+        L.moe_norm_forward.argtypes = [NP] + [P] * 9
+        L.moe_norm_backward_workspace_bytes.argtypes = [NP]
+        L.moe_norm_backward.argtypes = [NP] + [P] * 10 + [SZ, P]
+        L.moe_adamw_step.argtypes = [ctypes.POINTER(AdamWConfig), P, I32, P, P, P, P]
+        for name in ("moe_few_workspace_bytes", "moe_norm_backward_workspace_bytes"):
+            getattr(L, name).restype = I64
+        for name in ("moe_few_forward", "moe_norm_forward", "moe_norm_backward", "moe_adamw_step"):
             getattr(L, name).restype = I32
         L.moe_pack_w13.argtypes = [CP, P, P, P, P]
         L.moe_pack_w2.argtypes = [CP, P, P, P]
@@ -714,6 +763,198 @@ def w4_ffn_forward(cfg: W4Config, topk_ids, topk_p, x, w13q, w13_scale, w2q, w2_
                                   workspace.data_ptr(), workspace.nbytes, _stream(stream))
     if rc:
         raise MoEError("moe_w4_ffn_forward", rc)
+
+
+# ------------------------------------------------------------------ the layer for a few tokens
+def _on(dev: int, t, dtype, *shape) -> bool:
+    """_is, on this device."""
+    return t.dtype is dtype and t.shape == shape and t.is_contiguous() and t.get_device() == dev
+
+
+def _refuse_on(fn: str, dev: int, stream, **named) -> None:
+    """Names the first argument that is not what the call needs, as _refuse does; an
+    argument that may be None is left out by its caller."""
+    import torch
+    _refuse(fn, **named)
+    if dev < 0 or dev != torch.cuda.current_device():
+        raise ValueError("%s: the tensors are on device %d, the current one is %d" % (
+            fn, dev, torch.cuda.current_device()))
+    for name, (t, *_) in named.items():
+        if t.get_device() != dev:
+            raise ValueError("%s: %s is on device %d, others on %d" % (fn, name, t.get_device(), dev))
+    if stream is not None and stream.device.index != dev:
+        raise ValueError("%s: the stream is of device %d, the tensors on %d" % (fn, stream.device.index, dev))
+
+
+def _here(dev: int, stream) -> bool:
+    """The device is the current one, and the stream (if any) is one of its own."""
+    import torch
+    return dev >= 0 and dev == torch.cuda.current_device() and (stream is None or stream.device.index == dev)
+
+
+def few_workspace_bytes(cfg: FewConfig) -> int:
+    return _q("moe_few_workspace_bytes", cfg)
+
+
+def alloc_few_workspace(cfg: FewConfig, device):
+    import torch
+    return torch.empty(max(few_workspace_bytes(cfg), 256), dtype=torch.uint8, device=device)
+
+
+def few_forward(cfg: FewConfig, x, w_router, bias, w13, w2, y, workspace, add=None, n_valid=None,
+                topk_ids=None, topk_p=None, stream=None) -> None:
+    """The whole layer for a few tokens: router, top-K, experts, combine (+ add, which
+    may be y). n_valid: a device int32 tensor of one value, the live tokens; later rows
+    are left as they are. topk_ids [N,K] i32 and topk_p [N,K] f32 receive the choice."""
+    import torch
+    N, H, E, K, I = cfg.n_tokens, cfg.hidden, cfg.n_experts, cfg.top_k, cfg.inter
+    bf, f32, i32, dev = torch.bfloat16, torch.float32, torch.int32, x.get_device()
+    if not (_on(dev, x, bf, N, H) and _on(dev, w_router, f32, H, E) and (bias is None or _on(dev, bias, f32, E))
+            and _on(dev, w13, bf, E, 2 * I, H) and _on(dev, w2, bf, E, H, I) and _on(dev, y, bf, N, H)
+            and (add is None or _on(dev, add, bf, N, H)) and (n_valid is None or _on(dev, n_valid, i32, 1))
+            and (topk_ids is None or _on(dev, topk_ids, i32, N, K)) and (topk_p is None or _on(dev, topk_p, f32, N, K))
+            and workspace.get_device() == dev and workspace.is_contiguous() and _here(dev, stream)):
+        named = dict(x=(x, bf, N, H), w_router=(w_router, f32, H, E), bias=(bias, f32, E), w13=(w13, bf, E, 2 * I, H),
+                     w2=(w2, bf, E, H, I), y=(y, bf, N, H), add=(add, bf, N, H), n_valid=(n_valid, i32, 1),
+                     topk_ids=(topk_ids, i32, N, K), topk_p=(topk_p, f32, N, K),
+                     workspace=(workspace, workspace.dtype, *workspace.shape))
+        _refuse_on("few_forward", dev, stream, **{k: v for k, v in named.items() if v[0] is not None})
+    rc = lib().moe_few_forward(ctypes.byref(cfg), x.data_ptr(), w_router.data_ptr(), _ptr(bias), w13.data_ptr(),
+                               w2.data_ptr(), _ptr(add), _ptr(n_valid), y.data_ptr(), _ptr(topk_ids), _ptr(topk_p),
+                               workspace.data_ptr(), workspace.nbytes, _stream(stream))
+    if rc:
+        raise MoEError("moe_few_forward", rc)
+
+
+# ------------------------------------------------------------------ layer norm
+def norm_forward(cfg: NormConfig, x, weight, y, bias=None, add=None, sum=None, mean=None, rstd=None,
+                 stream=None) -> None:
+    """y = norm(x + add) * weight + bias, rows [N,H] bf16, weight and bias [H] f32. With
+    add, sum receives x + add (may be x or add): the rows that norm_backward takes, with
+    mean (NORM_LAYER only) and rstd [N] f32."""
+    import torch
+    N, H, bf, f32, dev = cfg.n_tokens, cfg.hidden, torch.bfloat16, torch.float32, x.get_device()
+    if not (_on(dev, x, bf, N, H) and _on(dev, weight, f32, H) and _on(dev, y, bf, N, H)
+            and (bias is None or _on(dev, bias, f32, H)) and (add is None or _on(dev, add, bf, N, H))
+            and (sum is None or _on(dev, sum, bf, N, H)) and (mean is None or _on(dev, mean, f32, N))
+            and (rstd is None or _on(dev, rstd, f32, N)) and _here(dev, stream)):
+        named = dict(x=(x, bf, N, H), weight=(weight, f32, H), y=(y, bf, N, H), bias=(bias, f32, H), add=(add, bf, N, H),
+                     sum=(sum, bf, N, H), mean=(mean, f32, N), rstd=(rstd, f32, N))
+        _refuse_on("norm_forward", dev, stream, **{k: v for k, v in named.items() if v[0] is not None})
+    rc = lib().moe_norm_forward(ctypes.byref(cfg), x.data_ptr(), _ptr(add), weight.data_ptr(), _ptr(bias), _ptr(sum),
+                                y.data_ptr(), _ptr(mean), _ptr(rstd), _stream(stream))
+    if rc:
+        raise MoEError("moe_norm_forward", rc)
+
+
+def norm_backward_workspace_bytes(cfg: NormConfig) -> int:
+    return _q("moe_norm_backward_workspace_bytes", cfg)
+
+
+def alloc_norm_backward_workspace(cfg: NormConfig, device):
+    import torch
+    return torch.empty(max(norm_backward_workspace_bytes(cfg), 256), dtype=torch.uint8, device=device)
+
+
+def norm_backward(cfg: NormConfig, x, weight, mean, rstd, dy, dx, dweight, workspace, dbias=None, dx_add=None,
+                  stream=None) -> None:
+    """Gradients of norm_forward: dx [N,H] bf16 (+ dx_add, which may be dx) of the rows x
+    that were normed (sum, where there was an add), dweight and dbias [H] f32
+    (overwritten). mean: None for NORM_RMS."""
+    import torch
+    N, H, bf, f32, dev = cfg.n_tokens, cfg.hidden, torch.bfloat16, torch.float32, x.get_device()
+    if not (_on(dev, x, bf, N, H) and _on(dev, weight, f32, H) and (mean is None or _on(dev, mean, f32, N))
+            and _on(dev, rstd, f32, N) and _on(dev, dy, bf, N, H) and _on(dev, dx, bf, N, H)
+            and _on(dev, dweight, f32, H) and (dbias is None or _on(dev, dbias, f32, H))
+            and (dx_add is None or _on(dev, dx_add, bf, N, H)) and workspace.get_device() == dev
+            and workspace.is_contiguous() and _here(dev, stream)):
+        named = dict(x=(x, bf, N, H), weight=(weight, f32, H), mean=(mean, f32, N), rstd=(rstd, f32, N), dy=(dy, bf, N, H),
+                     dx=(dx, bf, N, H), dweight=(dweight, f32, H), dbias=(dbias, f32, H), dx_add=(dx_add, bf, N, H),
+                     workspace=(workspace, workspace.dtype, *workspace.shape))
+        _refuse_on("norm_backward", dev, stream, **{k: v for k, v in named.items() if v[0] is not None})
+    rc = lib().moe_norm_backward(ctypes.byref(cfg), x.data_ptr(), weight.data_ptr(), _ptr(mean), rstd.data_ptr(),
+                                 dy.data_ptr(), _ptr(dx_add), dx.data_ptr(), dweight.data_ptr(), _ptr(dbias),
+                                 workspace.data_ptr(), workspace.nbytes, _stream(stream))
+    if rc:
+        raise MoEError("moe_norm_backward", rc)
+
+
+# ------------------------------------------------------------------ AdamW
+class AdamW:
+    """AdamW over a list of tensors and their gradient buffers, one launch a step.
+
+    params: f32 or bf16 CUDA tensors of one device; a bf16 one gets an f32 master.
+    grads: a buffer each, f32 or bf16, of the same shape (those that ffn_backward,
+    router_backward, shared_backward and norm_backward write). Both are used where they
+    lie at every step. weight_decay: one number, or one a tensor. state_bits 32, or 8:
+    E4M3 codes of m and sqrt(v) with one scale per 256 values, rounded at random (by a
+    hash of seed, step and place).
+
+    The state is flat, each tensor from a multiple of 256 on (offsets): m, v (f32, or u8
+    codes), m_scale and v_scale (8 bits: one f32 per 256), master (of the bf16 params
+    alone), and steps [2] i32 on the device (steps[0]: steps taken). Saving these and
+    copying them back into another AdamW of the same list resumes it."""
+
+    def __init__(self, params, grads, lr, betas=(0.9, 0.999), eps=1e-8, weight_decay=0.01, state_bits=32, seed=0):
+        import torch
+        self.params, self.grads = list(params), list(grads)
+        P = len(self.params)
+        decay = list(weight_decay) if isinstance(weight_decay, (list, tuple)) else [weight_decay] * P
+        if len(self.grads) != P or len(decay) != P or P == 0:
+            raise ValueError("AdamW: %d params, %d gradients, %d weight decays" % (P, len(self.grads), len(decay)))
+        if state_bits not in (8, 32):
+            raise ValueError("AdamW: state_bits must be 8 or 32, got %r" % (state_bits,))
+        bf, f32 = torch.bfloat16, torch.float32
+        dev = self.params[0].device
+        for i, (p, g) in enumerate(zip(self.params, self.grads)):
+            for name, t in (("params", p), ("grads", g)):
+                if t.dtype not in (bf, f32) or not t.is_contiguous() or not t.is_cuda or t.device != dev or t.shape != p.shape:
+                    raise ValueError("AdamW: %s[%d] must be a contiguous float32 or bfloat16 tensor of shape %s on %s, got %s %s on %s%s" % (
+                        name, i, tuple(p.shape), dev if dev.type == "cuda" else "a CUDA device", str(t.dtype).replace("torch.", ""),
+                        tuple(t.shape), t.device, "" if t.is_contiguous() else ", not contiguous"))
+        self.device, self.state_bits = dev, state_bits
+        self.cfg = AdamWConfig(betas[0], betas[1], lr, eps, state_bits, seed)
+        self.offsets, moffs, at, mat = [], [], 0, 0
+        for p in self.params:
+            blocks = -(-p.numel() // 256) * 256
+            self.offsets.append(at)
+            moffs.append(mat)
+            at += blocks
+            mat += blocks if p.dtype is bf else 0
+        kind = torch.uint8 if state_bits == 8 else f32
+        self.m, self.v = (torch.zeros(at, dtype=kind, device=dev) for _ in range(2))
+        self.m_scale, self.v_scale = (torch.zeros(at // 256, dtype=f32, device=dev) if state_bits == 8 else None for _ in range(2))
+        self.master = torch.zeros(mat, dtype=f32, device=dev) if any(p.dtype is bf for p in self.params) else None
+        self.steps = torch.zeros(2, dtype=torch.int32, device=dev)
+        self._table = (_AdamWTensorC * P)()
+        size = 1 if state_bits == 8 else 4
+        for i, (p, g) in enumerate(zip(self.params, self.grads)):
+            n, a, ma = p.numel(), self.offsets[i], moffs[i]
+            master = None
+            if p.dtype is bf:
+                self.master[ma: ma + n].copy_(p.detach().view(-1))
+                master = self.master.data_ptr() + 4 * ma
+            scales = [None if s is None else s.data_ptr() + 4 * (a // 256) for s in (self.m_scale, self.v_scale)]
+            self._table[i] = _AdamWTensorC(p.data_ptr(), master, g.data_ptr(), self.m.data_ptr() + size * a,
+                                           self.v.data_ptr() + size * a, *scales, n, a, float(decay[i]), int(g.dtype is bf))
+
+    def step(self, grad_scale=None, lr=None, stream=None) -> None:
+        """One step from the gradients as they are. grad_scale: a device f32 tensor of one
+        value that multiplies them (a NaN or an infinity in it skips the step). lr: a
+        number from now on, or a device f32 tensor of one value for this call."""
+        import torch
+        dev, before = self.steps.get_device(), self.cfg.lr
+        if lr is not None and not isinstance(lr, torch.Tensor):
+            self.cfg.lr, lr = float(lr), None
+        if not ((grad_scale is None or _on(dev, grad_scale, torch.float32, 1)) and (lr is None or _on(dev, lr, torch.float32, 1))
+                and _here(dev, stream)):
+            named = dict(steps=(self.steps, torch.int32, 2), grad_scale=(grad_scale, torch.float32, 1), lr=(lr, torch.float32, 1))
+            _refuse_on("AdamW.step", dev, stream, **{k: v for k, v in named.items() if v[0] is not None})
+        rc = lib().moe_adamw_step(ctypes.byref(self.cfg), ctypes.byref(self._table), len(self._table), _ptr(lr),
+                                  _ptr(grad_scale), self.steps.data_ptr(), _stream(stream))
+        if rc:
+            self.cfg.lr = before
+            raise MoEError("moe_adamw_step", rc)
 
 
 def launch_count() -> int:

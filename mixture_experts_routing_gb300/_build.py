@@ -17,8 +17,9 @@ CSRC = os.path.join(PKG, "csrc")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libmoe.so")
 SOURCES = ["route.cu", "router_mma.cu", "gemm.cu", "wgrad.cu", "combine.cu", "shared.cu", "shared_few.cu", "w4.cu",
-           "moe_abi.cu", "ladder.cu"]
-HEADERS = ["ptx.cuh", "act.cuh", "moe_internal.h", "shared_internal.h", "tmap.h"]
+           "few.cu", "norm.cu", "adamw.cu", "moe_abi.cu", "ladder.cu"]
+HEADERS = ["ptx.cuh", "act.cuh", "moe_internal.h", "shared_internal.h", "layer_internal.h", "route_math.cuh",
+           "tmap.h"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 

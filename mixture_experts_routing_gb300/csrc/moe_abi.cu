@@ -2,10 +2,13 @@
 // carving, and the launch sequence of each entry point. No allocation, no
 // host synchronisation, no device-to-host reads (except moe_device_error, which
 // is documented as a synchronising diagnostic).
+#include <math.h>
+
 #include <atomic>
 #include <mutex>
 
 #include "../../include/moe.h"
+#include "layer_internal.h"
 #include "moe_internal.h"
 #include "shared_internal.h"
 
@@ -31,6 +34,8 @@ uint32_t* error_word_ptr() {
 }
 
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+
+bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
 
 int64_t roundup(int64_t a, int64_t b) { return (a + b - 1) / b * b; }
 
@@ -866,6 +871,194 @@ int moe_w4_ffn_forward(const moe_w4_config_t* cfg, const int32_t* topk_ids, cons
   a.ws = static_cast<uint8_t*>(workspace);
   a.y = static_cast<uint16_t*>(y);
   return finish(moe::launch_w4_ffn(a, stream));
+}
+
+// ---------------------------------------------------------------- the layer for a few tokens
+static int check_few(const moe_few_config_t* c) {
+  if (!c || c->n_tokens < 0 || c->hidden <= 0 || c->n_experts <= 0 || c->top_k <= 0 ||
+      c->top_k > c->n_experts || c->inter <= 0 || (c->renorm != 0 && c->renorm != 1) ||
+      (c->activation != MOE_ACT_SWIGLU && c->activation != MOE_ACT_GEGLU))
+    return MOE_ERR_INVALID_ARG;
+  if (c->n_tokens > moe::kFewMaxTokens || c->n_experts > moe::kMaxExperts ||
+      c->top_k > moe::kMaxTopK || c->hidden % 64 != 0 || c->inter % 64 != 0 ||
+      c->hidden > (1 << 14) || c->inter > (1 << 14))
+    return MOE_ERR_UNSUPPORTED_SHAPE;
+  return MOE_OK;
+}
+
+int64_t moe_few_workspace_bytes(const moe_few_config_t* cfg) {
+  const int rc = check_few(cfg);
+  return rc != MOE_OK ? rc
+                      : moe::few_workspace_bytes(cfg->n_tokens, cfg->hidden, cfg->n_experts, cfg->top_k, cfg->inter);
+}
+
+int moe_few_forward(const moe_few_config_t* cfg, const void* x, const float* w_router,
+                    const float* bias, const void* w13, const void* w2, const void* add,
+                    const int32_t* n_valid, void* y, int32_t* topk_ids, float* topk_p,
+                    void* workspace, size_t ws_bytes, cudaStream_t stream) {
+  const int rc = check_few(cfg);
+  if (rc != MOE_OK) return rc;
+  if (cfg->n_tokens == 0) return MOE_OK;
+  if (!workspace || (int64_t)ws_bytes < moe_few_workspace_bytes(cfg) || !aligned16(workspace))
+    return MOE_ERR_WORKSPACE;
+  if (!x || !w_router || !w13 || !w2 || !y || !aligned16(x) || !aligned16(w13) || !aligned16(w2) ||
+      !aligned16(add) || !aligned16(y) || !aligned4(w_router) || !aligned4(bias) ||
+      !aligned4(n_valid) || !aligned4(topk_ids) || !aligned4(topk_p))
+    return MOE_ERR_INVALID_ARG;
+  moe::FewArgs a{};
+  a.err = error_word_ptr();
+  if (!a.err) return MOE_ERR_CUDA;
+  a.N = cfg->n_tokens;
+  a.H = cfg->hidden;
+  a.E = cfg->n_experts;
+  a.K = cfg->top_k;
+  a.I = cfg->inter;
+  a.renorm = cfg->renorm;
+  a.activation = cfg->activation;
+  a.x = static_cast<const uint16_t*>(x);
+  a.wr = w_router;
+  a.bias = bias;
+  a.w13 = static_cast<const uint16_t*>(w13);
+  a.w2 = static_cast<const uint16_t*>(w2);
+  a.add = static_cast<const uint16_t*>(add);
+  a.n_dev = n_valid;
+  a.y = static_cast<uint16_t*>(y);
+  a.topk_ids = topk_ids;
+  a.topk_p = topk_p;
+  a.ws = static_cast<uint8_t*>(workspace);
+  return finish(moe::launch_few(a, stream));
+}
+
+// ---------------------------------------------------------------- layer norm
+static int check_norm(const moe_norm_config_t* c) {
+  if (!c || c->n_tokens < 0 || c->hidden <= 0 ||
+      (c->kind != MOE_NORM_LAYER && c->kind != MOE_NORM_RMS) || !(c->eps >= 0.0f) ||
+      !isfinite(c->eps))
+    return MOE_ERR_INVALID_ARG;
+  if (c->hidden % 8 != 0 || c->hidden > (1 << 14)) return MOE_ERR_UNSUPPORTED_SHAPE;
+  return MOE_OK;
+}
+
+static moe::NormArgs norm_args(const moe_norm_config_t* cfg) {
+  moe::NormArgs a{};
+  a.N = cfg->n_tokens;
+  a.H = cfg->hidden;
+  a.rms = cfg->kind == MOE_NORM_RMS;
+  a.eps = cfg->eps;
+  return a;
+}
+
+int moe_norm_forward(const moe_norm_config_t* cfg, const void* x, const void* add,
+                     const float* weight, const float* bias, void* sum, void* y, float* mean,
+                     float* rstd, cudaStream_t stream) {
+  const int rc = check_norm(cfg);
+  if (rc != MOE_OK) return rc;
+  if ((add != nullptr) != (sum != nullptr) || (sum && sum == y) ||
+      (cfg->kind == MOE_NORM_RMS && mean))
+    return MOE_ERR_INVALID_ARG;
+  if (cfg->n_tokens == 0) return MOE_OK;
+  if (!x || !weight || !y || !aligned16(x) || !aligned16(add) || !aligned16(weight) ||
+      !aligned16(bias) || !aligned16(sum) || !aligned16(y) || !aligned4(mean) || !aligned4(rstd))
+    return MOE_ERR_INVALID_ARG;
+  moe::NormArgs a = norm_args(cfg);
+  a.x = static_cast<const uint16_t*>(x);
+  a.add = static_cast<const uint16_t*>(add);
+  a.w = weight;
+  a.b = bias;
+  a.sum = static_cast<uint16_t*>(sum);
+  a.y = static_cast<uint16_t*>(y);
+  a.mean = mean;
+  a.rstd = rstd;
+  return finish(moe::launch_norm_forward(a, stream));
+}
+
+int64_t moe_norm_backward_workspace_bytes(const moe_norm_config_t* cfg) {
+  const int rc = check_norm(cfg);
+  return rc != MOE_OK ? rc : moe::norm_backward_workspace_bytes(cfg->n_tokens, cfg->hidden);
+}
+
+int moe_norm_backward(const moe_norm_config_t* cfg, const void* x, const float* weight,
+                      const float* mean, const float* rstd, const void* dy, const void* dx_add,
+                      void* dx, float* dweight, float* dbias, void* workspace, size_t ws_bytes,
+                      cudaStream_t stream) {
+  const int rc = check_norm(cfg);
+  if (rc != MOE_OK) return rc;
+  if (!dweight || !aligned16(dweight) || !aligned16(dbias)) return MOE_ERR_INVALID_ARG;
+  if (cfg->n_tokens == 0) {  // no row: zero gradients
+    if (cudaMemsetAsync(dweight, 0, (size_t)cfg->hidden * 4, stream) != cudaSuccess ||
+        (dbias && cudaMemsetAsync(dbias, 0, (size_t)cfg->hidden * 4, stream) != cudaSuccess))
+      return finish(-1);
+    return MOE_OK;
+  }
+  if (!workspace || (int64_t)ws_bytes < moe_norm_backward_workspace_bytes(cfg) ||
+      !aligned16(workspace))
+    return MOE_ERR_WORKSPACE;
+  if (!x || !weight || !rstd || !dy || !dx || (cfg->kind == MOE_NORM_LAYER) != (mean != nullptr) ||
+      !aligned16(x) || !aligned16(weight) || !aligned4(mean) || !aligned4(rstd) ||
+      !aligned16(dy) || !aligned16(dx_add) || !aligned16(dx))
+    return MOE_ERR_INVALID_ARG;
+  moe::NormArgs a = norm_args(cfg);
+  a.x = static_cast<const uint16_t*>(x);
+  a.add = static_cast<const uint16_t*>(dx_add);
+  a.w = weight;
+  a.mean = const_cast<float*>(mean);
+  a.rstd = const_cast<float*>(rstd);
+  a.dy = static_cast<const uint16_t*>(dy);
+  a.dx = static_cast<uint16_t*>(dx);
+  a.dw = dweight;
+  a.db = dbias;
+  a.part = static_cast<float*>(workspace);
+  return finish(moe::launch_norm_backward(a, stream));
+}
+
+// ---------------------------------------------------------------- AdamW
+int moe_adamw_step(const moe_adamw_config_t* cfg, const moe_adamw_tensor_t* tensors,
+                   int n_tensors, const float* lr_dev, const float* grad_scale, int32_t* steps,
+                   cudaStream_t stream) {
+  if (!cfg || !isfinite(cfg->lr) || !(cfg->beta1 >= 0.0 && cfg->beta1 < 1.0) ||
+      !(cfg->beta2 >= 0.0 && cfg->beta2 < 1.0) || !(cfg->eps > 0.0f) || !isfinite(cfg->eps) ||
+      (cfg->state_bits != 8 && cfg->state_bits != 32) || n_tensors < 0 ||
+      n_tensors > (1 << 20) || (n_tensors > 0 && !tensors) || !steps || !aligned4(steps) ||
+      !aligned4(lr_dev) || !aligned4(grad_scale))
+    return MOE_ERR_INVALID_ARG;
+  const bool small = cfg->state_bits == 8;
+  for (int i = 0; i < n_tensors; ++i) {  // every tensor before the first launch
+    const moe_adamw_tensor_t& t = tensors[i];
+    if (t.n < 0 || t.n > ((int64_t)1 << 40) || t.first < 0 || t.first > ((int64_t)1 << 60) ||
+        !isfinite(t.weight_decay) || (t.grad_bf16 != 0 && t.grad_bf16 != 1))
+      return MOE_ERR_INVALID_ARG;
+    if (t.n == 0) continue;
+    if (!t.param || !t.grad || !t.m || !t.v || !aligned16(t.param) || !aligned16(t.master) ||
+        !aligned16(t.grad) || !aligned16(t.m) || !aligned16(t.v) ||
+        (small && (!t.m_scale || !t.v_scale || !aligned4(t.m_scale) || !aligned4(t.v_scale))))
+      return MOE_ERR_INVALID_ARG;
+  }
+  moe::AdamwArgs a{};
+  a.lr = cfg->lr;
+  a.beta1 = cfg->beta1;
+  a.beta2 = cfg->beta2;
+  a.eps = cfg->eps;
+  a.bits = cfg->state_bits;
+  a.seed = cfg->seed;
+  a.lr_dev = lr_dev;
+  a.grad_scale = grad_scale;
+  a.steps = steps;
+  int done = 0, launched = 0;
+  do {  // one launch a table; a step of no tensors still counts as one
+    moe::AdamwTensor t[moe::kAdamwTensors];
+    int n = 0;
+    for (; done < n_tensors && n < moe::kAdamwTensors; ++done) {
+      const moe_adamw_tensor_t& q = tensors[done];
+      if (q.n > 0)
+        t[n++] = {q.param, q.master,  q.grad, q.m, q.v, q.m_scale, q.v_scale, q.n, q.first, q.weight_decay,
+                  q.grad_bf16};
+    }
+    if (n == 0 && done < n_tensors) continue;
+    const int k = moe::launch_adamw(a, t, n, done == n_tensors, stream);
+    if (k < 0) return finish(k);
+    launched += k;
+  } while (done < n_tensors);
+  return finish(launched);
 }
 
 const char* moe_status_string(int status) {
