@@ -1,16 +1,43 @@
-// The whole layer for a few tokens in bf16.
+// The whole layer for a few tokens in bf16: two kernels.
+//
+//   logits   l[t,e] = x_t . W_r[:,e] + b[e]. A cluster of eight blocks shares the
+//            contraction of 16 experts and adds its parts through distributed shared
+//            memory; on the way it clears the work counters of the second kernel.
+//   experts  every block picks the experts of all tokens for itself (a warp a token),
+//            then the blocks stream the chosen experts' weights, tile by tile:
+//              FC1   8 gate and 8 up rows of an expert times its tokens; h = act(g) u
+//              FC2   16 rows of W_down times the same tokens' h, to o [route][column]
+//            The last block to finish a column tile adds up its tokens' routes.
+//
+// The time is that of reading the weights, so a tile is a run of 16 weight rows that
+// passes once through a ring in shared memory (TMA boxes of 8 rows x 256 columns) into
+// mma.sync, weights as the 16 rows, tokens as the 8 columns: the eight warps split the
+// columns of a stage, so a tile needs no split between blocks, and there are enough tiles
+// to keep all SMs busy from one token on (128-row tiles of the 5th-generation tensor
+// cores would leave 8 experts x 2048 features with fewer tiles than there are turns to
+// share out). A block draws its tiles from one counter, FC1's before FC2's, so a block
+// that waits for an expert's h waits only for tiles that running blocks already hold: the
+// kernel needs no co-residency, and the ring fills with W_down while it waits.
 #include "act.cuh"
 #include "layer_internal.h"
 #include "moe_internal.h"
 #include "ptx.cuh"
 #include "route_math.cuh"
+#include "tmap.h"
 
 namespace moe {
 namespace {
 
+// ---------------------------------------------------------------- workspace
 struct FewWs {
-  size_t logits, ids, p, h, total;
+  size_t logits, count, h, o, total;
 };
+
+constexpr int kMaxUnits = kMaxExperts + kFewMaxTokens * kMaxTopK / 8;  // an expert's tokens, 8 or more at a time
+
+// [0] next tile, [1 + u] parts of unit u's h that are written, then of every 4 columns the
+// units that have been added to o
+__host__ __device__ inline int count_words(int H) { return 1 + kMaxUnits + H / 4; }
 
 FewWs layout(int N, int H, int E, int K, int I) {
   FewWs w{};
@@ -21,120 +48,618 @@ FewWs layout(int N, int H, int E, int K, int I) {
     return at;
   };
   w.logits = take((size_t)N * E * 4);
-  w.ids = take((size_t)N * K * 4);
-  w.p = take((size_t)N * K * 4);
+  w.count = take((size_t)count_words(H) * 4);
   w.h = take((size_t)N * K * I * 2);
+  w.o = take((size_t)N * K * H * 4);
   w.total = off;
   return w;
 }
 
-__global__ void __launch_bounds__(256) few_logits_kernel(const FewArgs a, float* logits) {
-  griddep_wait();
-  griddep_launch_dependents();
-  __shared__ float part[8][32];
-  const int t = blockIdx.y, c = threadIdx.x & 31, s = threadIdx.x >> 5, e = blockIdx.x * 32 + c;
-  if (t >= live_tokens(a.n_dev, a.N)) return;
-  float sum = 0.0f;
-  if (e < a.E)
-    for (int h = s; h < a.H; h += 8)
-      sum = fmaf(__uint_as_float((uint32_t)a.x[(size_t)t * a.H + h] << 16), a.wr[(size_t)h * a.E + e], sum);
-  part[s][c] = sum;
-  __syncthreads();
-  if (s || e >= a.E) return;
-  for (int i = 1; i < 8; ++i) sum += part[i][c];
-  logits[(size_t)t * a.E + e] = sum + (a.bias ? a.bias[e] : 0.0f);
-}
+// ---------------------------------------------------------------- logits
+constexpr int kLogitThreads = 256;
+constexpr int kLogitSplit = 8;   // blocks of a cluster: parts of the contraction
+constexpr int kLogitCols = 16;   // experts of a cluster
+constexpr int kLogitTok = 8;     // tokens at a time
 
-__global__ void __launch_bounds__(32) few_select_kernel(const FewArgs a, const float* logits, int* ids, float* ps) {
+// A thread takes four experts and every 64th pair of rows of the block's part; a row pair
+// of x is one 32-bit load. Four pairs' weights are under way at once: with one, a decode
+// step's 14 rows a thread waited for memory seven times. Chain of a logit: H / 1024
+// pairs, 3 lanes, 8 warps, 8 blocks. blockIdx.y: eight tokens.
+__global__ void __cluster_dims__(kLogitSplit, 1, 1) __launch_bounds__(kLogitThreads)
+    few_logits_kernel(const FewArgs a, float* logits, int32_t* count) {
+  __shared__ float warp_part[8][kLogitTok][kLogitCols];
+  __shared__ __align__(16) float part[kLogitTok][kLogitCols];
   griddep_wait();
   griddep_launch_dependents();
-  const int t = blockIdx.x, lane = threadIdx.x;
-  if (t >= live_tokens(a.n_dev, a.N)) return;
+  if (blockIdx.y == 0)
+    for (int i = blockIdx.x * kLogitThreads + threadIdx.x; i < count_words(a.H); i += gridDim.x * kLogitThreads)
+      count[i] = 0;
+  const int t0 = blockIdx.y * kLogitTok, n = min(kLogitTok, live_tokens(a.n_dev, a.N) - t0);
+  if (n <= 0) return;  // the whole cluster
+  const int rank = blockIdx.x % kLogitSplit, e0 = blockIdx.x / kLogitSplit * kLogitCols;
+  const int q = threadIdx.x & 3, r = threadIdx.x >> 2, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int pairs = a.H / 2, p0 = (int)((int64_t)rank * pairs / kLogitSplit), p1 = (int)((int64_t)(rank + 1) * pairs / kLogitSplit);
+  const int e = e0 + 4 * q;
+  const bool vec = (a.E & 3) == 0 && (reinterpret_cast<uintptr_t>(a.wr) & 15) == 0;
+  constexpr int kStep = kLogitThreads / 4, kAhead = 4;
+  float acc[kLogitTok][4] = {};
+  for (int p = p0 + r; p < p1; p += kAhead * kStep) {
+    float w[kAhead][2][4];
+#pragma unroll
+    for (int s = 0; s < kAhead; ++s) {
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const float* row = a.wr + (size_t)(2 * (p + s * kStep) + i) * a.E + e;
+        const bool in = p + s * kStep < p1;
+        if (vec) {
+          const float4 v = in && e < a.E ? *reinterpret_cast<const float4*>(row) : make_float4(0.f, 0.f, 0.f, 0.f);
+          w[s][i][0] = v.x; w[s][i][1] = v.y; w[s][i][2] = v.z; w[s][i][3] = v.w;
+        } else {
+#pragma unroll
+          for (int j = 0; j < 4; ++j) w[s][i][j] = in && e + j < a.E ? row[j] : 0.0f;
+        }
+      }
+    }
+#pragma unroll
+    for (int t = 0; t < kLogitTok; ++t) {
+      if (t < n) {
+#pragma unroll
+        for (int s = 0; s < kAhead; ++s) {
+          if (p + s * kStep < p1) {
+            const uint32_t x = reinterpret_cast<const uint32_t*>(a.x + (size_t)(t0 + t) * a.H)[p + s * kStep];
+            const float x0 = __uint_as_float(x << 16), x1 = __uint_as_float(x & 0xFFFF0000u);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) acc[t][j] = fmaf(x1, w[s][1][j], fmaf(x0, w[s][0][j], acc[t][j]));
+          }
+        }
+      }
+    }
+  }
+#pragma unroll
+  for (int t = 0; t < kLogitTok; ++t) {
+    if (t < n) {
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+#pragma unroll
+        for (int o = 4; o < 32; o <<= 1) acc[t][j] += __shfl_xor_sync(0xFFFFFFFFu, acc[t][j], o);
+        if (lane < 4) warp_part[warp][t][4 * q + j] = acc[t][j];
+      }
+    }
+  }
+  __syncthreads();
+  if (threadIdx.x < n * kLogitCols) {
+    const int t = threadIdx.x / kLogitCols, c = threadIdx.x % kLogitCols;
+    float s = 0.0f;
+#pragma unroll
+    for (int w = 0; w < 8; ++w) s += warp_part[w][t][c];
+    part[t][c] = s;
+  }
+  cluster_sync_all();
+  const int c = threadIdx.x;
+  if (rank < n && c < kLogitCols && e0 + c < a.E) {  // block `rank` adds up token t0 + rank
+    float s = 0.0f;
+#pragma unroll
+    for (int k = 0; k < kLogitSplit; ++k) {
+      float v;
+      asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(mapa_shared(smem_u32(&part[rank][c]), (uint32_t)k)));
+      s += v;
+    }
+    logits[(size_t)(t0 + rank) * a.E + e0 + c] = s + (a.bias ? a.bias[e0 + c] : 0.0f);
+  }
+  cluster_sync_all();  // no block leaves while another reads its part
+}
+static_assert(kLogitTok <= kLogitSplit, "one token of the chunk per block of the cluster");
+
+// ---------------------------------------------------------------- experts
+constexpr int kMmaWarps = 8, kEpiWarps = 4;
+constexpr int kFewThreads = (kMmaWarps + 2 + kEpiWarps) * 32;
+constexpr int kRows = 16;        // weight rows of a tile
+constexpr int kBoxCols = 256;    // columns of a copy of 8 rows: 4 KB, in 128-byte swizzled pieces of 64 columns
+constexpr uint32_t kBoxBytes = 8 * kBoxCols * 2;
+constexpr int kMaxStages = 8;
+constexpr uint32_t kRingBytes = 209u << 10;  // with the buffers of the sums
+constexpr uint32_t kErrWaitUnit = 1u << 4;  // an expert's h never became complete
+
+struct FewShared {
+  uint64_t wfull[kMaxStages], afull[kMaxStages], empty[kMaxStages], named[kMaxStages], rfull[2], rempty[2];
+  int tile[kMaxStages];            // of the stage, -1: no more
+  int red_tile[2];
+  int ids[kFewMaxTokens * kMaxTopK];
+  float p[kFewMaxTokens * kMaxTopK];
+  uint16_t list[kFewMaxTokens * kMaxTopK];  // routes by expert, tokens ascending
+  uint32_t mask[kMaxExperts][2];   // tokens of an expert
+  uint16_t base[kMaxExperts];      // an expert's first route in list
+  uint16_t unit0[kMaxExperts];     // and its first unit
+  uint16_t unit_e[kMaxUnits], unit_at[kMaxUnits], unit_n[kMaxUnits];
+  uint8_t unit_done[kMaxUnits];    // seen complete by the activations' warp
+  int warp_sum[kMaxExperts / 32][3];
+  int units, most;                 // units; the most tokens of an expert
+};
+
+// The K experts of one token by a warp (as route_align picks them, from fp32
+// probabilities: ties to the lower id). Lane l holds experts l, l+32, ...
+__device__ __forceinline__ void pick(const FewArgs& a, const float* logits, int t, FewShared& s, bool out) {
+  const int lane = threadIdx.x & 31;
   float v[8], top = -INFINITY;
+#pragma unroll
   for (int j = 0; j < 8; ++j) {
     const int e = lane + 32 * j;
-    v[j] = e < a.E ? logits[(size_t)t * a.E + e] : -INFINITY;
-    top = fmaxf(top, v[j]);
+    v[j] = e < a.E ? __ldcg(logits + (size_t)t * a.E + e) : -INFINITY;
   }
+#pragma unroll
+  for (int j = 0; j < 8; ++j) top = fmaxf(top, v[j]);
+#pragma unroll
   for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, o));
   float sum = 0.0f;
+#pragma unroll
   for (int j = 0; j < 8; ++j) {
-    if (lane + 32 * j < a.E) sum += v[j] = route_exp(v[j] - top);
+    v[j] = lane + 32 * j < a.E ? route_exp(__fsub_rn(v[j], top)) : 0.0f;
+    sum += v[j];
   }
+#pragma unroll
   for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, o);
-  uint32_t taken = 0;
+  uint32_t key[8];  // p's bits order like p >= 0; a NaN is above all; taken or absent: 0, below p + 1
+#pragma unroll
+  for (int j = 0; j < 8; ++j)
+    key[j] = lane + 32 * j < a.E ? (__float_as_uint(__fdiv_rn(v[j], sum)) & 0x7FFFFFFFu) + 1u : 0u;
   float d = 0.0f, my_p = 0.0f;
   int my_id = 0;
-  for (int j = 0; j < 8; ++j) v[j] = v[j] / sum;
   for (int k = 0; k < a.K; ++k) {
-    uint32_t best = 0, mine = 0xFFFFFFFFu;
-    for (int j = 0; j < 8; ++j)
-      if (lane + 32 * j < a.E && !((taken >> j) & 1u)) best = max(best, __float_as_uint(v[j]) & 0x7FFFFFFFu);
+    uint32_t best = 0;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) best = max(best, key[j]);
     best = __reduce_max_sync(0xFFFFFFFFu, best);
+    uint32_t mine = 0xFFFFFFFFu;
+#pragma unroll
     for (int j = 7; j >= 0; --j)
-      if (lane + 32 * j < a.E && !((taken >> j) & 1u) && (__float_as_uint(v[j]) & 0x7FFFFFFFu) == best) mine = lane + 32 * j;
+      if (key[j] == best) mine = lane + 32 * j;
     const int e = (int)__reduce_min_sync(0xFFFFFFFFu, mine);
-    if ((e & 31) == lane) taken |= 1u << (e >> 5);
-    const float p = __uint_as_float(best);
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+      if (e == lane + 32 * j) key[j] = 0;
+    const float p = __uint_as_float(best - 1u);
     d += p;
     if (lane == k) { my_id = e; my_p = p; }
   }
   if (lane < a.K) {
-    const float p = a.renorm ? my_p / d : my_p;
-    const size_t at = (size_t)t * a.K + lane;
-    ids[at] = my_id;
-    ps[at] = p;
-    if (a.topk_ids) a.topk_ids[at] = my_id;
-    if (a.topk_p) a.topk_p[at] = p;
+    const float p = a.renorm ? __fdiv_rn(my_p, d) : my_p;
+    const int at = t * a.K + lane;
+    s.ids[at] = my_id;
+    s.p[at] = p;
+    if (p != 0.0f) atomicOr(&s.mask[my_id][t >> 5], 1u << (t & 31));  // p = 0 (or NaN: != 0) : not read
+    if (out && a.topk_ids) a.topk_ids[at] = my_id;
+    if (out && a.topk_p) a.topk_p[at] = p;
   }
 }
 
-// sum of n products of two bf16 rows over a warp's lanes (n a multiple of 8)
-__device__ __forceinline__ float dot_row(const uint16_t* x, const uint16_t* w, int n, int lane) {
-  float s = 0.0f;
-  for (int k = lane * 8; k < n; k += 256) {
-    const uint4 p = *reinterpret_cast<const uint4*>(x + k), q = *reinterpret_cast<const uint4*>(w + k);
-    const uint32_t* pp = &p.x;
-    const uint32_t* qq = &q.x;
+// The units (an expert's tokens, at most `per` at a time) from the masks; all threads.
+// The blocks build the same lists, each for itself.
+__device__ __forceinline__ void build_units(const FewArgs& a, int n, FewShared& s) {
+  const int e = threadIdx.x, lane = e & 31, warp = e >> 5;
+  int c = 0;
+  if (e < kMaxExperts) {
+    c = __popc(s.mask[e][0]) + __popc(s.mask[e][1]);
+    const int most = __reduce_max_sync(0xFFFFFFFFu, c);
+    if (lane == 0) s.warp_sum[warp][2] = most;
+  }
+  __syncthreads();
+  int most = 0;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      s = fmaf(__uint_as_float(pp[i] << 16), __uint_as_float(qq[i] << 16), s);
-      s = fmaf(__uint_as_float(pp[i] & 0xFFFF0000u), __uint_as_float(qq[i] & 0xFFFF0000u), s);
+  for (int w = 0; w < kMaxExperts / 32; ++w) most = max(most, s.warp_sum[w][2]);
+  const int per = most <= 8 ? 8 : most <= 16 ? 16 : 32;
+  const int u = (c + per - 1) / per;
+  int cs = c, us = u;  // inclusive sums over the warp's experts
+  if (e < kMaxExperts) {
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int x = __shfl_up_sync(0xFFFFFFFFu, cs, o), y = __shfl_up_sync(0xFFFFFFFFu, us, o);
+      if (lane >= o) { cs += x; us += y; }
+    }
+    if (lane == 31) { s.warp_sum[warp][0] = cs; s.warp_sum[warp][1] = us; }
+  }
+  __syncthreads();
+  if (e < kMaxExperts) {
+    int c0 = cs - c, u0 = us - u, all = 0;
+#pragma unroll
+    for (int w = 0; w < kMaxExperts / 32; ++w) {
+      if (w < warp) { c0 += s.warp_sum[w][0]; u0 += s.warp_sum[w][1]; }
+      all += s.warp_sum[w][1];
+    }
+    s.base[e] = (uint16_t)c0;
+    for (int i = 0; i < u; ++i) {
+      s.unit_e[u0 + i] = (uint16_t)e;
+      s.unit_at[u0 + i] = (uint16_t)(c0 + i * per);
+      s.unit_n[u0 + i] = (uint16_t)min(per, c - i * per);
+      s.unit_done[u0 + i] = 0;
+    }
+    if (e == 0) { s.units = all; s.most = most; }
+  }
+  __syncthreads();
+  for (int r = threadIdx.x; r < n * a.K; r += kFewThreads) {
+    const int t = r / a.K, id = s.ids[r];
+    const uint32_t m0 = s.mask[id][0], m1 = s.mask[id][1], bit = 1u << (t & 31);
+    if (((t < 32 ? m0 : m1) & bit) == 0 || s.p[r] == 0.0f) continue;
+    const int rank = t < 32 ? __popc(m0 & (bit - 1u)) : __popc(m0) + __popc(m1 & (bit - 1u));
+    s.list[s.base[id] + rank] = (uint16_t)r;
+  }
+  __syncthreads();
+}
+
+__device__ __forceinline__ void ldmatrix4(uint32_t (&r)[4], uint32_t at) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(at)
+               : "memory");
+}
+__device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+__device__ __forceinline__ int ld_acquire(const int32_t* p) {
+  int v;
+  asm volatile("ld.acquire.gpu.global.s32 %0, [%1];" : "=r"(v) : "l"(p) : "memory");
+  return v;
+}
+__device__ __forceinline__ void red_release(int32_t* p) {
+  asm volatile("red.release.gpu.global.add.s32 [%0], 1;" ::"l"(p) : "memory");
+}
+__device__ __forceinline__ int add_acq_rel(int32_t* p) {
+  int v;
+  asm volatile("atom.acq_rel.gpu.global.add.s32 %0, [%1], 1;" : "=r"(v) : "l"(p) : "memory");
+  return v;
+}
+
+// Sizes by the groups of 8 tokens of a unit.
+template <int G>
+struct Ring {
+  static constexpr int kCols = G == 4 ? 256 : 512;  // of a stage; many tokens: fewer, so that several stages fit
+  static constexpr uint32_t kPitch = kCols * 2 + 16;  // of the activations' rows: 16 bytes apart in banks
+  static constexpr uint32_t kWeights = kCols * 2 * kRows;
+  static constexpr uint32_t kStage = (kWeights + kPitch * 8 * G + 1023u) & ~1023u;
+  static constexpr uint32_t kRed = kMmaWarps * G * 512u;  // of one buffer of the sums
+  static constexpr uint32_t kFit = (kRingBytes - 1024u - 2 * kRed) / kStage;
+  static constexpr uint32_t kStages = kFit < kMaxStages ? kFit : kMaxStages;
+};
+
+// A place in the ring: stage, and the parity of its turn.
+template <int G>
+struct Turn {
+  uint32_t st = 0, par = 0;
+  __device__ __forceinline__ void next() {
+    if (++st == Ring<G>::kStages) {
+      st = 0;
+      par ^= 1u;
     }
   }
+};
+
+struct TileOf {
+  int fc2, unit, row;  // row: first feature, or first column
+  int cols;            // contraction
+};
+
+// FC1 tiles: expert by expert, so that the first ones are complete early. FC2 tiles: column
+// tile by column tile, so that outputs are finished all along and not at the end alone.
+__device__ __forceinline__ TileOf tile_of(const FewArgs& a, const FewShared& s, int tile) {
+  TileOf t;
+  const int per = a.I / 8, tiles1 = s.units * per;
+  t.fc2 = tile >= tiles1;
+  if (!t.fc2) {
+    t.unit = tile / per;
+    t.row = (tile - t.unit * per) * 8;
+    t.cols = a.H;
+  } else {
+    const int i = tile - tiles1, c = i / s.units;
+    t.unit = i - c * s.units;
+    t.row = c * kRows;
+    t.cols = a.I;
+  }
+  return t;
+}
+
+// ---------------------------------------------------------------- roles
+template <int G>
+__device__ __forceinline__ void weights_role(const CUtensorMap& tm1, const CUtensorMap& tm2, const FewArgs& a, FewShared& s,
+                                             int32_t* count, int first, uint32_t ring) {
+  using R = Ring<G>;
+  const int lane = threadIdx.x & 31;
+  const int tiles = s.units * (a.I / 8 + a.H / kRows);
+  const uint64_t policy = policy_evict_first();
+  int tile = __shfl_sync(0xFFFFFFFFu, first, 0);
+  uint32_t it = 0;
+  Turn<G> at;
+  bool ok = true;
+  while (ok && tile < tiles) {
+    int next = 0;
+    if (lane == 0) next = atomicAdd(count, 1);  // known by the end of this tile
+    const TileOf t = tile_of(a, s, tile);
+    const int row = s.unit_e[t.unit] * (t.fc2 ? a.H : 2 * a.I) + t.row, second = row + (t.fc2 ? 8 : a.I);
+    const CUtensorMap* tm = t.fc2 ? &tm2 : &tm1;
+    for (int k = 0; k < t.cols; k += R::kCols, ++it, at.next()) {
+      if (it >= R::kStages && !mbar_wait_warp(smem_u32(&s.empty[at.st]), at.par ^ 1u, a.err, kErrWaitEmpty)) { ok = false; break; }
+      if (lane == 0) {
+        const uint32_t bar = smem_u32(&s.wfull[at.st]), dst = ring + at.st * R::kStage;
+        const int boxes = min(R::kCols, t.cols - k + kBoxCols - 1) / kBoxCols;
+        s.tile[at.st] = tile;
+        mbar_arrive(smem_u32(&s.named[at.st]));
+        mbar_arrive_expect_tx(bar, (uint32_t)boxes * 2u * kBoxBytes);  // columns past the end count as zeros
+        for (int i = 0; i < boxes; ++i) {
+          tma_load_3d(dst + i * 2 * kBoxBytes, tm, 0, row, (k + i * kBoxCols) / 64, bar, policy);
+          tma_load_3d(dst + (i * 2 + 1) * kBoxBytes, tm, 0, second, (k + i * kBoxCols) / 64, bar, policy);
+        }
+      }
+      __syncwarp();
+    }
+    tile = __shfl_sync(0xFFFFFFFFu, next, 0);
+  }
+  // the end, told through one more stage; and no copy of this warp is under way when it leaves
+  ok = ok && (it < R::kStages || mbar_wait_warp(smem_u32(&s.empty[at.st]), at.par ^ 1u, a.err, kErrWaitEmpty));
+  if (ok && lane == 0) {
+    s.tile[at.st] = -1;
+    mbar_arrive(smem_u32(&s.named[at.st]));
+    mbar_arrive(smem_u32(&s.wfull[at.st]));
+  }
+  __syncwarp();
+  // the copy before the end's stage has been used; its barrier is a phase further
+  for (uint32_t j = it >= R::kStages ? it - R::kStages + (ok ? 1 : 0) : 0; j < it; ++j)
+    if (!mbar_wait_warp(smem_u32(&s.wfull[j % R::kStages]), (j / R::kStages) & 1u, a.err, kErrWaitFull)) break;
+}
+
+template <int G>
+__device__ __forceinline__ void activations_role(const FewArgs& a, FewShared& s, const int32_t* count, const uint16_t* h, uint32_t ring) {
+  using R = Ring<G>;
+  const int lane = threadIdx.x & 31;
+  int tile = -2, k = 0, rows = 0;
+  TileOf t{};
+  uint64_t from = 0;  // lane i: the row of the unit's token i
+  for (Turn<G> at;; at.next()) {
+    if (!mbar_wait_warp(smem_u32(&s.named[at.st]), at.par, a.err, kErrWaitEmpty)) break;
+    const int now = s.tile[at.st];
+    if (now < 0) {
+      mbar_arrive(smem_u32(&s.afull[at.st]));
+      break;
+    }
+    if (now != tile) {
+      tile = now;
+      k = 0;
+      t = tile_of(a, s, tile);
+      if (t.fc2 && !s.unit_done[t.unit]) {  // h is complete when all tiles of all its features say so
+        const int want = a.I / 8 * kEpiWarps;
+        const uint64_t t0 = globaltimer_ns();
+        bool ok = true;
+        for (uint32_t i = 1; ld_acquire(count + 1 + t.unit) < want; ++i) {
+          if ((i & 255u) == 0u && globaltimer_ns() - t0 > 2000000000ull) {
+            atomicOr(a.err, kErrWaitUnit);
+            ok = false;
+            break;
+          }
+        }
+        ok = __all_sync(0xFFFFFFFFu, ok);
+        if (!ok) break;
+        __threadfence();
+        if (lane == 0) s.unit_done[t.unit] = 1;
+        __syncwarp();
+      }
+      rows = s.unit_n[t.unit];
+      if (lane < rows) {
+        const int r = s.list[s.unit_at[t.unit] + lane];
+        from = reinterpret_cast<uint64_t>(t.fc2 ? h + (size_t)r * a.I : a.x + (size_t)(r / a.K) * a.H);
+      }
+    } else {
+      k += R::kCols;
+    }
+    const int pieces = min(R::kCols, t.cols - k) / 8;
+    const uint32_t dst = ring + at.st * R::kStage + R::kWeights + lane * 16;
+#pragma unroll 4
+    for (int i = 0; i < rows; ++i) {
+      const uint16_t* src = reinterpret_cast<const uint16_t*>(__shfl_sync(0xFFFFFFFFu, from, i)) + k + lane * 8;
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xFFFFFFFFu, s, o);
-  return s;
+      for (int j = 0; j < R::kCols / 8; j += 32)
+        if (lane + j < pieces) cp_async_16(dst + i * R::kPitch + j * 16, src + j * 8, 16);
+    }
+    cp_async_mbar_arrive_noinc(smem_u32(&s.afull[at.st]));
+  }
+  cp_async_wait_all();
+}
+
+// A warp takes an eighth of a stage's columns: 64 (one swizzled piece of a box) or 32.
+template <int G>
+__device__ __forceinline__ void products_role(const FewArgs& a, FewShared& s, uint32_t ring, uint32_t red) {
+  using R = Ring<G>;
+  constexpr int kWarpCols = R::kCols / kMmaWarps, kSteps = kWarpCols / 16;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, col0 = warp * kWarpCols;
+  // weights: rows 0-7 and 8-15 in boxes of their own; 16-byte piece c of row r at (c ^ r) of its 128 bytes
+  const uint32_t wrow = (uint32_t)(col0 / kBoxCols * 2 + ((lane >> 3) & 1)) * kBoxBytes + col0 % kBoxCols / 64 * 1024 + (lane & 7) * 128;
+  uint32_t woff[kSteps];
+#pragma unroll
+  for (int j = 0; j < kSteps; ++j) woff[j] = ring + wrow + (((col0 % 64 / 8 + 2 * j + (lane >> 4)) ^ (lane & 7)) << 4);
+  // activations: two steps of 16 columns at a time
+  const uint32_t boff = ring + R::kWeights + (lane & 7) * R::kPitch + (uint32_t)(col0 * 2 + (lane >> 3) * 16);
+  float acc[G][4];
+  int tile = -2, left = 0, done = 0;
+  for (Turn<G> at;; at.next()) {
+    if (!mbar_wait_warp(smem_u32(&s.wfull[at.st]), at.par, a.err, kErrWaitFull) ||
+        !mbar_wait_warp(smem_u32(&s.afull[at.st]), at.par, a.err, kErrWaitFull))
+      break;
+    const int now = s.tile[at.st];
+    const uint32_t b = done & 1;
+    if (now < 0) {  // the end, for the epilogue too
+      if (done < 2 || mbar_wait_warp(smem_u32(&s.rempty[b]), (done / 2 - 1) & 1u, a.err, kErrWaitAccum)) {
+        if (warp == 0 && lane == 0) s.red_tile[b] = -1;
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_u32(&s.rfull[b]));
+      }
+      break;
+    }
+    if (now != tile) {
+      tile = now;
+      left = tile < s.units * (a.I / 8) ? a.H : a.I;
+#pragma unroll
+      for (int g = 0; g < G; ++g) acc[g][0] = acc[g][1] = acc[g][2] = acc[g][3] = 0.0f;
+    }
+    if (col0 < left) {
+      const uint32_t base = at.st * R::kStage;
+      uint32_t w[kSteps][4], x[G][kSteps / 2][4];
+#pragma unroll
+      for (int j = 0; j < kSteps; ++j) ldmatrix4(w[j], woff[j] + base);
+#pragma unroll
+      for (int g = 0; g < G; ++g)
+#pragma unroll
+        for (int j = 0; j < kSteps / 2; ++j) ldmatrix4(x[g][j], boff + base + g * 8 * R::kPitch + j * 64);
+#pragma unroll
+      for (int j = 0; j < kSteps; ++j)
+#pragma unroll
+        for (int g = 0; g < G; ++g) mma16816(acc[g], w[j], x[g][j / 2][j % 2 * 2], x[g][j / 2][j % 2 * 2 + 1]);
+    }
+    __syncwarp();
+    if (lane == 0) mbar_arrive(smem_u32(&s.empty[at.st]));
+    left -= R::kCols;
+    if (left > 0) continue;
+    // the warps' sums of the tile, [warp][group][row][token]
+    if (done >= 2 && !mbar_wait_warp(smem_u32(&s.rempty[b]), (done / 2 - 1) & 1u, a.err, kErrWaitAccum)) break;
+    if (warp == 0 && lane == 0) s.red_tile[b] = tile;
+#pragma unroll
+    for (int g = 0; g < G; ++g) {
+      const uint32_t to = red + b * R::kRed + (uint32_t)(warp * G + g) * 512u + (lane >> 2) * 32 + (lane & 3) * 8;
+      asm volatile("st.shared.v2.f32 [%0], {%1,%2};" ::"r"(to), "f"(acc[g][0]), "f"(acc[g][1]) : "memory");
+      asm volatile("st.shared.v2.f32 [%0], {%1,%2};" ::"r"(to + 256), "f"(acc[g][2]), "f"(acc[g][3]) : "memory");
+    }
+    __syncwarp();
+    if (lane == 0) mbar_arrive(smem_u32(&s.rfull[b]));
+    ++done;
+  }
+}
+
+// FC1: a warp's two of the eight features; FC2: its four of the 16 columns.
+template <int ACT, int G>
+__device__ __forceinline__ void outputs_role(const FewArgs& a, FewShared& s, int n, int32_t* count, uint16_t* h, float* o,
+                                             const float* red) {
+  using R = Ring<G>;
+  const int w = (threadIdx.x >> 5) - kMmaWarps - 2, lane = threadIdx.x & 31;
+  int32_t* col_count = count + 1 + kMaxUnits;
+  int last_tile = -1, arrived = 0;  // the column tile before this one: its count is read a tile later
+  auto finish_columns = [&]() {
+    if (last_tile < 0 || __shfl_sync(0xFFFFFFFFu, arrived, 0) != s.units - 1) return;
+    __threadfence();
+    const int c = last_tile + 4 * w + (lane & 3);
+    for (int t = lane >> 2; t < n; t += 8) {
+      float v[kMaxTopK];
+      const size_t at = (size_t)t * a.K * a.H + c;
+#pragma unroll
+      for (int k = 0; k < kMaxTopK; ++k) v[k] = k < a.K && s.p[t * a.K + k] != 0.0f ? __ldcg(o + at + (size_t)k * a.H) : 0.0f;
+      float y = 0.0f;
+#pragma unroll
+      for (int k = 0; k < kMaxTopK; ++k)
+        if (k < a.K && s.p[t * a.K + k] != 0.0f) y = fmaf(s.p[t * a.K + k], v[k], y);
+      if (a.add) y += __uint_as_float((uint32_t)a.add[(size_t)t * a.H + c] << 16);
+      reinterpret_cast<__nv_bfloat16*>(a.y)[(size_t)t * a.H + c] = __float2bfloat16_rn(y);
+    }
+  };
+  for (int done = 0;; ++done) {
+    const uint32_t b = done & 1;
+    if (!mbar_wait_warp(smem_u32(&s.rfull[b]), (done >> 1) & 1u, a.err, kErrWaitAccum)) break;
+    const int tile = s.red_tile[b];
+    if (tile < 0) {
+      finish_columns();
+      break;
+    }
+    const TileOf t = tile_of(a, s, tile);
+    const int tok = s.unit_n[t.unit], at = s.unit_at[t.unit];
+    const float* r = red + b * (R::kRed / 4);
+    if (!t.fc2) {
+      for (int i = lane; i < 2 * tok; i += 32) {
+        const int f = 2 * w + (i & 1), c = i >> 1;
+        float g = 0.0f, u = 0.0f;
+#pragma unroll
+        for (int m = 0; m < kMmaWarps; ++m) {
+          const float* q = r + (m * G + (c >> 3)) * 128 + f * 8 + (c & 7);
+          g += q[0];
+          u += q[64];
+        }
+        reinterpret_cast<__nv_bfloat16*>(h)[(size_t)s.list[at + c] * a.I + t.row + f] = __float2bfloat16_rn(act_fwd<ACT>(g) * u);
+      }
+      __syncwarp();
+      if (lane == 0) {
+        mbar_arrive(smem_u32(&s.rempty[b]));
+        red_release(count + 1 + t.unit);
+      }
+    } else {
+      for (int i = lane; i < 4 * tok; i += 32) {
+        const int f = 4 * w + (i & 3), c = i >> 2;
+        float v = 0.0f;
+#pragma unroll
+        for (int m = 0; m < kMmaWarps; ++m) v += r[(m * G + (c >> 3)) * 128 + f * 8 + (c & 7)];
+        o[(size_t)s.list[at + c] * a.H + t.row + f] = v;
+      }
+      __syncwarp();
+      finish_columns();
+      if (lane == 0) {
+        mbar_arrive(smem_u32(&s.rempty[b]));
+        arrived = add_acq_rel(col_count + t.row / 4 + w);
+      }
+      last_tile = t.row;
+    }
+    __syncwarp();
+  }
+}
+
+template <int ACT, int G>
+__device__ __forceinline__ void roles(const CUtensorMap& tm1, const CUtensorMap& tm2, const FewArgs& a, FewShared& s, int n,
+                                      int32_t* count, int first, uint16_t* h, float* o, uint8_t* smem) {
+  const uint32_t ring = (smem_u32(smem) + 1023u) & ~1023u, red = ring + Ring<G>::kStages * Ring<G>::kStage;
+  const int warp = threadIdx.x >> 5;
+  if (warp == kMmaWarps)
+    weights_role<G>(tm1, tm2, a, s, count, first, ring);
+  else if (warp == kMmaWarps + 1)
+    activations_role<G>(a, s, count, h, ring);
+  else if (warp < kMmaWarps)
+    products_role<G>(a, s, ring, red);
+  else
+    outputs_role<ACT, G>(a, s, n, count, h, o, reinterpret_cast<const float*>(smem + (red - smem_u32(smem))));
 }
 
 template <int ACT>
-__global__ void __launch_bounds__(256) few_fc1_kernel(const FewArgs a, const int* ids, uint16_t* h) {
+__global__ void __launch_bounds__(kFewThreads, 1)
+    few_experts_kernel(const __grid_constant__ CUtensorMap tm1, const __grid_constant__ CUtensorMap tm2, const FewArgs a,
+                       const float* logits, int32_t* count, uint16_t* h, float* o) {
+  extern __shared__ uint8_t smem[];
+  __shared__ FewShared s;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < kMaxStages; ++i) {
+      mbar_init(smem_u32(&s.wfull[i]), 1);
+      mbar_init(smem_u32(&s.afull[i]), 32);
+      mbar_init(smem_u32(&s.named[i]), 1);
+      mbar_init(smem_u32(&s.empty[i]), kMmaWarps);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(smem_u32(&s.rfull[i]), kMmaWarps);
+      mbar_init(smem_u32(&s.rempty[i]), kEpiWarps);
+    }
+    mbar_fence_init();
+    tma_prefetch_desc(&tm1);
+    tma_prefetch_desc(&tm2);
+  }
+  for (int i = threadIdx.x; i < 2 * kMaxExperts; i += kFewThreads) (&s.mask[0][0])[i] = 0;
   griddep_wait();
   griddep_launch_dependents();
-  const int route = blockIdx.y, t = route / a.K, lane = threadIdx.x & 31, f = blockIdx.x * 8 + (threadIdx.x >> 5);
-  if (t >= live_tokens(a.n_dev, a.N) || f >= a.I) return;
-  const uint16_t* w = a.w13 + (size_t)ids[route] * 2 * a.I * a.H;
-  const float g = dot_row(a.x + (size_t)t * a.H, w + (size_t)f * a.H, a.H, lane);
-  const float u = dot_row(a.x + (size_t)t * a.H, w + ((size_t)a.I + f) * a.H, a.H, lane);
-  if (lane == 0) reinterpret_cast<__nv_bfloat16*>(h)[(size_t)route * a.I + f] = __float2bfloat16_rn(act_fwd<ACT>(g) * u);
-}
-
-__global__ void __launch_bounds__(256) few_fc2_kernel(const FewArgs a, const int* ids, const float* ps, const uint16_t* h) {
-  griddep_wait();
-  griddep_launch_dependents();
-  const int t = blockIdx.y, lane = threadIdx.x & 31, c = blockIdx.x * 8 + (threadIdx.x >> 5);
-  if (t >= live_tokens(a.n_dev, a.N) || c >= a.H) return;
-  float y = 0.0f;
-  for (int k = 0; k < a.K; ++k) {
-    const int route = t * a.K + k;
-    const float p = ps[route];
-    if (p != 0.0f)
-      y += p * dot_row(h + (size_t)route * a.I, a.w2 + ((size_t)ids[route] * a.H + c) * a.I, a.I, lane);
-  }
-  if (lane == 0) {
-    if (a.add) y += __uint_as_float((uint32_t)a.add[(size_t)t * a.H + c] << 16);
-    reinterpret_cast<__nv_bfloat16*>(a.y)[(size_t)t * a.H + c] = __float2bfloat16_rn(y);
-  }
+  int first = 0;  // this block's first tile, under way while the experts are picked
+  if (warp == kMmaWarps && lane == 0) first = atomicAdd(count, 1);
+  const int n = live_tokens(a.n_dev, a.N);
+  __syncthreads();
+  for (int t = warp; t < n; t += kFewThreads / 32) pick(a, logits, t, s, blockIdx.x == 0);
+  __syncthreads();
+  build_units(a, n, s);
+  if (s.units == 0) return;
+  if (s.most <= 8)
+    roles<ACT, 1>(tm1, tm2, a, s, n, count, first, h, o, smem);
+  else if (s.most <= 16)
+    roles<ACT, 2>(tm1, tm2, a, s, n, count, first, h, o, smem);
+  else
+    roles<ACT, 4>(tm1, tm2, a, s, n, count, first, h, o, smem);
 }
 
 }  // namespace
@@ -142,21 +667,29 @@ __global__ void __launch_bounds__(256) few_fc2_kernel(const FewArgs a, const int
 int64_t few_workspace_bytes(int N, int H, int E, int K, int I) { return (int64_t)layout(N, H, E, K, I).total; }
 
 int launch_few(const FewArgs& a, cudaStream_t s) {
+  static DeviceOnce once;
+  int sms = 0;
+  cudaError_t e = once_per_device(once, &sms, [](int dev, int* v) {
+    cudaError_t err = cudaFuncSetAttribute(few_experts_kernel<0>, cudaFuncAttributeMaxDynamicSharedMemorySize, kRingBytes);
+    if (err == cudaSuccess)
+      err = cudaFuncSetAttribute(few_experts_kernel<1>, cudaFuncAttributeMaxDynamicSharedMemorySize, kRingBytes);
+    return err != cudaSuccess ? err : cudaDeviceGetAttribute(v, cudaDevAttrMultiProcessorCount, dev);
+  });
+  if (e != cudaSuccess) return -(int)e;
+  CUtensorMap tm1, tm2;
+  if (!make_map_mn3d(&tm1, a.w13, (uint64_t)a.H, 2ull * a.E * a.I, 8, kBoxCols / 64) ||
+      !make_map_mn3d(&tm2, a.w2, (uint64_t)a.I, (uint64_t)a.E * a.H, 8, kBoxCols / 64))
+    return -(int)cudaErrorInvalidValue;
   const FewWs w = layout(a.N, a.H, a.E, a.K, a.I);
   float* logits = reinterpret_cast<float*>(a.ws + w.logits);
-  int* ids = reinterpret_cast<int*>(a.ws + w.ids);
-  float* ps = reinterpret_cast<float*>(a.ws + w.p);
-  uint16_t* h = reinterpret_cast<uint16_t*>(a.ws + w.h);
-  cudaError_t e = launch_pdl(few_logits_kernel, dim3((a.E + 31) / 32, a.N), dim3(256), 0, s, a, logits);
+  int32_t* count = reinterpret_cast<int32_t*>(a.ws + w.count);
+  e = launch_pdl(few_logits_kernel, dim3((a.E + kLogitCols - 1) / kLogitCols * kLogitSplit, (a.N + kLogitTok - 1) / kLogitTok), dim3(kLogitThreads), 0, s, a,
+                 logits, count);
   if (e == cudaSuccess)
-    e = launch_pdl(few_select_kernel, dim3(a.N), dim3(32), 0, s, a, (const float*)logits, ids, ps);
-  if (e == cudaSuccess)
-    e = launch_pdl(a.activation ? few_fc1_kernel<1> : few_fc1_kernel<0>, dim3((a.I + 7) / 8, a.N * a.K), dim3(256), 0,
-                   s, a, (const int*)ids, h);
-  if (e == cudaSuccess)
-    e = launch_pdl(few_fc2_kernel, dim3((a.H + 7) / 8, a.N), dim3(256), 0, s, a, (const int*)ids, (const float*)ps,
-                   (const uint16_t*)h);
-  return e != cudaSuccess ? -(int)e : 4;
+    e = launch_pdl(a.activation ? few_experts_kernel<1> : few_experts_kernel<0>, dim3(sms), dim3(kFewThreads), kRingBytes, s,
+                   tm1, tm2, a, (const float*)logits, count, reinterpret_cast<uint16_t*>(a.ws + w.h),
+                   reinterpret_cast<float*>(a.ws + w.o));
+  return e != cudaSuccess ? -(int)e : 2;
 }
 
 }  // namespace moe
