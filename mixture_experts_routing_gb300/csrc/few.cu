@@ -11,7 +11,7 @@
 //
 // The time is that of reading the weights, so a tile is a run of 16 weight rows that
 // passes once through a ring in shared memory (TMA boxes of 8 rows x 256 columns) into
-// mma.sync, weights as the 16 rows, tokens as the 8 columns: the eight warps split the
+// mma.sync, weights as the 16 rows, tokens as the 8 columns: the four warps split the
 // columns of a stage, so a tile needs no split between blocks, and there are enough tiles
 // to keep all SMs busy from one token on (128-row tiles of the 5th-generation tensor
 // cores would leave 8 experts x 2048 features with fewer tiles than there are turns to
@@ -35,9 +35,9 @@ struct FewWs {
 
 constexpr int kMaxUnits = kMaxExperts + kFewMaxTokens * kMaxTopK / 8;  // an expert's tokens, 8 or more at a time
 
-// [0] next tile, [1 + u] parts of unit u's h that are written, then of every 4 columns the
-// units that have been added to o
-__host__ __device__ inline int count_words(int H) { return 1 + kMaxUnits + H / 4; }
+// [0] next tile, [1 + u] tiles of unit u's h that are written, then of every 16 columns the
+// units whose products are in o
+__host__ __device__ inline int count_words(int H) { return 1 + kMaxUnits + H / 16; }
 
 FewWs layout(int N, int H, int E, int K, int I) {
   FewWs w{};
@@ -151,7 +151,7 @@ __global__ void __cluster_dims__(kLogitSplit, 1, 1) __launch_bounds__(kLogitThre
 static_assert(kLogitTok <= kLogitSplit, "one token of the chunk per block of the cluster");
 
 // ---------------------------------------------------------------- experts
-constexpr int kMmaWarps = 8, kEpiWarps = 4;
+constexpr int kMmaWarps = 4, kEpiWarps = 4;
 constexpr int kFewThreads = (kMmaWarps + 2 + kEpiWarps) * 32;
 constexpr int kRows = 16;        // weight rows of a tile
 constexpr int kBoxCols = 256;    // columns of a copy of 8 rows: 4 KB, in 128-byte swizzled pieces of 64 columns
@@ -161,9 +161,9 @@ constexpr uint32_t kRingBytes = 209u << 10;  // with the buffers of the sums
 constexpr uint32_t kErrWaitUnit = 1u << 4;  // an expert's h never became complete
 
 struct FewShared {
-  uint64_t wfull[kMaxStages], afull[kMaxStages], empty[kMaxStages], named[kMaxStages], rfull[2], rempty[2];
+  uint64_t wfull[kMaxStages], afull[kMaxStages], empty[kMaxStages], named[kMaxStages], rfull[kEpiWarps], rempty[kEpiWarps];
   int tile[kMaxStages];            // of the stage, -1: no more
-  int red_tile[2];
+  int red_tile[kEpiWarps];
   int ids[kFewMaxTokens * kMaxTopK];
   float p[kFewMaxTokens * kMaxTopK];
   uint16_t list[kFewMaxTokens * kMaxTopK];  // routes by expert, tokens ascending
@@ -306,12 +306,6 @@ __device__ __forceinline__ int ld_acquire(const int32_t* p) {
 __device__ __forceinline__ void red_release(int32_t* p) {
   asm volatile("red.release.gpu.global.add.s32 [%0], 1;" ::"l"(p) : "memory");
 }
-__device__ __forceinline__ int add_acq_rel(int32_t* p) {
-  int v;
-  asm volatile("atom.acq_rel.gpu.global.add.s32 %0, [%1], 1;" : "=r"(v) : "l"(p) : "memory");
-  return v;
-}
-
 // Sizes by the groups of 8 tokens of a unit.
 template <int G>
 struct Ring {
@@ -320,7 +314,7 @@ struct Ring {
   static constexpr uint32_t kWeights = kCols * 2 * kRows;
   static constexpr uint32_t kStage = (kWeights + kPitch * 8 * G + 1023u) & ~1023u;
   static constexpr uint32_t kRed = kMmaWarps * G * 512u;  // of one buffer of the sums
-  static constexpr uint32_t kFit = (kRingBytes - 1024u - 2 * kRed) / kStage;
+  static constexpr uint32_t kFit = (kRingBytes - 1024u - kEpiWarps * kRed) / kStage;
   static constexpr uint32_t kStages = kFit < kMaxStages ? kFit : kMaxStages;
 };
 
@@ -426,21 +420,24 @@ __device__ __forceinline__ void activations_role(const FewArgs& a, FewShared& s,
       tile = now;
       k = 0;
       t = tile_of(a, s, tile);
-      if (t.fc2 && !s.unit_done[t.unit]) {  // h is complete when all tiles of all its features say so
-        const int want = a.I / 8 * kEpiWarps;
+      if (t.fc2 && !s.unit_done[t.unit]) {
+        // h is complete when all tiles of its features have said so; 32 units are asked at
+        // once, since each answer takes a microsecond under load
+        const int u = (t.unit & ~31) + lane, want = a.I / 8;
         const uint64_t t0 = globaltimer_ns();
-        bool ok = true;
-        for (uint32_t i = 1; ld_acquire(count + 1 + t.unit) < want; ++i) {
-          if ((i & 255u) == 0u && globaltimer_ns() - t0 > 2000000000ull) {
+        uint32_t have = 0;
+        for (uint32_t i = 1;; ++i) {
+          have = __ballot_sync(0xFFFFFFFFu, u < s.units && ld_acquire(count + 1 + u) >= want);
+          if ((have >> (t.unit & 31)) & 1u) break;
+          if ((i & 255u) == 0u && __shfl_sync(0xFFFFFFFFu, (int)(globaltimer_ns() - t0 > 2000000000ull), 0)) {
             atomicOr(a.err, kErrWaitUnit);
-            ok = false;
+            have = 0;
             break;
           }
         }
-        ok = __all_sync(0xFFFFFFFFu, ok);
-        if (!ok) break;
+        if (have == 0) break;
         __threadfence();
-        if (lane == 0) s.unit_done[t.unit] = 1;
+        if ((have >> lane) & 1u) s.unit_done[u] = 1;
         __syncwarp();
       }
       rows = s.unit_n[t.unit];
@@ -465,19 +462,19 @@ __device__ __forceinline__ void activations_role(const FewArgs& a, FewShared& s,
   cp_async_wait_all();
 }
 
-// A warp takes an eighth of a stage's columns: 64 (one swizzled piece of a box) or 32.
+// A warp takes a quarter of a stage's columns, 64 (one swizzled piece of a box) at a time.
 template <int G>
 __device__ __forceinline__ void products_role(const FewArgs& a, FewShared& s, uint32_t ring, uint32_t red) {
   using R = Ring<G>;
-  constexpr int kWarpCols = R::kCols / kMmaWarps, kSteps = kWarpCols / 16;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, col0 = warp * kWarpCols;
-  // weights: rows 0-7 and 8-15 in boxes of their own; 16-byte piece c of row r at (c ^ r) of its 128 bytes
-  const uint32_t wrow = (uint32_t)(col0 / kBoxCols * 2 + ((lane >> 3) & 1)) * kBoxBytes + col0 % kBoxCols / 64 * 1024 + (lane & 7) * 128;
-  uint32_t woff[kSteps];
+  constexpr int kPieces = R::kCols / 64 / kMmaWarps;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  // weights: rows 0-7 and 8-15 in boxes of their own; 16-byte part c of row r at (c ^ r) of its 128 bytes
+  uint32_t woff[4];
 #pragma unroll
-  for (int j = 0; j < kSteps; ++j) woff[j] = ring + wrow + (((col0 % 64 / 8 + 2 * j + (lane >> 4)) ^ (lane & 7)) << 4);
+  for (int j = 0; j < 4; ++j)
+    woff[j] = ring + ((lane >> 3) & 1) * kBoxBytes + (lane & 7) * 128 + (((2 * j + (lane >> 4)) ^ (lane & 7)) << 4);
   // activations: two steps of 16 columns at a time
-  const uint32_t boff = ring + R::kWeights + (lane & 7) * R::kPitch + (uint32_t)(col0 * 2 + (lane >> 3) * 16);
+  const uint32_t boff = ring + R::kWeights + (lane & 7) * R::kPitch + (lane >> 3) * 16;
   float acc[G][4];
   int tile = -2, left = 0, done = 0;
   for (Turn<G> at;; at.next()) {
@@ -485,9 +482,10 @@ __device__ __forceinline__ void products_role(const FewArgs& a, FewShared& s, ui
         !mbar_wait_warp(smem_u32(&s.afull[at.st]), at.par, a.err, kErrWaitFull))
       break;
     const int now = s.tile[at.st];
-    const uint32_t b = done & 1;
-    if (now < 0) {  // the end, for the epilogue too
-      if (done < 2 || mbar_wait_warp(smem_u32(&s.rempty[b]), (done / 2 - 1) & 1u, a.err, kErrWaitAccum)) {
+    if (now < 0) {  // the end, for every warp of the outputs
+      for (int i = 0; i < kEpiWarps; ++i, ++done) {
+        const int b = done % kEpiWarps;
+        if (done >= kEpiWarps && !mbar_wait_warp(smem_u32(&s.rempty[b]), (done / kEpiWarps - 1) & 1u, a.err, kErrWaitAccum)) break;
         if (warp == 0 && lane == 0) s.red_tile[b] = -1;
         __syncwarp();
         if (lane == 0) mbar_arrive(smem_u32(&s.rfull[b]));
@@ -500,26 +498,32 @@ __device__ __forceinline__ void products_role(const FewArgs& a, FewShared& s, ui
 #pragma unroll
       for (int g = 0; g < G; ++g) acc[g][0] = acc[g][1] = acc[g][2] = acc[g][3] = 0.0f;
     }
-    if (col0 < left) {
-      const uint32_t base = at.st * R::kStage;
-      uint32_t w[kSteps][4], x[G][kSteps / 2][4];
+    const uint32_t base = at.st * R::kStage;
 #pragma unroll
-      for (int j = 0; j < kSteps; ++j) ldmatrix4(w[j], woff[j] + base);
+    for (int p = 0; p < kPieces; ++p) {
+      const int piece = warp + p * kMmaWarps;  // a box holds four
+      if (piece * 64 < left) {
+        const uint32_t wat = base + (piece / 4 * 2) * kBoxBytes + (piece & 3) * 1024, xat = boff + base + piece * 128;
+        uint32_t w[4][4], x[G][2][4];
 #pragma unroll
-      for (int g = 0; g < G; ++g)
+        for (int j = 0; j < 4; ++j) ldmatrix4(w[j], woff[j] + wat);
 #pragma unroll
-        for (int j = 0; j < kSteps / 2; ++j) ldmatrix4(x[g][j], boff + base + g * 8 * R::kPitch + j * 64);
+        for (int g = 0; g < G; ++g)
 #pragma unroll
-      for (int j = 0; j < kSteps; ++j)
+          for (int j = 0; j < 2; ++j) ldmatrix4(x[g][j], xat + g * 8 * R::kPitch + j * 64);
 #pragma unroll
-        for (int g = 0; g < G; ++g) mma16816(acc[g], w[j], x[g][j / 2][j % 2 * 2], x[g][j / 2][j % 2 * 2 + 1]);
+        for (int j = 0; j < 4; ++j)
+#pragma unroll
+          for (int g = 0; g < G; ++g) mma16816(acc[g], w[j], x[g][j / 2][j % 2 * 2], x[g][j / 2][j % 2 * 2 + 1]);
+      }
     }
     __syncwarp();
     if (lane == 0) mbar_arrive(smem_u32(&s.empty[at.st]));
     left -= R::kCols;
     if (left > 0) continue;
     // the warps' sums of the tile, [warp][group][row][token]
-    if (done >= 2 && !mbar_wait_warp(smem_u32(&s.rempty[b]), (done / 2 - 1) & 1u, a.err, kErrWaitAccum)) break;
+    const int b = done % kEpiWarps;
+    if (done >= kEpiWarps && !mbar_wait_warp(smem_u32(&s.rempty[b]), (done / kEpiWarps - 1) & 1u, a.err, kErrWaitAccum)) break;
     if (warp == 0 && lane == 0) s.red_tile[b] = tile;
 #pragma unroll
     for (int g = 0; g < G; ++g) {
@@ -533,45 +537,64 @@ __device__ __forceinline__ void products_role(const FewArgs& a, FewShared& s, ui
   }
 }
 
-// FC1: a warp's two of the eight features; FC2: its four of the 16 columns.
+// A warp takes every fourth tile, from a buffer of its own: making a tile's values visible
+// to the other blocks costs it about a microsecond, which three other tiles hide.
 template <int ACT, int G>
 __device__ __forceinline__ void outputs_role(const FewArgs& a, FewShared& s, int n, int32_t* count, uint16_t* h, float* o,
                                              const float* red) {
   using R = Ring<G>;
   const int w = (threadIdx.x >> 5) - kMmaWarps - 2, lane = threadIdx.x & 31;
   int32_t* col_count = count + 1 + kMaxUnits;
-  int last_tile = -1, arrived = 0;  // the column tile before this one: its count is read a tile later
+  const float* r = red + w * (R::kRed / 4);
+  int last_row = -1, arrived = 0;  // the column tile before this one: its count is read a tile later
   auto finish_columns = [&]() {
-    if (last_tile < 0 || __shfl_sync(0xFFFFFFFFu, arrived, 0) != s.units - 1) return;
+    if (last_row < 0 || __shfl_sync(0xFFFFFFFFu, arrived, 0) != s.units - 1) return;
     __threadfence();
-    const int c = last_tile + 4 * w + (lane & 3);
+    const int c = last_row + 4 * (lane & 3);
     for (int t = lane >> 2; t < n; t += 8) {
-      float v[kMaxTopK];
-      const size_t at = (size_t)t * a.K * a.H + c;
+      float4 v[kMaxTopK / 2], y = make_float4(0.f, 0.f, 0.f, 0.f);
+      for (int k0 = 0; k0 < a.K; k0 += kMaxTopK / 2) {
+        const float* p = s.p + t * a.K + k0;
+        const float* from = o + ((size_t)t * a.K + k0) * a.H + c;
+        // a route of probability 0 has no product
 #pragma unroll
-      for (int k = 0; k < kMaxTopK; ++k) v[k] = k < a.K && s.p[t * a.K + k] != 0.0f ? __ldcg(o + at + (size_t)k * a.H) : 0.0f;
-      float y = 0.0f;
+        for (int k = 0; k < kMaxTopK / 2; ++k)
+          if (k0 + k < a.K && p[k] != 0.0f) v[k] = __ldcg(reinterpret_cast<const float4*>(from + (size_t)k * a.H));
 #pragma unroll
-      for (int k = 0; k < kMaxTopK; ++k)
-        if (k < a.K && s.p[t * a.K + k] != 0.0f) y = fmaf(s.p[t * a.K + k], v[k], y);
-      if (a.add) y += __uint_as_float((uint32_t)a.add[(size_t)t * a.H + c] << 16);
-      reinterpret_cast<__nv_bfloat16*>(a.y)[(size_t)t * a.H + c] = __float2bfloat16_rn(y);
+        for (int k = 0; k < kMaxTopK / 2; ++k) {
+          if (k0 + k < a.K && p[k] != 0.0f) {
+            y.x = fmaf(p[k], v[k].x, y.x);
+            y.y = fmaf(p[k], v[k].y, y.y);
+            y.z = fmaf(p[k], v[k].z, y.z);
+            y.w = fmaf(p[k], v[k].w, y.w);
+          }
+        }
+      }
+      const size_t at = (size_t)t * a.H + c;
+      if (a.add) {
+        const uint2 q = *reinterpret_cast<const uint2*>(a.add + at);
+        y.x += __uint_as_float(q.x << 16);
+        y.y += __uint_as_float(q.x & 0xFFFF0000u);
+        y.z += __uint_as_float(q.y << 16);
+        y.w += __uint_as_float(q.y & 0xFFFF0000u);
+      }
+      const __nv_bfloat162 lo = __floats2bfloat162_rn(y.x, y.y), hi = __floats2bfloat162_rn(y.z, y.w);
+      *reinterpret_cast<uint2*>(a.y + at) =
+          make_uint2(*reinterpret_cast<const uint32_t*>(&lo), *reinterpret_cast<const uint32_t*>(&hi));
     }
   };
-  for (int done = 0;; ++done) {
-    const uint32_t b = done & 1;
-    if (!mbar_wait_warp(smem_u32(&s.rfull[b]), (done >> 1) & 1u, a.err, kErrWaitAccum)) break;
-    const int tile = s.red_tile[b];
+  for (uint32_t par = 0;; par ^= 1u) {
+    if (!mbar_wait_warp(smem_u32(&s.rfull[w]), par, a.err, kErrWaitAccum)) break;
+    const int tile = s.red_tile[w];
     if (tile < 0) {
       finish_columns();
       break;
     }
     const TileOf t = tile_of(a, s, tile);
     const int tok = s.unit_n[t.unit], at = s.unit_at[t.unit];
-    const float* r = red + b * (R::kRed / 4);
     if (!t.fc2) {
-      for (int i = lane; i < 2 * tok; i += 32) {
-        const int f = 2 * w + (i & 1), c = i >> 1;
+      for (int i = lane; i < 8 * tok; i += 32) {
+        const int f = i & 7, c = i >> 3;
         float g = 0.0f, u = 0.0f;
 #pragma unroll
         for (int m = 0; m < kMmaWarps; ++m) {
@@ -583,12 +606,12 @@ __device__ __forceinline__ void outputs_role(const FewArgs& a, FewShared& s, int
       }
       __syncwarp();
       if (lane == 0) {
-        mbar_arrive(smem_u32(&s.rempty[b]));
+        mbar_arrive(smem_u32(&s.rempty[w]));
         red_release(count + 1 + t.unit);
       }
     } else {
-      for (int i = lane; i < 4 * tok; i += 32) {
-        const int f = 4 * w + (i & 3), c = i >> 2;
+      for (int i = lane; i < 16 * tok; i += 32) {
+        const int f = i & 15, c = i >> 4;
         float v = 0.0f;
 #pragma unroll
         for (int m = 0; m < kMmaWarps; ++m) v += r[(m * G + (c >> 3)) * 128 + f * 8 + (c & 7)];
@@ -597,10 +620,11 @@ __device__ __forceinline__ void outputs_role(const FewArgs& a, FewShared& s, int
       __syncwarp();
       finish_columns();
       if (lane == 0) {
-        mbar_arrive(smem_u32(&s.rempty[b]));
-        arrived = add_acq_rel(col_count + t.row / 4 + w);
+        mbar_arrive(smem_u32(&s.rempty[w]));
+        __threadfence();
+        arrived = atomicAdd(col_count + t.row / kRows, 1);
       }
-      last_tile = t.row;
+      last_row = t.row;
     }
     __syncwarp();
   }
@@ -635,9 +659,9 @@ __global__ void __launch_bounds__(kFewThreads, 1)
       mbar_init(smem_u32(&s.named[i]), 1);
       mbar_init(smem_u32(&s.empty[i]), kMmaWarps);
     }
-    for (int i = 0; i < 2; ++i) {
+    for (int i = 0; i < kEpiWarps; ++i) {
       mbar_init(smem_u32(&s.rfull[i]), kMmaWarps);
-      mbar_init(smem_u32(&s.rempty[i]), kEpiWarps);
+      mbar_init(smem_u32(&s.rempty[i]), 1);
     }
     mbar_fence_init();
     tma_prefetch_desc(&tm1);
