@@ -10,7 +10,7 @@
 //            The last block to finish a column tile adds up its tokens' routes.
 //
 // The time is that of reading the weights, so a tile is a run of 16 weight rows that
-// passes once through a ring in shared memory (TMA boxes of 8 rows x 256 columns) into
+// passes once through a ring in shared memory (one TMA copy of 16 rows x 512 columns a stage) into
 // mma.sync, weights as the 16 rows, tokens as the 8 columns: the four warps split the
 // columns of a stage, so a tile needs no split between blocks, and there are enough tiles
 // to keep all SMs busy from one token on (128-row tiles of the 5th-generation tensor
@@ -154,8 +154,10 @@ static_assert(kLogitTok <= kLogitSplit, "one token of the chunk per block of the
 constexpr int kMmaWarps = 4, kEpiWarps = 4;
 constexpr int kFewThreads = (kMmaWarps + 2 + kEpiWarps) * 32;
 constexpr int kRows = 16;        // weight rows of a tile
-constexpr int kBoxCols = 256;    // columns of a copy of 8 rows: 4 KB, in 128-byte swizzled pieces of 64 columns
-constexpr uint32_t kBoxBytes = 8 * kBoxCols * 2;
+// Columns of a stage. Its 16 rows are one copy, [64 columns][rows 0-7, rows 8-15][row], each row
+// of 64 columns swizzled over its 128 bytes: four copies of 4 KB kept the copying warp busy
+// longer than memory took (few tokens, 7168 x 2048: 117 us instead of 128).
+constexpr int kCols = 512;
 constexpr int kMaxStages = 8;
 constexpr uint32_t kRingBytes = 209u << 10;  // with the buffers of the sums
 constexpr uint32_t kErrWaitUnit = 1u << 4;  // an expert's h never became complete
@@ -309,7 +311,6 @@ __device__ __forceinline__ void red_release(int32_t* p) {
 // Sizes by the groups of 8 tokens of a unit.
 template <int G>
 struct Ring {
-  static constexpr int kCols = G == 4 ? 256 : 512;  // of a stage; many tokens: fewer, so that several stages fit
   static constexpr uint32_t kPitch = kCols * 2 + 16;  // of the activations' rows: 16 bytes apart in banks
   static constexpr uint32_t kWeights = kCols * 2 * kRows;
   static constexpr uint32_t kStage = (kWeights + kPitch * 8 * G + 1023u) & ~1023u;
@@ -370,20 +371,18 @@ __device__ __forceinline__ void weights_role(const CUtensorMap& tm1, const CUten
     int next = 0;
     if (lane == 0) next = atomicAdd(count, 1);  // known by the end of this tile
     const TileOf t = tile_of(a, s, tile);
-    const int row = s.unit_e[t.unit] * (t.fc2 ? a.H : 2 * a.I) + t.row, second = row + (t.fc2 ? 8 : a.I);
-    const CUtensorMap* tm = t.fc2 ? &tm2 : &tm1;
-    for (int k = 0; k < t.cols; k += R::kCols, ++it, at.next()) {
+    const int e = s.unit_e[t.unit];
+    for (int k = 0; k < t.cols; k += kCols, ++it, at.next()) {
       if (it >= R::kStages && !mbar_wait_warp(smem_u32(&s.empty[at.st]), at.par ^ 1u, a.err, kErrWaitEmpty)) { ok = false; break; }
       if (lane == 0) {
         const uint32_t bar = smem_u32(&s.wfull[at.st]), dst = ring + at.st * R::kStage;
-        const int boxes = min(R::kCols, t.cols - k + kBoxCols - 1) / kBoxCols;
         s.tile[at.st] = tile;
         mbar_arrive(smem_u32(&s.named[at.st]));
-        mbar_arrive_expect_tx(bar, (uint32_t)boxes * 2u * kBoxBytes);  // columns past the end count as zeros
-        for (int i = 0; i < boxes; ++i) {
-          tma_load_3d(dst + i * 2 * kBoxBytes, tm, 0, row, (k + i * kBoxCols) / 64, bar, policy);
-          tma_load_3d(dst + (i * 2 + 1) * kBoxBytes, tm, 0, second, (k + i * kBoxCols) / 64, bar, policy);
-        }
+        mbar_arrive_expect_tx(bar, R::kWeights);  // columns past the end count as zeros
+        if (t.fc2)
+          tma_load_3d(dst, &tm2, 0, e * a.H + t.row, k / 64, bar, policy);
+        else
+          tma_load_4d(dst, &tm1, 0, t.row, 2 * e, k / 64, bar, policy);
       }
       __syncwarp();
     }
@@ -446,15 +445,15 @@ __device__ __forceinline__ void activations_role(const FewArgs& a, FewShared& s,
         from = reinterpret_cast<uint64_t>(t.fc2 ? h + (size_t)r * a.I : a.x + (size_t)(r / a.K) * a.H);
       }
     } else {
-      k += R::kCols;
+      k += kCols;
     }
-    const int pieces = min(R::kCols, t.cols - k) / 8;
+    const int pieces = min(kCols, t.cols - k) / 8;
     const uint32_t dst = ring + at.st * R::kStage + R::kWeights + lane * 16;
 #pragma unroll 4
     for (int i = 0; i < rows; ++i) {
       const uint16_t* src = reinterpret_cast<const uint16_t*>(__shfl_sync(0xFFFFFFFFu, from, i)) + k + lane * 8;
 #pragma unroll
-      for (int j = 0; j < R::kCols / 8; j += 32)
+      for (int j = 0; j < kCols / 8; j += 32)
         if (lane + j < pieces) cp_async_16(dst + i * R::kPitch + j * 16, src + j * 8, 16);
     }
     cp_async_mbar_arrive_noinc(smem_u32(&s.afull[at.st]));
@@ -466,13 +465,13 @@ __device__ __forceinline__ void activations_role(const FewArgs& a, FewShared& s,
 template <int G>
 __device__ __forceinline__ void products_role(const FewArgs& a, FewShared& s, uint32_t ring, uint32_t red) {
   using R = Ring<G>;
-  constexpr int kPieces = R::kCols / 64 / kMmaWarps;
+  constexpr int kPieces = kCols / 64 / kMmaWarps;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  // weights: rows 0-7 and 8-15 in boxes of their own; 16-byte part c of row r at (c ^ r) of its 128 bytes
+  // weights: 16-byte part c of row r at (c ^ r) of its 128 bytes
   uint32_t woff[4];
 #pragma unroll
   for (int j = 0; j < 4; ++j)
-    woff[j] = ring + ((lane >> 3) & 1) * kBoxBytes + (lane & 7) * 128 + (((2 * j + (lane >> 4)) ^ (lane & 7)) << 4);
+    woff[j] = ring + (lane & 15) * 128 + (((2 * j + (lane >> 4)) ^ (lane & 7)) << 4);
   // activations: two steps of 16 columns at a time
   const uint32_t boff = ring + R::kWeights + (lane & 7) * R::kPitch + (lane >> 3) * 16;
   float acc[G][4];
@@ -501,9 +500,9 @@ __device__ __forceinline__ void products_role(const FewArgs& a, FewShared& s, ui
     const uint32_t base = at.st * R::kStage;
 #pragma unroll
     for (int p = 0; p < kPieces; ++p) {
-      const int piece = warp + p * kMmaWarps;  // a box holds four
+      const int piece = warp + p * kMmaWarps;
       if (piece * 64 < left) {
-        const uint32_t wat = base + (piece / 4 * 2) * kBoxBytes + (piece & 3) * 1024, xat = boff + base + piece * 128;
+        const uint32_t wat = base + piece * 2048, xat = boff + base + piece * 128;
         uint32_t w[4][4], x[G][2][4];
 #pragma unroll
         for (int j = 0; j < 4; ++j) ldmatrix4(w[j], woff[j] + wat);
@@ -519,7 +518,7 @@ __device__ __forceinline__ void products_role(const FewArgs& a, FewShared& s, ui
     }
     __syncwarp();
     if (lane == 0) mbar_arrive(smem_u32(&s.empty[at.st]));
-    left -= R::kCols;
+    left -= kCols;
     if (left > 0) continue;
     // the warps' sums of the tile, [warp][group][row][token]
     const int b = done % kEpiWarps;
@@ -701,8 +700,8 @@ int launch_few(const FewArgs& a, cudaStream_t s) {
   });
   if (e != cudaSuccess) return -(int)e;
   CUtensorMap tm1, tm2;
-  if (!make_map_mn3d(&tm1, a.w13, (uint64_t)a.H, 2ull * a.E * a.I, 8, kBoxCols / 64) ||
-      !make_map_mn3d(&tm2, a.w2, (uint64_t)a.I, (uint64_t)a.E * a.H, 8, kBoxCols / 64))
+  if (!make_map_halves(&tm1, a.w13, (uint64_t)a.H, (uint64_t)a.I, 2ull * a.E, 8, 2, kCols / 64) ||
+      !make_map_mn3d(&tm2, a.w2, (uint64_t)a.I, (uint64_t)a.E * a.H, kRows, kCols / 64))
     return -(int)cudaErrorInvalidValue;
   const FewWs w = layout(a.N, a.H, a.E, a.K, a.I);
   float* logits = reinterpret_cast<float*>(a.ws + w.logits);

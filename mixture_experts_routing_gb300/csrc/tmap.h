@@ -71,4 +71,21 @@ inline bool make_map_mn3d(CUtensorMap* m, const void* base, uint64_t cols, uint6
             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// A bf16 tensor [halves, rows, cols] as (64 columns, rows, halves, cols/64 chunks), boxes
+// {64, box_rows, box_halves, box_chunks}: shared memory receives
+// [chunk][half][row][64], swizzled as above.
+inline bool make_map_halves(CUtensorMap* m, const void* base, uint64_t cols, uint64_t rows,
+                            uint64_t halves, uint32_t box_rows, uint32_t box_halves,
+                            uint32_t box_chunks) {
+  PFN_cuTensorMapEncodeTiled_v12000 fn = encode_fn();
+  if (!fn || cols % 64 != 0) return false;
+  cuuint64_t dims[4] = {64, rows, halves, cols / 64};
+  cuuint64_t strides[3] = {cols * 2, rows * cols * 2, 128};
+  cuuint32_t box[4] = {64, box_rows, box_halves, box_chunks};
+  cuuint32_t es[4] = {1, 1, 1, 1};
+  return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(base), dims, strides, box, es,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 }  // namespace moe
