@@ -154,10 +154,11 @@ static_assert(kLogitTok <= kLogitSplit, "one token of the chunk per block of the
 constexpr int kMmaWarps = 4, kEpiWarps = 4;
 constexpr int kFewThreads = (kMmaWarps + 2 + kEpiWarps) * 32;
 constexpr int kRows = 16;        // weight rows of a tile
-// Columns of a stage. Its 16 rows are one copy, [64 columns][rows 0-7, rows 8-15][row], each row
-// of 64 columns swizzled over its 128 bytes: four copies of 4 KB kept the copying warp busy
-// longer than memory took (few tokens, 7168 x 2048: 117 us instead of 128).
-constexpr int kCols = 512;
+// Columns of a copy. A copy holds a tile's 16 rows as [64 columns][row], each row of 64
+// columns swizzled over its 128 bytes. Copies of 4 KB (8 rows x 256 columns) kept the copying
+// warp busy for longer than memory took: 1 token, 7168 x 2048: 128 us, in one copy 116.
+constexpr int kBoxCols = 512;
+constexpr uint32_t kBoxBytes = kBoxCols * 2 * kRows;
 constexpr int kMaxStages = 8;
 constexpr uint32_t kRingBytes = 209u << 10;  // with the buffers of the sums
 constexpr uint32_t kErrWaitUnit = 1u << 4;  // an expert's h never became complete
@@ -294,7 +295,7 @@ __device__ __forceinline__ void ldmatrix4(uint32_t (&r)[4], uint32_t at) {
                : "memory");
 }
 __device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
-  asm volatile(
+  asm(
       "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
       : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
@@ -311,6 +312,10 @@ __device__ __forceinline__ void red_release(int32_t* p) {
 // Sizes by the groups of 8 tokens of a unit.
 template <int G>
 struct Ring {
+  // Columns of a stage: long ones leave the warps of the products fewer waits (1 token, 7168 x
+  // 2048: 140 us with 512, 124 with 1024), where the tokens leave room for four (16 tokens of
+  // 512 x 1024: 48 us with five stages of 512, 52 with two of 1024).
+  static constexpr int kCols = G == 1 ? 1024 : 512;
   static constexpr uint32_t kPitch = kCols * 2 + 16;  // of the activations' rows: 16 bytes apart in banks
   static constexpr uint32_t kWeights = kCols * 2 * kRows;
   static constexpr uint32_t kStage = (kWeights + kPitch * 8 * G + 1023u) & ~1023u;
@@ -372,17 +377,20 @@ __device__ __forceinline__ void weights_role(const CUtensorMap& tm1, const CUten
     if (lane == 0) next = atomicAdd(count, 1);  // known by the end of this tile
     const TileOf t = tile_of(a, s, tile);
     const int e = s.unit_e[t.unit];
-    for (int k = 0; k < t.cols; k += kCols, ++it, at.next()) {
+    for (int k = 0; k < t.cols; k += R::kCols, ++it, at.next()) {
       if (it >= R::kStages && !mbar_wait_warp(smem_u32(&s.empty[at.st]), at.par ^ 1u, a.err, kErrWaitEmpty)) { ok = false; break; }
       if (lane == 0) {
         const uint32_t bar = smem_u32(&s.wfull[at.st]), dst = ring + at.st * R::kStage;
         s.tile[at.st] = tile;
         mbar_arrive(smem_u32(&s.named[at.st]));
-        mbar_arrive_expect_tx(bar, R::kWeights);  // columns past the end count as zeros
-        if (t.fc2)
-          tma_load_3d(dst, &tm2, 0, e * a.H + t.row, k / 64, bar, policy);
-        else
-          tma_load_4d(dst, &tm1, 0, t.row, 2 * e, k / 64, bar, policy);
+        const int boxes = R::kCols == kBoxCols || t.cols - k <= kBoxCols ? 1 : R::kCols / kBoxCols;
+        mbar_arrive_expect_tx(bar, boxes * kBoxBytes);  // columns past the end count as zeros
+        for (int i = 0; i < boxes; ++i) {
+          if (t.fc2)
+            tma_load_3d(dst + i * kBoxBytes, &tm2, 0, e * a.H + t.row, (k + i * kBoxCols) / 64, bar, policy);
+          else
+            tma_load_4d(dst + i * kBoxBytes, &tm1, 0, t.row, 2 * e, (k + i * kBoxCols) / 64, bar, policy);
+        }
       }
       __syncwarp();
     }
@@ -445,15 +453,15 @@ __device__ __forceinline__ void activations_role(const FewArgs& a, FewShared& s,
         from = reinterpret_cast<uint64_t>(t.fc2 ? h + (size_t)r * a.I : a.x + (size_t)(r / a.K) * a.H);
       }
     } else {
-      k += kCols;
+      k += R::kCols;
     }
-    const int pieces = min(kCols, t.cols - k) / 8;
+    const int pieces = min(R::kCols, t.cols - k) / 8;
     const uint32_t dst = ring + at.st * R::kStage + R::kWeights + lane * 16;
 #pragma unroll 4
     for (int i = 0; i < rows; ++i) {
       const uint16_t* src = reinterpret_cast<const uint16_t*>(__shfl_sync(0xFFFFFFFFu, from, i)) + k + lane * 8;
 #pragma unroll
-      for (int j = 0; j < kCols / 8; j += 32)
+      for (int j = 0; j < R::kCols / 8; j += 32)
         if (lane + j < pieces) cp_async_16(dst + i * R::kPitch + j * 16, src + j * 8, 16);
     }
     cp_async_mbar_arrive_noinc(smem_u32(&s.afull[at.st]));
@@ -465,7 +473,7 @@ __device__ __forceinline__ void activations_role(const FewArgs& a, FewShared& s,
 template <int G>
 __device__ __forceinline__ void products_role(const FewArgs& a, FewShared& s, uint32_t ring, uint32_t red) {
   using R = Ring<G>;
-  constexpr int kPieces = kCols / 64 / kMmaWarps;
+  constexpr int kPieces = R::kCols / 64 / kMmaWarps;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   // weights: 16-byte part c of row r at (c ^ r) of its 128 bytes
   uint32_t woff[4];
@@ -474,7 +482,8 @@ __device__ __forceinline__ void products_role(const FewArgs& a, FewShared& s, ui
     woff[j] = ring + (lane & 15) * 128 + (((2 * j + (lane >> 4)) ^ (lane & 7)) << 4);
   // activations: two steps of 16 columns at a time
   const uint32_t boff = ring + R::kWeights + (lane & 7) * R::kPitch + (lane >> 3) * 16;
-  float acc[G][4];
+  constexpr int kChains = G == 1 ? kPieces : 1;  // sums that do not wait for one another
+  float acc[kChains][G][4];
   int tile = -2, left = 0, done = 0;
   for (Turn<G> at;; at.next()) {
     if (!mbar_wait_warp(smem_u32(&s.wfull[at.st]), at.par, a.err, kErrWaitFull) ||
@@ -495,40 +504,51 @@ __device__ __forceinline__ void products_role(const FewArgs& a, FewShared& s, ui
       tile = now;
       left = tile < s.units * (a.I / 8) ? a.H : a.I;
 #pragma unroll
-      for (int g = 0; g < G; ++g) acc[g][0] = acc[g][1] = acc[g][2] = acc[g][3] = 0.0f;
+      for (int c = 0; c < kChains; ++c)
+#pragma unroll
+        for (int g = 0; g < G; ++g) acc[c][g][0] = acc[c][g][1] = acc[c][g][2] = acc[c][g][3] = 0.0f;
     }
     const uint32_t base = at.st * R::kStage;
+    uint32_t wf[kPieces][4][4], xf[kPieces][G][2][4];
 #pragma unroll
     for (int p = 0; p < kPieces; ++p) {
       const int piece = warp + p * kMmaWarps;
       if (piece * 64 < left) {
         const uint32_t wat = base + piece * 2048, xat = boff + base + piece * 128;
-        uint32_t w[4][4], x[G][2][4];
 #pragma unroll
-        for (int j = 0; j < 4; ++j) ldmatrix4(w[j], woff[j] + wat);
+        for (int j = 0; j < 4; ++j) ldmatrix4(wf[p][j], woff[j] + wat);
 #pragma unroll
         for (int g = 0; g < G; ++g)
 #pragma unroll
-          for (int j = 0; j < 2; ++j) ldmatrix4(x[g][j], xat + g * 8 * R::kPitch + j * 64);
-#pragma unroll
-        for (int j = 0; j < 4; ++j)
-#pragma unroll
-          for (int g = 0; g < G; ++g) mma16816(acc[g], w[j], x[g][j / 2][j % 2 * 2], x[g][j / 2][j % 2 * 2 + 1]);
+          for (int j = 0; j < 2; ++j) ldmatrix4(xf[p][g][j], xat + g * 8 * R::kPitch + j * 64);
       }
     }
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+#pragma unroll
+      for (int p = 0; p < kPieces; ++p)
+        if ((warp + p * kMmaWarps) * 64 < left) {
+#pragma unroll
+          for (int g = 0; g < G; ++g)
+            mma16816(acc[p % kChains][g], wf[p][j], xf[p][g][j / 2][j % 2 * 2], xf[p][g][j / 2][j % 2 * 2 + 1]);
+        }
     __syncwarp();
     if (lane == 0) mbar_arrive(smem_u32(&s.empty[at.st]));
-    left -= kCols;
+    left -= R::kCols;
     if (left > 0) continue;
     // the warps' sums of the tile, [warp][group][row][token]
     const int b = done % kEpiWarps;
     if (done >= kEpiWarps && !mbar_wait_warp(smem_u32(&s.rempty[b]), (done / kEpiWarps - 1) & 1u, a.err, kErrWaitAccum)) break;
     if (warp == 0 && lane == 0) s.red_tile[b] = tile;
 #pragma unroll
+    for (int c = 1; c < kChains; ++c)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) acc[0][0][i] += acc[c][0][i];
+#pragma unroll
     for (int g = 0; g < G; ++g) {
       const uint32_t to = red + b * R::kRed + (uint32_t)(warp * G + g) * 512u + (lane >> 2) * 32 + (lane & 3) * 8;
-      asm volatile("st.shared.v2.f32 [%0], {%1,%2};" ::"r"(to), "f"(acc[g][0]), "f"(acc[g][1]) : "memory");
-      asm volatile("st.shared.v2.f32 [%0], {%1,%2};" ::"r"(to + 256), "f"(acc[g][2]), "f"(acc[g][3]) : "memory");
+      asm volatile("st.shared.v2.f32 [%0], {%1,%2};" ::"r"(to), "f"(acc[0][g][0]), "f"(acc[0][g][1]) : "memory");
+      asm volatile("st.shared.v2.f32 [%0], {%1,%2};" ::"r"(to + 256), "f"(acc[0][g][2]), "f"(acc[0][g][3]) : "memory");
     }
     __syncwarp();
     if (lane == 0) mbar_arrive(smem_u32(&s.rfull[b]));
@@ -550,36 +570,48 @@ __device__ __forceinline__ void outputs_role(const FewArgs& a, FewShared& s, int
     if (last_row < 0 || __shfl_sync(0xFFFFFFFFu, arrived, 0) != s.units - 1) return;
     __threadfence();
     const int c = last_row + 4 * (lane & 3);
-    for (int t = lane >> 2; t < n; t += 8) {
-      float4 v[kMaxTopK / 2], y = make_float4(0.f, 0.f, 0.f, 0.f);
-      for (int k0 = 0; k0 < a.K; k0 += kMaxTopK / 2) {
-        const float* p = s.p + t * a.K + k0;
-        const float* from = o + ((size_t)t * a.K + k0) * a.H + c;
-        // a route of probability 0 has no product
+    constexpr int kTwo = 2;  // tokens of a lane under way at once
+    for (int t0 = lane >> 2; t0 < n; t0 += 8 * kTwo) {
+      float4 y[kTwo] = {};
+      for (int k0 = 0; k0 < a.K; k0 += 8) {
+        float4 v[kTwo][8];
+        float p[kTwo][8];
 #pragma unroll
-        for (int k = 0; k < kMaxTopK / 2; ++k)
-          if (k0 + k < a.K && p[k] != 0.0f) v[k] = __ldcg(reinterpret_cast<const float4*>(from + (size_t)k * a.H));
+        for (int i = 0; i < kTwo; ++i) {
+          const int t = t0 + 8 * i;
 #pragma unroll
-        for (int k = 0; k < kMaxTopK / 2; ++k) {
-          if (k0 + k < a.K && p[k] != 0.0f) {
-            y.x = fmaf(p[k], v[k].x, y.x);
-            y.y = fmaf(p[k], v[k].y, y.y);
-            y.z = fmaf(p[k], v[k].z, y.z);
-            y.w = fmaf(p[k], v[k].w, y.w);
+          for (int k = 0; k < 8; ++k) {
+            p[i][k] = t < n && k0 + k < a.K ? s.p[t * a.K + k0 + k] : 0.0f;
+            // a route of probability 0 has no product
+            v[i][k] = p[i][k] != 0.0f ? __ldcg(reinterpret_cast<const float4*>(o + ((size_t)t * a.K + k0 + k) * a.H + c))
+                                      : make_float4(0.f, 0.f, 0.f, 0.f);
           }
         }
+#pragma unroll
+        for (int i = 0; i < kTwo; ++i)
+#pragma unroll
+          for (int k = 0; k < 8; ++k) {
+            y[i].x = fmaf(p[i][k], v[i][k].x, y[i].x);
+            y[i].y = fmaf(p[i][k], v[i][k].y, y[i].y);
+            y[i].z = fmaf(p[i][k], v[i][k].z, y[i].z);
+            y[i].w = fmaf(p[i][k], v[i][k].w, y[i].w);
+          }
       }
-      const size_t at = (size_t)t * a.H + c;
-      if (a.add) {
-        const uint2 q = *reinterpret_cast<const uint2*>(a.add + at);
-        y.x += __uint_as_float(q.x << 16);
-        y.y += __uint_as_float(q.x & 0xFFFF0000u);
-        y.z += __uint_as_float(q.y << 16);
-        y.w += __uint_as_float(q.y & 0xFFFF0000u);
+#pragma unroll
+      for (int i = 0; i < kTwo; ++i) {
+        if (t0 + 8 * i >= n) break;
+        const size_t at = (size_t)(t0 + 8 * i) * a.H + c;
+        if (a.add) {
+          const uint2 q = *reinterpret_cast<const uint2*>(a.add + at);
+          y[i].x += __uint_as_float(q.x << 16);
+          y[i].y += __uint_as_float(q.x & 0xFFFF0000u);
+          y[i].z += __uint_as_float(q.y << 16);
+          y[i].w += __uint_as_float(q.y & 0xFFFF0000u);
+        }
+        const __nv_bfloat162 lo = __floats2bfloat162_rn(y[i].x, y[i].y), hi = __floats2bfloat162_rn(y[i].z, y[i].w);
+        *reinterpret_cast<uint2*>(a.y + at) =
+            make_uint2(*reinterpret_cast<const uint32_t*>(&lo), *reinterpret_cast<const uint32_t*>(&hi));
       }
-      const __nv_bfloat162 lo = __floats2bfloat162_rn(y.x, y.y), hi = __floats2bfloat162_rn(y.z, y.w);
-      *reinterpret_cast<uint2*>(a.y + at) =
-          make_uint2(*reinterpret_cast<const uint32_t*>(&lo), *reinterpret_cast<const uint32_t*>(&hi));
     }
   };
   for (uint32_t par = 0;; par ^= 1u) {
@@ -700,8 +732,8 @@ int launch_few(const FewArgs& a, cudaStream_t s) {
   });
   if (e != cudaSuccess) return -(int)e;
   CUtensorMap tm1, tm2;
-  if (!make_map_halves(&tm1, a.w13, (uint64_t)a.H, (uint64_t)a.I, 2ull * a.E, 8, 2, kCols / 64) ||
-      !make_map_mn3d(&tm2, a.w2, (uint64_t)a.I, (uint64_t)a.E * a.H, kRows, kCols / 64))
+  if (!make_map_halves(&tm1, a.w13, (uint64_t)a.H, (uint64_t)a.I, 2ull * a.E, 8, 2, kBoxCols / 64) ||
+      !make_map_mn3d(&tm2, a.w2, (uint64_t)a.I, (uint64_t)a.E * a.H, kRows, kBoxCols / 64))
     return -(int)cudaErrorInvalidValue;
   const FewWs w = layout(a.N, a.H, a.E, a.K, a.I);
   float* logits = reinterpret_cast<float*>(a.ws + w.logits);
