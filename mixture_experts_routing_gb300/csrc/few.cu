@@ -159,6 +159,7 @@ constexpr int kRows = 16;        // weight rows of a tile
 // warp busy for longer than memory took: 1 token, 7168 x 2048: 128 us, in one copy 116.
 constexpr int kBoxCols = 512;
 constexpr uint32_t kBoxBytes = kBoxCols * 2 * kRows;
+constexpr int kDrawn = 3;        // tiles drawn ahead
 constexpr int kMaxStages = 8;
 constexpr uint32_t kRingBytes = 209u << 10;  // with the buffers of the sums
 constexpr uint32_t kErrWaitUnit = 1u << 4;  // an expert's h never became complete
@@ -179,59 +180,84 @@ struct FewShared {
   int units, most;                 // units; the most tokens of an expert
 };
 
-// The K experts of one token by a warp (as route_align picks them, from fp32
-// probabilities: ties to the lower id). Lane l holds experts l, l+32, ...
-__device__ __forceinline__ void pick(const FewArgs& a, const float* logits, int t, FewShared& s, bool out) {
+// The K experts of two tokens by a warp (as route_align picks them, from fp32 probabilities:
+// ties to the lower id); their steps fill each other's waits. Lane l holds experts l, l+32,
+// ..., PER of them. n: the live tokens.
+template <int PER>
+__device__ __forceinline__ void pick(const FewArgs& a, const float* logits, int t0, int n, FewShared& s, bool out) {
   const int lane = threadIdx.x & 31;
-  float v[8], top = -INFINITY;
+  float v[2][PER], top[2], sum[2], d[2] = {}, my_p[2] = {};
+  uint32_t key[2][PER];  // p's bits order like p >= 0; a NaN is above all; taken or absent: 0, below p + 1
+  int my_id[2] = {};
 #pragma unroll
-  for (int j = 0; j < 8; ++j) {
-    const int e = lane + 32 * j;
-    v[j] = e < a.E ? __ldcg(logits + (size_t)t * a.E + e) : -INFINITY;
+  for (int i = 0; i < 2; ++i) {
+    const int t = min(t0 + i, n - 1);
+#pragma unroll
+    for (int j = 0; j < PER; ++j) {
+      const int e = lane + 32 * j;
+      v[i][j] = e < a.E ? __ldcg(logits + (size_t)t * a.E + e) : -INFINITY;
+    }
   }
 #pragma unroll
-  for (int j = 0; j < 8; ++j) top = fmaxf(top, v[j]);
+  for (int i = 0; i < 2; ++i) {
+    top[i] = v[i][0];
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, o));
-  float sum = 0.0f;
-#pragma unroll
-  for (int j = 0; j < 8; ++j) {
-    v[j] = lane + 32 * j < a.E ? route_exp(__fsub_rn(v[j], top)) : 0.0f;
-    sum += v[j];
+    for (int j = 1; j < PER; ++j) top[i] = fmaxf(top[i], v[i][j]);
   }
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, o);
-  uint32_t key[8];  // p's bits order like p >= 0; a NaN is above all; taken or absent: 0, below p + 1
+  for (int o = 16; o > 0; o >>= 1)
 #pragma unroll
-  for (int j = 0; j < 8; ++j)
-    key[j] = lane + 32 * j < a.E ? (__float_as_uint(__fdiv_rn(v[j], sum)) & 0x7FFFFFFFu) + 1u : 0u;
-  float d = 0.0f, my_p = 0.0f;
-  int my_id = 0;
+    for (int i = 0; i < 2; ++i) top[i] = fmaxf(top[i], __shfl_xor_sync(0xFFFFFFFFu, top[i], o));
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    sum[i] = 0.0f;
+#pragma unroll
+    for (int j = 0; j < PER; ++j) {
+      v[i][j] = lane + 32 * j < a.E ? route_exp(__fsub_rn(v[i][j], top[i])) : 0.0f;
+      sum[i] += v[i][j];
+    }
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1)
+#pragma unroll
+    for (int i = 0; i < 2; ++i) sum[i] += __shfl_xor_sync(0xFFFFFFFFu, sum[i], o);
+#pragma unroll
+  for (int i = 0; i < 2; ++i)
+#pragma unroll
+    for (int j = 0; j < PER; ++j)
+      key[i][j] = lane + 32 * j < a.E ? (__float_as_uint(__fdiv_rn(v[i][j], sum[i])) & 0x7FFFFFFFu) + 1u : 0u;
   for (int k = 0; k < a.K; ++k) {
-    uint32_t best = 0;
 #pragma unroll
-    for (int j = 0; j < 8; ++j) best = max(best, key[j]);
-    best = __reduce_max_sync(0xFFFFFFFFu, best);
-    uint32_t mine = 0xFFFFFFFFu;
+    for (int i = 0; i < 2; ++i) {
+      uint32_t best = key[i][0];
 #pragma unroll
-    for (int j = 7; j >= 0; --j)
-      if (key[j] == best) mine = lane + 32 * j;
-    const int e = (int)__reduce_min_sync(0xFFFFFFFFu, mine);
+      for (int j = 1; j < PER; ++j) best = max(best, key[i][j]);
+      best = __reduce_max_sync(0xFFFFFFFFu, best);
+      uint32_t mine = 0xFFFFFFFFu;
 #pragma unroll
-    for (int j = 0; j < 8; ++j)
-      if (e == lane + 32 * j) key[j] = 0;
-    const float p = __uint_as_float(best - 1u);
-    d += p;
-    if (lane == k) { my_id = e; my_p = p; }
+      for (int j = PER - 1; j >= 0; --j)
+        if (key[i][j] == best) mine = lane + 32 * j;
+      const uint32_t e = __reduce_min_sync(0xFFFFFFFFu, mine);
+#pragma unroll
+      for (int j = 0; j < PER; ++j)
+        if (e == (uint32_t)(lane + 32 * j)) key[i][j] = 0;
+      const float p = __uint_as_float(best - 1u);
+      d[i] += p;
+      if (lane == k) { my_id[i] = (int)e; my_p[i] = p; }
+    }
   }
-  if (lane < a.K) {
-    const float p = a.renorm ? __fdiv_rn(my_p, d) : my_p;
-    const int at = t * a.K + lane;
-    s.ids[at] = my_id;
-    s.p[at] = p;
-    if (p != 0.0f) atomicOr(&s.mask[my_id][t >> 5], 1u << (t & 31));  // p = 0 (or NaN: != 0) : not read
-    if (out && a.topk_ids) a.topk_ids[at] = my_id;
-    if (out && a.topk_p) a.topk_p[at] = p;
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const int t = t0 + i;
+    if (lane < a.K && t < n) {
+      const float p = a.renorm ? __fdiv_rn(my_p[i], d[i]) : my_p[i];
+      const int at = t * a.K + lane;
+      s.ids[at] = my_id[i];
+      s.p[at] = p;
+      if (p != 0.0f) atomicOr(&s.mask[my_id[i]][t >> 5], 1u << (t & 31));  // p = 0 is not read; a NaN is not 0
+      if (out && a.topk_ids) a.topk_ids[at] = my_id[i];
+      if (out && a.topk_p) a.topk_p[at] = p;
+    }
   }
 }
 
@@ -363,22 +389,19 @@ __device__ __forceinline__ TileOf tile_of(const FewArgs& a, const FewShared& s, 
 // ---------------------------------------------------------------- roles
 template <int G>
 __device__ __forceinline__ void weights_role(const CUtensorMap& tm1, const CUtensorMap& tm2, const FewArgs& a, FewShared& s,
-                                             int32_t* count, int first, uint32_t ring) {
+                                             int32_t* count, int (&drawn)[kDrawn], uint32_t ring) {
   using R = Ring<G>;
   const int lane = threadIdx.x & 31;
   const int tiles = s.units * (a.I / 8 + a.H / kRows);
   const uint64_t policy = policy_evict_first();
-  int tile = __shfl_sync(0xFFFFFFFFu, first, 0);
   uint32_t it = 0;
   Turn<G> at;
   bool ok = true;
-  while (ok && tile < tiles) {
-    int next = 0;
-    if (lane == 0) next = atomicAdd(count, 1);  // known by the end of this tile
+  auto load = [&](int tile) {
     const TileOf t = tile_of(a, s, tile);
     const int e = s.unit_e[t.unit];
     for (int k = 0; k < t.cols; k += R::kCols, ++it, at.next()) {
-      if (it >= R::kStages && !mbar_wait_warp(smem_u32(&s.empty[at.st]), at.par ^ 1u, a.err, kErrWaitEmpty)) { ok = false; break; }
+      if (it >= R::kStages && !mbar_wait_warp(smem_u32(&s.empty[at.st]), at.par ^ 1u, a.err, kErrWaitEmpty)) return false;
       if (lane == 0) {
         const uint32_t bar = smem_u32(&s.wfull[at.st]), dst = ring + at.st * R::kStage;
         s.tile[at.st] = tile;
@@ -394,7 +417,21 @@ __device__ __forceinline__ void weights_role(const CUtensorMap& tm1, const CUten
       }
       __syncwarp();
     }
-    tile = __shfl_sync(0xFFFFFFFFu, next, 0);
+    return true;
+  };
+  // Three numbers are under way, each in a register of its own: a short tile's copies are
+  // issued in half the time that the counter takes to answer.
+  bool more = true;
+  while (more) {
+#pragma unroll
+    for (int i = 0; i < kDrawn; ++i) {
+      const int tile = __shfl_sync(0xFFFFFFFFu, drawn[i], 0);
+      more = tile < tiles;
+      if (!more) break;
+      if (lane == 0) drawn[i] = atomicAdd(count, 1);
+      more = ok = load(tile);
+      if (!more) break;
+    }
   }
   // the end, told through one more stage; and no copy of this warp is under way when it leaves
   ok = ok && (it < R::kStages || mbar_wait_warp(smem_u32(&s.empty[at.st]), at.par ^ 1u, a.err, kErrWaitEmpty));
@@ -663,11 +700,11 @@ __device__ __forceinline__ void outputs_role(const FewArgs& a, FewShared& s, int
 
 template <int ACT, int G>
 __device__ __forceinline__ void roles(const CUtensorMap& tm1, const CUtensorMap& tm2, const FewArgs& a, FewShared& s, int n,
-                                      int32_t* count, int first, uint16_t* h, float* o, uint8_t* smem) {
+                                      int32_t* count, int (&drawn)[kDrawn], uint16_t* h, float* o, uint8_t* smem) {
   const uint32_t ring = (smem_u32(smem) + 1023u) & ~1023u, red = ring + Ring<G>::kStages * Ring<G>::kStage;
   const int warp = threadIdx.x >> 5;
   if (warp == kMmaWarps)
-    weights_role<G>(tm1, tm2, a, s, count, first, ring);
+    weights_role<G>(tm1, tm2, a, s, count, drawn, ring);
   else if (warp == kMmaWarps + 1)
     activations_role<G>(a, s, count, h, ring);
   else if (warp < kMmaWarps)
@@ -701,20 +738,28 @@ __global__ void __launch_bounds__(kFewThreads, 1)
   for (int i = threadIdx.x; i < 2 * kMaxExperts; i += kFewThreads) (&s.mask[0][0])[i] = 0;
   griddep_wait();
   griddep_launch_dependents();
-  int first = 0;  // this block's first tile, under way while the experts are picked
-  if (warp == kMmaWarps && lane == 0) first = atomicAdd(count, 1);
+  int drawn[kDrawn] = {};  // this block's first tiles, under way while the experts are picked
+  if (warp == kMmaWarps && lane == 0) {
+#pragma unroll
+    for (int i = 0; i < kDrawn; ++i) drawn[i] = atomicAdd(count, 1);
+  }
   const int n = live_tokens(a.n_dev, a.N);
   __syncthreads();
-  for (int t = warp; t < n; t += kFewThreads / 32) pick(a, logits, t, s, blockIdx.x == 0);
+  for (int t = 2 * warp; t < n; t += 2 * (kFewThreads / 32)) {
+    if (a.E <= 32) pick<1>(a, logits, t, n, s, blockIdx.x == 0);
+    else if (a.E <= 64) pick<2>(a, logits, t, n, s, blockIdx.x == 0);
+    else if (a.E <= 128) pick<4>(a, logits, t, n, s, blockIdx.x == 0);
+    else pick<8>(a, logits, t, n, s, blockIdx.x == 0);
+  }
   __syncthreads();
   build_units(a, n, s);
   if (s.units == 0) return;
   if (s.most <= 8)
-    roles<ACT, 1>(tm1, tm2, a, s, n, count, first, h, o, smem);
+    roles<ACT, 1>(tm1, tm2, a, s, n, count, drawn, h, o, smem);
   else if (s.most <= 16)
-    roles<ACT, 2>(tm1, tm2, a, s, n, count, first, h, o, smem);
+    roles<ACT, 2>(tm1, tm2, a, s, n, count, drawn, h, o, smem);
   else
-    roles<ACT, 4>(tm1, tm2, a, s, n, count, first, h, o, smem);
+    roles<ACT, 4>(tm1, tm2, a, s, n, count, drawn, h, o, smem);
 }
 
 }  // namespace
