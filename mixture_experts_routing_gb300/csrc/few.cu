@@ -173,21 +173,23 @@ struct FewShared {
   uint16_t list[kFewMaxTokens * kMaxTopK];  // routes by expert, tokens ascending
   uint32_t mask[kMaxExperts][2];   // tokens of an expert
   uint16_t base[kMaxExperts];      // an expert's first route in list
-  uint16_t unit0[kMaxExperts];     // and its first unit
   uint16_t unit_e[kMaxUnits], unit_at[kMaxUnits], unit_n[kMaxUnits];
   uint8_t unit_done[kMaxUnits];    // seen complete by the activations' warp
   int warp_sum[kMaxExperts / 32][3];
   int units, most;                 // units; the most tokens of an expert
+  uint32_t by_per, by_run;         // 2^32 / (FC1 tiles of a unit) and / (16 units), rounded up
 };
 
-// The K experts of two tokens by a warp (as route_align picks them, from fp32 probabilities:
-// ties to the lower id); their steps fill each other's waits. Lane l holds experts l, l+32,
-// ..., PER of them. n: the live tokens.
+// The K experts of two tokens by a warp (as route_align picks them, ties to the lower id);
+// their steps fill each other's waits. The picks go by exp(l - max), the probabilities
+// before they are divided by their sum, which is needed for K of them at most, and not at
+// all where these are divided by their own sum. Lane l holds experts l, l+32, ..., PER of
+// them. n: the live tokens.
 template <int PER>
 __device__ __forceinline__ void pick(const FewArgs& a, const float* logits, int t0, int n, FewShared& s, bool out) {
   const int lane = threadIdx.x & 31;
-  float v[2][PER], top[2], sum[2], d[2] = {}, my_p[2] = {};
-  uint32_t key[2][PER];  // p's bits order like p >= 0; a NaN is above all; taken or absent: 0, below p + 1
+  float v[2][PER], top[2], sum[2] = {}, d[2] = {}, my_v[2] = {};
+  uint32_t key[2][PER];  // v's bits order like v >= 0; a NaN is above all; taken or absent: 0, below v + 1
   int my_id[2] = {};
 #pragma unroll
   for (int i = 0; i < 2; ++i) {
@@ -209,23 +211,20 @@ __device__ __forceinline__ void pick(const FewArgs& a, const float* logits, int 
 #pragma unroll
     for (int i = 0; i < 2; ++i) top[i] = fmaxf(top[i], __shfl_xor_sync(0xFFFFFFFFu, top[i], o));
 #pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    sum[i] = 0.0f;
-#pragma unroll
-    for (int j = 0; j < PER; ++j) {
-      v[i][j] = lane + 32 * j < a.E ? route_exp(__fsub_rn(v[i][j], top[i])) : 0.0f;
-      sum[i] += v[i][j];
-    }
-  }
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1)
-#pragma unroll
-    for (int i = 0; i < 2; ++i) sum[i] += __shfl_xor_sync(0xFFFFFFFFu, sum[i], o);
-#pragma unroll
   for (int i = 0; i < 2; ++i)
 #pragma unroll
-    for (int j = 0; j < PER; ++j)
-      key[i][j] = lane + 32 * j < a.E ? (__float_as_uint(__fdiv_rn(v[i][j], sum[i])) & 0x7FFFFFFFu) + 1u : 0u;
+    for (int j = 0; j < PER; ++j) {
+      const bool in = lane + 32 * j < a.E;
+      v[i][j] = in ? route_exp(__fsub_rn(v[i][j], top[i])) : 0.0f;
+      sum[i] += v[i][j];
+      key[i][j] = in ? (__float_as_uint(v[i][j]) & 0x7FFFFFFFu) + 1u : 0u;
+    }
+  if (!a.renorm) {
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1)
+#pragma unroll
+      for (int i = 0; i < 2; ++i) sum[i] += __shfl_xor_sync(0xFFFFFFFFu, sum[i], o);
+  }
   for (int k = 0; k < a.K; ++k) {
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
@@ -243,14 +242,14 @@ __device__ __forceinline__ void pick(const FewArgs& a, const float* logits, int 
         if (e == (uint32_t)(lane + 32 * j)) key[i][j] = 0;
       const float p = __uint_as_float(best - 1u);
       d[i] += p;
-      if (lane == k) { my_id[i] = (int)e; my_p[i] = p; }
+      if (lane == k) { my_id[i] = (int)e; my_v[i] = p; }
     }
   }
 #pragma unroll
   for (int i = 0; i < 2; ++i) {
     const int t = t0 + i;
     if (lane < a.K && t < n) {
-      const float p = a.renorm ? __fdiv_rn(my_p[i], d[i]) : my_p[i];
+      const float p = __fdiv_rn(my_v[i], a.renorm ? d[i] : sum[i]);
       const int at = t * a.K + lane;
       s.ids[at] = my_id[i];
       s.p[at] = p;
@@ -301,7 +300,14 @@ __device__ __forceinline__ void build_units(const FewArgs& a, int n, FewShared& 
       s.unit_n[u0 + i] = (uint16_t)min(per, c - i * per);
       s.unit_done[u0 + i] = 0;
     }
-    if (e == 0) { s.units = all; s.most = most; }
+    if (e == 0) {
+      s.units = all;
+      s.most = most;
+      // exact quotients: dividend x divisor stays below 2^32 (at most 384 units of 2048 tiles
+      // by 2048, and 384 x 1024 by 16 x 384)
+      s.by_per = 0xFFFFFFFFu / (uint32_t)(a.I / 8) + 1u;
+      s.by_run = 0xFFFFFFFFu / (uint32_t)max(16, 16 * all) + 1u;
+    }
   }
   __syncthreads();
   for (int r = threadIdx.x; r < n * a.K; r += kFewThreads) {
@@ -327,9 +333,9 @@ __device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], 
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
-__device__ __forceinline__ int ld_acquire(const int32_t* p) {
+__device__ __forceinline__ int ld_relaxed(const int32_t* p) {
   int v;
-  asm volatile("ld.acquire.gpu.global.s32 %0, [%1];" : "=r"(v) : "l"(p) : "memory");
+  asm volatile("ld.relaxed.gpu.global.s32 %0, [%1];" : "=r"(v) : "l"(p) : "memory");
   return v;
 }
 __device__ __forceinline__ void red_release(int32_t* p) {
@@ -367,20 +373,22 @@ struct TileOf {
   int cols;            // contraction
 };
 
-// FC1 tiles: expert by expert, so that the first ones are complete early. FC2 tiles: column
-// tile by column tile, so that outputs are finished all along and not at the end alone.
+// FC1 tiles: unit by unit, so that the first ones are complete early. FC2 tiles: 16 column
+// tiles of every unit at a time: outputs are finished all along and not at the end alone, and
+// neighbouring blocks read neighbouring rows.
 __device__ __forceinline__ TileOf tile_of(const FewArgs& a, const FewShared& s, int tile) {
   TileOf t;
   const int per = a.I / 8, tiles1 = s.units * per;
   t.fc2 = tile >= tiles1;
   if (!t.fc2) {
-    t.unit = tile / per;
+    t.unit = (int)__umulhi((uint32_t)tile, s.by_per);
     t.row = (tile - t.unit * per) * 8;
     t.cols = a.H;
   } else {
-    const int i = tile - tiles1, c = i / s.units;
-    t.unit = i - c * s.units;
-    t.row = c * kRows;
+    const int i = tile - tiles1, run = 16 * s.units, c16 = (int)__umulhi((uint32_t)i, s.by_run), r = i - c16 * run;
+    const int wide = min(16, a.H / kRows - 16 * c16);
+    t.unit = wide == 16 ? r >> 4 : r / wide;
+    t.row = (16 * c16 + r - t.unit * wide) * kRows;
     t.cols = a.I;
   }
   return t;
@@ -465,23 +473,22 @@ __device__ __forceinline__ void activations_role(const FewArgs& a, FewShared& s,
       k = 0;
       t = tile_of(a, s, tile);
       if (t.fc2 && !s.unit_done[t.unit]) {
-        // h is complete when all tiles of its features have said so; 32 units are asked at
-        // once, since each answer takes a microsecond under load
-        const int u = (t.unit & ~31) + lane, want = a.I / 8;
+        // h is complete when all tiles of its features have said so
+        const int want = a.I / 8;
         const uint64_t t0 = globaltimer_ns();
-        uint32_t have = 0;
-        for (uint32_t i = 1;; ++i) {
-          have = __ballot_sync(0xFFFFFFFFu, u < s.units && ld_acquire(count + 1 + u) >= want);
-          if ((have >> (t.unit & 31)) & 1u) break;
-          if ((i & 255u) == 0u && __shfl_sync(0xFFFFFFFFu, (int)(globaltimer_ns() - t0 > 2000000000ull), 0)) {
+        bool ok = true;
+        for (uint32_t i = 1; ld_relaxed(count + 1 + t.unit) < want; ++i) {
+          if ((i & 255u) == 0u && globaltimer_ns() - t0 > 2000000000ull) {
             atomicOr(a.err, kErrWaitUnit);
-            have = 0;
+            ok = false;
             break;
           }
         }
-        if (have == 0) break;
+        if (!__all_sync(0xFFFFFFFFu, ok)) break;
+        // the answer took a microsecond under load: the other units are asked together
+        for (int u = lane; u < s.units; u += 32)
+          if (ld_relaxed(count + 1 + u) >= want) s.unit_done[u] = 1;
         __threadfence();
-        if ((have >> lane) & 1u) s.unit_done[u] = 1;
         __syncwarp();
       }
       rows = s.unit_n[t.unit];
@@ -602,11 +609,20 @@ __device__ __forceinline__ void outputs_role(const FewArgs& a, FewShared& s, int
   const int w = (threadIdx.x >> 5) - kMmaWarps - 2, lane = threadIdx.x & 31;
   int32_t* col_count = count + 1 + kMaxUnits;
   const float* r = red + w * (R::kRed / 4);
-  int last_row = -1, arrived = 0;  // the column tile before this one: its count is read a tile later
-  auto finish_columns = [&]() {
-    if (last_row < 0 || __shfl_sync(0xFFFFFFFFu, arrived, 0) != s.units - 1) return;
+  // An FC2 tile's products are counted when the warp gets its next tile: by then they have
+  // reached memory and the fence finds little to wait for; the count is read after that tile.
+  int last_row = -1, counted = -1, arrived = 0;
+  auto count_last = [&]() {
+    counted = last_row;
+    if (last_row >= 0 && lane == 0) {
+      __threadfence();
+      arrived = atomicAdd(col_count + last_row / kRows, 1);
+    }
+  };
+  auto finish_counted = [&]() {  // the outputs of the columns whose last products were counted
+    if (counted < 0 || __shfl_sync(0xFFFFFFFFu, arrived, 0) != s.units - 1) return;
     __threadfence();
-    const int c = last_row + 4 * (lane & 3);
+    const int c = counted + 4 * (lane & 3);
     constexpr int kTwo = 2;  // tokens of a lane under way at once
     for (int t0 = lane >> 2; t0 < n; t0 += 8 * kTwo) {
       float4 y[kTwo] = {};
@@ -655,7 +671,8 @@ __device__ __forceinline__ void outputs_role(const FewArgs& a, FewShared& s, int
     if (!mbar_wait_warp(smem_u32(&s.rfull[w]), par, a.err, kErrWaitAccum)) break;
     const int tile = s.red_tile[w];
     if (tile < 0) {
-      finish_columns();
+      count_last();
+      finish_counted();
       break;
     }
     const TileOf t = tile_of(a, s, tile);
@@ -678,6 +695,7 @@ __device__ __forceinline__ void outputs_role(const FewArgs& a, FewShared& s, int
         red_release(count + 1 + t.unit);
       }
     } else {
+      count_last();
       for (int i = lane; i < 16 * tok; i += 32) {
         const int f = i & 15, c = i >> 4;
         float v = 0.0f;
@@ -686,12 +704,8 @@ __device__ __forceinline__ void outputs_role(const FewArgs& a, FewShared& s, int
         o[(size_t)s.list[at + c] * a.H + t.row + f] = v;
       }
       __syncwarp();
-      finish_columns();
-      if (lane == 0) {
-        mbar_arrive(smem_u32(&s.rempty[w]));
-        __threadfence();
-        arrived = atomicAdd(col_count + t.row / kRows, 1);
-      }
+      if (lane == 0) mbar_arrive(smem_u32(&s.rempty[w]));
+      finish_counted();
       last_row = t.row;
     }
     __syncwarp();
