@@ -679,12 +679,12 @@ typedef struct moe_adamw_tensor {
   float* m_scale;    /* [ceil(n/256)] f32 with state_bits 8, else NULL */
   float* v_scale;
   int64_t n;         /* values, 0 or more */
-  int64_t first;     /* index of the first value in the hash (0 or more) */
+  int64_t first;     /* index of the first value in the hash: 0 or more, a multiple of 256 */
   float weight_decay;
   int32_t grad_bf16;
 } moe_adamw_tensor_t;
 
-/*  lr, beta1, beta2 (0 up to, not including, 1), eps (over 0): finite, the betas in 64
+/*  lr, beta1, beta2 (0 up to, not including, 1), eps (1e-30 or more): finite, the betas in 64
  *  bits since 1-beta of an f32 beta near 1 has few digits left; state_bits 32 or 8;
  *  seed of the rounding (8 bits) */
 typedef struct moe_adamw_config {

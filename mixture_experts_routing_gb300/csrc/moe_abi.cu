@@ -1016,7 +1016,7 @@ int moe_adamw_step(const moe_adamw_config_t* cfg, const moe_adamw_tensor_t* tens
                    int n_tensors, const float* lr_dev, const float* grad_scale, int32_t* steps,
                    cudaStream_t stream) {
   if (!cfg || !isfinite(cfg->lr) || !(cfg->beta1 >= 0.0 && cfg->beta1 < 1.0) ||
-      !(cfg->beta2 >= 0.0 && cfg->beta2 < 1.0) || !(cfg->eps > 0.0f) || !isfinite(cfg->eps) ||
+      !(cfg->beta2 >= 0.0 && cfg->beta2 < 1.0) || !(cfg->eps >= 1e-30f) || !isfinite(cfg->eps) ||
       (cfg->state_bits != 8 && cfg->state_bits != 32) || n_tensors < 0 ||
       n_tensors > (1 << 20) || (n_tensors > 0 && !tensors) || !steps || !aligned4(steps) ||
       !aligned4(lr_dev) || !aligned4(grad_scale))
@@ -1024,7 +1024,7 @@ int moe_adamw_step(const moe_adamw_config_t* cfg, const moe_adamw_tensor_t* tens
   const bool small = cfg->state_bits == 8;
   for (int i = 0; i < n_tensors; ++i) {  // every tensor before the first launch
     const moe_adamw_tensor_t& t = tensors[i];
-    if (t.n < 0 || t.n > ((int64_t)1 << 40) || t.first < 0 || t.first > ((int64_t)1 << 60) ||
+    if (t.n < 0 || t.n > ((int64_t)1 << 40) || t.first < 0 || t.first > ((int64_t)1 << 60) || t.first % moe::kAdamwBlock != 0 ||
         !isfinite(t.weight_decay) || (t.grad_bf16 != 0 && t.grad_bf16 != 1))
       return MOE_ERR_INVALID_ARG;
     if (t.n == 0) continue;

@@ -121,7 +121,7 @@ def adamw(**over):
 
 
 @pytest.mark.parametrize("field,value", [
-    ("beta1", 1.0), ("beta1", -0.1), ("beta2", math.nan), ("beta2", 1.5), ("lr", math.inf), ("lr", math.nan), ("eps", 0.0), ("eps", -1.0),
+    ("beta1", 1.0), ("beta1", -0.1), ("beta2", math.nan), ("beta2", 1.5), ("lr", math.inf), ("lr", math.nan), ("eps", 0.0), ("eps", 1e-31), ("eps", -1.0),
     ("eps", math.inf), ("state_bits", 16),
 ])
 def test_adamw_config(field, value):
@@ -130,7 +130,7 @@ def test_adamw_config(field, value):
 
 @pytest.mark.parametrize("change", [
     dict(param=None), dict(param=8), dict(master=8), dict(grad=None), dict(grad=8), dict(m=None), dict(m=8), dict(v=None), dict(v=8),
-    dict(m_scale=None), dict(m_scale=2), dict(v_scale=None), dict(n=-1), dict(n=1 << 41), dict(first=-1), dict(weight_decay=math.nan),
+    dict(m_scale=None), dict(m_scale=2), dict(v_scale=None), dict(n=-1), dict(n=1 << 41), dict(first=-1), dict(first=8), dict(weight_decay=math.nan),
     dict(weight_decay=math.inf), dict(grad_bf16=2),
 ])
 def test_adamw_tensors(change):
