@@ -45,7 +45,10 @@ struct NormArgs {
   float* dw;
   float* db;               // or null
   float* part;             // backward workspace
+  uint32_t* err;           // device error word (bounded waits)
 };
+
+constexpr int kNormMaxParts = 256;  // blocks of the backward: partial sums of dw and db
 
 int launch_norm_forward(const NormArgs& a, cudaStream_t s);
 int64_t norm_backward_workspace_bytes(int64_t N, int H);

@@ -945,6 +945,7 @@ static moe::NormArgs norm_args(const moe_norm_config_t* cfg) {
   a.H = cfg->hidden;
   a.rms = cfg->kind == MOE_NORM_RMS;
   a.eps = cfg->eps;
+  a.err = error_word_ptr();
   return a;
 }
 
@@ -961,6 +962,7 @@ int moe_norm_forward(const moe_norm_config_t* cfg, const void* x, const void* ad
       !aligned16(bias) || !aligned16(sum) || !aligned16(y) || !aligned4(mean) || !aligned4(rstd))
     return MOE_ERR_INVALID_ARG;
   moe::NormArgs a = norm_args(cfg);
+  if (!a.err) return MOE_ERR_CUDA;
   a.x = static_cast<const uint16_t*>(x);
   a.add = static_cast<const uint16_t*>(add);
   a.w = weight;
@@ -998,6 +1000,7 @@ int moe_norm_backward(const moe_norm_config_t* cfg, const void* x, const float* 
       !aligned16(dy) || !aligned16(dx_add) || !aligned16(dx))
     return MOE_ERR_INVALID_ARG;
   moe::NormArgs a = norm_args(cfg);
+  if (!a.err) return MOE_ERR_CUDA;
   a.x = static_cast<const uint16_t*>(x);
   a.add = static_cast<const uint16_t*>(dx_add);
   a.w = weight;
