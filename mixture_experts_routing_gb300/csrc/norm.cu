@@ -24,30 +24,60 @@ constexpr uint32_t kRingBytes = 200u << 10;
 constexpr int kMaxStages = 8;
 constexpr uint32_t kErrWaitRows = 1u << 5;  // rows never arrived
 
-__device__ __forceinline__ void unpack8(const uint4& q, float (&v)[8]) {
-  v[0] = __uint_as_float(q.x << 16);
-  v[1] = __uint_as_float(q.x & 0xFFFF0000u);
-  v[2] = __uint_as_float(q.y << 16);
-  v[3] = __uint_as_float(q.y & 0xFFFF0000u);
-  v[4] = __uint_as_float(q.z << 16);
-  v[5] = __uint_as_float(q.z & 0xFFFF0000u);
-  v[6] = __uint_as_float(q.w << 16);
-  v[7] = __uint_as_float(q.w & 0xFFFF0000u);
+// Two fp32 values in one register pair, worked on by one instruction: the kernels are short of
+// issue slots before they are short of memory (the backward of 7168 columns took 350
+// instructions a thread and row, and 57 us, without them).
+struct F2 {
+  uint64_t v;
+};
+__device__ __forceinline__ F2 f2(float lo, float hi) {
+  F2 r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r.v) : "f"(lo), "f"(hi));
+  return r;
+}
+__device__ __forceinline__ F2 f2(float x) { return f2(x, x); }
+__device__ __forceinline__ float2 split(F2 a) {
+  float2 r;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(a.v));
+  return r;
+}
+__device__ __forceinline__ F2 add2(F2 a, F2 b) {
+  F2 r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
+  return r;
+}
+__device__ __forceinline__ F2 mul2(F2 a, F2 b) {
+  F2 r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
+  return r;
+}
+__device__ __forceinline__ F2 fma2(F2 a, F2 b, F2 c) {
+  F2 r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r.v) : "l"(a.v), "l"(b.v), "l"(c.v));
+  return r;
 }
 
-__device__ __forceinline__ uint32_t pack2(float lo, float hi) {
-  const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
+__device__ __forceinline__ F2 unpack2(uint32_t q) { return f2(__uint_as_float(q << 16), __uint_as_float(q & 0xFFFF0000u)); }
+__device__ __forceinline__ void unpack8(const uint4& q, F2 (&v)[4]) {
+  v[0] = unpack2(q.x);
+  v[1] = unpack2(q.y);
+  v[2] = unpack2(q.z);
+  v[3] = unpack2(q.w);
+}
+__device__ __forceinline__ uint32_t pack2(F2 a) {
+  const float2 f = split(a);
+  const __nv_bfloat162 v = __floats2bfloat162_rn(f.x, f.y);
   return *reinterpret_cast<const uint32_t*>(&v);
 }
-
-__device__ __forceinline__ uint4 pack8(const float (&v)[8]) {
-  return make_uint4(pack2(v[0], v[1]), pack2(v[2], v[3]), pack2(v[4], v[5]), pack2(v[6], v[7]));
+__device__ __forceinline__ uint4 pack8(const F2 (&v)[4]) {
+  return make_uint4(pack2(v[0]), pack2(v[1]), pack2(v[2]), pack2(v[3]));
 }
-
-__device__ __forceinline__ void load8(const float* p, float (&v)[8]) {
+__device__ __forceinline__ void load8(const float* p, F2 (&v)[4]) {
   const float4 a = reinterpret_cast<const float4*>(p)[0], b = reinterpret_cast<const float4*>(p)[1];
-  v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
-  v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
+  v[0] = f2(a.x, a.y);
+  v[1] = f2(a.z, a.w);
+  v[2] = f2(b.x, b.y);
+  v[3] = f2(b.z, b.w);
 }
 
 __device__ __forceinline__ uint4 lds16(uint32_t at) {
@@ -60,65 +90,70 @@ __device__ __forceinline__ uint4 lds16(uint32_t at) {
 // warps), `rows` rows at a time.
 struct Plan {
   int lanes, rows, threads;
-  int64_t steps;     // row groups
+  uint32_t steps;    // row groups
   int stages;
   uint32_t stage;    // bytes: `tensors` x rows x H x 2
 };
 
-// Sums of v over a row's threads, the same in all of them. slot: a float per warp and value;
-// it is written again two calls later at the earliest, behind another barrier.
-template <int NV>
-__device__ __forceinline__ void row_sum(float (&v)[NV], const Plan& p, float (*slot)[NV]) {
-  const int width = p.lanes < 32 ? p.lanes : 32;
+// The sum of v (a value, or a pair) over a row's threads, the same in all of them. WIDE: a
+// row takes several warps, which meet in slot, one entry a warp (written again two calls
+// later at the earliest, behind another barrier); else it takes `lanes` lanes of one.
+__device__ __forceinline__ float add(float a, float b) { return a + b; }
+__device__ __forceinline__ F2 add(F2 a, F2 b) { return add2(a, b); }
+__device__ __forceinline__ float from_lane(float v, int o) { return __shfl_xor_sync(0xFFFFFFFFu, v, o); }
+__device__ __forceinline__ F2 from_lane(F2 v, int o) {
+  const float2 f = split(v);
+  return f2(__shfl_xor_sync(0xFFFFFFFFu, f.x, o), __shfl_xor_sync(0xFFFFFFFFu, f.y, o));
+}
+__device__ __forceinline__ void clear(float& v) { v = 0.0f; }
+__device__ __forceinline__ void clear(F2& v) { v = f2(0.0f); }
+template <bool WIDE, typename T>
+__device__ __forceinline__ T row_sum(T v, int lanes, int first_warp, T* slot) {
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1)
-    if (o < width)
-#pragma unroll
-      for (int i = 0; i < NV; ++i) v[i] += __shfl_xor_sync(0xFFFFFFFFu, v[i], o);
-  if (p.lanes <= 32) return;
-  const int warp = threadIdx.x >> 5, per = p.lanes >> 5, first = warp / per * per;
-  if ((threadIdx.x & 31) == 0)
-#pragma unroll
-    for (int i = 0; i < NV; ++i) slot[warp][i] = v[i];
+    if (WIDE || o < lanes) v = add(v, from_lane(v, o));
+  if (!WIDE) return v;
+  const int lane = threadIdx.x & 31;
+  if (lane == 0) slot[threadIdx.x >> 5] = v;
   __syncthreads();
-  const int l = threadIdx.x & 31;
+  clear(v);
+  if (lane < (lanes >> 5)) v = slot[first_warp + lane];
 #pragma unroll
-  for (int i = 0; i < NV; ++i) v[i] = l < per ? slot[first + l][i] : 0.0f;
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1)
-#pragma unroll
-    for (int i = 0; i < NV; ++i) v[i] += __shfl_xor_sync(0xFFFFFFFFu, v[i], o);
+  for (int o = 16; o > 0; o >>= 1) v = add(v, from_lane(v, o));
+  return v;
 }
 
 // The block's ring of row groups: TENSORS arrays, each `rows` rows of it, a bulk copy each.
 template <int TENSORS>
 struct Rows {
   uint64_t* full;
-  uint32_t base;
-  int64_t N;
+  uint32_t base, N;
   int H;
   Plan p;
   const uint16_t* from[TENSORS];
 
-  __device__ __forceinline__ uint32_t at(int stage, int tensor) const {
-    return base + (uint32_t)stage * p.stage + (uint32_t)tensor * (p.stage / TENSORS);
-  }
-  __device__ __forceinline__ void load(int64_t step, int stage) const {  // one thread
-    const int64_t row = step * p.rows;
-    const uint32_t bytes = (uint32_t)(min((int64_t)p.rows, N - row) * H * 2), bar = smem_u32(&full[stage]);
-    mbar_arrive_expect_tx(bar, bytes * TENSORS);
+  // By the first threads of the first warps, a copy each (a block has as many warps, or its
+  // first one does them all); the copies may land before the bytes are announced.
+  __device__ __forceinline__ bool loads() const { return threadIdx.x < 32 * TENSORS && (threadIdx.x & 31) == 0; }
+  __device__ __forceinline__ void load(uint32_t step, int stage) const {
+    const int warp = threadIdx.x >> 5;
+    const uint32_t row = step * p.rows, part = p.stage / TENSORS;
+    const uint32_t bytes = min((uint32_t)p.rows, N - row) * H * 2, bar = smem_u32(&full[stage]);
+    if (warp == 0) mbar_arrive_expect_tx(bar, bytes * TENSORS);
+    const int last = p.threads >= 32 * TENSORS ? warp + 1 : TENSORS;
 #pragma unroll
-    for (int i = 0; i < TENSORS; ++i) bulk_load(at(stage, i), from[i] + row * H, bytes, bar);
+    for (int i = 0; i < TENSORS; ++i)
+      if (i >= warp && i < last) bulk_load(base + stage * p.stage + i * part, from[i] + (size_t)row * H, bytes, bar);
   }
 };
 
-// KV: groups of 8 columns a thread holds.
-template <bool RMS, bool ADD, int KV>
-__global__ void __launch_bounds__(kMaxThreads, 1) norm_forward_kernel(const NormArgs a, const Plan p) {
+// KV: groups of 8 columns a thread holds. T: threads of a block at most, 1024 / T blocks an SM.
+template <bool RMS, bool ADD, int KV, bool WIDE, int T>
+__global__ void __launch_bounds__(T, kMaxThreads / T) norm_forward_kernel(const NormArgs a, const Plan p) {
   constexpr int kTensors = ADD ? 2 : 1;
   extern __shared__ uint8_t smem[];
   __shared__ __align__(8) uint64_t full[kMaxStages];
-  __shared__ float slots[4][kMaxThreads / 32][1];
+  __shared__ float slots[2][2][T / 32];
   if (threadIdx.x == 0) {
     for (int i = 0; i < p.stages; ++i) mbar_init(smem_u32(&full[i]), 1);
     mbar_fence_init();
@@ -126,107 +161,106 @@ __global__ void __launch_bounds__(kMaxThreads, 1) norm_forward_kernel(const Norm
   __syncthreads();
   griddep_wait();
   griddep_launch_dependents();
-  Rows<kTensors> rows{full, (smem_u32(smem) + 127u) & ~127u, a.N, a.H, p, {}};
+  Rows<kTensors> rows{full, (smem_u32(smem) + 127u) & ~127u, (uint32_t)a.N, a.H, p, {}};
   rows.from[0] = a.x;
   if (ADD) rows.from[kTensors - 1] = a.add;
-  if (threadIdx.x == 0)
-    for (int i = 0; i < p.stages; ++i) {
-      const int64_t step = blockIdx.x + (int64_t)i * gridDim.x;
-      if (step < p.steps) rows.load(step, i);
-    }
+  const bool loads = rows.loads();
+  if (loads)
+    for (int i = 0; i < p.stages; ++i)
+      if (blockIdx.x + i * gridDim.x < p.steps) rows.load(blockIdx.x + i * gridDim.x, i);
   const int H = a.H, mine = threadIdx.x / p.lanes, lane = threadIdx.x - mine * p.lanes;
+  const int first_warp = WIDE ? mine * (p.lanes >> 5) : 0, column2 = p.lanes * 8;
   const float inv_h = 1.0f / (float)H;
-  float w[KV][8], b[KV][8];
+  bool in[KV];
+  F2 w[KV][4], b[KV][4];
 #pragma unroll
   for (int j = 0; j < KV; ++j) {
-    const int c = (j * p.lanes + lane) * 8;
-    if (c < H) {
+    const int c = lane * 8 + j * column2;
+    in[j] = c < H;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) w[j][i] = b[j][i] = f2(0.0f);
+    if (in[j]) {
       load8(a.w + c, w[j]);
       if (a.b) load8(a.b + c, b[j]);
     }
-    if (c >= H || !a.b) {
-#pragma unroll
-      for (int i = 0; i < 8; ++i) b[j][i] = 0.0f;
-    }
   }
+  const uint32_t N = (uint32_t)a.N, rows_on = gridDim.x * p.rows, tensor = p.stage / kTensors;
+  const uint32_t mine_at = rows.base + (uint32_t)(mine * H + lane * 8) * 2;
+  uint32_t row = blockIdx.x * p.rows + mine, from = mine_at, par = 0;
   int stage = 0, turn = 0;
-  uint32_t par = 0;
   bool ok = true;  // after a wait that ran out: no more copies and waits, but every barrier
-  for (int64_t step = blockIdx.x; step < p.steps; step += gridDim.x) {
+  for (uint32_t step = blockIdx.x; step < p.steps; step += gridDim.x, row += rows_on, turn ^= 1) {
     ok = ok && mbar_wait(smem_u32(&full[stage]), par, a.err, kErrWaitRows);
-    const int64_t row = step * p.rows + mine;
-    const bool live = row < a.N;  // the last group may have fewer rows
-    float v[KV][8], sum[1] = {0.0f};
+    const bool live = row < N;  // the last group may have fewer rows
+    const size_t at = (size_t)row * H + lane * 8;
+    F2 v[KV][4], sum = f2(0.0f);
 #pragma unroll
     for (int j = 0; j < KV; ++j) {
-      const int c = (j * p.lanes + lane) * 8;
+      uint4 q = make_uint4(0, 0, 0, 0);
+      const bool here = in[j] && live;
+      if (here) q = lds16(from + j * column2 * 2);
+      unpack8(q, v[j]);
+      if (ADD && here) {
+        F2 r[4];
+        unpack8(lds16(from + tensor + j * column2 * 2), r);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) v[j][i] = 0.0f;
-      if (c < H && live) {
-        unpack8(lds16(rows.at(stage, 0) + (uint32_t)(mine * H + c) * 2), v[j]);
-        if (ADD) {
-          float r[8];
-          unpack8(lds16(rows.at(stage, 1) + (uint32_t)(mine * H + c) * 2), r);
+        for (int i = 0; i < 4; ++i) v[j][i] = add2(v[j][i], r[i]);
+        q = pack8(v[j]);
+        *reinterpret_cast<uint4*>(a.sum + at + j * column2) = q;
+        unpack8(q, v[j]);
+      }
+      if (!RMS) {
 #pragma unroll
-          for (int i = 0; i < 8; ++i) v[j][i] += r[i];
-          const uint4 q = pack8(v[j]);
-          *reinterpret_cast<uint4*>(a.sum + row * H + c) = q;
-          unpack8(q, v[j]);
-        }
-#pragma unroll
-        for (int i = 0; i < 8; ++i) sum[0] += v[j][i];
+        for (int i = 0; i < 4; ++i) sum = add2(sum, v[j][i]);
       }
     }
     float mean = 0.0f;
     if (!RMS) {
-      row_sum(sum, p, slots[turn]);
-      mean = sum[0] * inv_h;
+      const float2 s = split(sum);
+      mean = row_sum<WIDE>(s.x + s.y, p.lanes, first_warp, slots[turn][0]) * inv_h;
     }
-    float sq[1] = {0.0f};
+    F2 sq = f2(0.0f);
 #pragma unroll
     for (int j = 0; j < KV; ++j) {
-      if ((j * p.lanes + lane) * 8 < H) {
+      if (RMS || in[j]) {  // columns past the row are zeros, not minus the mean
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          v[j][i] -= mean;
-          sq[0] += v[j][i] * v[j][i];
+        for (int i = 0; i < 4; ++i) {
+          if (!RMS) v[j][i] = add2(v[j][i], f2(-mean));
+          sq = fma2(v[j][i], v[j][i], sq);
         }
       }
     }
-    row_sum(sq, p, slots[turn + 1]);
-    turn ^= 2;
+    const float2 s = split(sq);
+    const float var = row_sum<WIDE>(s.x + s.y, p.lanes, first_warp, slots[turn][1]) * inv_h;
     // every thread has the stage's rows in registers behind this barrier (row_sum has one of
     // its own where a row takes several warps)
-    if (p.lanes <= 32) __syncthreads();
-    if (threadIdx.x == 0) {
-      const int64_t next = step + (int64_t)p.stages * gridDim.x;
-      if (ok && next < p.steps) rows.load(next, stage);
-    }
-    if (++stage == p.stages) { stage = 0; par ^= 1u; }
+    if (!WIDE) __syncthreads();
+    if (loads && ok && step + p.stages * gridDim.x < p.steps) rows.load(step + p.stages * gridDim.x, stage);
+    from += p.stage;
+    if (++stage == p.stages) { stage = 0; from = mine_at; par ^= 1u; }
     if (!live) continue;
-    const float r = 1.0f / sqrtf(sq[0] * inv_h + a.eps);
+    const float r = 1.0f / sqrtf(var + a.eps);
     if (lane == 0) {
       if (!RMS && a.mean) a.mean[row] = mean;
       if (a.rstd) a.rstd[row] = r;
     }
 #pragma unroll
     for (int j = 0; j < KV; ++j) {
-      const int c = (j * p.lanes + lane) * 8;
-      if (c >= H) continue;
-      float o[8];
+      if (!in[j]) continue;
+      F2 o[4];
 #pragma unroll
-      for (int i = 0; i < 8; ++i) o[i] = fmaf(v[j][i] * r, w[j][i], b[j][i]);
-      *reinterpret_cast<uint4*>(a.y + row * H + c) = pack8(o);
+      for (int i = 0; i < 4; ++i) o[i] = fma2(mul2(v[j][i], f2(r)), w[j][i], b[j][i]);
+      *reinterpret_cast<uint4*>(a.y + at + j * column2) = pack8(o);
     }
   }
 }
 
-template <bool RMS, bool ADD, int KV>
+template <bool RMS, bool ADD, int KV, bool WIDE>
 __global__ void __launch_bounds__(kMaxThreads, 1) norm_backward_kernel(const NormArgs a, const Plan p) {
   constexpr int kTensors = ADD ? 3 : 2;
   extern __shared__ uint8_t smem[];
   __shared__ __align__(8) uint64_t full[kMaxStages];
-  __shared__ float slots[2][kMaxThreads / 32][2];
+  __shared__ F2 slots[2][kMaxThreads / 32];
   if (threadIdx.x == 0) {
     for (int i = 0; i < p.stages; ++i) mbar_init(smem_u32(&full[i]), 1);
     mbar_fence_init();
@@ -238,80 +272,89 @@ __global__ void __launch_bounds__(kMaxThreads, 1) norm_backward_kernel(const Nor
   // registers too the sums would spill, and the ring leaves the first-level cache no room
   const uint32_t base = ((smem_u32(smem) + 127u) & ~127u) + (KV == 1 ? ((uint32_t)a.H * 4 + 127u) & ~127u : 0u);
   float* ws = reinterpret_cast<float*>(smem + (base - smem_u32(smem))) - a.H;
-  Rows<kTensors> rows{full, base, a.N, a.H, p, {}};
+  Rows<kTensors> rows{full, base, (uint32_t)a.N, a.H, p, {}};
   rows.from[0] = a.x;
   rows.from[1] = a.dy;
   if (ADD) rows.from[kTensors - 1] = a.add;
-  if (threadIdx.x == 0)
-    for (int i = 0; i < p.stages; ++i) {
-      const int64_t step = blockIdx.x + (int64_t)i * gridDim.x;
-      if (step < p.steps) rows.load(step, i);
-    }
+  const bool loads = rows.loads();
+  if (loads)
+    for (int i = 0; i < p.stages; ++i)
+      if (blockIdx.x + i * gridDim.x < p.steps) rows.load(blockIdx.x + i * gridDim.x, i);
   const int H = a.H, mine = threadIdx.x / p.lanes, lane = threadIdx.x - mine * p.lanes;
+  const int first_warp = WIDE ? mine * (p.lanes >> 5) : 0, column2 = p.lanes * 8;
   const float inv_h = 1.0f / (float)H;
   if (KV == 1)
     for (int c = threadIdx.x * 4; c < H; c += p.threads * 4)
       *reinterpret_cast<float4*>(ws + c) = *reinterpret_cast<const float4*>(a.w + c);
   __syncthreads();
-  float dw[KV][8] = {}, db[KV][8] = {};
+  F2 dw[KV][4], db[KV][4];
+#pragma unroll
+  for (int j = 0; j < KV; ++j)
+#pragma unroll
+    for (int i = 0; i < 4; ++i) dw[j][i] = db[j][i] = f2(0.0f);
+  const uint32_t N = (uint32_t)a.N, rows_on = gridDim.x * p.rows, tensor = p.stage / kTensors;
+  const uint32_t mine_at = base + (uint32_t)(mine * H + lane * 8) * 2;
+  uint32_t row = blockIdx.x * p.rows + mine, from = mine_at, par = 0;
   int stage = 0, turn = 0;
-  uint32_t par = 0;
   bool ok = true;  // after a wait that ran out: no more copies and waits, but every barrier
-  for (int64_t step = blockIdx.x; step < p.steps; step += gridDim.x, turn ^= 1) {
-    const int64_t row = step * p.rows + mine;
-    const bool live = row < a.N;
-    float mean = 0.0f, r = 0.0f;
-    if (live) {
-      if (!RMS) mean = a.mean[row];
-      r = a.rstd[row];
+  float next_mean = 0.0f, next_r = 0.0f;  // a step ahead: their way from memory is longer than a step
+  auto stats = [&](uint32_t row) {
+    if (row < N) {
+      if (!RMS) next_mean = a.mean[row];
+      next_r = a.rstd[row];
     }
+  };
+  stats(row);
+  for (uint32_t step = blockIdx.x; step < p.steps; step += gridDim.x, row += rows_on, turn ^= 1) {
+    const bool live = row < N;
+    const float mean = next_mean, r = next_r;
+    stats(row + rows_on);
     ok = ok && mbar_wait(smem_u32(&full[stage]), par, a.err, kErrWaitRows);
-    float z[KV][8], g[KV][8], s[2] = {0.0f, 0.0f};
-    uint4 add[KV];
+    F2 z[KV][4], g[KV][4], sg = f2(0.0f), sgz = f2(0.0f);
+    uint4 res[KV];
 #pragma unroll
     for (int j = 0; j < KV; ++j) {
-      const int c = (j * p.lanes + lane) * 8;
+      const int c = lane * 8 + j * column2;
       if (c < H && live) {
-        const uint32_t off = (uint32_t)(mine * H + c) * 2;
-        float w[8];
-        unpack8(lds16(rows.at(stage, 0) + off), z[j]);
-        unpack8(lds16(rows.at(stage, 1) + off), g[j]);
-        if (ADD) add[j] = lds16(rows.at(stage, kTensors - 1) + off);
+        const uint32_t off = from + j * column2 * 2;
+        F2 w[4];
+        unpack8(lds16(off), z[j]);
+        unpack8(lds16(off + tensor), g[j]);
+        if (ADD) res[j] = lds16(off + 2 * tensor);
         load8(KV == 1 ? ws + c : a.w + c, w);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          z[j][i] = (z[j][i] - mean) * r;
-          dw[j][i] = fmaf(g[j][i], z[j][i], dw[j][i]);
-          db[j][i] += g[j][i];
-          g[j][i] *= w[i];
-          s[0] = fmaf(g[j][i], z[j][i], s[0]);
-          if (!RMS) s[1] += g[j][i];
+        for (int i = 0; i < 4; ++i) {
+          if (!RMS) z[j][i] = add2(z[j][i], f2(-mean));
+          z[j][i] = mul2(z[j][i], f2(r));
+          dw[j][i] = fma2(g[j][i], z[j][i], dw[j][i]);
+          db[j][i] = add2(db[j][i], g[j][i]);
+          g[j][i] = mul2(g[j][i], w[i]);
+          sgz = fma2(g[j][i], z[j][i], sgz);
+          if (!RMS) sg = add2(sg, g[j][i]);
         }
       }
     }
-    row_sum(s, p, slots[turn]);
-    if (p.lanes <= 32) __syncthreads();
-    if (threadIdx.x == 0) {
-      const int64_t next = step + (int64_t)p.stages * gridDim.x;
-      if (ok && next < p.steps) rows.load(next, stage);
-    }
-    if (++stage == p.stages) { stage = 0; par ^= 1u; }
+    const float2 u = split(sgz), t = split(sg);
+    const float2 s = split(row_sum<WIDE>(f2(u.x + u.y, t.x + t.y), p.lanes, first_warp, slots[turn]));
+    if (!WIDE) __syncthreads();
+    if (loads && ok && step + p.stages * gridDim.x < p.steps) rows.load(step + p.stages * gridDim.x, stage);
+    from += p.stage;
+    if (++stage == p.stages) { stage = 0; from = mine_at; par ^= 1u; }
     if (!live) continue;
-    const float mz = s[0] * inv_h, mg = RMS ? 0.0f : s[1] * inv_h;
+    const size_t at = (size_t)row * H + lane * 8;
+    const F2 mz = f2(-s.x * inv_h), mg = f2(-s.y * inv_h);
 #pragma unroll
     for (int j = 0; j < KV; ++j) {
-      const int c = (j * p.lanes + lane) * 8;
-      if (c >= H) continue;
-      float o[8];
+      if (lane * 8 + j * column2 >= H) continue;
+      F2 o[4], t[4];
+      if (ADD) unpack8(res[j], t);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) o[i] = r * (g[j][i] - z[j][i] * mz - mg);
-      if (ADD) {
-        float t[8];
-        unpack8(add[j], t);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) o[i] += t[i];
+      for (int i = 0; i < 4; ++i) {
+        o[i] = fma2(z[j][i], mz, g[j][i]);
+        if (!RMS) o[i] = add2(o[i], mg);
+        o[i] = ADD ? fma2(o[i], f2(r), t[i]) : mul2(o[i], f2(r));
       }
-      *reinterpret_cast<uint4*>(a.dx + row * H + c) = pack8(o);
+      *reinterpret_cast<uint4*>(a.dx + at + j * column2) = pack8(o);
     }
   }
   // the block's sums: its rows' groups are added in order through shared memory
@@ -325,15 +368,22 @@ __global__ void __launch_bounds__(kMaxThreads, 1) norm_backward_kernel(const Nor
         const int c = (j * p.lanes + lane) * 8;
         if (c >= H) continue;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const float x = turn2 ? sums[c + i] + dw[j][i] : dw[j][i], y = turn2 ? sums[H + c + i] + db[j][i] : db[j][i];
-          if (turn2 == p.rows - 1) {
-            part[c + i] = x;
-            part[H + c + i] = y;
-          } else {
-            sums[c + i] = x;
-            sums[H + c + i] = y;
+        for (int i = 0; i < 8; i += 4) {
+          const float2 x0 = split(dw[j][i / 2]), x1 = split(dw[j][i / 2 + 1]), y0 = split(db[j][i / 2]), y1 = split(db[j][i / 2 + 1]);
+          float4 x = make_float4(x0.x, x0.y, x1.x, x1.y), y = make_float4(y0.x, y0.y, y1.x, y1.y);
+          float4* xs = reinterpret_cast<float4*>(sums + c + i);
+          float4* ys = reinterpret_cast<float4*>(sums + H + c + i);
+          if (turn2) {
+            const float4 u = *xs, v = *ys;
+            x = make_float4(x.x + u.x, x.y + u.y, x.z + u.z, x.w + u.w);
+            y = make_float4(y.x + v.x, y.y + v.y, y.z + v.z, y.w + v.w);
           }
+          if (turn2 == p.rows - 1) {
+            xs = reinterpret_cast<float4*>(part + c + i);
+            ys = reinterpret_cast<float4*>(part + H + c + i);
+          }
+          *xs = x;
+          *ys = y;
         }
       }
     }
@@ -341,44 +391,49 @@ __global__ void __launch_bounds__(kMaxThreads, 1) norm_backward_kernel(const Nor
   }
 }
 
-// dw and db from the blocks' partial sums: 32 columns a block, eight runs of the parts, added
-// in order.
+// dw and db from the blocks' partial sums: 32 groups of 4 columns a block, eight runs of the
+// parts, added in order.
 __global__ void __launch_bounds__(256) norm_parts_kernel(const float* part, int parts, int H, float* dw, float* db) {
-  __shared__ float sums[8][32];
+  __shared__ float4 sums[8][32];
   griddep_wait();
   griddep_launch_dependents();
-  const int c = blockIdx.x * 32 + (threadIdx.x & 31), q = threadIdx.x >> 5;
-  float t = 0.0f;
-  if (c < 2 * H) {
+  const int c = (blockIdx.x * 32 + (threadIdx.x & 31)) * 4, q = threadIdx.x >> 5;
+  float4 t = make_float4(0.f, 0.f, 0.f, 0.f);
+  const bool wanted = c < (db ? 2 * H : H);
+  if (wanted) {
     const int p0 = q * parts / 8, p1 = (q + 1) * parts / 8;
 #pragma unroll 8
-    for (int p = p0; p < p1; ++p) t += part[(int64_t)p * 2 * H + c];
+    for (int p = p0; p < p1; ++p) {
+      const float4 v = *reinterpret_cast<const float4*>(part + (int64_t)p * 2 * H + c);
+      t = make_float4(t.x + v.x, t.y + v.y, t.z + v.z, t.w + v.w);
+    }
   }
   sums[q][threadIdx.x & 31] = t;
   __syncthreads();
-  if (q || c >= 2 * H) return;
+  if (q || !wanted) return;
 #pragma unroll
-  for (int i = 1; i < 8; ++i) t += sums[i][threadIdx.x];
-  if (c < H) dw[c] = t;
-  else if (db) db[c - H] = t;
+  for (int i = 1; i < 8; ++i) {
+    const float4 v = sums[i][threadIdx.x];
+    t = make_float4(t.x + v.x, t.y + v.y, t.z + v.z, t.w + v.w);
+  }
+  *reinterpret_cast<float4*>(c < H ? dw + c : db + (c - H)) = t;
 }
 
 constexpr int kWide = 8192;  // columns from which a thread takes 16 of a row instead of 8
 
 uint32_t weight_bytes(int H) { return H > kWide ? 0u : ((uint32_t)H * 4 + 127u) & ~127u; }
 
-Plan plan_of(int64_t N, int H, int tensors, uint32_t ring) {
+Plan plan_of(int64_t N, int H, int tensors, uint32_t ring, int kv, int threads) {
   Plan p{};
-  const int groups = (H / 8 + (H > kWide)) / (H > kWide ? 2 : 1);
+  const int groups = (H / 8 + kv - 1) / kv;
   p.lanes = 1;
   while (p.lanes < 32 && p.lanes < groups) p.lanes *= 2;
   if (groups > 32) p.lanes = (groups + 31) / 32 * 32;
-  p.rows = kMaxThreads / p.lanes;
-  p.threads = (p.rows * p.lanes + 31) / 32 * 32;
+  p.rows = threads / p.lanes;
   const uint32_t row = (uint32_t)H * 2 * tensors;
   while (p.rows > 1 && (uint64_t)p.rows * row > ring / 3) p.rows /= 2;
   p.threads = p.rows * p.lanes;
-  p.steps = (N + p.rows - 1) / p.rows;
+  p.steps = (uint32_t)((N + p.rows - 1) / p.rows);
   p.stage = (uint32_t)p.rows * row;
   p.stages = (int)(ring / p.stage);
   if (p.stages > kMaxStages) p.stages = kMaxStages;
@@ -392,10 +447,12 @@ cudaError_t ring_smem(K* kernel) {
 
 template <bool RMS, bool ADD>
 cudaError_t opt_in() {
-  cudaError_t e = ring_smem(norm_forward_kernel<RMS, ADD, 1>);
-  if (e == cudaSuccess) e = ring_smem(norm_forward_kernel<RMS, ADD, 2>);
-  if (e == cudaSuccess) e = ring_smem(norm_backward_kernel<RMS, ADD, 1>);
-  if (e == cudaSuccess) e = ring_smem(norm_backward_kernel<RMS, ADD, 2>);
+  cudaError_t e = ring_smem(norm_forward_kernel<RMS, ADD, 2, false, 512>);
+  if (e == cudaSuccess) e = ring_smem(norm_forward_kernel<RMS, ADD, 2, true, 512>);
+  if (e == cudaSuccess) e = ring_smem(norm_forward_kernel<RMS, ADD, 2, true, 1024>);
+  if (e == cudaSuccess) e = ring_smem(norm_backward_kernel<RMS, ADD, 1, false>);
+  if (e == cudaSuccess) e = ring_smem(norm_backward_kernel<RMS, ADD, 1, true>);
+  if (e == cudaSuccess) e = ring_smem(norm_backward_kernel<RMS, ADD, 2, true>);
   return e;
 }
 
@@ -412,21 +469,27 @@ int sm_count(cudaError_t* err) {
   return sms;
 }
 
-unsigned grid_of(const Plan& p, int sms) { return (unsigned)(p.steps < sms ? p.steps : sms); }
+unsigned grid_of(const Plan& p, int blocks) { return p.steps < (unsigned)blocks ? p.steps : (unsigned)blocks; }
 
-template <int KV>
-cudaError_t forward(const NormArgs& a, const Plan& p, unsigned grid, cudaStream_t s) {
-  auto k = a.rms ? (a.add ? norm_forward_kernel<true, true, KV> : norm_forward_kernel<true, false, KV>)
-                 : (a.add ? norm_forward_kernel<false, true, KV> : norm_forward_kernel<false, false, KV>);
-  return launch_pdl(k, dim3(grid), dim3(p.threads), p.stages * p.stage + 128, s, a, p);
+template <bool RMS, bool ADD>
+cudaError_t forward(const NormArgs& a, int sms, cudaStream_t s) {
+  const int threads = a.H > kWide ? 1024 : 512, blocks = kMaxThreads / threads;
+  const Plan p = plan_of(a.N, a.H, ADD ? 2 : 1, kRingBytes / blocks, 2, threads);
+  auto k = a.H > kWide     ? norm_forward_kernel<RMS, ADD, 2, true, 1024>
+           : p.lanes > 32 ? norm_forward_kernel<RMS, ADD, 2, true, 512>
+                          : norm_forward_kernel<RMS, ADD, 2, false, 512>;
+  return launch_pdl(k, dim3(grid_of(p, sms * blocks)), dim3(p.threads), p.stages * p.stage + 128, s, a, p);
 }
 
-template <int KV>
-cudaError_t backward(const NormArgs& a, const Plan& p, unsigned grid, cudaStream_t s) {
-  auto k = a.rms ? (a.add ? norm_backward_kernel<true, true, KV> : norm_backward_kernel<true, false, KV>)
-                 : (a.add ? norm_backward_kernel<false, true, KV> : norm_backward_kernel<false, false, KV>);
+template <bool RMS, bool ADD>
+cudaError_t backward(const NormArgs& a, int sms, unsigned* grid, cudaStream_t s) {
+  const Plan p = plan_of(a.N, a.H, ADD ? 3 : 2, kRingBytes - weight_bytes(a.H), a.H > kWide ? 2 : 1, kMaxThreads);
+  *grid = grid_of(p, sms);
+  auto k = a.H > kWide     ? norm_backward_kernel<RMS, ADD, 2, true>
+           : p.lanes > 32 ? norm_backward_kernel<RMS, ADD, 1, true>
+                          : norm_backward_kernel<RMS, ADD, 1, false>;
   const uint32_t ring = p.stages * p.stage, sums = 8u * (uint32_t)a.H;  // the block's sums take the ring's place
-  return launch_pdl(k, dim3(grid), dim3(p.threads), weight_bytes(a.H) + (ring > sums ? ring : sums) + 128, s, a, p);
+  return launch_pdl(k, dim3(*grid), dim3(p.threads), weight_bytes(a.H) + (ring > sums ? ring : sums) + 128, s, a, p);
 }
 
 }  // namespace
@@ -435,8 +498,8 @@ int launch_norm_forward(const NormArgs& a, cudaStream_t s) {
   cudaError_t e = cudaSuccess;
   const int sms = sm_count(&e);
   if (e != cudaSuccess) return -(int)e;
-  const Plan p = plan_of(a.N, a.H, a.add ? 2 : 1, kRingBytes);
-  e = a.H > kWide ? forward<2>(a, p, grid_of(p, sms), s) : forward<1>(a, p, grid_of(p, sms), s);
+  e = a.rms ? (a.add ? forward<true, true>(a, sms, s) : forward<true, false>(a, sms, s))
+            : (a.add ? forward<false, true>(a, sms, s) : forward<false, false>(a, sms, s));
   return e != cudaSuccess ? -(int)e : 1;
 }
 
@@ -449,11 +512,11 @@ int launch_norm_backward(const NormArgs& a, cudaStream_t s) {
   int sms = sm_count(&e);
   if (e != cudaSuccess) return -(int)e;
   if (sms > kNormMaxParts) sms = kNormMaxParts;
-  const Plan p = plan_of(a.N, a.H, a.add ? 3 : 2, kRingBytes - weight_bytes(a.H));
-  const unsigned grid = grid_of(p, sms);
-  e = a.H > kWide ? backward<2>(a, p, grid, s) : backward<1>(a, p, grid, s);
+  unsigned grid = 0;
+  e = a.rms ? (a.add ? backward<true, true>(a, sms, &grid, s) : backward<true, false>(a, sms, &grid, s))
+            : (a.add ? backward<false, true>(a, sms, &grid, s) : backward<false, false>(a, sms, &grid, s));
   if (e != cudaSuccess) return -(int)e;
-  e = launch_pdl(norm_parts_kernel, dim3((2 * a.H + 31) / 32), dim3(256), 0, s, (const float*)a.part, (int)grid, a.H,
+  e = launch_pdl(norm_parts_kernel, dim3((2 * a.H + 127) / 128), dim3(256), 0, s, (const float*)a.part, (int)grid, a.H,
                  a.dw, a.db);
   return e != cudaSuccess ? -(int)e : 2;
 }
