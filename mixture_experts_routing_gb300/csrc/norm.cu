@@ -95,32 +95,51 @@ struct Plan {
   uint32_t stage;    // bytes: `tensors` x rows x H x 2
 };
 
-// The sum of v (a value, or a pair) over a row's threads, the same in all of them. WIDE: a
-// row takes several warps, which meet in slot, one entry a warp (written again two calls
-// later at the earliest, behind another barrier); else it takes `lanes` lanes of one.
-__device__ __forceinline__ float add(float a, float b) { return a + b; }
-__device__ __forceinline__ F2 add(F2 a, F2 b) { return add2(a, b); }
-__device__ __forceinline__ float from_lane(float v, int o) { return __shfl_xor_sync(0xFFFFFFFFu, v, o); }
-__device__ __forceinline__ F2 from_lane(F2 v, int o) {
-  const float2 f = split(v);
-  return f2(__shfl_xor_sync(0xFFFFFFFFu, f.x, o), __shfl_xor_sync(0xFFFFFFFFu, f.y, o));
-}
-__device__ __forceinline__ void clear(float& v) { v = 0.0f; }
-__device__ __forceinline__ void clear(F2& v) { v = f2(0.0f); }
-template <bool WIDE, typename T>
-__device__ __forceinline__ T row_sum(T v, int lanes, int first_warp, T* slot) {
+// Sums over a row's threads, the same in all of them. WIDE: a row takes several warps, which
+// meet in slot (a value a warp; written again two calls later at the earliest, behind another
+// barrier); else it takes `lanes` lanes of one warp.
+template <bool WIDE>
+__device__ __forceinline__ float row_sum(float v, int lanes, int first_warp, float* slot) {
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1)
-    if (WIDE || o < lanes) v = add(v, from_lane(v, o));
+    if (WIDE || o < lanes) v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
   if (!WIDE) return v;
   const int lane = threadIdx.x & 31;
   if (lane == 0) slot[threadIdx.x >> 5] = v;
   __syncthreads();
-  clear(v);
-  if (lane < (lanes >> 5)) v = slot[first_warp + lane];
+  v = lane < (lanes >> 5) ? slot[first_warp + lane] : 0.0f;
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) v = add(v, from_lane(v, o));
+  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
   return v;
+}
+// The sums of a and of b (shuffles share a pipe with the loads from shared memory, so half a
+// warp takes each of them: ten shuffles instead of twenty).
+template <bool WIDE>
+__device__ __forceinline__ float2 row_sums(float a, float b, int lanes, int first_warp, float (*slot)[kMaxThreads / 32]) {
+  if (!WIDE) {
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1)
+      if (o < lanes) {
+        a += __shfl_xor_sync(0xFFFFFFFFu, a, o);
+        b += __shfl_xor_sync(0xFFFFFFFFu, b, o);
+      }
+    return make_float2(a, b);
+  }
+  const int lane = threadIdx.x & 31;
+  const bool low = lane < 16;
+  float v = (low ? a : b) + __shfl_xor_sync(0xFFFFFFFFu, low ? b : a, 16);
+#pragma unroll
+  for (int o = 8; o > 0; o >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
+  if ((lane & 15) == 0) slot[lane >> 4][threadIdx.x >> 5] = v;
+  __syncthreads();
+  const int warps = lanes >> 5, l = lane & 15;
+  const float* s = slot[lane >> 4] + first_warp;
+  v = l < warps ? s[l] : 0.0f;
+  if (l + 16 < warps) v += s[l + 16];
+#pragma unroll
+  for (int o = 8; o > 0; o >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
+  const float w = __shfl_xor_sync(0xFFFFFFFFu, v, 16);
+  return low ? make_float2(v, w) : make_float2(w, v);
 }
 
 // The block's ring of row groups: TENSORS arrays, each `rows` rows of it, a bulk copy each.
@@ -260,7 +279,7 @@ __global__ void __launch_bounds__(kMaxThreads, 1) norm_backward_kernel(const Nor
   constexpr int kTensors = ADD ? 3 : 2;
   extern __shared__ uint8_t smem[];
   __shared__ __align__(8) uint64_t full[kMaxStages];
-  __shared__ F2 slots[2][kMaxThreads / 32];
+  __shared__ float slots[2][2][kMaxThreads / 32];
   if (threadIdx.x == 0) {
     for (int i = 0; i < p.stages; ++i) mbar_init(smem_u32(&full[i]), 1);
     mbar_fence_init();
@@ -335,7 +354,9 @@ __global__ void __launch_bounds__(kMaxThreads, 1) norm_backward_kernel(const Nor
       }
     }
     const float2 u = split(sgz), t = split(sg);
-    const float2 s = split(row_sum<WIDE>(f2(u.x + u.y, t.x + t.y), p.lanes, first_warp, slots[turn]));
+    float2 s;
+    if (RMS) s = make_float2(row_sum<WIDE>(u.x + u.y, p.lanes, first_warp, slots[turn][0]), 0.0f);
+    else s = row_sums<WIDE>(u.x + u.y, t.x + t.y, p.lanes, first_warp, slots[turn]);
     if (!WIDE) __syncthreads();
     if (loads && ok && step + p.stages * gridDim.x < p.steps) rows.load(step + p.stages * gridDim.x, stage);
     from += p.stage;
@@ -391,29 +412,31 @@ __global__ void __launch_bounds__(kMaxThreads, 1) norm_backward_kernel(const Nor
   }
 }
 
-// dw and db from the blocks' partial sums: 32 groups of 4 columns a block, eight runs of the
-// parts, added in order.
-__global__ void __launch_bounds__(256) norm_parts_kernel(const float* part, int parts, int H, float* dw, float* db) {
-  __shared__ float4 sums[8][32];
+// dw and db from the blocks' partial sums: 8 groups of 4 columns a block, the parts in 32 runs
+// (five parts each, under way at once: with 8 runs of 19 the kernel took 9 us for 2048 columns),
+// added in order.
+constexpr int kRuns = 32, kGroups = 8;
+__global__ void __launch_bounds__(kRuns * kGroups) norm_parts_kernel(const float* part, int parts, int H, float* dw, float* db) {
+  __shared__ float4 sums[kRuns][kGroups];
   griddep_wait();
   griddep_launch_dependents();
-  const int c = (blockIdx.x * 32 + (threadIdx.x & 31)) * 4, q = threadIdx.x >> 5;
+  const int g = threadIdx.x % kGroups, q = threadIdx.x / kGroups, c = (blockIdx.x * kGroups + g) * 4;
   float4 t = make_float4(0.f, 0.f, 0.f, 0.f);
   const bool wanted = c < (db ? 2 * H : H);
   if (wanted) {
-    const int p0 = q * parts / 8, p1 = (q + 1) * parts / 8;
+    const int p0 = q * parts / kRuns, p1 = (q + 1) * parts / kRuns;
 #pragma unroll 8
     for (int p = p0; p < p1; ++p) {
       const float4 v = *reinterpret_cast<const float4*>(part + (int64_t)p * 2 * H + c);
       t = make_float4(t.x + v.x, t.y + v.y, t.z + v.z, t.w + v.w);
     }
   }
-  sums[q][threadIdx.x & 31] = t;
+  sums[q][g] = t;
   __syncthreads();
   if (q || !wanted) return;
 #pragma unroll
-  for (int i = 1; i < 8; ++i) {
-    const float4 v = sums[i][threadIdx.x];
+  for (int i = 1; i < kRuns; ++i) {
+    const float4 v = sums[i][g];
     t = make_float4(t.x + v.x, t.y + v.y, t.z + v.z, t.w + v.w);
   }
   *reinterpret_cast<float4*>(c < H ? dw + c : db + (c - H)) = t;
@@ -516,7 +539,8 @@ int launch_norm_backward(const NormArgs& a, cudaStream_t s) {
   e = a.rms ? (a.add ? backward<true, true>(a, sms, &grid, s) : backward<true, false>(a, sms, &grid, s))
             : (a.add ? backward<false, true>(a, sms, &grid, s) : backward<false, false>(a, sms, &grid, s));
   if (e != cudaSuccess) return -(int)e;
-  e = launch_pdl(norm_parts_kernel, dim3((2 * a.H + 127) / 128), dim3(256), 0, s, (const float*)a.part, (int)grid, a.H,
+  e = launch_pdl(norm_parts_kernel, dim3((2 * a.H + 4 * kGroups - 1) / (4 * kGroups)), dim3(kRuns * kGroups), 0, s,
+                 (const float*)a.part, (int)grid, a.H,
                  a.dw, a.db);
   return e != cudaSuccess ? -(int)e : 2;
 }
