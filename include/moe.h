@@ -573,7 +573,7 @@ typedef struct moe_few_config {
 int64_t moe_few_workspace_bytes(const moe_few_config_t* cfg);
 
 /* y[t] = add[t] + sum_k p'[t,k] W2[e] (act(W_gate[e] x_t) * (W_up[e] x_t)), e the
- * K experts of the largest probabilities (ties to the lower id), p' as in
+ * K experts of the largest logits (equal ones: the lower id), p' as in
  * moe_route_align.
  *  x        [N,H] bf16
  *  w_router [H,E] f32; bias [E] f32 or NULL. A logit of -inf (a bias of -inf) shuts

@@ -151,8 +151,9 @@ __global__ void __cluster_dims__(kLogitSplit, 1, 1) __launch_bounds__(kLogitThre
 static_assert(kLogitTok <= kLogitSplit, "one token of the chunk per block of the cluster");
 
 // ---------------------------------------------------------------- experts
-constexpr int kMmaWarps = 4, kEpiWarps = 4;
-constexpr int kFewThreads = (kMmaWarps + 2 + kEpiWarps) * 32;
+constexpr int kMmaWarps = 4, kEpiWarps = 4, kFinishWarps = 2;
+constexpr int kFewThreads = (kMmaWarps + 2 + kEpiWarps + kFinishWarps) * 32;
+constexpr int kPosts = 8;        // column tiles posted to the finishing warps
 constexpr int kRows = 16;        // weight rows of a tile
 // Columns of a copy. A copy holds a tile's 16 rows as [64 columns][row], each row of 64
 // columns swizzled over its 128 bytes. Copies of 4 KB (8 rows x 256 columns) kept the copying
@@ -168,6 +169,8 @@ struct FewShared {
   uint64_t wfull[kMaxStages], afull[kMaxStages], empty[kMaxStages], named[kMaxStages], rfull[kEpiWarps], rempty[kEpiWarps];
   int tile[kMaxStages];            // of the stage, -1: no more
   int red_tile[kEpiWarps];
+  uint64_t pfull[kPosts], pempty[kPosts];
+  int post_row[kPosts], post_first[kPosts], posts;
   int ids[kFewMaxTokens * kMaxTopK];
   float p[kFewMaxTokens * kMaxTopK];
   uint16_t list[kFewMaxTokens * kMaxTopK];  // routes by expert, tokens ascending
@@ -180,83 +183,64 @@ struct FewShared {
   uint32_t by_per, by_run;         // 2^32 / (FC1 tiles of a unit) and / (16 units), rounded up
 };
 
-// The K experts of two tokens by a warp (as route_align picks them, ties to the lower id);
-// their steps fill each other's waits. The picks go by exp(l - max), the probabilities
-// before they are divided by their sum, which is needed for K of them at most, and not at
-// all where these are divided by their own sum. Lane l holds experts l, l+32, ..., PER of
-// them. n: the live tokens.
+// The K experts of a token by a warp. The picks go by the logits (ties to the lower id):
+// probabilities are needed of the K picked alone, and their sum over all experts only where
+// it is not divided out again. Lane l holds experts l, l+32, ..., PER of them. One token at a
+// time: two in turns filled each other's waits, but the larger code came from memory at
+// every launch (1 token, 7168 x 2048: 115.0 us with both forms, 113.7 with this one).
 template <int PER>
-__device__ __forceinline__ void pick(const FewArgs& a, const float* logits, int t0, int n, FewShared& s, bool out) {
+__device__ __forceinline__ void pick(const FewArgs& a, const float* logits, int t, FewShared& s, bool out) {
   const int lane = threadIdx.x & 31;
-  float v[2][PER], top[2], sum[2] = {}, d[2] = {}, my_v[2] = {};
-  uint32_t key[2][PER];  // v's bits order like v >= 0; a NaN is above all; taken or absent: 0, below v + 1
-  int my_id[2] = {};
+  uint32_t key[PER], first[PER];  // orders like the logit, a NaN above all; 0: taken or absent
 #pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    const int t = min(t0 + i, n - 1);
-#pragma unroll
-    for (int j = 0; j < PER; ++j) {
-      const int e = lane + 32 * j;
-      v[i][j] = e < a.E ? __ldcg(logits + (size_t)t * a.E + e) : -INFINITY;
-    }
+  for (int j = 0; j < PER; ++j) {
+    const int e = lane + 32 * j;
+    key[j] = e < a.E ? __float_as_uint(__ldcg(logits + (size_t)t * a.E + e)) : 0u;
   }
 #pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    top[i] = v[i][0];
-#pragma unroll
-    for (int j = 1; j < PER; ++j) top[i] = fmaxf(top[i], v[i][j]);
+  for (int j = 0; j < PER; ++j) {
+    const float l = __uint_as_float(key[j]);
+    const uint32_t b = __float_as_uint(l + 0.0f);  // -0 and 0 are equal
+    key[j] = lane + 32 * j >= a.E ? 0u : isnan(l) ? 0xFFFFFFFFu : (b & 0x80000000u) ? ~b : b | 0x80000000u;
+    first[j] = key[j];
   }
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1)
-#pragma unroll
-    for (int i = 0; i < 2; ++i) top[i] = fmaxf(top[i], __shfl_xor_sync(0xFFFFFFFFu, top[i], o));
-#pragma unroll
-  for (int i = 0; i < 2; ++i)
-#pragma unroll
-    for (int j = 0; j < PER; ++j) {
-      const bool in = lane + 32 * j < a.E;
-      v[i][j] = in ? route_exp(__fsub_rn(v[i][j], top[i])) : 0.0f;
-      sum[i] += v[i][j];
-      key[i][j] = in ? (__float_as_uint(v[i][j]) & 0x7FFFFFFFu) + 1u : 0u;
-    }
-  if (!a.renorm) {
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1)
-#pragma unroll
-      for (int i = 0; i < 2; ++i) sum[i] += __shfl_xor_sync(0xFFFFFFFFu, sum[i], o);
-  }
+  auto value = [](uint32_t k) { return __uint_as_float(k == 0xFFFFFFFFu ? 0x7FC00000u : (k & 0x80000000u) ? k & 0x7FFFFFFFu : ~k); };
+  float top = 0.0f, my_l = 0.0f;
+  int my_id = 0;
   for (int k = 0; k < a.K; ++k) {
+    uint32_t best = key[0];
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      uint32_t best = key[i][0];
+    for (int j = 1; j < PER; ++j) best = max(best, key[j]);
+    best = __reduce_max_sync(0xFFFFFFFFu, best);
+    uint32_t mine = 0xFFFFFFFFu;
 #pragma unroll
-      for (int j = 1; j < PER; ++j) best = max(best, key[i][j]);
-      best = __reduce_max_sync(0xFFFFFFFFu, best);
-      uint32_t mine = 0xFFFFFFFFu;
+    for (int j = PER - 1; j >= 0; --j)
+      if (key[j] == best) mine = lane + 32 * j;
+    const uint32_t e = __reduce_min_sync(0xFFFFFFFFu, mine);
 #pragma unroll
-      for (int j = PER - 1; j >= 0; --j)
-        if (key[i][j] == best) mine = lane + 32 * j;
-      const uint32_t e = __reduce_min_sync(0xFFFFFFFFu, mine);
+    for (int j = 0; j < PER; ++j)
+      if (e == (uint32_t)(lane + 32 * j)) key[j] = 0;
+    if (k == 0) top = value(best);
+    if (lane == k) { my_id = (int)e; my_l = value(best); }
+  }
+  my_l = lane < a.K ? route_exp(__fsub_rn(my_l, top)) : 0.0f;
+  float all = my_l;
+  if (!a.renorm) {
+    all = 0.0f;
 #pragma unroll
-      for (int j = 0; j < PER; ++j)
-        if (e == (uint32_t)(lane + 32 * j)) key[i][j] = 0;
-      const float p = __uint_as_float(best - 1u);
-      d[i] += p;
-      if (lane == k) { my_id[i] = (int)e; my_v[i] = p; }
-    }
+    for (int j = 0; j < PER; ++j)
+      if (lane + 32 * j < a.E) all += route_exp(__fsub_rn(value(first[j]), top));
   }
 #pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    const int t = t0 + i;
-    if (lane < a.K && t < n) {
-      const float p = __fdiv_rn(my_v[i], a.renorm ? d[i] : sum[i]);
-      const int at = t * a.K + lane;
-      s.ids[at] = my_id[i];
-      s.p[at] = p;
-      if (p != 0.0f) atomicOr(&s.mask[my_id[i]][t >> 5], 1u << (t & 31));  // p = 0 is not read; a NaN is not 0
-      if (out && a.topk_ids) a.topk_ids[at] = my_id[i];
-      if (out && a.topk_p) a.topk_p[at] = p;
-    }
+  for (int o = 16; o > 0; o >>= 1) all += __shfl_xor_sync(0xFFFFFFFFu, all, o);
+  if (lane < a.K) {
+    const float p = __fdiv_rn(my_l, all);
+    const int at = t * a.K + lane;
+    s.ids[at] = my_id;
+    s.p[at] = p;
+    if (p != 0.0f) atomicOr(&s.mask[my_id][t >> 5], 1u << (t & 31));  // p = 0 is not read; a NaN is not 0
+    if (out && a.topk_ids) a.topk_ids[at] = my_id;
+    if (out && a.topk_p) a.topk_p[at] = p;
   }
 }
 
@@ -473,21 +457,32 @@ __device__ __forceinline__ void activations_role(const FewArgs& a, FewShared& s,
       k = 0;
       t = tile_of(a, s, tile);
       if (t.fc2 && !s.unit_done[t.unit]) {
-        // h is complete when all tiles of its features have said so
+        // h is complete when all tiles of its features have said so. An answer takes a
+        // microsecond under load, so all units are asked at once.
         const int want = a.I / 8;
         const uint64_t t0 = globaltimer_ns();
         bool ok = true;
-        for (uint32_t i = 1; ld_relaxed(count + 1 + t.unit) < want; ++i) {
-          if ((i & 255u) == 0u && globaltimer_ns() - t0 > 2000000000ull) {
-            atomicOr(a.err, kErrWaitUnit);
+        for (uint32_t i = 1;; ++i) {
+          bool have = false;
+          for (int u0 = lane; u0 < s.units; u0 += 128) {
+            int v[4];
+#pragma unroll
+            for (int q = 0; q < 4; ++q) v[q] = ld_relaxed(count + 1 + min(u0 + 32 * q, kMaxUnits - 1));
+#pragma unroll
+            for (int q = 0; q < 4; ++q)
+              if (u0 + 32 * q < s.units && v[q] >= want) {
+                s.unit_done[u0 + 32 * q] = 1;
+                have |= u0 + 32 * q == t.unit;
+              }
+          }
+          if (__any_sync(0xFFFFFFFFu, have)) break;
+          if ((i & 255u) == 0u && __any_sync(0xFFFFFFFFu, globaltimer_ns() - t0 > 2000000000ull)) {
+            if (lane == 0) atomicOr(a.err, kErrWaitUnit);
             ok = false;
             break;
           }
         }
-        if (!__all_sync(0xFFFFFFFFu, ok)) break;
-        // the answer took a microsecond under load: the other units are asked together
-        for (int u = lane; u < s.units; u += 32)
-          if (ld_relaxed(count + 1 + u) >= want) s.unit_done[u] = 1;
+        if (!ok) break;
         __threadfence();
         __syncwarp();
       }
@@ -600,31 +595,36 @@ __device__ __forceinline__ void products_role(const FewArgs& a, FewShared& s, ui
   }
 }
 
-// A warp takes every fourth tile, from a buffer of its own: making a tile's values visible
-// to the other blocks costs it about a microsecond, which three other tiles hide.
-template <int ACT, int G>
-__device__ __forceinline__ void outputs_role(const FewArgs& a, FewShared& s, int n, int32_t* count, uint16_t* h, float* o,
-                                             const float* red) {
-  using R = Ring<G>;
-  const int w = (threadIdx.x >> 5) - kMmaWarps - 2, lane = threadIdx.x & 31;
-  int32_t* col_count = count + 1 + kMaxUnits;
-  const float* r = red + w * (R::kRed / 4);
-  // An FC2 tile's products are counted when the warp gets its next tile: by then they have
-  // reached memory and the fence finds little to wait for; the count is read after that tile.
-  int last_row = -1, counted = -1, arrived = 0;
-  auto count_last = [&]() {
-    counted = last_row;
-    if (last_row >= 0 && lane == 0) {
-      __threadfence();
-      arrived = atomicAdd(col_count + last_row / kRows, 1);
-    }
-  };
-  auto finish_counted = [&]() {  // the outputs of the columns whose last products were counted
-    if (counted < 0 || __shfl_sync(0xFFFFFFFFu, arrived, 0) != s.units - 1) return;
-    __threadfence();
-    const int c = counted + 4 * (lane & 3);
-    constexpr int kTwo = 2;  // tokens of a lane under way at once
-    for (int t0 = lane >> 2; t0 < n; t0 += 8 * kTwo) {
+// Column tiles whose products are all in o, from the warps of the outputs to the finishing
+// ones. A post is 16 columns and every `parts`-th group of 16 tokens; post i goes to
+// finishing warp i % kFinishWarps. By one thread.
+__device__ __forceinline__ void post(const FewArgs& a, FewShared& s, int row, int parts) {
+  const int first = atomicAdd(&s.posts, parts);
+  for (int i = 0; i < parts; ++i) {
+    const uint32_t at = (uint32_t)(first + i), slot = at % kPosts, turn = at / kPosts;
+    if (turn > 0 && !mbar_wait(smem_u32(&s.pempty[slot]), (turn - 1) & 1u, a.err, kErrWaitAccum)) return;
+    s.post_row[slot] = row;
+    s.post_first[slot] = i | (parts << 16);
+    mbar_arrive(smem_u32(&s.pfull[slot]));
+  }
+}
+
+// y of the posted columns: four lanes a token, two tokens a lane under way at once. Warps of
+// their own: the reads of a tile's routes take microseconds, and while a warp of the outputs
+// spent them its buffer stood still (33 tokens of 2048 x 768: 199 us with two tokens under
+// way there, 212 with one).
+__device__ __forceinline__ void finish_role(const FewArgs& a, FewShared& s, int n, const float* o) {
+  const int lane = threadIdx.x & 31;
+  for (uint32_t at = (threadIdx.x >> 5) - (kMmaWarps + 2 + kEpiWarps);; at += kFinishWarps) {
+    const uint32_t slot = at % kPosts;
+    if (!mbar_wait_warp(smem_u32(&s.pfull[slot]), (at / kPosts) & 1u, a.err, kErrWaitAccum)) break;
+    const int row = s.post_row[slot], part = s.post_first[slot] & 0xFFFF, parts = s.post_first[slot] >> 16;
+    __syncwarp();
+    if (lane == 0) mbar_arrive(smem_u32(&s.pempty[slot]));
+    if (row < 0) break;
+    const int c = row + 4 * (lane & 3);
+    constexpr int kTwo = 2;
+    for (int t0 = 16 * part + (lane >> 2); t0 < n; t0 += 16 * parts) {
       float4 y[kTwo] = {};
       for (int k0 = 0; k0 < a.K; k0 += 8) {
         float4 v[kTwo][8];
@@ -653,26 +653,58 @@ __device__ __forceinline__ void outputs_role(const FewArgs& a, FewShared& s, int
 #pragma unroll
       for (int i = 0; i < kTwo; ++i) {
         if (t0 + 8 * i >= n) break;
-        const size_t at = (size_t)(t0 + 8 * i) * a.H + c;
+        const size_t to = (size_t)(t0 + 8 * i) * a.H + c;
         if (a.add) {
-          const uint2 q = *reinterpret_cast<const uint2*>(a.add + at);
+          const uint2 q = *reinterpret_cast<const uint2*>(a.add + to);
           y[i].x += __uint_as_float(q.x << 16);
           y[i].y += __uint_as_float(q.x & 0xFFFF0000u);
           y[i].z += __uint_as_float(q.y << 16);
           y[i].w += __uint_as_float(q.y & 0xFFFF0000u);
         }
         const __nv_bfloat162 lo = __floats2bfloat162_rn(y[i].x, y[i].y), hi = __floats2bfloat162_rn(y[i].z, y[i].w);
-        *reinterpret_cast<uint2*>(a.y + at) =
+        *reinterpret_cast<uint2*>(a.y + to) =
             make_uint2(*reinterpret_cast<const uint32_t*>(&lo), *reinterpret_cast<const uint32_t*>(&hi));
       }
     }
+  }
+}
+
+// A warp takes every fourth tile, from a buffer of its own: making a tile's values visible
+// to the other blocks costs it about a microsecond, which three other tiles hide.
+template <int ACT, int G>
+__device__ __forceinline__ void outputs_role(const FewArgs& a, FewShared& s, int32_t* count, uint16_t* h, float* o,
+                                             const float* red) {
+  using R = Ring<G>;
+  const int w = (threadIdx.x >> 5) - kMmaWarps - 2, lane = threadIdx.x & 31;
+  int32_t* col_count = count + 1 + kMaxUnits;
+  const float* r = red + w * (R::kRed / 4);
+  // An FC2 tile's products are counted when the warp gets its next tile: by then they have
+  // reached memory and the fence finds little to wait for; the count is read after that tile.
+  int last_row = -1, counted = -1, arrived = 0;
+  auto count_last = [&]() {
+    counted = last_row;
+    if (last_row >= 0 && lane == 0) {
+      __threadfence();
+      arrived = atomicAdd(col_count + last_row / kRows, 1);
+    }
   };
+  auto complete = [&]() { return counted >= 0 && __shfl_sync(0xFFFFFFFFu, arrived, 0) == s.units - 1; };
   for (uint32_t par = 0;; par ^= 1u) {
-    if (!mbar_wait_warp(smem_u32(&s.rfull[w]), par, a.err, kErrWaitAccum)) break;
-    const int tile = s.red_tile[w];
+    // also after a wait that ran out, every warp comes to the barrier
+    const bool ok = mbar_wait_warp(smem_u32(&s.rfull[w]), par, a.err, kErrWaitAccum);
+    const int tile = ok ? s.red_tile[w] : -1;
     if (tile < 0) {
-      count_last();
-      finish_counted();
+      // the last columns are what the launch ends with: all finishing warps share their tokens
+      if (ok) {
+        count_last();
+        if (complete() && lane == 0) {
+          __threadfence();
+          post(a, s, counted, kFinishWarps);
+        }
+      }
+      __syncwarp();
+      asm volatile("bar.sync 1, %0;" ::"n"(kEpiWarps * 32) : "memory");
+      if (w == 0 && lane == 0) post(a, s, -1, kFinishWarps);
       break;
     }
     const TileOf t = tile_of(a, s, tile);
@@ -705,7 +737,10 @@ __device__ __forceinline__ void outputs_role(const FewArgs& a, FewShared& s, int
       }
       __syncwarp();
       if (lane == 0) mbar_arrive(smem_u32(&s.rempty[w]));
-      finish_counted();
+      if (complete() && lane == 0) {
+        __threadfence();
+        post(a, s, counted, 1);
+      }
       last_row = t.row;
     }
     __syncwarp();
@@ -713,7 +748,7 @@ __device__ __forceinline__ void outputs_role(const FewArgs& a, FewShared& s, int
 }
 
 template <int ACT, int G>
-__device__ __forceinline__ void roles(const CUtensorMap& tm1, const CUtensorMap& tm2, const FewArgs& a, FewShared& s, int n,
+__device__ __forceinline__ void roles(const CUtensorMap& tm1, const CUtensorMap& tm2, const FewArgs& a, FewShared& s,
                                       int32_t* count, int (&drawn)[kDrawn], uint16_t* h, float* o, uint8_t* smem) {
   const uint32_t ring = (smem_u32(smem) + 1023u) & ~1023u, red = ring + Ring<G>::kStages * Ring<G>::kStage;
   const int warp = threadIdx.x >> 5;
@@ -723,8 +758,8 @@ __device__ __forceinline__ void roles(const CUtensorMap& tm1, const CUtensorMap&
     activations_role<G>(a, s, count, h, ring);
   else if (warp < kMmaWarps)
     products_role<G>(a, s, ring, red);
-  else
-    outputs_role<ACT, G>(a, s, n, count, h, o, reinterpret_cast<const float*>(smem + (red - smem_u32(smem))));
+  else if (warp < kMmaWarps + 2 + kEpiWarps)
+    outputs_role<ACT, G>(a, s, count, h, o, reinterpret_cast<const float*>(smem + (red - smem_u32(smem))));
 }
 
 template <int ACT>
@@ -745,6 +780,11 @@ __global__ void __launch_bounds__(kFewThreads, 1)
       mbar_init(smem_u32(&s.rfull[i]), kMmaWarps);
       mbar_init(smem_u32(&s.rempty[i]), 1);
     }
+    for (int i = 0; i < kPosts; ++i) {
+      mbar_init(smem_u32(&s.pfull[i]), 1);
+      mbar_init(smem_u32(&s.pempty[i]), 1);
+    }
+    s.posts = 0;
     mbar_fence_init();
     tma_prefetch_desc(&tm1);
     tma_prefetch_desc(&tm2);
@@ -759,21 +799,23 @@ __global__ void __launch_bounds__(kFewThreads, 1)
   }
   const int n = live_tokens(a.n_dev, a.N);
   __syncthreads();
-  for (int t = 2 * warp; t < n; t += 2 * (kFewThreads / 32)) {
-    if (a.E <= 32) pick<1>(a, logits, t, n, s, blockIdx.x == 0);
-    else if (a.E <= 64) pick<2>(a, logits, t, n, s, blockIdx.x == 0);
-    else if (a.E <= 128) pick<4>(a, logits, t, n, s, blockIdx.x == 0);
-    else pick<8>(a, logits, t, n, s, blockIdx.x == 0);
+  for (int t = warp; t < n; t += kFewThreads / 32) {
+    if (a.E <= 32) pick<1>(a, logits, t, s, blockIdx.x == 0);
+    else if (a.E <= 64) pick<2>(a, logits, t, s, blockIdx.x == 0);
+    else if (a.E <= 128) pick<4>(a, logits, t, s, blockIdx.x == 0);
+    else pick<8>(a, logits, t, s, blockIdx.x == 0);
   }
   __syncthreads();
   build_units(a, n, s);
   if (s.units == 0) return;
-  if (s.most <= 8)
-    roles<ACT, 1>(tm1, tm2, a, s, n, count, drawn, h, o, smem);
+  if (warp >= kMmaWarps + 2 + kEpiWarps)
+    finish_role(a, s, n, o);
+  else if (s.most <= 8)
+    roles<ACT, 1>(tm1, tm2, a, s, count, drawn, h, o, smem);
   else if (s.most <= 16)
-    roles<ACT, 2>(tm1, tm2, a, s, n, count, drawn, h, o, smem);
+    roles<ACT, 2>(tm1, tm2, a, s, count, drawn, h, o, smem);
   else
-    roles<ACT, 4>(tm1, tm2, a, s, n, count, drawn, h, o, smem);
+    roles<ACT, 4>(tm1, tm2, a, s, count, drawn, h, o, smem);
 }
 
 }  // namespace
