@@ -1,12 +1,14 @@
 """A Mixture-of-Experts layer with a shared expert: one training step, then decode
 steps with the routed experts in 4 bits.
 
-    python examples/moe_layer.py [--tokens 1024] [--decode 4] [--activation swiglu]
+    python examples/moe_layer.py [--tokens 1024] [--decode 4] [--activation swiglu] [--block]
 
 Training: routed experts and shared expert forward, the shared expert's activations
 kept in 8 bits, and both backwards; the layer's output and input gradient are built
 up in place (`add=y`, `dx_add=dx`). Decode: router, 4-bit experts, shared expert on
-a few tokens. Sizes are those of the small Qwen3-style layer of the benchmarks.
+a few tokens. --block puts the layer between two norms with residual sums, updates its
+weights with AdamW (states in 8 bits) and decodes in bf16 with the updated weights.
+Sizes are those of the small Qwen3-style layer of the benchmarks.
 """
 from __future__ import annotations
 
@@ -43,8 +45,12 @@ class Layer:
 
     def train_step(self):
         """y, dx and every weight gradient of x and dy."""
+        y = self.forward()
+        return (y, *self.backward())
+
+    def forward(self):
+        """y of x; what the backward needs is kept."""
         c, s, dev = self.cfg, self.shared, self.device
-        f32 = dict(dtype=torch.float32, device=dev)
         routes, ws = moe.alloc_routes(c, dev), moe.alloc_workspace(c, dev)
         h, o, y = moe.alloc_buffers(c, dev)
         preact = torch.empty((h.shape[0], 2 * c.inter), dtype=torch.bfloat16, device=dev)
@@ -54,7 +60,14 @@ class Layer:
         moe.ffn_forward_train(c, routes, self.x, self.w13, self.w2, h, o, preact)
         moe.combine(c, routes, o, y)
         moe.shared_forward_train(s, self.x, self.sw13, self.sw2, sh, y, ck, ck_sf, add=y)
+        self.kept = routes, ws, preact, ck, ck_sf
+        return y
 
+    def backward(self):
+        """dx and every weight gradient of dy."""
+        c, s, dev = self.cfg, self.shared, self.device
+        f32 = dict(dtype=torch.float32, device=dev)
+        routes, ws, preact, ck, ck_sf = self.kept
         dx = torch.empty_like(self.x)
         grads = {"w13": torch.empty(self.w13.shape, **f32), "w2": torch.empty(self.w2.shape, **f32),
                  "router": torch.empty(self.w_router.shape, **f32),
@@ -68,7 +81,7 @@ class Layer:
         moe.shared_backward(s, self.x, self.sw13, self.sw2, ck, ck_sf, self.dy, dx,
                             grads["shared_w13"], grads["shared_w2"],
                             moe.alloc_shared_backward_workspace(s, dev), dx_add=dx)
-        return y, dx, grads
+        return dx, grads
 
     def pack_for_decode(self, group=128):
         """The routed experts in 4 bits, once."""
@@ -90,13 +103,92 @@ class Layer:
         return y
 
 
+class Block(Layer):
+    """The layer in a pre-norm block: s = x + r, a = norm(s), y = layer(a), t = s + y,
+    z = norm(t); RMS norms, as such layers have them. Every weight is trained."""
+
+    def __init__(self, n=1024, lr=1e-2, **kw):
+        super().__init__(n, **kw)
+        h = self.cfg.hidden
+        g = torch.Generator(device=self.device)
+        g.manual_seed(kw.get("seed", 0) + 1)
+        self.tokens = self.x
+        self.residual, self.dz = (torch.randn((n, h), device=self.device, generator=g).bfloat16() for _ in range(2))
+        self.norm_w = [1 + 0.1 * torch.randn(h, device=self.device, generator=g) for _ in range(2)]
+        self.weights = {"router": self.w_router, "w13": self.w13, "w2": self.w2, "shared_w13": self.sw13, "shared_w2": self.sw2,
+                        "norm0": self.norm_w[0], "norm1": self.norm_w[1]}
+        self.grads = {k: torch.empty(w.shape, dtype=torch.float32, device=self.device) for k, w in self.weights.items()}
+        self.opt = moe.AdamW(list(self.weights.values()), list(self.grads.values()), lr=lr, betas=(0.9, 0.95), state_bits=8,
+                             weight_decay=[0.0 if k.startswith("norm") else 0.1 for k in self.weights])
+
+    def norm(self, i, x, add):
+        """The residual sum, its norm, and 1 / rms of its rows."""
+        cfg = moe.NormConfig(x.shape[0], x.shape[1], kind=moe.NORM_RMS)
+        s, y, rstd = torch.empty_like(x), torch.empty_like(x), torch.empty(x.shape[0], device=x.device)
+        moe.norm_forward(cfg, x, self.norm_w[i], y, add=add, sum=s, rstd=rstd)
+        return s, y, rstd
+
+    def norm_grad(self, i, s, rstd, dy, dx_add=None):
+        cfg = moe.NormConfig(s.shape[0], s.shape[1], kind=moe.NORM_RMS)
+        dx = torch.empty_like(s)
+        moe.norm_backward(cfg, s, self.norm_w[i], None, rstd, dy, dx, self.grads["norm%d" % i],
+                          moe.alloc_norm_backward_workspace(cfg, self.device), dx_add=dx_add)
+        return dx
+
+    def block_step(self):
+        """Forward, gradients of x (and of r alike) and of every weight, update."""
+        s, a, rstd0 = self.norm(0, self.tokens, self.residual)
+        self.x = a
+        y = self.forward()
+        t, z, rstd1 = self.norm(1, s, y)
+        self.dy = self.norm_grad(1, t, rstd1, self.dz)  # the gradient of t, hence of y and of s
+        da, grads = self.backward()
+        for k, g in grads.items():
+            self.grads[k].copy_(g)
+        dx = self.norm_grad(0, s, rstd0, da, dx_add=self.dy)
+        self.opt.step()
+        return z, dx
+
+    def block_decode(self, x, residual):
+        """z for a few tokens, with the routed experts' layer in one call."""
+        n, c, dev = x.shape[0], self.cfg, self.device
+        few = moe.FewConfig(n, c.hidden, c.n_experts, c.top_k, c.inter, activation=c.activation)
+        shared = moe.SharedConfig(n, c.hidden, self.shared.inter, activation=c.activation)
+        h, y = moe.alloc_shared_buffers(shared, dev)
+        s, a, _ = self.norm(0, x, residual)
+        moe.shared_forward(shared, a, self.sw13, self.sw2, h, y)
+        moe.few_forward(few, a, self.w_router, None, self.w13, self.w2, y, moe.alloc_few_workspace(few, dev), add=y)
+        return self.norm(1, s, y)[1]
+
+
+def main_block(a, activation):
+    block = Block(a.tokens, activation=activation)
+    before = {k: w.clone() for k, w in block.weights.items()}
+    z, dx = block.block_step()
+    print("block: z rms %.3f, dx rms %.3f, weights moved by %s" % (
+        z.float().square().mean().sqrt(), dx.float().square().mean().sqrt(),
+        ", ".join("%s %.2g" % (k, (w.float() - before[k].float()).abs().mean()) for k, w in block.weights.items())))
+    n = min(a.decode, 64)
+    d = block.block_decode(block.tokens[:n].contiguous(), block.residual[:n].contiguous())
+    print("block decode: %d tokens with the updated weights, rms %.3f" % (n, d.float().square().mean().sqrt()))
+    torch.cuda.synchronize()
+    err = moe.device_error()
+    if err:
+        raise RuntimeError("device error word %d" % err)
+    return block, before, z, dx, d
+
+
 def main(argv=None):
     ap = argparse.ArgumentParser(description=__doc__.splitlines()[0])
     ap.add_argument("--tokens", type=int, default=1024)
     ap.add_argument("--decode", type=int, default=4, help="tokens of a decode step")
     ap.add_argument("--activation", choices=("swiglu", "geglu"), default="swiglu")
+    ap.add_argument("--block", action="store_true", help="the layer between norms: a training step with its update, decode in bf16")
     a = ap.parse_args(argv)
-    layer = Layer(a.tokens, activation=moe.ACT_GEGLU if a.activation == "geglu" else moe.ACT_SWIGLU)
+    activation = moe.ACT_GEGLU if a.activation == "geglu" else moe.ACT_SWIGLU
+    if a.block:
+        return main_block(a, activation)
+    layer = Layer(a.tokens, activation=activation)
     y, dx, grads = layer.train_step()
     print("train: y rms %.3f, dx rms %.3f, gradients %s" % (
         y.float().square().mean().sqrt(), dx.float().square().mean().sqrt(),

@@ -628,7 +628,9 @@ typedef struct moe_norm_config {
  *  mean   [N] f32 output (LAYER only), rstd [N] f32 output r: for the backward, or
  *         NULL each
  * All 16-byte aligned but mean and rstd. The row stays in registers: mean and var
- * are two sums over it in fp32, var from the differences to the mean. */
+ * are two sums over it in fp32, var from the differences to the mean. A row with an
+ * infinity or a NaN is NaN in y; one whose squares pass fp32's range (values over
+ * 1e17 or so) has rstd 0. */
 int moe_norm_forward(const moe_norm_config_t* cfg, const void* x, const void* add,
                      const float* weight, const float* bias, void* sum, void* y, float* mean,
                      float* rstd, cudaStream_t stream);
@@ -704,7 +706,7 @@ typedef struct moe_adamw_config {
  *  steps      DEVICE i32[2], 4-byte aligned: steps[0] = t-1, the steps taken so far,
  *             advanced by the call; steps[1] is the call's, 0 between calls. Both 0
  *             at first. Calls that share it must not overlap
- * param, master, grad, m, v 16-byte aligned. Tensors must not overlap. */
+ * param, master, grad, m, v 16-byte aligned. Tensors must not overlap. Deterministic. */
 int moe_adamw_step(const moe_adamw_config_t* cfg, const moe_adamw_tensor_t* tensors,
                    int n_tensors, const float* lr_dev, const float* grad_scale, int32_t* steps,
                    cudaStream_t stream);

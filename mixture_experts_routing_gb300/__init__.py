@@ -786,10 +786,23 @@ def _refuse_on(fn: str, dev: int, stream, **named) -> None:
         raise ValueError("%s: the stream is of device %d, the tensors on %d" % (fn, stream.device.index, dev))
 
 
+_device = None  # () -> the current device, without the checks of torch.cuda.current_device
+
+
 def _here(dev: int, stream) -> bool:
     """The device is the current one, and the stream (if any) is one of its own."""
-    import torch
-    return dev >= 0 and dev == torch.cuda.current_device() and (stream is None or stream.device.index == dev)
+    global _device
+    if _device is None:
+        import torch
+        _device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
+    return dev >= 0 and dev == _device() and (stream is None or stream.device.index == dev)
+
+
+def _stream_on(dev: int, stream) -> int:
+    """_stream, where the current device is known to be dev."""
+    if stream is not None:
+        return stream.cuda_stream
+    return _current[0](dev) if _current else _stream(None)
 
 
 def few_workspace_bytes(cfg: FewConfig) -> int:
@@ -821,7 +834,7 @@ def few_forward(cfg: FewConfig, x, w_router, bias, w13, w2, y, workspace, add=No
         _refuse_on("few_forward", dev, stream, **{k: v for k, v in named.items() if v[0] is not None})
     rc = lib().moe_few_forward(ctypes.byref(cfg), x.data_ptr(), w_router.data_ptr(), _ptr(bias), w13.data_ptr(),
                                w2.data_ptr(), _ptr(add), _ptr(n_valid), y.data_ptr(), _ptr(topk_ids), _ptr(topk_p),
-                               workspace.data_ptr(), workspace.nbytes, _stream(stream))
+                               workspace.data_ptr(), workspace.nbytes, _stream_on(dev, stream))
     if rc:
         raise MoEError("moe_few_forward", rc)
 
@@ -842,7 +855,7 @@ def norm_forward(cfg: NormConfig, x, weight, y, bias=None, add=None, sum=None, m
                      sum=(sum, bf, N, H), mean=(mean, f32, N), rstd=(rstd, f32, N))
         _refuse_on("norm_forward", dev, stream, **{k: v for k, v in named.items() if v[0] is not None})
     rc = lib().moe_norm_forward(ctypes.byref(cfg), x.data_ptr(), _ptr(add), weight.data_ptr(), _ptr(bias), _ptr(sum),
-                                y.data_ptr(), _ptr(mean), _ptr(rstd), _stream(stream))
+                                y.data_ptr(), _ptr(mean), _ptr(rstd), _stream_on(dev, stream))
     if rc:
         raise MoEError("moe_norm_forward", rc)
 
@@ -874,7 +887,7 @@ def norm_backward(cfg: NormConfig, x, weight, mean, rstd, dy, dx, dweight, works
         _refuse_on("norm_backward", dev, stream, **{k: v for k, v in named.items() if v[0] is not None})
     rc = lib().moe_norm_backward(ctypes.byref(cfg), x.data_ptr(), weight.data_ptr(), _ptr(mean), rstd.data_ptr(),
                                  dy.data_ptr(), _ptr(dx_add), dx.data_ptr(), dweight.data_ptr(), _ptr(dbias),
-                                 workspace.data_ptr(), workspace.nbytes, _stream(stream))
+                                 workspace.data_ptr(), workspace.nbytes, _stream_on(dev, stream))
     if rc:
         raise MoEError("moe_norm_backward", rc)
 
@@ -912,6 +925,8 @@ class AdamW:
                     raise ValueError("AdamW: %s[%d] must be a contiguous float32 or bfloat16 tensor of shape %s on %s, got %s %s on %s%s" % (
                         name, i, tuple(p.shape), dev if dev.type == "cuda" else "a CUDA device", str(t.dtype).replace("torch.", ""),
                         tuple(t.shape), t.device, "" if t.is_contiguous() else ", not contiguous"))
+        if len({p.data_ptr() for p in self.params if p.numel()}) < sum(1 for p in self.params if p.numel()):
+            raise ValueError("AdamW: a tensor is in params twice")
         self.device, self.state_bits = dev, state_bits
         self.cfg = AdamWConfig(betas[0], betas[1], lr, eps, state_bits, seed)
         self.offsets, moffs, at, mat = [], [], 0, 0
@@ -951,7 +966,7 @@ class AdamW:
             named = dict(steps=(self.steps, torch.int32, 2), grad_scale=(grad_scale, torch.float32, 1), lr=(lr, torch.float32, 1))
             _refuse_on("AdamW.step", dev, stream, **{k: v for k, v in named.items() if v[0] is not None})
         rc = lib().moe_adamw_step(ctypes.byref(self.cfg), ctypes.byref(self._table), len(self._table), _ptr(lr),
-                                  _ptr(grad_scale), self.steps.data_ptr(), _stream(stream))
+                                  _ptr(grad_scale), self.steps.data_ptr(), _stream_on(dev, stream))
         if rc:
             self.cfg.lr = before
             raise MoEError("moe_adamw_step", rc)

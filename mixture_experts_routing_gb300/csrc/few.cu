@@ -163,7 +163,6 @@ constexpr uint32_t kBoxBytes = kBoxCols * 2 * kRows;
 constexpr int kDrawn = 3;        // tiles drawn ahead
 constexpr int kMaxStages = 8;
 constexpr uint32_t kRingBytes = 209u << 10;  // with the buffers of the sums
-constexpr uint32_t kErrWaitUnit = 1u << 4;  // an expert's h never became complete
 
 struct FewShared {
   uint64_t wfull[kMaxStages], afull[kMaxStages], empty[kMaxStages], named[kMaxStages], rfull[kEpiWarps], rempty[kEpiWarps];

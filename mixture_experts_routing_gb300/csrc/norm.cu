@@ -22,7 +22,6 @@ namespace {
 constexpr int kMaxThreads = 1024;
 constexpr uint32_t kRingBytes = 200u << 10;
 constexpr int kMaxStages = 8;
-constexpr uint32_t kErrWaitRows = 1u << 5;  // rows never arrived
 
 // Two fp32 values in one register pair, worked on by one instruction: the kernels are short of
 // issue slots before they are short of memory (the backward of 7168 columns took 350

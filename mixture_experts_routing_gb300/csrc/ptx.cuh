@@ -12,6 +12,8 @@ enum : uint32_t {
   kErrWaitEmpty = 1u << 1,    // producer: stage never released
   kErrWaitAccum = 1u << 2,    // epilogue: accumulator never completed
   kErrWaitRouter = 1u << 3,   // router logits: a stage of x / W_r never arrived
+  kErrWaitUnit = 1u << 4,     // few tokens: an expert's h never became complete
+  kErrWaitRows = 1u << 5,     // layer norm: rows never arrived
 };
 
 __device__ __forceinline__ uint32_t smem_u32(const void* p) {

@@ -302,6 +302,8 @@ def test_refusals():
     for bad in (dict(params=[p], grads=[g[:63]]), dict(params=[p.half()], grads=[g]), dict(params=[p[::2]], grads=[g[:32]]), dict(params=[p], grads=[g.cpu()])):
         with pytest.raises(ValueError):
             moe.AdamW(lr=1e-3, **bad)
+    with pytest.raises(ValueError, match="twice"):
+        moe.AdamW([p, p], [g, g.clone()], lr=1e-3)
     opt = moe.AdamW([torch.zeros(65, device=DEV)[1:]], [g], lr=1e-3)
     with pytest.raises(moe.MoEError):  # not 16-byte aligned
         opt.step()
