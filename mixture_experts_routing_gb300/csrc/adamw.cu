@@ -4,8 +4,14 @@
 //   p -= lr (m / (1-b1^t) / (sqrt(v / (1-b2^t)) + eps) + decay p)
 //
 // The tensors' table is a kernel argument. The work is cut into blocks of 256 values
-// of one tensor (those that share a scale in 8 bits); a warp takes a block, a lane
-// eight consecutive values of it.
+// of one tensor (those that share a scale in 8 bits); a warp takes a block, a lane eight
+// values of it.
+//
+// 32 bits: bound by memory, 44 million bf16 weights with f32 masters and bf16 gradients in
+// 192 us, 6.4 TB/s of the 6.8 that a copy reaches. 8 bits: 277 million with f32 gradients
+// in 824 us, 6.1 TB/s; a value takes some 60 instructions, 72 % of the issue slots are used,
+// and the exact root and the hash are what could go of them (799 us without either). Loading
+// the next block ahead of this one's work cost the fourth block an SM (955 us).
 #include "act.cuh"
 #include "layer_internal.h"
 #include "moe_internal.h"

@@ -18,6 +18,12 @@
 // share out). A block draws its tiles from one counter, FC1's before FC2's, so a block
 // that waits for an expert's h waits only for tiles that running blocks already hold: the
 // kernel needs no co-residency, and the ring fills with W_down while it waits.
+//
+// Measured, called in a row with changing inputs: 1 token, 8 of 256 experts of 7168 x 2048,
+// 113 us (705 MB: 6.3 TB/s over the whole call, 7 once the weights flow, of 6.8 that a copy
+// reaches); 33 tokens, 8 of 128 of 2048 x 768, 181 to 214 us by the experts hit; 64 tokens,
+// 2 of 8 of 512 x 1024, 34 us, which is the chain of its waits. The logits take 2 us of one
+// token's call (2048 columns) to 5 us of 33 tokens'.
 #include "act.cuh"
 #include "layer_internal.h"
 #include "moe_internal.h"

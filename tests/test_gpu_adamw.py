@@ -278,6 +278,31 @@ def test_captured_replayed_and_resumed(bits):
         assert all(torch.equal(p, q) for p, q in zip(s.params, a.params))
 
 
+@pytest.mark.parametrize("bits", [32, 8])
+def test_weights_and_gradients_of_both_types_in_one_list(bits):
+    """Each tensor moves as it does in a list of its own type (8 bits: but for the places in the hash)."""
+    g = gen(11)
+    shapes = [(64, 33), (1000,), (2, 3, 50), (7,), (300, 300)]
+    types = [(torch.bfloat16, torch.float32), (torch.float32, torch.float32), (torch.bfloat16, torch.bfloat16), (torch.float32, torch.bfloat16), (torch.bfloat16, torch.float32)]
+    params = [(torch.randn(s, device=DEV, generator=g) * 0.1).to(p).requires_grad_(p is torch.float32) for s, (p, _) in zip(shapes, types)]
+    grads = [torch.randn(s, device=DEV, generator=g).to(t) for s, (_, t) in zip(shapes, types)]
+    old = [p.detach().clone() for p in params]
+    opt = moe.AdamW(params, grads, lr=1e-2, betas=(0.9, 0.99), weight_decay=[0.1, 0, 0.2, 0, 0.3], state_bits=bits)
+    opt.step()
+    ok()
+    for i, (p, q, gr) in enumerate(zip(params, old, grads)):
+        alone = q.clone()
+        one = moe.AdamW([alone], [gr], lr=1e-2, betas=(0.9, 0.99), weight_decay=[0.1, 0, 0.2, 0, 0.3][i], state_bits=bits)
+        one.step()
+        ok()
+        assert torch.equal(alone, p.detach()), i
+        a, n = opt.offsets[i], q.numel()
+        if bits == 32:
+            assert torch.equal(opt.m[a: a + n], one.m[:n]) and torch.equal(opt.v[a: a + n], one.v[:n])
+        else:
+            assert torch.equal(opt.m_scale[a // 256: -(-(a + n) // 256)], one.m_scale)
+
+
 def test_more_than_2_31_values():
     n = (1 << 31) + 1000  # 8-bit states, bf16 gradients: values on both sides of the border
     p = torch.zeros(n, dtype=torch.float32, device=DEV)

@@ -326,6 +326,40 @@ def test_weights_behind_2_32_bytes():
     assert ((y.double() - s.y.double()).norm() / s.y.double().norm()).item() < 2.0 ** -8
 
 
+def test_a_router_that_lies_at_an_odd_place():
+    s = Layer(5, 256, 12, 3, 128)
+    s.run()
+    want = s.y.clone()
+    room = torch.zeros(256 * 12 + 1, device=DEV)
+    room[1:] = s.wr.flatten()
+    s.wr = room[1:].view(256, 12)  # 4-byte aligned alone
+    bias = torch.zeros(13, device=DEV)
+    bias[1:] = s.b if s.b is not None else 0
+    s.b = bias[1:]
+    s.y.fill_(math.nan)
+    s.run()
+    ok()
+    assert torch.equal(s.y, want)
+    s.check()
+
+
+def test_the_current_stream_is_the_one_taken():
+    s = Layer(9, 512, 16, 4, 256)
+    s.run()
+    torch.cuda.synchronize()
+    want = s.y.clone()
+    side = torch.cuda.Stream()
+    with torch.cuda.stream(side):
+        s.x.mul_(2)  # the call has to come after this and before the next
+        s.run()
+        doubled = s.y.clone()
+        s.x.mul_(0.5)
+        s.run()
+    side.synchronize()
+    ok()
+    assert torch.equal(s.y, want) and not torch.equal(doubled, want)
+
+
 def test_no_tokens():
     s = Layer(0, 128, 4, 2, 64)
     s.run()
