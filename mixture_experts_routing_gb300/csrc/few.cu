@@ -184,7 +184,7 @@ struct FewShared {
   uint16_t unit_e[kMaxUnits], unit_at[kMaxUnits], unit_n[kMaxUnits];
   uint8_t unit_done[kMaxUnits];    // seen complete by the activations' warp
   int warp_sum[kMaxExperts / 32][3];
-  int units, most;                 // units; the most tokens of an expert
+  int units, groups;               // units; groups of 8 tokens in one at most
   uint32_t by_per, by_run;         // 2^32 / (FC1 tiles of a unit) and / (16 units), rounded up
 };
 
@@ -249,21 +249,31 @@ __device__ __forceinline__ void pick(const FewArgs& a, const float* logits, int 
   }
 }
 
-// The units (an expert's tokens, at most `per` at a time) from the masks; all threads.
+// The units (an expert's tokens, at most 8, 16 or 32 at a time) from the masks; all threads.
 // The blocks build the same lists, each for itself.
 __device__ __forceinline__ void build_units(const FewArgs& a, int n, FewShared& s) {
   const int e = threadIdx.x, lane = e & 31, warp = e >> 5;
   int c = 0;
   if (e < kMaxExperts) {
     c = __popc(s.mask[e][0]) + __popc(s.mask[e][1]);
-    const int most = __reduce_max_sync(0xFFFFFFFFu, c);
-    if (lane == 0) s.warp_sum[warp][2] = most;
+    const int u8 = __reduce_add_sync(0xFFFFFFFFu, (c + 7) / 8), u16 = __reduce_add_sync(0xFFFFFFFFu, (c + 15) / 16);
+    const int u32 = __reduce_add_sync(0xFFFFFFFFu, (c + 31) / 32);
+    if (lane == 0) s.warp_sum[warp][0] = u8, s.warp_sum[warp][1] = u16, s.warp_sum[warp][2] = u32;
   }
   __syncthreads();
-  int most = 0;
+  int u8 = 0, u16 = 0, u32 = 0;
 #pragma unroll
-  for (int w = 0; w < kMaxExperts / 32; ++w) most = max(most, s.warp_sum[w][2]);
-  const int per = most <= 8 ? 8 : most <= 16 ? 16 : 32;
+  for (int w = 0; w < kMaxExperts / 32; ++w) {
+    u8 += s.warp_sum[w][0];
+    u16 += s.warp_sum[w][1];
+    u32 += s.warp_sum[w][2];
+  }
+  // Units of 16 and of 32 tokens take 1.3 and 1.55 times one of 8 (their stages are shorter);
+  // an expert's second unit has its weights from the second-level cache. 64 tokens, 6 of 64
+  // experts of 4096 x 1408 (6 tokens each, some over 8): 380, 457, 552 us with 8, 16, 32;
+  // 64 tokens, 2 of 8 of 512 x 1024 (16 each): 42, 37, 35.
+  const int per = 10 * u8 <= 13 * u16 && 20 * u8 <= 31 * u32 ? 8 : 26 * u16 <= 31 * u32 ? 16 : 32;
+  __syncthreads();  // the sums are written again below
   const int u = (c + per - 1) / per;
   int cs = c, us = u;  // inclusive sums over the warp's experts
   if (e < kMaxExperts) {
@@ -291,7 +301,7 @@ __device__ __forceinline__ void build_units(const FewArgs& a, int n, FewShared& 
     }
     if (e == 0) {
       s.units = all;
-      s.most = most;
+      s.groups = per / 8;
       // exact quotients: dividend x divisor stays below 2^32 (at most 384 units of 2048 tiles
       // by 2048, and 384 x 1024 by 16 x 384)
       s.by_per = 0xFFFFFFFFu / (uint32_t)(a.I / 8) + 1u;
@@ -815,9 +825,9 @@ __global__ void __launch_bounds__(kFewThreads, 1)
   if (s.units == 0) return;
   if (warp >= kMmaWarps + 2 + kEpiWarps)
     finish_role(a, s, n, o);
-  else if (s.most <= 8)
+  else if (s.groups == 1)
     roles<ACT, 1>(tm1, tm2, a, s, count, drawn, h, o, smem);
-  else if (s.most <= 16)
+  else if (s.groups == 2)
     roles<ACT, 2>(tm1, tm2, a, s, count, drawn, h, o, smem);
   else
     roles<ACT, 4>(tm1, tm2, a, s, count, drawn, h, o, smem);
