@@ -21,7 +21,7 @@
 //
 // Measured, called in a row with changing inputs: 1 token, 8 of 256 experts of 7168 x 2048,
 // 113 us (705 MB: 6.3 TB/s over the whole call, 7 once the weights flow, of 6.8 that a copy
-// reaches); 33 tokens, 8 of 128 of 2048 x 768, 181 to 214 us by the experts hit; 64 tokens,
+// reaches); 33 tokens, 8 of 128 of 2048 x 768, 163 to 176 us by the experts hit; 64 tokens,
 // 2 of 8 of 512 x 1024, 34 us, which is the chain of its waits. The logits take 2 us of one
 // token's call (2048 columns) to 5 us of 33 tokens'.
 #include "act.cuh"
@@ -161,11 +161,6 @@ constexpr int kMmaWarps = 4, kEpiWarps = 4, kFinishWarps = 2;
 constexpr int kFewThreads = (kMmaWarps + 2 + kEpiWarps + kFinishWarps) * 32;
 constexpr int kPosts = 8;        // column tiles posted to the finishing warps
 constexpr int kRows = 16;        // weight rows of a tile
-// Columns of a copy. A copy holds a tile's 16 rows as [64 columns][row], each row of 64
-// columns swizzled over its 128 bytes. Copies of 4 KB (8 rows x 256 columns) kept the copying
-// warp busy for longer than memory took: 1 token, 7168 x 2048: 128 us, in one copy 116.
-constexpr int kBoxCols = 512;
-constexpr uint32_t kBoxBytes = kBoxCols * 2 * kRows;
 constexpr int kDrawn = 3;        // tiles drawn ahead
 constexpr int kMaxStages = 8;
 constexpr uint32_t kRingBytes = 209u << 10;  // with the buffers of the sums
@@ -340,13 +335,19 @@ __device__ __forceinline__ int ld_relaxed(const int32_t* p) {
 __device__ __forceinline__ void red_release(int32_t* p) {
   asm volatile("red.release.gpu.global.add.s32 [%0], 1;" ::"l"(p) : "memory");
 }
+// Columns of a stage, by the groups of 8 tokens of a unit. A stage's 16 rows are one copy,
+// [64 columns][row], each row of 64 columns swizzled over its 128 bytes: copies of 4 KB kept
+// the copying warp busy for longer than memory took (1 token, 7168 x 2048: 128 us, with one
+// of 16 KB 116; 33 tokens, 2048 x 768: 195 us with two of 16 KB, 188 with one of 32).
+__host__ __device__ constexpr int stage_cols(int groups) { return groups == 1 ? 1024 : 512; }
+
 // Sizes by the groups of 8 tokens of a unit.
 template <int G>
 struct Ring {
   // Columns of a stage: long ones leave the warps of the products fewer waits (1 token, 7168 x
   // 2048: 140 us with 512, 124 with 1024), where the tokens leave room for four (16 tokens of
   // 512 x 1024: 48 us with five stages of 512, 52 with two of 1024).
-  static constexpr int kCols = G == 1 ? 1024 : 512;
+  static constexpr int kCols = stage_cols(G);
   static constexpr uint32_t kPitch = kCols * 2 + 16;  // of the activations' rows: 16 bytes apart in banks
   static constexpr uint32_t kWeights = kCols * 2 * kRows;
   static constexpr uint32_t kStage = (kWeights + kPitch * 8 * G + 1023u) & ~1023u;
@@ -413,14 +414,11 @@ __device__ __forceinline__ void weights_role(const CUtensorMap& tm1, const CUten
         const uint32_t bar = smem_u32(&s.wfull[at.st]), dst = ring + at.st * R::kStage;
         s.tile[at.st] = tile;
         mbar_arrive(smem_u32(&s.named[at.st]));
-        const int boxes = R::kCols == kBoxCols || t.cols - k <= kBoxCols ? 1 : R::kCols / kBoxCols;
-        mbar_arrive_expect_tx(bar, boxes * kBoxBytes);  // columns past the end count as zeros
-        for (int i = 0; i < boxes; ++i) {
-          if (t.fc2)
-            tma_load_3d(dst + i * kBoxBytes, &tm2, 0, e * a.H + t.row, (k + i * kBoxCols) / 64, bar, policy);
-          else
-            tma_load_4d(dst + i * kBoxBytes, &tm1, 0, t.row, 2 * e, (k + i * kBoxCols) / 64, bar, policy);
-        }
+        mbar_arrive_expect_tx(bar, R::kWeights);  // columns past the end count as zeros
+        if (t.fc2)
+          tma_load_3d(dst, &tm2, 0, e * a.H + t.row, k / 64, bar, policy);
+        else
+          tma_load_4d(dst, &tm1, 0, t.row, 2 * e, k / 64, bar, policy);
       }
       __syncwarp();
     }
@@ -777,9 +775,13 @@ __device__ __forceinline__ void roles(const CUtensorMap& tm1, const CUtensorMap&
     outputs_role<ACT, G>(a, s, count, h, o, reinterpret_cast<const float*>(smem + (red - smem_u32(smem))));
 }
 
+struct Maps {
+  CUtensorMap w13[2], w2[2];  // boxes as wide as the stages of one group, and of more
+};
+
 template <int ACT>
 __global__ void __launch_bounds__(kFewThreads, 1)
-    few_experts_kernel(const __grid_constant__ CUtensorMap tm1, const __grid_constant__ CUtensorMap tm2, const FewArgs a,
+    few_experts_kernel(const __grid_constant__ Maps tm, const FewArgs a,
                        const float* logits, int32_t* count, uint16_t* h, float* o) {
   extern __shared__ uint8_t smem[];
   __shared__ FewShared s;
@@ -801,8 +803,8 @@ __global__ void __launch_bounds__(kFewThreads, 1)
     }
     s.posts = 0;
     mbar_fence_init();
-    tma_prefetch_desc(&tm1);
-    tma_prefetch_desc(&tm2);
+    tma_prefetch_desc(&tm.w13[0]);
+    tma_prefetch_desc(&tm.w2[0]);
   }
   for (int i = threadIdx.x; i < 2 * kMaxExperts; i += kFewThreads) (&s.mask[0][0])[i] = 0;
   griddep_wait();
@@ -826,11 +828,11 @@ __global__ void __launch_bounds__(kFewThreads, 1)
   if (warp >= kMmaWarps + 2 + kEpiWarps)
     finish_role(a, s, n, o);
   else if (s.groups == 1)
-    roles<ACT, 1>(tm1, tm2, a, s, count, drawn, h, o, smem);
+    roles<ACT, 1>(tm.w13[0], tm.w2[0], a, s, count, drawn, h, o, smem);
   else if (s.groups == 2)
-    roles<ACT, 2>(tm1, tm2, a, s, count, drawn, h, o, smem);
+    roles<ACT, 2>(tm.w13[1], tm.w2[1], a, s, count, drawn, h, o, smem);
   else
-    roles<ACT, 4>(tm1, tm2, a, s, count, drawn, h, o, smem);
+    roles<ACT, 4>(tm.w13[1], tm.w2[1], a, s, count, drawn, h, o, smem);
 }
 
 }  // namespace
@@ -847,10 +849,11 @@ int launch_few(const FewArgs& a, cudaStream_t s) {
     return err != cudaSuccess ? err : cudaDeviceGetAttribute(v, cudaDevAttrMultiProcessorCount, dev);
   });
   if (e != cudaSuccess) return -(int)e;
-  CUtensorMap tm1, tm2;
-  if (!make_map_halves(&tm1, a.w13, (uint64_t)a.H, (uint64_t)a.I, 2ull * a.E, 8, 2, kBoxCols / 64) ||
-      !make_map_mn3d(&tm2, a.w2, (uint64_t)a.I, (uint64_t)a.E * a.H, kRows, kBoxCols / 64))
-    return -(int)cudaErrorInvalidValue;
+  Maps tm;
+  for (int i = 0; i < 2; ++i)
+    if (!make_map_halves(&tm.w13[i], a.w13, (uint64_t)a.H, (uint64_t)a.I, 2ull * a.E, 8, 2, stage_cols(1 + i) / 64) ||
+        !make_map_mn3d(&tm.w2[i], a.w2, (uint64_t)a.I, (uint64_t)a.E * a.H, kRows, stage_cols(1 + i) / 64))
+      return -(int)cudaErrorInvalidValue;
   const FewWs w = layout(a.N, a.H, a.E, a.K, a.I);
   float* logits = reinterpret_cast<float*>(a.ws + w.logits);
   int32_t* count = reinterpret_cast<int32_t*>(a.ws + w.count);
@@ -858,7 +861,7 @@ int launch_few(const FewArgs& a, cudaStream_t s) {
                  logits, count);
   if (e == cudaSuccess)
     e = launch_pdl(a.activation ? few_experts_kernel<1> : few_experts_kernel<0>, dim3(sms), dim3(kFewThreads), kRingBytes, s,
-                   tm1, tm2, a, (const float*)logits, count, reinterpret_cast<uint16_t*>(a.ws + w.h),
+                   tm, a, (const float*)logits, count, reinterpret_cast<uint16_t*>(a.ws + w.h),
                    reinterpret_cast<float*>(a.ws + w.o));
   return e != cudaSuccess ? -(int)e : 2;
 }
