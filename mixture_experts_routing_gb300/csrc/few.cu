@@ -10,8 +10,8 @@
 //            The last block to finish a column tile adds up its tokens' routes.
 //
 // The time is that of reading the weights, so a tile is a run of 16 weight rows that
-// passes once through a ring in shared memory (one TMA copy of 16 rows x 512 columns a stage) into
-// mma.sync, weights as the 16 rows, tokens as the 8 columns: the four warps split the
+// passes once through a ring in shared memory (a TMA copy of 16 rows x 1024 or 512 columns
+// a stage) into mma.sync, weights as the 16 rows, tokens as the 8 columns: four warps split the
 // columns of a stage, so a tile needs no split between blocks, and there are enough tiles
 // to keep all SMs busy from one token on (128-row tiles of the 5th-generation tensor
 // cores would leave 8 experts x 2048 features with fewer tiles than there are turns to
@@ -335,6 +335,7 @@ __device__ __forceinline__ int ld_relaxed(const int32_t* p) {
 __device__ __forceinline__ void red_release(int32_t* p) {
   asm volatile("red.release.gpu.global.add.s32 [%0], 1;" ::"l"(p) : "memory");
 }
+
 // Columns of a stage, by the groups of 8 tokens of a unit. A stage's 16 rows are one copy,
 // [64 columns][row], each row of 64 columns swizzled over its 128 bytes: copies of 4 KB kept
 // the copying warp busy for longer than memory took (1 token, 7168 x 2048: 128 us, with one

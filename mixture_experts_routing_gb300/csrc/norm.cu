@@ -148,18 +148,17 @@ struct Rows {
   Plan p;
   const uint16_t* from[TENSORS];
 
-  // By the first threads of the first warps, a copy each (a block has as many warps, or its
-  // first one does them all); the copies may land before the bytes are announced.
+  // By the first threads of the first warps, a copy each (a block has eight warps at least);
+  // the copies may land before the bytes are announced.
   __device__ __forceinline__ bool loads() const { return threadIdx.x < 32 * TENSORS && (threadIdx.x & 31) == 0; }
   __device__ __forceinline__ void load(uint32_t step, int stage) const {
     const int warp = threadIdx.x >> 5;
     const uint32_t row = step * p.rows, part = p.stage / TENSORS;
     const uint32_t bytes = min((uint32_t)p.rows, N - row) * H * 2, bar = smem_u32(&full[stage]);
     if (warp == 0) mbar_arrive_expect_tx(bar, bytes * TENSORS);
-    const int last = p.threads >= 32 * TENSORS ? warp + 1 : TENSORS;
 #pragma unroll
     for (int i = 0; i < TENSORS; ++i)
-      if (i >= warp && i < last) bulk_load(base + stage * p.stage + i * part, from[i] + (size_t)row * H, bytes, bar);
+      if (i == warp) bulk_load(base + stage * p.stage + i * part, from[i] + (size_t)row * H, bytes, bar);
   }
 };
 
