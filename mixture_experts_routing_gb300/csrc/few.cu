@@ -22,7 +22,7 @@
 // Measured, called in a row with changing inputs: 1 token, 8 of 256 experts of 7168 x 2048,
 // 113 us (705 MB: 6.3 TB/s over the whole call, 7 once the weights flow, of 6.8 that a copy
 // reaches); 33 tokens, 8 of 128 of 2048 x 768, 163 to 176 us by the experts hit; 64 tokens,
-// 2 of 8 of 512 x 1024, 34 us, which is the chain of its waits. The logits take 2 us of one
+// 2 of 8 of 512 x 1024, 32 us, which is the chain of its waits. The logits take 2 us of one
 // token's call (2048 columns) to 5 us of 33 tokens'.
 #include "act.cuh"
 #include "layer_internal.h"
@@ -183,6 +183,25 @@ struct FewShared {
   uint32_t by_per, by_run;         // 2^32 / (FC1 tiles of a unit) and / (16 units), rounded up
 };
 
+// A logit as a key that orders like it, a NaN above all and 0 for none; and back.
+__device__ __forceinline__ uint32_t key_of(float l) {
+  const uint32_t b = __float_as_uint(l + 0.0f);  // -0 and 0 are equal
+  return isnan(l) ? 0xFFFFFFFFu : (b & 0x80000000u) ? ~b : b | 0x80000000u;
+}
+__device__ __forceinline__ float logit_of(uint32_t k) {
+  return __uint_as_float(k == 0xFFFFFFFFu ? 0x7FC00000u : (k & 0x80000000u) ? k & 0x7FFFFFFFu : ~k);
+}
+
+// Pick k of token t.
+__device__ __forceinline__ void keep_pick(const FewArgs& a, FewShared& s, int t, int k, int id, float p, bool out) {
+  const int at = t * a.K + k;
+  s.ids[at] = id;
+  s.p[at] = p;
+  if (p != 0.0f) atomicOr(&s.mask[id][t >> 5], 1u << (t & 31));  // p = 0 is not read; a NaN is not 0
+  if (out && a.topk_ids) a.topk_ids[at] = id;
+  if (out && a.topk_p) a.topk_p[at] = p;
+}
+
 // The K experts of a token by a warp. The picks go by the logits (ties to the lower id):
 // probabilities are needed of the K picked alone, and their sum over all experts only where
 // it is not divided out again. Lane l holds experts l, l+32, ..., PER of them. One token at a
@@ -191,20 +210,14 @@ struct FewShared {
 template <int PER>
 __device__ __forceinline__ void pick(const FewArgs& a, const float* logits, int t, FewShared& s, bool out) {
   const int lane = threadIdx.x & 31;
-  uint32_t key[PER], first[PER];  // orders like the logit, a NaN above all; 0: taken or absent
+  uint32_t key[PER], first[PER];
 #pragma unroll
   for (int j = 0; j < PER; ++j) {
     const int e = lane + 32 * j;
-    key[j] = e < a.E ? __float_as_uint(__ldcg(logits + (size_t)t * a.E + e)) : 0u;
+    first[j] = e < a.E ? __float_as_uint(__ldcg(logits + (size_t)t * a.E + e)) : 0u;
   }
 #pragma unroll
-  for (int j = 0; j < PER; ++j) {
-    const float l = __uint_as_float(key[j]);
-    const uint32_t b = __float_as_uint(l + 0.0f);  // -0 and 0 are equal
-    key[j] = lane + 32 * j >= a.E ? 0u : isnan(l) ? 0xFFFFFFFFu : (b & 0x80000000u) ? ~b : b | 0x80000000u;
-    first[j] = key[j];
-  }
-  auto value = [](uint32_t k) { return __uint_as_float(k == 0xFFFFFFFFu ? 0x7FC00000u : (k & 0x80000000u) ? k & 0x7FFFFFFFu : ~k); };
+  for (int j = 0; j < PER; ++j) key[j] = first[j] = lane + 32 * j < a.E ? key_of(__uint_as_float(first[j])) : 0u;
   float top = 0.0f, my_l = 0.0f;
   int my_id = 0;
   for (int k = 0; k < a.K; ++k) {
@@ -220,8 +233,8 @@ __device__ __forceinline__ void pick(const FewArgs& a, const float* logits, int 
 #pragma unroll
     for (int j = 0; j < PER; ++j)
       if (e == (uint32_t)(lane + 32 * j)) key[j] = 0;
-    if (k == 0) top = value(best);
-    if (lane == k) { my_id = (int)e; my_l = value(best); }
+    if (k == 0) top = logit_of(best);
+    if (lane == k) { my_id = (int)e; my_l = logit_of(best); }
   }
   my_l = lane < a.K ? route_exp(__fsub_rn(my_l, top)) : 0.0f;
   float all = my_l;
@@ -229,19 +242,39 @@ __device__ __forceinline__ void pick(const FewArgs& a, const float* logits, int 
     all = 0.0f;
 #pragma unroll
     for (int j = 0; j < PER; ++j)
-      if (lane + 32 * j < a.E) all += route_exp(__fsub_rn(value(first[j]), top));
+      if (lane + 32 * j < a.E) all += route_exp(__fsub_rn(logit_of(first[j]), top));
   }
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) all += __shfl_xor_sync(0xFFFFFFFFu, all, o);
-  if (lane < a.K) {
-    const float p = __fdiv_rn(my_l, all);
-    const int at = t * a.K + lane;
-    s.ids[at] = my_id;
-    s.p[at] = p;
-    if (p != 0.0f) atomicOr(&s.mask[my_id][t >> 5], 1u << (t & 31));  // p = 0 is not read; a NaN is not 0
-    if (out && a.topk_ids) a.topk_ids[at] = my_id;
-    if (out && a.topk_p) a.topk_p[at] = p;
+  if (lane < a.K) keep_pick(a, s, t, lane, my_id, __fdiv_rn(my_l, all), out);
+}
+
+// The same with at most eight experts: four tokens t0 .. t0+3 a warp, eight lanes each (64
+// tokens, top-2 of 8: a turn of all warps instead of six).
+__device__ __forceinline__ void pick_eighths(const FewArgs& a, const float* logits, int t0, int n, FewShared& s, bool out) {
+  const int lane = threadIdx.x & 31, e = lane & 7, t = t0 + (lane >> 3);
+  const bool in = t < n && e < a.E;
+  const uint32_t first = in ? key_of(__ldcg(logits + (size_t)t * a.E + e)) : 0u;
+  uint32_t key = first;
+  float top = 0.0f, my_l = 0.0f;
+  int my_id = 0;
+  for (int k = 0; k < a.K; ++k) {
+    uint32_t best = key, id = 0;
+#pragma unroll
+    for (int o = 4; o > 0; o >>= 1) best = max(best, __shfl_xor_sync(0xFFFFFFFFu, best, o));
+    id = key == best ? e : 8;
+#pragma unroll
+    for (int o = 4; o > 0; o >>= 1) id = min(id, __shfl_xor_sync(0xFFFFFFFFu, id, o));
+    if (id == (uint32_t)e) key = 0;
+    if (k == 0) top = logit_of(best);
+    if (e == k) { my_id = (int)id; my_l = logit_of(best); }
   }
+  my_l = e < a.K ? route_exp(__fsub_rn(my_l, top)) : 0.0f;
+  float all = my_l;
+  if (!a.renorm) all = in ? route_exp(__fsub_rn(logit_of(first), top)) : 0.0f;
+#pragma unroll
+  for (int o = 4; o > 0; o >>= 1) all += __shfl_xor_sync(0xFFFFFFFFu, all, o);
+  if (e < a.K && t < n) keep_pick(a, s, t, e, my_id, __fdiv_rn(my_l, all), out);
 }
 
 // The units (an expert's tokens, at most 8, 16 or 32 at a time) from the masks; all threads.
@@ -817,12 +850,16 @@ __global__ void __launch_bounds__(kFewThreads, 1)
   }
   const int n = live_tokens(a.n_dev, a.N);
   __syncthreads();
-  for (int t = warp; t < n; t += kFewThreads / 32) {
-    if (a.E <= 32) pick<1>(a, logits, t, s, blockIdx.x == 0);
-    else if (a.E <= 64) pick<2>(a, logits, t, s, blockIdx.x == 0);
-    else if (a.E <= 128) pick<4>(a, logits, t, s, blockIdx.x == 0);
-    else pick<8>(a, logits, t, s, blockIdx.x == 0);
-  }
+  const bool out = blockIdx.x == 0;
+  if (a.E <= 8)
+    for (int t = 4 * warp; t < n; t += 4 * (kFewThreads / 32)) pick_eighths(a, logits, t, n, s, out);
+  else
+    for (int t = warp; t < n; t += kFewThreads / 32) {
+      if (a.E <= 32) pick<1>(a, logits, t, s, out);
+      else if (a.E <= 64) pick<2>(a, logits, t, s, out);
+      else if (a.E <= 128) pick<4>(a, logits, t, s, out);
+      else pick<8>(a, logits, t, s, out);
+    }
   __syncthreads();
   build_units(a, n, s);
   if (s.units == 0) return;

@@ -126,9 +126,10 @@ def test_one_expert_for_all_and_all_for_each():
     s.check()
 
 
+@pytest.mark.parametrize("e", [6, 16, 200])
 @pytest.mark.parametrize("live", [0, 1, 7, 8, 9, 20, 33])
-def test_rows_behind_the_live_ones_are_left(live):
-    s = Layer(33, 512, 16, 4, 256)
+def test_rows_behind_the_live_ones_are_left(live, e):
+    s = Layer(33, 512, e, 4, 256)
     s.x[live:] = math.nan
     s.add[live:] = math.nan
     n = torch.tensor([live], dtype=torch.int32, device=DEV)
@@ -214,8 +215,9 @@ def test_a_bad_weight_reaches_its_tokens_only():
     assert torch.equal(s.y, clean)
 
 
-def test_equal_logits_go_to_the_lower_experts():
-    s = Layer(12, 128, 40, 6, 64, bias=False)
+@pytest.mark.parametrize("e", [7, 8, 40, 256])
+def test_equal_logits_go_to_the_lower_experts(e):
+    s = Layer(12, 128, e, 6, 64, bias=False)
     s.wr.zero_()
     s.run()
     ok()
