@@ -581,12 +581,13 @@ int64_t moe_few_workspace_bytes(const moe_few_config_t* cfg);
  *           for want of others, its weights are not read. A token whose logits are
  *           all -inf, or hold a NaN or +inf, has NaN probabilities and a NaN row.
  *  w13      [E,2I,H] bf16 packed (moe_pack_w13); w2 [E,H,I] bf16 (moe_pack_w2)
- *  add      [N,H] bf16, or NULL; may be y itself
+ *  add      [N,H] bf16, or NULL
  *  n_valid  NULL, or a DEVICE int32 with the number of live tokens n (clamped to
  *           0..N), read when the kernels run: rows n and up of x and add are not
  *           read, those of y, topk_ids and topk_p stay as they are. One captured
  *           graph serves every batch up to N
- *  y        [N,H] bf16 output
+ *  y        [N,H] bf16 output; may be x, or add, or both: a row's outputs are written
+ *           when every product of x has been read
  *  topk_ids [N,K] i32, topk_p [N,K] f32: the choice, or NULL each
  *  workspace/ws_bytes  moe_few_workspace_bytes, 16-byte aligned, as all but the
  *           f32 and i32 arguments. Calls that share it must not overlap

@@ -816,8 +816,8 @@ def alloc_few_workspace(cfg: FewConfig, device):
 
 def few_forward(cfg: FewConfig, x, w_router, bias, w13, w2, y, workspace, add=None, n_valid=None,
                 topk_ids=None, topk_p=None, stream=None) -> None:
-    """The whole layer for a few tokens: router, top-K, experts, combine (+ add, which
-    may be y). n_valid: a device int32 tensor of one value, the live tokens; later rows
+    """The whole layer for up to 64 tokens: router, top-K, experts, combine (+ add). y may
+    be x, or add, or both. n_valid: a device int32 tensor of one value, the live tokens; later rows
     are left as they are. topk_ids [N,K] i32 and topk_p [N,K] f32 receive the choice."""
     import torch
     N, H, E, K, I = cfg.n_tokens, cfg.hidden, cfg.n_experts, cfg.top_k, cfg.inter

@@ -162,6 +162,20 @@ def test_the_addend_is_the_output():
     assert torch.equal(y, want)
 
 
+@pytest.mark.parametrize("n,h,e,k,i", [(1, 7168, 16, 8, 2048), (33, 2048, 128, 8, 768), (64, 512, 8, 2, 1024), (20, 1024, 2, 1, 64)])
+def test_the_output_in_the_place_of_the_input(n, h, e, k, i):
+    """x += layer(x): no block may write a row that another still reads."""
+    s = Layer(n, h, e, k, i)
+    s.add = s.x.clone()
+    s.run()
+    x = s.x.clone()
+    for _ in range(20):
+        x.copy_(s.x)
+        moe.few_forward(s.cfg, x, s.wr, s.b, s.w13, s.w2, x, s.ws, add=x)
+        ok()
+        assert torch.equal(x, s.y)
+
+
 @pytest.mark.parametrize("k", [2, 5])
 def test_experts_shut_out_are_not_read(k):
     s = Layer(20, 256, 8, k, 128)
