@@ -925,8 +925,11 @@ class AdamW:
                     raise ValueError("AdamW: %s[%d] must be a contiguous float32 or bfloat16 tensor of shape %s on %s, got %s %s on %s%s" % (
                         name, i, tuple(p.shape), dev if dev.type == "cuda" else "a CUDA device", str(t.dtype).replace("torch.", ""),
                         tuple(t.shape), t.device, "" if t.is_contiguous() else ", not contiguous"))
-        if len({p.data_ptr() for p in self.params if p.numel()}) < sum(1 for p in self.params if p.numel()):
-            raise ValueError("AdamW: a tensor is in params twice")
+        end = 0
+        for at, size in sorted((p.data_ptr(), p.nbytes) for p in self.params if p.numel()):
+            if at < end:
+                raise ValueError("AdamW: a tensor is in params twice, or two of them overlap")
+            end = at + size
         self.device, self.state_bits = dev, state_bits
         self.cfg = AdamWConfig(betas[0], betas[1], lr, eps, state_bits, seed)
         self.offsets, moffs, at, mat = [], [], 0, 0
@@ -959,12 +962,14 @@ class AdamW:
         number from now on, or a device f32 tensor of one value for this call."""
         import torch
         dev, before = self.steps.get_device(), self.cfg.lr
+        new = before
         if lr is not None and not isinstance(lr, torch.Tensor):
-            self.cfg.lr, lr = float(lr), None
+            new, lr = float(lr), None
         if not ((grad_scale is None or _on(dev, grad_scale, torch.float32, 1)) and (lr is None or _on(dev, lr, torch.float32, 1))
                 and _here(dev, stream)):
             named = dict(steps=(self.steps, torch.int32, 2), grad_scale=(grad_scale, torch.float32, 1), lr=(lr, torch.float32, 1))
             _refuse_on("AdamW.step", dev, stream, **{k: v for k, v in named.items() if v[0] is not None})
+        self.cfg.lr = new
         rc = lib().moe_adamw_step(ctypes.byref(self.cfg), ctypes.byref(self._table), len(self._table), _ptr(lr),
                                   _ptr(grad_scale), self.steps.data_ptr(), _stream_on(dev, stream))
         if rc:

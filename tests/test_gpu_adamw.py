@@ -337,3 +337,24 @@ def test_refusals():
         opt.step(grad_scale=torch.tensor([1.0]))
     with pytest.raises(moe.MoEError):
         opt.step(lr=math.nan)
+
+
+def test_a_refused_step_keeps_the_rate():
+    p, g = torch.zeros(64, device=DEV), torch.ones(64, device=DEV)
+    opt = moe.AdamW([p], [g], lr=0.25, weight_decay=0.0)
+    with pytest.raises(ValueError, match="grad_scale"):
+        opt.step(grad_scale=torch.tensor([1.0]), lr=0.5)
+    with pytest.raises(moe.MoEError):
+        opt.step(lr=math.inf)
+    opt.step()
+    # the first step is lr g / (|g| + eps): -0.25 up to roundings of m, v and their corrections
+    assert (p + 0.25).abs().max().item() < 0.25 * 2.0 ** -20
+
+
+def test_overlapping_tensors_are_refused():
+    p, g = torch.zeros(1024, device=DEV), torch.zeros(512, device=DEV)
+    with pytest.raises(ValueError, match="overlap"):
+        moe.AdamW([p[256:768], p[:512]], [g, g], lr=1e-3)
+    with pytest.raises(ValueError, match="overlap"):
+        moe.AdamW([p[:512], p[256:256 + 64].view(torch.bfloat16)], [g, g[:128]], lr=1e-3)
+    moe.AdamW([p[512:], p[:512], p[:0]], [g, g, g[:0]], lr=1e-3)
