@@ -671,6 +671,9 @@ int moe_norm_backward(const moe_norm_config_t* cfg, const void* x, const float* 
  * the probabilities that keep the mean: v changes by 1-b2 of itself a step, far
  * less than half a code, and would never decay if rounded to the nearest. The
  * random bits are a hash of (seed, t, first + index), so a step can be repeated.
+ * sqrt(v) has the smallest code, 4.4e-6 of the block's largest, at least: under code 0
+ * the next step would divide m by its own g^2 alone. A weight whose gradients stay
+ * below that part of its block's largest moves less than with states in 32 bits.
  * A block whose largest value is under 2^-100 is stored as zeros; one that holds an
  * infinity or a NaN gets a NaN scale and reads as NaN. */
 typedef struct moe_adamw_tensor {

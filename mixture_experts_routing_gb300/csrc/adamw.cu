@@ -54,16 +54,18 @@ __device__ __forceinline__ float scale_of(uint32_t top, float* inv) {
 // bits, and the lower 20 are what is rounded. The dither, 16 bits of d from bit SHIFT on and
 // a half of the last of them, carries into the code with their probability. It does not
 // reach over 448: 2^20 - 8 at most, and a value is at most two units above its code.
-// small: 2^-120 is already in inv (exact for inv of 2^-6 or more).
+// scaled: 2^-120 is already in inv (exact for inv of 2^-6 or more). least: the smallest code.
 template <int SHIFT, bool SIGN>
-__device__ __forceinline__ uint32_t codes4(const float* v, float inv, bool scaled, const uint32_t* d) {
+__device__ __forceinline__ uint32_t codes4(const float* v, float inv, bool scaled, const uint32_t* d, uint32_t least) {
   uint32_t x[4];
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     float f = __fmul_rn(fabsf(v[i]), inv);
     if (!scaled) f = __fmul_rn(f, 0x1p-120f);
     const uint32_t dither = SHIFT ? (d[i] >> 12) & 0xFFFF0u : (d[i] << 4) & 0xFFFF0u;
-    x[i] = (__float_as_uint(f) + dither + 8u) << 4;  // the code in bits 24-30
+    x[i] = __float_as_uint(f) + dither + 8u;
+    if (!SIGN) x[i] = max(x[i], least << 20);
+    x[i] <<= 4;  // the code in bits 24-30
     if (SIGN) x[i] = (x[i] & 0x7FFFFFFFu) | (__float_as_uint(v[i]) & 0x80000000u);
   }
   return __byte_perm(__byte_perm(x[0], x[1], 0x0073), __byte_perm(x[2], x[3], 0x0073), 0x5410);
@@ -274,6 +276,11 @@ __global__ void __launch_bounds__(256, 4) adamw_kernel(const __grid_constant__ T
         const uint64_t idx = (uint64_t)(w.first + at);
         const uint32_t base = ((uint32_t)idx + 4u * lane) * 0x9E3779B1u + (uint32_t)(idx >> 32) * 0x85EBCA77u + key;
         const bool scaled = fminf(im, iv) >= 0x1p-6f;  // else a state passes 28672 (or a block is of zeros)
+        // A root of code 0 would leave the next step an m that may have been rounded up to a code
+        // of its own over (1-b2) g^2 alone: updates of hundreds of lr where a block's values are
+        // 10^4 apart (two of lr with code 1, which reads high what lies below 2^-9 / 448 of the
+        // largest: such a weight moves less than it would). Blocks of zeros stay at 0.
+        const uint32_t least = iv > 0.0f;
         if (scaled) {
           im *= 0x1p-120f;
           iv *= 0x1p-120f;
@@ -283,8 +290,8 @@ __global__ void __launch_bounds__(256, 4) adamw_kernel(const __grid_constant__ T
           uint32_t d[4];
 #pragma unroll
           for (int i = 0; i < 4; ++i) d[i] = mix32(base + (uint32_t)(h * 128 + i) * 0x9E3779B1u);
-          const uint32_t qm = scaled ? codes4<0, true>(m + 4 * h, im, true, d) : codes4<0, true>(m + 4 * h, im, false, d);
-          const uint32_t qv = scaled ? codes4<16, false>(v + 4 * h, iv, true, d) : codes4<16, false>(v + 4 * h, iv, false, d);
+          const uint32_t qm = scaled ? codes4<0, true>(m + 4 * h, im, true, d, 0u) : codes4<0, true>(m + 4 * h, im, false, d, 0u);
+          const uint32_t qv = scaled ? codes4<16, false>(v + 4 * h, iv, true, d, least) : codes4<16, false>(v + 4 * h, iv, false, d, least);
           store_codes(static_cast<uint8_t*>(w.m) + at, lane, h, full, left, qm);
           store_codes(static_cast<uint8_t*>(w.v) + at, lane, h, full, left, qv);
         }

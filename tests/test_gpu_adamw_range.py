@@ -1,0 +1,86 @@
+"""AdamW where one step does not show it: 8-bit states of blocks whose values differ by many
+orders of magnitude, and both dithers of their codes."""
+import math
+
+import numpy as np
+import pytest
+import torch
+
+import mixture_experts_routing_gb300 as moe
+from test_gpu_adamw import Set
+from test_gpu_w4 import DEV, gen, ok
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.mark.parametrize("b2", [0.95, 0.999])
+def test_8_bit_updates_stay_bounded_far_below_the_block_s_largest(b2):
+    """In every block some values have the gradient 1 at every step, the others at most q / 2 with
+    random signs and many zeros, q = 2^-9 / 448 being the smallest code's value next to the largest.
+    The block's largest m is 1 - b1^t and its largest sqrt(v) is sqrt(1 - b2^t); by induction the
+    others stay at codes up to 1, and at code 1 exactly for sqrt(v). So an update over lr is at most
+    (b1 (1 - b1^(t-1)) q + (1 - b1) |g|) / (1 - b1^t) over the root of
+    (b2 (1 - b2^(t-1)) q^2 + (1 - b2) g^2) / (1 - b2^t), which is no more than the sum of the two
+    quotients. fp32 and eps are covered by one part in a hundred."""
+    n, b1, q, g = 256 * 64, 0.9, 2.0 ** -9 / 448, gen(7)
+    p, grad = torch.zeros(n, device=DEV), torch.zeros(n, device=DEV)
+    opt = moe.AdamW([p], [grad], lr=1.0, betas=(b1, b2), weight_decay=0.0, state_bits=8)
+    size = q / 2 * 10 ** (-4 * torch.rand(n, device=DEV, generator=g))
+    for t in range(1, 301):
+        grad.copy_(size * torch.sign(torch.rand(n, device=DEV, generator=g) - 0.5) * (torch.rand(n, device=DEV, generator=g) < 0.7))
+        grad.view(-1, 256)[:, :8] = 1.0
+        p.zero_()
+        opt.step()
+        c1, c2 = 1 - b1 ** t, 1 - b2 ** t
+        bound = (1 - b1) / c1 * math.sqrt(c2 / (1 - b2))
+        if t > 1:
+            bound += b1 * (1 - b1 ** (t - 1)) / c1 * math.sqrt(c2 / (b2 * (1 - b2 ** (t - 1))))
+        assert p.abs().max().item() <= 1.01 * bound, t
+    ok()
+
+
+def test_the_smallest_code_of_a_root():
+    """sqrt(v) of a block that is not all zeros has code 1 at least; a block of zeros has code 0."""
+    n = 256 * 30
+    s = Set([n], True, True, 8)
+    g = s.grads[0].view(-1, 256)
+    g.mul_(torch.exp(4 * torch.randn(g.shape, device=DEV, generator=gen(1))))
+    g[3] = 0
+    g[4] *= 1e-36  # its squares are 0 in fp32
+    for _ in range(5):
+        s.opt.step()
+    ok()
+    v, m = s.opt.v.view(-1, 256), s.opt.m.view(-1, 256)
+    rest = torch.ones(30, dtype=torch.bool, device=DEV)
+    rest[3:5] = False
+    assert (v[3:5] == 0).all() and (s.opt.v_scale[3:5] == 0).all() and (m[3] & 127 == 0).all()
+    assert (v[rest] >= 1).all() and (v[rest] <= 126).all() and (v[rest] == 1).any()
+    assert ((m[rest] & 127) == 0).any()  # m is rounded to 0 as to any other code
+
+
+def test_the_dithers_of_both_states_are_those_of_the_hash():
+    """Codes of a step from zero states, value by value: m = 0.1 g takes the lower 16 bits of the
+    hash, sqrt(v) = 0.1 |g| the upper ones."""
+    n = 70000
+    s = Set([n], True, True, 8, betas=(0.9, 0.99), seed=77)
+    g = s.grads[0].double().cpu().numpy()
+    s.opt.step()
+    ok()
+
+    def mix(v):
+        v = (v ^ (v >> np.uint32(16))) * np.uint32(0x7FEB352D)
+        v = (v ^ (v >> np.uint32(15))) * np.uint32(0x846CA68B)
+        return v ^ (v >> np.uint32(16))
+
+    with np.errstate(over="ignore"):
+        d = mix(np.arange(n, dtype=np.uint32) * np.uint32(0x9E3779B1) + mix(np.array([0x9E3779B1 + 77], dtype=np.uint32)))
+    for codes, value, bits, least in ((s.opt.m, 0.1 * g, d & np.uint32(0xFFFF), 0.0), (s.opt.v, 0.1 * np.abs(g), d >> np.uint32(16), 2.0 ** -9)):
+        b, frac = (np.zeros(-(-n // 256) * 256) for _ in range(2))
+        b[:n], frac[:n] = value, (bits.astype(np.float64) + 0.5) / 65536
+        b, frac = b.reshape(-1, 256), frac.reshape(-1, 256)
+        a = np.abs(b) / (np.abs(b).max(1, keepdims=True) / 448)
+        step = np.exp2(np.maximum(np.floor(np.log2(np.maximum(a, 2.0 ** -30))), -6) - 3)
+        want = np.where(b < 0, -1, 1) * np.clip(np.floor(a / step + frac) * step, least, 448)
+        got = codes.view(torch.float8_e4m3fn).double().cpu().numpy().reshape(-1, 256)
+        # fp32 puts a value on the other side of its dither with a probability of 2^-20 or so
+        assert (got != want).ravel()[:n].mean() < 1e-4
