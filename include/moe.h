@@ -662,7 +662,9 @@ int moe_norm_backward(const moe_norm_config_t* cfg, const void* x, const float* 
  * pages), over any number of tensors in one launch per 240 of them:
  *   g = grad_scale * grad; m = b1 m + (1-b1) g; v = b2 v + (1-b2) g^2
  *   p -= lr (m/(1-b1^t) / (sqrt(v/(1-b2^t)) + eps) + weight_decay p)
- * in fp32. A bf16 weight is the rounding of its f32 master, which the step keeps.
+ * in fp32, a weight rounded once (one that gets no gradient stays as it is where
+ * lr weight_decay is below 2^-25). A bf16 weight is the rounding of its f32 master,
+ * which the step keeps.
  *
  * States in 8 bits: m and sqrt(v) as E4M3 codes, one f32 scale per 256 consecutive
  * values of a tensor (the last block may be shorter): scale = max|value| / 448,

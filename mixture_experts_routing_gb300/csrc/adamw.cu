@@ -243,7 +243,7 @@ __global__ void __launch_bounds__(256, 4) adamw_kernel(const __grid_constant__ T
         load8(static_cast<const float*>(w.m) + at, lane, full, left, m);
         load8(static_cast<const float*>(w.v) + at, lane, full, left, v);
       }
-      const float keep = 1.0f - lr * w.decay;
+      const float decay = lr * w.decay;
       float ma = 0.0f, va = 0.0f;
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
@@ -258,7 +258,9 @@ __global__ void __launch_bounds__(256, 4) adamw_kernel(const __grid_constant__ T
         } else {
           root = sqrt_approx(v[i]);
         }
-        p[i] = fmaf(p[i], keep, -lr1 * m[i] * rcp_approx(fmaf(root, rc2, eps)));
+        // both small terms first, then one rounding of the weight: 1 - decay as a factor would be a
+        // multiple of 2^-24, so that a decay of 1e-7 became 1.2e-7 and one of 2.5e-8 nothing
+        p[i] -= fmaf(lr1 * m[i], rcp_approx(fmaf(root, rc2, eps)), p[i] * decay);
       }
       store8(pp, lane, full, left, p);
       if (w.master) store8_bf16(static_cast<uint16_t*>(w.param) + at, lane, full, left, p);

@@ -1,5 +1,5 @@
 """AdamW where one step does not show it: 8-bit states of blocks whose values differ by many
-orders of magnitude, and both dithers of their codes."""
+orders of magnitude, both dithers of their codes, weight decay far below a weight's rounding."""
 import math
 
 import numpy as np
@@ -7,8 +7,8 @@ import pytest
 import torch
 
 import mixture_experts_routing_gb300 as moe
-from test_gpu_adamw import Set
-from test_gpu_w4 import DEV, gen, ok
+from test_gpu_adamw import Set, decode
+from test_gpu_w4 import DEV, F64, gen, ok
 
 pytestmark = pytest.mark.gpu
 
@@ -84,3 +84,31 @@ def test_the_dithers_of_both_states_are_those_of_the_hash():
         got = codes.view(torch.float8_e4m3fn).double().cpu().numpy().reshape(-1, 256)
         # fp32 puts a value on the other side of its dither with a probability of 2^-20 or so
         assert (got != want).ravel()[:n].mean() < 1e-4
+
+
+@pytest.mark.parametrize("bits", [32, 8])
+@pytest.mark.parametrize("lr,decay", [(2.5e-6, 0.01), (1e-5, 0.01), (1e-6, 0.1)])
+def test_small_decays_add_up(lr, decay, bits):
+    """lr decay is 2.5e-8 to 1e-7, below half a step of an fp32 value next to 1. The shrinkage, as the
+    projection on the start of what is left of p once the updates are taken out, against 64 bits. A
+    weight (about 0.05, a step of 3.7e-9) is rounded once a step, after an update of some lr, so the
+    roundings are independent: 2^-24 of it each at most, over T steps and n values 2^-24 sqrt(T / n) of
+    the projection, 6e-9 for T = 2000 and n = 2^18, of which six are 4e-8. T lr decay is 5e-5 at
+    least, and 2 % of it 1e-6. The updates' own errors, 2^-19 of lr in sum with random signs, are
+    smaller still. 8 bits: the updates follow from the states that were stored."""
+    n, T, g = 1 << 18, 2000, gen(3)
+    p = torch.randn(n, device=DEV, generator=g) * 0.05
+    start, grad = p.to(F64), torch.empty(n, device=DEV)
+    opt = moe.AdamW([p], [grad], lr=lr, betas=(0.9, 0.95), weight_decay=decay, state_bits=bits)
+    want = start.clone()
+    b1, b2 = 0.9, 0.95
+    for t in range(1, T + 1):
+        grad.normal_(generator=g)
+        m = opt.m.to(F64) if bits == 32 else decode(opt.m, opt.m_scale)
+        v = opt.v.to(F64) if bits == 32 else decode(opt.v, opt.v_scale).square()
+        m, v = b1 * m + (1 - b1) * grad.to(F64), b2 * v + (1 - b2) * grad.to(F64).square()
+        want -= lr * (m / (1 - b1 ** t) / (torch.sqrt(v / (1 - b2 ** t)) + 1e-8) + decay * want)
+        opt.step()
+    ok()
+    off = ((p.to(F64) - want) @ start / (start @ start)).item()
+    assert abs(off) <= 0.02 * T * lr * decay
