@@ -629,9 +629,9 @@ typedef struct moe_norm_config {
  *  mean   [N] f32 output (LAYER only), rstd [N] f32 output r: for the backward, or
  *         NULL each
  * All 16-byte aligned but mean and rstd. The row stays in registers: mean and var
- * are two sums over it in fp32, var from the differences to the mean. A row with an
- * infinity or a NaN is NaN in y; one whose squares pass fp32's range (values over
- * 1e17 or so) has rstd 0. */
+ * are two sums over it in fp32, var from the differences to the mean. A row whose s
+ * holds an infinity or a NaN is NaN in y and rstd; one whose squares pass fp32's range
+ * (values over 1e17 or so) has rstd 0 and y = b (NaN where the mean's sum passes it). */
 int moe_norm_forward(const moe_norm_config_t* cfg, const void* x, const void* add,
                      const float* weight, const float* bias, void* sum, void* y, float* mean,
                      float* rstd, cudaStream_t stream);

@@ -246,7 +246,19 @@ __global__ void __launch_bounds__(T, kMaxThreads / T) norm_forward_kernel(const 
       }
     }
     const float2 s = split(sq);
-    const float var = row_sum<WIDE>(s.x + s.y, p.lanes, first_warp, slots[turn][1]) * inv_h;
+    float mine_sq = s.x + s.y;
+    // A row that holds an infinity is NaN throughout. The mean makes it so; without one 1 / inf
+    // would bring the others to 0. (Finite values whose squares are infinite stay finite.)
+    if (RMS && isinf(mine_sq)) {
+#pragma unroll
+      for (int j = 0; j < KV; ++j)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const float2 u = split(v[j][i]);
+          if (isinf(u.x) || isinf(u.y)) mine_sq = __uint_as_float(0x7FC00000u);
+        }
+    }
+    const float var = row_sum<WIDE>(mine_sq, p.lanes, first_warp, slots[turn][1]) * inv_h;
     // every thread has the stage's rows in registers behind this barrier (row_sum has one of
     // its own where a row takes several warps)
     if (!WIDE) __syncthreads();
