@@ -26,6 +26,7 @@ constexpr uint32_t kRingBytes = 200u << 10;
 // Three groups of rows under way, 130 KB of the backward's 7168 columns, measured best (4096
 // rows of them: 48.7 us with two, 46.5 with three, 47.7 with as many as fit).
 constexpr int kMaxStages = 3;
+constexpr uint32_t kNone = 0xFFFFFFFFu;  // no step
 
 // Two fp32 values in one register pair, worked on by one instruction: the kernels are short of
 // issue slots before they are short of memory (the backward of 7168 columns took 350
@@ -160,6 +161,15 @@ struct Rows {
     for (int i = 0; i < TENSORS; ++i)
       if (i == warp) bulk_load(base + stage * p.stage + i * part, from[i] + (size_t)row * H, bytes, bar);
   }
+
+  // After a wait that ran out at step `failed`: this thread's copies for it and for the steps
+  // behind it are waited for, with the same limit each, so that none is under way when the
+  // block leaves.
+  __device__ __forceinline__ void drain(uint32_t failed, uint32_t* err) const {
+    const uint32_t turn = (failed - blockIdx.x) / gridDim.x;
+    for (uint32_t i = 0; i < (uint32_t)p.stages && failed + i * gridDim.x < p.steps; ++i)
+      mbar_wait(smem_u32(&full[(turn + i) % p.stages]), (turn + i) / p.stages & 1u, err, kErrWaitRows);
+  }
 };
 
 // KV: groups of 8 columns a thread holds. T: threads of a block at most, 1024 / T blocks an SM.
@@ -203,9 +213,9 @@ __global__ void __launch_bounds__(T, kMaxThreads / T) norm_forward_kernel(const 
   const uint32_t mine_at = rows.base + (uint32_t)(mine * H + lane * 8) * 2;
   uint32_t row = blockIdx.x * p.rows + mine, from = mine_at, par = 0;
   int stage = 0, turn = 0;
-  bool ok = true;  // after a wait that ran out: no more copies and waits, but every barrier
+  uint32_t failed = kNone;  // the step of a wait that ran out: no more copies and waits after it, but every barrier
   for (uint32_t step = blockIdx.x; step < p.steps; step += gridDim.x, row += rows_on, turn ^= 1) {
-    ok = ok && mbar_wait(smem_u32(&full[stage]), par, a.err, kErrWaitRows);
+    if (failed == kNone && !mbar_wait(smem_u32(&full[stage]), par, a.err, kErrWaitRows)) failed = step;
     const bool live = row < N;  // the last group may have fewer rows
     const size_t at = (size_t)row * H + lane * 8;
     F2 v[KV][4], sum = f2(0.0f);
@@ -262,7 +272,7 @@ __global__ void __launch_bounds__(T, kMaxThreads / T) norm_forward_kernel(const 
     // every thread has the stage's rows in registers behind this barrier (row_sum has one of
     // its own where a row takes several warps)
     if (!WIDE) __syncthreads();
-    if (loads && ok && step + p.stages * gridDim.x < p.steps) rows.load(step + p.stages * gridDim.x, stage);
+    if (loads && failed == kNone && step + p.stages * gridDim.x < p.steps) rows.load(step + p.stages * gridDim.x, stage);
     from += p.stage;
     if (++stage == p.stages) { stage = 0; from = mine_at; par ^= 1u; }
     if (!live) continue;
@@ -280,6 +290,7 @@ __global__ void __launch_bounds__(T, kMaxThreads / T) norm_forward_kernel(const 
       *reinterpret_cast<uint4*>(a.y + at + j * column2) = pack8(o);
     }
   }
+  if (loads && failed != kNone) rows.drain(failed, a.err);
 }
 
 template <bool RMS, bool ADD, int KV, bool WIDE>
@@ -323,7 +334,7 @@ __global__ void __launch_bounds__(kMaxThreads, 1) norm_backward_kernel(const Nor
   const uint32_t mine_at = base + (uint32_t)(mine * H + lane * 8) * 2;
   uint32_t row = blockIdx.x * p.rows + mine, from = mine_at, par = 0;
   int stage = 0, turn = 0;
-  bool ok = true;  // after a wait that ran out: no more copies and waits, but every barrier
+  uint32_t failed = kNone;  // the step of a wait that ran out: no more copies and waits after it, but every barrier
   float next_mean = 0.0f, next_r = 0.0f;  // a step ahead: their way from memory is longer than a step
   auto stats = [&](uint32_t row) {
     if (row < N) {
@@ -336,7 +347,7 @@ __global__ void __launch_bounds__(kMaxThreads, 1) norm_backward_kernel(const Nor
     const bool live = row < N;
     const float mean = next_mean, r = next_r;
     stats(row + rows_on);
-    ok = ok && mbar_wait(smem_u32(&full[stage]), par, a.err, kErrWaitRows);
+    if (failed == kNone && !mbar_wait(smem_u32(&full[stage]), par, a.err, kErrWaitRows)) failed = step;
     F2 z[KV][4], g[KV][4], sg = f2(0.0f), sgz = f2(0.0f);
     uint4 res[KV];
 #pragma unroll
@@ -366,7 +377,7 @@ __global__ void __launch_bounds__(kMaxThreads, 1) norm_backward_kernel(const Nor
     if (RMS) s = make_float2(row_sum<WIDE>(u.x + u.y, p.lanes, first_warp, reinterpret_cast<float*>(slots[turn])), 0.0f);
     else s = row_sums<WIDE>(u.x + u.y, t.x + t.y, p.lanes, first_warp, slots[turn]);
     if (!WIDE) __syncthreads();
-    if (loads && ok && step + p.stages * gridDim.x < p.steps) rows.load(step + p.stages * gridDim.x, stage);
+    if (loads && failed == kNone && step + p.stages * gridDim.x < p.steps) rows.load(step + p.stages * gridDim.x, stage);
     from += p.stage;
     if (++stage == p.stages) { stage = 0; from = mine_at; par ^= 1u; }
     if (!live) continue;
@@ -386,6 +397,7 @@ __global__ void __launch_bounds__(kMaxThreads, 1) norm_backward_kernel(const Nor
       *reinterpret_cast<uint4*>(a.dx + at + j * column2) = pack8(o);
     }
   }
+  if (loads && failed != kNone) rows.drain(failed, a.err);
   // the block's sums: its rows' groups are added in order through shared memory
   float* part = a.part + (int64_t)blockIdx.x * 2 * H;
   float* sums = reinterpret_cast<float*>(smem + (base - smem_u32(smem)));  // [2][H]: every copy has landed and was read
