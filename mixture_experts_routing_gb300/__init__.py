@@ -899,9 +899,11 @@ class AdamW:
     params: f32 or bf16 CUDA tensors of one device; a bf16 one gets an f32 master.
     grads: a buffer each, f32 or bf16, of the same shape (those that ffn_backward,
     router_backward, shared_backward and norm_backward write). Both are used where they
-    lie at every step. weight_decay: one number, or one a tensor. state_bits 32, or 8:
-    E4M3 codes of m and sqrt(v) with one scale per 256 values, rounded at random (by a
-    hash of seed, step and place).
+    lie at every step; a step refuses what is not 16-byte aligned, as a view may be. A
+    gradient may serve several params, and overlaps none. The state is made on the current
+    stream: a step on another one has to come after it. weight_decay: one number, or one a
+    tensor. state_bits 32, or 8: E4M3 codes of m and sqrt(v) with one scale per 256 values,
+    rounded at random (by a hash of seed, step and place).
 
     The state is flat, each tensor from a multiple of 256 on (offsets): m, v (f32, or u8
     codes), m_scale and v_scale (8 bits: one f32 per 256), master (of the bf16 params
@@ -925,11 +927,18 @@ class AdamW:
                     raise ValueError("AdamW: %s[%d] must be a contiguous float32 or bfloat16 tensor of shape %s on %s, got %s %s on %s%s" % (
                         name, i, tuple(p.shape), dev if dev.type == "cuda" else "a CUDA device", str(t.dtype).replace("torch.", ""),
                         tuple(t.shape), t.device, "" if t.is_contiguous() else ", not contiguous"))
-        end = 0
-        for at, size in sorted((p.data_ptr(), p.nbytes) for p in self.params if p.numel()):
-            if at < end:
+        # in order of their places: weights, and gradients, which several weights may share
+        weights_end = grads_end = 0
+        for at, size, weight in sorted([(p.data_ptr(), p.nbytes, True) for p in self.params if p.numel()]
+                                       + [(g.data_ptr(), g.nbytes, False) for g in self.grads if g.numel()]):
+            if weight and at < weights_end:
                 raise ValueError("AdamW: a tensor is in params twice, or two of them overlap")
-            end = at + size
+            if at < (grads_end if weight else weights_end):
+                raise ValueError("AdamW: a gradient overlaps a tensor of params")
+            if weight:
+                weights_end = at + size
+            else:
+                grads_end = max(grads_end, at + size)
         self.device, self.state_bits = dev, state_bits
         self.cfg = AdamWConfig(betas[0], betas[1], lr, eps, state_bits, seed)
         self.offsets, moffs, at, mat = [], [], 0, 0

@@ -1,5 +1,6 @@
 """AdamW where one step does not show it: 8-bit states of blocks whose values differ by many
-orders of magnitude, both dithers of their codes, weight decay far below a weight's rounding."""
+orders of magnitude, both dithers of their codes, weight decay far below a weight's rounding;
+tensors that overlap."""
 import math
 
 import numpy as np
@@ -112,3 +113,19 @@ def test_small_decays_add_up(lr, decay, bits):
     ok()
     off = ((p.to(F64) - want) @ start / (start @ start)).item()
     assert abs(off) <= 0.02 * T * lr * decay
+
+
+def test_gradients_that_overlap_weights_are_refused():
+    room = torch.zeros(4096, device=DEV)
+    p = room[1024:2048]
+    for g in (p, room[512:1536], room[1536:2560], room[1020:2044]):
+        with pytest.raises(ValueError, match="overlap"):
+            moe.AdamW([p], [g], lr=1e-3)
+    q = room[2048:3072]
+    with pytest.raises(ValueError, match="overlap"):  # another tensor's weights
+        moe.AdamW([p, q], [room[3072:], p], lr=1e-3)
+    with pytest.raises(ValueError, match="overlap"):
+        moe.AdamW([p], [room.view(torch.bfloat16)[2048:3072]], lr=1e-3)
+    # next to each other, and one gradient for two weights
+    moe.AdamW([p, q, room[:0]], [room[:1024], room[:1024], room[1100:1100]], lr=1e-3).step()
+    ok()
