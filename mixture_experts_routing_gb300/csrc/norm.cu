@@ -472,9 +472,8 @@ Plan plan_of(int64_t N, int H, int tensors, uint32_t ring, int kv, int threads) 
   p.lanes = 1;
   while (p.lanes < 32 && p.lanes < groups) p.lanes *= 2;
   if (groups > 32) p.lanes = (groups + 31) / 32 * 32;
-  p.rows = threads / p.lanes;
+  p.rows = threads / p.lanes;  // several of them fill a third of the ring at most, one of 16384 columns half of it
   const uint32_t row = (uint32_t)H * 2 * tensors;
-  while (p.rows > 1 && (uint64_t)p.rows * row > ring / 3) p.rows /= 2;
   p.threads = p.rows * p.lanes;
   p.steps = (uint32_t)((N + p.rows - 1) / p.rows);
   p.stage = (uint32_t)p.rows * row;
