@@ -1056,7 +1056,6 @@ int moe_adamw_step(const moe_adamw_config_t* cfg, const moe_adamw_tensor_t* tens
         t[n++] = {q.param, q.master,  q.grad, q.m, q.v, q.m_scale, q.v_scale, q.n, q.first, q.weight_decay,
                   q.grad_bf16};
     }
-    if (n == 0 && done < n_tensors) continue;
     const int k = moe::launch_adamw(a, t, n, done == n_tensors, stream);
     if (k < 0) return finish(k);
     launched += k;

@@ -8,7 +8,7 @@ import pytest
 import torch
 
 import mixture_experts_routing_gb300 as moe
-from test_gpu_adamw import Set, decode
+from test_gpu_adamw import Set, check, decode
 from test_gpu_w4 import DEV, F64, gen, ok
 
 pytestmark = pytest.mark.gpu
@@ -129,3 +129,13 @@ def test_gradients_that_overlap_weights_are_refused():
     # next to each other, and one gradient for two weights
     moe.AdamW([p, q, room[:0]], [room[:1024], room[:1024], room[1100:1100]], lr=1e-3).step()
     ok()
+
+
+@pytest.mark.parametrize("sizes", [[0] * 300 + [5] + [0] * 300, [9] * 240 + [0] * 3, [9] * 241 + [0] * 240, [0] * 481], ids=lambda s: "%d" % len(s))
+def test_empty_tensors_anywhere_in_a_long_list(sizes):
+    s = Set(sizes, True, True, 32)
+    for t in (1, 2):
+        before = s.state()
+        s.opt.step()
+        ok()
+        check(s, before, t)
