@@ -1,4 +1,5 @@
-"""Layer norm: whole rows that hold an infinity, rows whose squares pass fp32's range."""
+"""Layer norm: whole rows that hold an infinity, rows whose squares pass fp32's range, values
+around the statistics."""
 import math
 
 import pytest
@@ -6,7 +7,7 @@ import torch
 
 import mixture_experts_routing_gb300 as moe
 from test_gpu_norm import KINDS, Rows
-from test_gpu_w4 import ok
+from test_gpu_w4 import DEV, ok
 
 pytestmark = pytest.mark.gpu
 
@@ -40,3 +41,14 @@ def test_a_row_whose_squares_pass_the_range(h):
     r.forward()
     ok()
     assert r.rstd[2] == 0 and torch.equal(r.y[2], r.b.to(torch.bfloat16))
+
+
+@pytest.mark.parametrize("n,h", [(19, 1096), (5, 64), (3, 8200)])
+def test_values_behind_the_statistics_are_left(n, h):
+    r = Rows(n, h, moe.NORM_LAYER)
+    r.forward()
+    mean, rstd = (torch.full((n + 16,), 7.0, device=DEV) for _ in range(2))
+    moe.norm_forward(r.cfg, r.x, r.w, r.y, bias=r.b, add=r.add, sum=r.sum, mean=mean[:n], rstd=rstd[:n])
+    ok()
+    assert (mean[n:] == 7).all() and (rstd[n:] == 7).all()
+    assert torch.equal(mean[:n], r.mean) and torch.equal(rstd[:n], r.rstd)
