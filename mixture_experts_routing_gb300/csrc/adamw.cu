@@ -34,6 +34,10 @@ struct Table {
 static_assert(sizeof(Table) < 32000, "a kernel's arguments are at most 32764 bytes");
 
 // Two rounds of xor-shift and odd multiplication: 32 bits of which each depends on all of v.
+// Shifts and multipliers are published ones, of the least bias found for this form (C. Wellons,
+// "Prospecting for Hash Functions", 2018). The factors of the index and of the step are the
+// prime next to 2^32 over the golden ratio (Knuth's multiplicative hashing) and, for the index's
+// upper half, a prime that Y. Collet's 32-bit hash uses: any odd ones would do.
 __device__ __host__ __forceinline__ uint32_t mix32(uint32_t v) {
   v = (v ^ (v >> 16)) * 0x7FEB352Du;
   v = (v ^ (v >> 15)) * 0x846CA68Bu;
