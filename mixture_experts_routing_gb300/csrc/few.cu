@@ -10,8 +10,9 @@
 //            The last block to finish a column tile adds up its tokens' routes.
 //
 // The time is that of reading the weights, so a tile is a run of 16 weight rows that
-// passes once through a ring in shared memory (a TMA copy of 16 rows x 1024 or 512 columns
-// a stage) into mma.sync, weights as the 16 rows, tokens as the 8 columns: four warps split the
+// passes through a ring in shared memory (a TMA copy of 16 rows x 1024 or 512 columns a
+// stage) into mma.sync, once for each unit of the expert's tokens (8, 16 or 32: see
+// build_units), weights as the 16 rows, tokens as the 8 columns: four warps split the
 // columns of a stage, so a tile needs no split between blocks, and there are enough tiles
 // to keep all SMs busy from one token on (128-row tiles of the 5th-generation tensor
 // cores would leave 8 experts x 2048 features with fewer tiles than there are turns to
@@ -22,8 +23,9 @@
 // Measured, called in a row with changing inputs: 1 token, 8 of 256 experts of 7168 x 2048,
 // 113 us (705 MB: 6.3 TB/s over the whole call, 7 once the weights flow, of 6.8 that a copy
 // reaches); 33 tokens, 8 of 128 of 2048 x 768, 163 to 176 us by the experts hit; 64 tokens,
-// 2 of 8 of 512 x 1024, 32 us, which is the chain of its waits. The logits take 2 us of one
-// token's call (2048 columns) to 5 us of 33 tokens'.
+// 2 of 8 of 512 x 1024, 32 us: some 18 are the chain of its waits, the rest eight tiles an SM
+// of 16 to 32 KB, each of which pays a tile's set-up and a copy of its unit's tokens. The logits
+// take 2 us of one token's call (2048 columns) to 5 us of 33 tokens'.
 #include "act.cuh"
 #include "layer_internal.h"
 #include "moe_internal.h"
@@ -297,9 +299,10 @@ __device__ __forceinline__ void build_units(const FewArgs& a, int n, FewShared& 
     u32 += s.warp_sum[w][2];
   }
   // Units of 16 and of 32 tokens take 1.3 and 1.55 times one of 8 (their stages are shorter);
-  // an expert's second unit has its weights from the second-level cache. 64 tokens, 6 of 64
-  // experts of 4096 x 1408 (6 tokens each, some over 8): 380, 457, 552 us with 8, 16, 32;
-  // 64 tokens, 2 of 8 of 512 x 1024 (16 each): 42, 37, 35.
+  // an expert's second unit finds weights of the first in the second-level cache, at the sizes
+  // measured. 64 tokens, 6 of 64 experts (6 tokens each, some over 8), with 8, 16, 32: 4096 x
+  // 1408 380, 457, 552 us, 7168 x 2048 895, 1086, 1304; 4 of 32 of 7168 x 2048 (8 each) 546,
+  // 587, 687; 2 of 8 (16 each) 258, 263, 243, of 512 x 1024 42, 37, 35.
   const int per = 10 * u8 <= 13 * u16 && 20 * u8 <= 31 * u32 ? 8 : 26 * u16 <= 31 * u32 ? 16 : 32;
   __syncthreads();  // the sums are written again below
   const int u = (c + per - 1) / per;
@@ -766,6 +769,8 @@ __device__ __forceinline__ void outputs_role(const FewArgs& a, FewShared& s, int
           g += q[0];
           u += q[64];
         }
+        // bf16, as the tensor cores take it and the ordinary layer has it: without an addend y is off
+        // by 1.4 times what h in 32 bits gives (7 tokens, 4096 x 1408: 0.0024 against 0.0017)
         reinterpret_cast<__nv_bfloat16*>(h)[(size_t)s.list[at + c] * a.I + t.row + f] = __float2bfloat16_rn(act_fwd<ACT>(g) * u);
       }
       __syncwarp();
