@@ -9,9 +9,11 @@
 //
 // 32 bits: bound by memory, 44 million bf16 weights with f32 masters and bf16 gradients in
 // 192 us, 6.4 TB/s of the 6.8 that a copy reaches. 8 bits: 277 million with f32 gradients
-// in 824 us, 6.1 TB/s; a value takes some 60 instructions, 72 % of the issue slots are used,
-// and the exact root and the hash are what could go of them (799 us without either). Loading
-// the next block ahead of this one's work cost the fourth block an SM (955 us).
+// in 837 us, 6.0 TB/s; a value takes some 90 instructions of a lane, 72 % of the issue slots are
+// used. At 824 us, before roots had a smallest code (+4) and decay was added to the update first
+// (+9), it took 799 without the exact root or without the hash, and 955 with the next block
+// loaded ahead of this one's work, which cost the fourth block an SM. A launch carries its whole
+// table, 21 KB: of a call's 5.6 us of host time for a few tensors 0.9.
 #include "act.cuh"
 #include "layer_internal.h"
 #include "moe_internal.h"

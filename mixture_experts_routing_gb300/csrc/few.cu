@@ -302,7 +302,8 @@ __device__ __forceinline__ void build_units(const FewArgs& a, int n, FewShared& 
   // an expert's second unit finds weights of the first in the second-level cache, at the sizes
   // measured. 64 tokens, 6 of 64 experts (6 tokens each, some over 8), with 8, 16, 32: 4096 x
   // 1408 380, 457, 552 us, 7168 x 2048 895, 1086, 1304; 4 of 32 of 7168 x 2048 (8 each) 546,
-  // 587, 687; 2 of 8 (16 each) 258, 263, 243, of 512 x 1024 42, 37, 35.
+  // 587, 687 (at the rule's border: it takes 16); 2 of 8 (16 each) 258, 263, 243, of 512 x 1024
+  // 42, 37, 35.
   const int per = 10 * u8 <= 13 * u16 && 20 * u8 <= 31 * u32 ? 8 : 26 * u16 <= 31 * u32 ? 16 : 32;
   __syncthreads();  // the sums are written again below
   const int u = (c + per - 1) / per;
